@@ -253,7 +253,7 @@ def _plain_route_bwd(s):
 
 def _plain_quantize(x):
     xf = x.float()
-    scale = xf.abs().amax(1) / 127
+    scale = (xf.abs().amax(1).double() / 127).float()  # torch divides by a plain number through its reciprocal
     div = torch.where(scale == 0, torch.ones_like(scale), scale)
     # the quotient in 64 bits: 32 would move values next to a half step
     return (xf.double() / div.double()[:, None]).round().clamp(-127, 127).to(torch.int8), scale
@@ -393,7 +393,7 @@ def exact(case, seed):
         return {"dlogits": sc * full - sc * (sc * full).sum(1, keepdim=True)}
     x = s["x"].double()
     sd = x.abs().max(1).values / 127
-    s32 = (s["x"].float().abs().max(1).values / 127).double()  # the step that the stored scale stands for
+    s32 = sd.float().double()  # the step that the stored scale stands for
     q = torch.where(s32[:, None] > 0, torch.round(x / s32[:, None].clamp(min=1e-300)), 0.0).clamp(-127, 127)
     lens = [b - a for a, b in zip(s["splits"], s["splits"][1:])]
     no = c["N"] // 2 if c["swiglu"] else c["N"]
