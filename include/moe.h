@@ -51,7 +51,9 @@ typedef enum moe_status {
 
 typedef enum moe_dtype {
     MOE_F32 = 0,   /* FP32 activations and expert weights, FP32 FMA arithmetic */
-    MOE_BF16 = 1   /* BF16 activations and expert weights, FP32 accumulation (tcgen05) */
+    MOE_BF16 = 1,  /* BF16 activations and expert weights, FP32 accumulation (tcgen05) */
+    MOE_F16 = 2    /* FP16 (IEEE binary16): the operators around the layer only (moe_layer_norm
+                      and what follows it below); a moe_config refuses it */
 } moe_dtype;
 
 /* Gate rule. c denotes the selection score, b the balance bias.
@@ -332,6 +334,127 @@ moe_status moe_backward_workspace_size(const moe_config* cfg, size_t* bytes);
 moe_status moe_backward(const moe_config* cfg, const void* x, const moe_weights* w,
                         const float* dout, const moe_grads* grads, void* ws, size_t ws_bytes,
                         void* bws, size_t bws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around the layer: the norm in front of it, group-limited routing,
+ * and 8-bit expert products for serving. Together they make a block
+ *   x -> moe_layer_norm -> router logits -> moe_group_route -> moe_dispatch
+ *     -> moe_quantize_rows -> moe_matmul_int8 (gate/up, SwiGLU)
+ *     -> moe_quantize_rows -> moe_matmul_int8 (down) -> weighted sum per token.
+ * The row operators take rows whose elements are contiguous and whose pitch
+ * (`*_stride`, in elements, >= the row's length) is the caller's; zero rows
+ * are allowed and launch nothing. Outputs must not overlap inputs. Pointers
+ * need their element's alignment; rows on 16-byte boundaries run faster.
+ * Each call can be captured into a CUDA graph; results do not depend on the
+ * order in which CTAs run.
+ * ------------------------------------------------------------------------ */
+
+/* Layer norm of R rows of d elements (d <= 2^24), x and y of type dtype:
+ *     mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps)
+ *     y  = (x - mu) rstd gamma + beta
+ * with FP32 statistics and arithmetic, y rounded once. gamma, beta [d] FP32,
+ * either may be NULL (1, 0); mean, rstd [R] FP32 outputs, either may be NULL.
+ * eps >= 0. */
+moe_status moe_layer_norm(int32_t R, int32_t d, int32_t dtype, const void* x, int64_t x_stride,
+                          const float* gamma, const float* beta, float eps, void* y, int64_t y_stride,
+                          float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace moe_layer_norm_backward needs where it returns dgamma or
+ * dbeta (per-CTA column sums). */
+moe_status moe_layer_norm_backward_workspace_size(int32_t R, int32_t d, size_t* bytes);
+
+/* Gradients of L = sum(dy y) given the forward's x, mean and rstd: with
+ * xh = (x - mu) rstd and g = dy gamma,
+ *     dx = rstd (g - mean(g) - xh mean(g xh)),  dgamma = sum_rows dy xh,
+ *     dbeta = sum_rows dy
+ * dy, x, dx of type dtype; dgamma, dbeta [d] FP32, overwritten (zeros for
+ * R = 0), either may be NULL. ws: 16-byte aligned, needed where one of them
+ * is asked for. Sums run in a fixed order: bit-reproducible. */
+moe_status moe_layer_norm_backward(int32_t R, int32_t d, int32_t dtype, const void* dy, int64_t dy_stride,
+                                   const void* x, int64_t x_stride, const float* mean, const float* rstd,
+                                   const float* gamma, void* dx, int64_t dx_stride, float* dgamma,
+                                   float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
+typedef enum moe_score {
+    MOE_SCORE_SIGMOID = 0,  /* s = sigmoid(r) */
+    MOE_SCORE_SOFTMAX = 1   /* s = softmax of r over all E */
+} moe_score;
+
+typedef struct moe_group_route_config {
+    int32_t T;            /* tokens, >= 0 */
+    int32_t E;            /* experts, 1..256 */
+    int32_t K;            /* experts taken per token, 1..16, <= topk_groups E / n_groups */
+    int32_t n_groups;     /* groups of E / n_groups consecutive experts, 1..32 (1: no groups) */
+    int32_t topk_groups;  /* groups kept per token */
+    int32_t group_rank;   /* a group's score: 1 = its largest choice, 2 = the sum of its two largest */
+    int32_t score;        /* moe_score */
+    int32_t renormalize;  /* 0 or 1: divide the K weights by their sum */
+    float scale;          /* factor on the weights */
+    int32_t dtype;        /* moe_dtype of logits and dlogits */
+} moe_group_route_config;
+
+/* Group-limited routing of T rows of E logits: choices c = s + bias, the
+ * topk_groups best groups, the K largest c among their experts, weights from
+ * the uncorrected s. Equal values rank the lower index first; what is taken
+ * is what 64-bit arithmetic on the given logits and bias takes. An expert
+ * whose logit or choice is -inf or NaN is never taken: masked experts, and
+ * rows that are masked whole, need no other form. Slots without an expert
+ * hold id -1 and weight 0 (moe_dispatch skips them and reports
+ * MOE_ERR_DEVICE_INDEX). Groups whose experts are all masked rank last.
+ *   logits [T, E] (dtype, pitch row_stride), bias [E] FP32 or NULL,
+ *   topk_idx [T, K] int32, topk_w [T, K] FP32, slot order by choice. */
+moe_status moe_group_route(const moe_group_route_config* cfg, const void* logits, int64_t row_stride,
+                           const float* bias, int32_t* topk_idx, float* topk_w, void* stream);
+
+/* Gradient of L = sum(dw topk_w) with respect to the logits, the selection
+ * (topk_idx, as moe_group_route gave it: the ids of a row are distinct) held
+ * fixed; the bias only chooses and has none. dlogits [T, E] contiguous
+ * (dtype) is overwritten; masked experts get 0. Ids outside [0, E) are
+ * skipped. */
+moe_status moe_group_route_backward(const moe_group_route_config* cfg, const void* logits,
+                                    int64_t row_stride, const int32_t* topk_idx, const float* dw,
+                                    void* dlogits, void* stream);
+
+/* R rows of K elements to 8-bit integers: scale[i] = max_k |x[i, k]| / 127,
+ * q[i, k] = x[i, k] / scale[i] to the nearest integer, ties to even (exactly:
+ * the quotient is not rounded first). A row of zeros has scale 0; a row with
+ * an infinity or a NaN has q = 0 and scale NaN. q [R, K] contiguous. */
+moe_status moe_quantize_rows(int32_t R, int32_t K, int32_t dtype, const void* x, int64_t x_stride,
+                             int8_t* q, float* scale, void* stream);
+
+typedef struct moe_int8_config {
+    int32_t M;          /* product rows, >= 0 */
+    int32_t Ma;         /* rows of a */
+    int32_t K;          /* reduction length, a multiple of 16, at most 131056 */
+    int32_t N;          /* channels of b per expert */
+    int32_t E;          /* experts, 1..256 */
+    int32_t swiglu;     /* 1: channels [0, N/2) are gates, [N/2, N) ups, the output SiLU(gate) up */
+    int32_t out_dtype;  /* moe_dtype of out */
+} moe_int8_config;
+
+/* Bytes of workspace moe_matmul_int8 needs for cfg; 0: ws may be NULL. */
+moe_status moe_matmul_int8_workspace_size(const moe_int8_config* cfg, size_t* bytes);
+
+/* 8-bit products with a scale per row of a and per channel of b, grouped by
+ * expert: product row i of expert e (offsets[e] <= i < offsets[e + 1]) reads
+ * row j = rows[i] of a (rows NULL: j = i), and
+ *     y[i, n] = a_scale[j] b_scale[e, n] sum_k a[j, k] b[e, n, k]
+ * with the sum exact, in integers, then FP32; out[i, n] = y[i, n], or with
+ * swiglu out[i, n] = SiLU(y[i, n]) y[i, N/2 + n], rounded once.
+ *   a [Ma, K] int8, pitch a_stride (a multiple of 16 elements), a_scale [Ma];
+ *   b [E, N, K] int8 contiguous, b_scale [E, N]; offsets [E + 1] int32
+ *   (ascending from 0, moe_dispatch's; NULL with E = 1: all rows), rows [M]
+ *   int32 or NULL (moe_dispatch's sorted_token); out [M, N or N/2].
+ *   a, b, out 16-byte aligned, ws 256-byte aligned.
+ * Rows from offsets[E] on are written as zeros. Offsets are clamped to
+ * [0, M]; a row index outside [0, Ma) makes its product row NaN and, where
+ * the workspace has 256 bytes or more, sets MOE_ERR_DEVICE_INDEX in its
+ * error word. The call adds to that word and never clears it: have it zeroed
+ * before the first call, moe_workspace_status reads and clears it. */
+moe_status moe_matmul_int8(const moe_int8_config* cfg, const int8_t* a, int64_t a_stride,
+                           const float* a_scale, const int8_t* b, const float* b_scale,
+                           const int32_t* offsets, const int32_t* rows, void* out, void* ws,
+                           size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, then reads and clears the device-side error word of
  * the workspace: MOE_OK, MOE_ERR_TIMEOUT (a bounded device wait ran out and

@@ -19,7 +19,7 @@ from . import build as _build
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA, \
     MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_INDEX = range(7)
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 GATES = {"softmax_topk": 0, "softmax_all_renorm": 1, "sigmoid": 2}
 
 HEADER = os.path.join(_build.ROOT, "include", "moe.h")
@@ -60,6 +60,16 @@ class Views(ctypes.Structure):
                  "sorted_token", "sorted_w", "inv")]
 
 
+class GroupRouteConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "E", "K", "n_groups", "topk_groups", "group_rank", "score", "renormalize")] + \
+        [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class Int8Config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "Ma", "K", "N", "E", "swiglu", "out_dtype")]
+
+
 _lib = None
 
 
@@ -72,7 +82,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"libmoe.so is not built ({path}); run "
                                "mixture_experts_ffn_fp32_gb300.build.build() first")
         L = ctypes.CDLL(path)
-        vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         cfgp = ctypes.POINTER(Config)
         sigs = {
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -92,6 +102,20 @@ def lib() -> ctypes.CDLL:
             "moe_backward_workspace_size": (ctypes.c_int, [cfgp, ctypes.POINTER(sz)]),
             "moe_backward": (ctypes.c_int, [cfgp, vp, ctypes.POINTER(Weights), vp,
                                             ctypes.POINTER(Grads), vp, sz, vp, sz, vp]),
+            "moe_layer_norm": (ctypes.c_int, [i32, i32, i32, vp, i64, vp, vp, ctypes.c_float, vp, i64,
+                                              vp, vp, vp]),
+            "moe_layer_norm_backward_workspace_size": (ctypes.c_int, [i32, i32, ctypes.POINTER(sz)]),
+            "moe_layer_norm_backward": (ctypes.c_int, [i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp,
+                                                       i64, vp, vp, vp, sz, vp]),
+            "moe_group_route": (ctypes.c_int, [ctypes.POINTER(GroupRouteConfig), vp, i64, vp, vp, vp,
+                                               vp]),
+            "moe_group_route_backward": (ctypes.c_int, [ctypes.POINTER(GroupRouteConfig), vp, i64, vp,
+                                                        vp, vp, vp]),
+            "moe_quantize_rows": (ctypes.c_int, [i32, i32, i32, vp, i64, vp, vp, vp]),
+            "moe_matmul_int8_workspace_size": (ctypes.c_int, [ctypes.POINTER(Int8Config),
+                                                              ctypes.POINTER(sz)]),
+            "moe_matmul_int8": (ctypes.c_int, [ctypes.POINTER(Int8Config), vp, i64, vp, vp, vp, vp, vp,
+                                               vp, vp, sz, vp]),
             "moe_timing_begin": (ctypes.c_int, [i32, ctypes.c_uint32]),
             "moe_timing_end": (ctypes.c_int, [ctypes.POINTER(ctypes.c_float), i32,
                                               ctypes.POINTER(i32), ctypes.POINTER(i32)]),
@@ -457,6 +481,254 @@ def sign_bias_update(counts: torch.Tensor, N: int, K: int, bias: torch.Tensor, a
 def workspace_status(ws: torch.Tensor, stream=None) -> int:
     """Synchronises and returns (and clears) the workspace's device error status."""
     return lib().moe_workspace_status(ws.data_ptr(), _stream(stream))
+
+
+# ---------------------------------------------------------------------------
+# Operators around the layer
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+_OUT_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """A [rows, n] CUDA tensor with contiguous rows at any pitch; returns its pitch."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or t.size(1) < 1:
+        raise ValueError(f"{name} must be a [rows, n] tensor with n >= 1, got {tuple(t.shape)}")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.size(1) > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.size(0) > 1:
+        if t.stride(0) < t.size(1):
+            raise ValueError(f"{name}'s rows must not overlap")
+        return t.stride(0)
+    return t.size(1)
+
+
+class _On:
+    """Outputs and scratch of a call belong to the stream it runs on, and its
+    inputs stay allocated until that stream is done with them, whichever
+    stream they were made on."""
+
+    def __init__(self, stream, *inputs):
+        self.stream, self.inputs = stream, inputs
+
+    def __enter__(self):
+        self.ctx = torch.cuda.stream(self.stream)
+        self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        self.ctx.__exit__(*exc)
+        for t in self.inputs:
+            if t is not None:
+                t.record_stream(self.stream)
+
+
+class _Here:
+    """_On for the current stream: nothing to arrange."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(stream, *inputs):
+    return _HERE if stream is None else _On(stream, *inputs)
+
+
+def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, stream=None) -> dict:
+    """moe_layer_norm: x [R, d] (FP32, BF16 or FP16; rows at any pitch), weight and
+    bias [d] FP32 or None. Returns y [R, d] in x's type and the FP32 statistics
+    mean and rstd [R] that the backward takes."""
+    xs = _rows(x, "x")
+    R, d = x.shape
+    if weight is not None:
+        _dev(weight, torch.float32, "weight", (d,))
+    if bias is not None:
+        _dev(bias, torch.float32, "bias", (d,))
+    with _on(stream, x, weight, bias):
+        y = torch.empty((R, d), dtype=x.dtype, device=x.device)
+        st = torch.empty((2, R), dtype=torch.float32, device=x.device)
+        mean, rstd = st.unbind(0)
+        _check(lib().moe_layer_norm(R, d, _DTYPES[x.dtype], x.data_ptr(), xs, _ptr(weight), _ptr(bias), eps,
+                                    y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _stream(stream)),
+               "moe_layer_norm")
+    return {"y": y, "mean": mean, "rstd": rstd}
+
+
+def layer_norm_backward_workspace_size(R: int, d: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_layer_norm_backward_workspace_size(R, d, ctypes.byref(n)),
+           "moe_layer_norm_backward_workspace_size")
+    return n.value
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight=None, weight_grads: bool = True, ws: torch.Tensor | None = None,
+                        stream=None) -> dict:
+    """moe_layer_norm_backward: dx [R, d] in x's type and, with weight_grads,
+    dweight and dbias [d] FP32, given layer_norm's mean and rstd. ws: uint8 of
+    layer_norm_backward_workspace_size(R, d) bytes (allocated when None)."""
+    xs = _rows(x, "x")
+    R, d = x.shape
+    dys = _rows(dy, "dy", x.dtype, x.shape)
+    _dev(mean, torch.float32, "mean", (R,))
+    _dev(rstd, torch.float32, "rstd", (R,))
+    if weight is not None:
+        _dev(weight, torch.float32, "weight", (d,))
+    with _on(stream, dy, x, mean, rstd, weight, ws):
+        out = {"dx": torch.empty((R, d), dtype=x.dtype, device=x.device)}
+        if weight_grads:
+            dwb = torch.empty((2, d), dtype=torch.float32, device=x.device)
+            out["dweight"], out["dbias"] = dwb.unbind(0)
+            if ws is None:
+                ws = torch.empty(layer_norm_backward_workspace_size(R, d), dtype=torch.uint8, device=x.device)
+        _check(lib().moe_layer_norm_backward(R, d, _DTYPES[x.dtype], dy.data_ptr(), dys, x.data_ptr(), xs,
+                                             mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
+                                             out["dx"].data_ptr(), d, _ptr(out.get("dweight")),
+                                             _ptr(out.get("dbias")), _ptr(ws), 0 if ws is None else ws.numel(),
+                                             _stream(stream)), "moe_layer_norm_backward")
+    return out
+
+
+def _group_config(logits, K, n_groups, topk_groups, group_rank, score, renormalize, scale):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    return GroupRouteConfig(logits.size(0), logits.size(1), K, n_groups, topk_groups, group_rank, SCORES[score],
+                            1 if renormalize else 0, scale, _DTYPES[logits.dtype])
+
+
+def group_route(logits: torch.Tensor, K: int, n_groups: int = 1, topk_groups: int = 1, bias=None,
+                score: str = "sigmoid", group_rank: int = 2, renormalize: bool = True, scale: float = 1.0,
+                stream=None) -> dict:
+    """moe_group_route: group-limited top-K routing of logits [T, E] (FP32, BF16 or
+    FP16; rows at any pitch). bias [E] FP32 enters the choice, not the weights;
+    group_rank 1 ranks groups by their best choice, 2 by the sum of their two
+    best. Experts whose logit is -inf are never taken; slots that stay empty
+    hold id -1, weight 0. Returns idx [T, K] int32 and w [T, K] FP32."""
+    ls = _rows(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _dev(bias, torch.float32, "bias", (E,))
+    cfg = _group_config(logits, K, n_groups, topk_groups, group_rank, score, renormalize, scale)
+    with _on(stream, logits, bias):
+        out = {"idx": torch.empty((T, max(K, 0)), dtype=torch.int32, device=logits.device),
+               "w": torch.empty((T, max(K, 0)), dtype=torch.float32, device=logits.device)}
+        _check(lib().moe_group_route(ctypes.byref(cfg), logits.data_ptr(), ls, _ptr(bias), out["idx"].data_ptr(),
+                                     out["w"].data_ptr(), _stream(stream)), "moe_group_route")
+    return out
+
+
+def group_route_backward(dw: torch.Tensor, idx: torch.Tensor, logits: torch.Tensor, score: str = "sigmoid",
+                         renormalize: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """moe_group_route_backward: the gradient with respect to the logits (their
+    type) of sum(dw * w), the selection idx held fixed."""
+    ls = _rows(logits, "logits")
+    T, E = logits.shape
+    if idx.dim() != 2:
+        raise ValueError(f"idx must be [T, K], got {tuple(idx.shape)}")
+    K = idx.size(1)
+    _dev(idx, torch.int32, "idx", (T, K))
+    _dev(dw, torch.float32, "dw", (T, K))
+    cfg = _group_config(logits, K, 1, 1, 1, score, renormalize, scale)
+    with _on(stream, dw, idx, logits):
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        _check(lib().moe_group_route_backward(ctypes.byref(cfg), logits.data_ptr(), ls, idx.data_ptr(),
+                                              dw.data_ptr(), out.data_ptr(), _stream(stream)),
+               "moe_group_route_backward")
+    return out
+
+
+def quantize_rows(x: torch.Tensor, stream=None) -> dict:
+    """moe_quantize_rows: x [R, K] (FP32, BF16 or FP16; rows at any pitch) to q
+    [R, K] int8 and scale [R] FP32 with x ~ q * scale. Weights [E, K, N] are laid
+    out for matmul_int8 by quantising the rows of their transpose:
+    ``quantize_rows(W.transpose(1, 2).reshape(E * N, K))``."""
+    xs = _rows(x, "x")
+    R, K = x.shape
+    with _on(stream, x):
+        out = {"q": torch.empty((R, K), dtype=torch.int8, device=x.device),
+               "scale": torch.empty((R,), dtype=torch.float32, device=x.device)}
+        _check(lib().moe_quantize_rows(R, K, _DTYPES[x.dtype], x.data_ptr(), xs, out["q"].data_ptr(),
+                                       out["scale"].data_ptr(), _stream(stream)), "moe_quantize_rows")
+    return out
+
+
+def _int8_config(M, Ma, K, N, E, swiglu, out_dtype) -> Int8Config:
+    if out_dtype not in _OUT_DTYPES:
+        raise ValueError(f"out_dtype must be one of {sorted(_OUT_DTYPES)}, got {out_dtype!r}")
+    return Int8Config(M, Ma, K, N, E, 1 if swiglu else 0, _DTYPES[_OUT_DTYPES[out_dtype]])
+
+
+def _int8_ws(cfg) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_matmul_int8_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_matmul_int8_workspace_size")
+    return n.value
+
+
+def alloc_int8_workspace(M: int, K: int, N: int, E: int = 1, swiglu: bool = False,
+                         device="cuda") -> torch.Tensor:
+    """A workspace for matmul_int8 calls of up to M product rows (its error word
+    zeroed; workspace_status reads and clears it)."""
+    n = max(_int8_ws(_int8_config(m, m, K, N, E, swiglu, "f32")) for m in {M, min(M, 1)})
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, offsets=None,
+                rows=None, swiglu: bool = False, out_dtype: str = "bf16", ws: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """moe_matmul_int8: 8-bit products grouped by expert. a [Ma, K] int8 and a_scale
+    [Ma] (quantize_rows), b [E, N, K] int8 and b_scale [E, N]; offsets [E + 1]
+    and rows [M] int32 as dispatch's offsets and sorted_token (None: one expert
+    takes every row; rows of a in order). With swiglu the channels of an
+    expert are its gates, then its ups, and the output is SiLU(gate) * up.
+    Returns out [M, N] ([M, N / 2] with swiglu). ws: see alloc_int8_workspace
+    (allocated when None)."""
+    if a.dim() != 2 or b.dim() != 3 or not a.is_cuda or a.dtype != torch.int8:
+        raise ValueError("a must be a [Ma, K] int8 CUDA tensor and b [E, N, K]")
+    E, N, K = b.shape
+    Ma = a.size(0)
+    if a.size(1) != K or (K > 1 and a.stride(1) != 1):
+        raise ValueError(f"a must have contiguous rows of {K} elements, got {tuple(a.shape)}")
+    _dev(b, torch.int8, "b")
+    _dev(a_scale, torch.float32, "a_scale", (Ma,))
+    _dev(b_scale, torch.float32, "b_scale", (E, N))
+    if offsets is not None:
+        _dev(offsets, torch.int32, "offsets", (E + 1,))
+    M = Ma
+    if rows is not None:
+        if rows.dim() != 1:
+            raise ValueError(f"rows must be [M], got {tuple(rows.shape)}")
+        _dev(rows, torch.int32, "rows")
+        M = rows.size(0)
+    cfg = _int8_config(M, Ma, K, N, E, swiglu, out_dtype)
+    with _on(stream, a, a_scale, b, b_scale, offsets, rows, ws):
+        if ws is None:
+            n = _int8_ws(cfg)
+            if n:
+                ws = torch.empty(n, dtype=torch.uint8, device=a.device)
+        out = torch.empty((M, N // 2 if swiglu else N), dtype=_OUT_DTYPES[out_dtype], device=a.device)
+        _check(lib().moe_matmul_int8(ctypes.byref(cfg), a.data_ptr(), a.stride(0) if Ma > 1 else K,
+                                     a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),
+                                     _ptr(rows), out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+                                     _stream(stream)), "moe_matmul_int8")
+    return out
 
 
 def launch_count() -> int:

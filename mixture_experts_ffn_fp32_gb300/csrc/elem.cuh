@@ -1,0 +1,96 @@
+// Element types of the operators around the layer (FP32, BF16, FP16): vector
+// loads to FP32, vector stores rounded once to nearest-even, and the warp and
+// CTA sums they share.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+template <typename T>
+MOE_DEV float to_f32(T v);
+template <>
+MOE_DEV float to_f32<float>(float v) { return v; }
+template <>
+MOE_DEV float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+MOE_DEV float to_f32<__half>(__half v) { return __half2float(v); }
+
+template <typename T>
+MOE_DEV T from_f32(float v);
+template <>
+MOE_DEV float from_f32<float>(float v) { return v; }
+template <>
+MOE_DEV __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+MOE_DEV __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// VEC consecutive elements as loaded: one 16-byte word, or one element.
+template <typename T, int VEC>
+struct Raw {
+    static_assert(VEC * sizeof(T) == 16, "a vector is 16 bytes");
+    uint4 v;
+    MOE_DEV void load(const T* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    MOE_DEV void clear() { v = make_uint4(0, 0, 0, 0); }
+    MOE_DEV void get(float (&f)[VEC]) const {
+        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = to_f32(e[i]);
+    }
+    MOE_DEV void set(const float (&f)[VEC]) {
+        T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) e[i] = from_f32<T>(f[i]);
+    }
+    MOE_DEV void store(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
+};
+template <typename T>
+struct Raw<T, 1> {
+    T v;
+    MOE_DEV void load(const T* p) { v = *p; }
+    MOE_DEV void clear() { v = from_f32<T>(0.0f); }
+    MOE_DEV void get(float (&f)[1]) const { f[0] = to_f32(v); }
+    MOE_DEV void set(const float (&f)[1]) { v = from_f32<T>(f[0]); }
+    MOE_DEV void store(T* p) const { *p = v; }
+};
+
+// sigmoid(v) = exp(v) / (1 + exp(v)) below zero, where exp(-v) would leave
+// FP32's range while v sigmoid(v) is still in it.
+MOE_DEV float sigmoid_f(float v) {
+    const float e = expf(-fabsf(v));
+    return (v >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+
+MOE_DEV float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sums of a and b over the TPR threads of a row, the same in all of them and
+// in a fixed order. TPR = 32: within the warp. Else over the CTA (TPR
+// threads), through `scratch`, two halves of 2 * TPR / 32 floats used in turn:
+// the sync of one call orders the reads of the call before last.
+template <int TPR>
+MOE_DEV void row_sum2(float& a, float& b, float* scratch, int& turn) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if constexpr (TPR > 32) {
+        constexpr int W = TPR / 32;
+        float* s = scratch + (turn & 1) * 2 * W;
+        ++turn;
+        const int w = threadIdx.x >> 5;
+        if (lane_id() == 0) {
+            s[w] = a;
+            s[W + w] = b;
+        }
+        __syncthreads();
+        const int l = static_cast<int>(lane_id());
+        a = warp_sum(l < W ? s[l] : 0.0f);
+        b = warp_sum(l < W ? s[W + l] : 0.0f);
+    }
+}
+
+}  // namespace moe

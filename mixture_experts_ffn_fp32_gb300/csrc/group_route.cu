@@ -1,0 +1,459 @@
+// Group-limited routing from given logits, forward and backward.
+//
+//   s = sigmoid(r), or softmax of r over the E experts;  c = s + b
+//   an expert counts where r > -inf and c > -inf (a NaN never does)
+//   group score = sum of the group's n largest c (n = 1 or 2; what it has of them)
+//   the topk_groups best groups stay, the K largest c of their experts are taken,
+//   equal values rank the lower index first; slots left over hold id -1, weight 0
+//   w = scale s_sel, or scale s_sel / sum s_sel
+//
+// Which experts are taken is decided as 64-bit arithmetic decides it, without
+// paying for it: FP32 scores come with an error bound, and only a token whose
+// taken ranks, or the groups on either side of the border, lie within it is
+// ranked again in FP64 (about one token in a thousand on random logits).
+//
+// One warp per token, E / 32 consecutive experts a lane; bound by the read of
+// the logits for large batches, by latency below a few thousand tokens.
+#include <math_constants.h>
+
+#include "elem.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int WARPS = 8;
+constexpr unsigned FULL = 0xffffffffu;
+
+// Largest value over the warp (no NaN among them).
+MOE_DEV float warp_max(float v) {
+    const int u = __float_as_int(v);  // order as signed integers: negative floats reversed
+    const int k = __reduce_max_sync(FULL, u ^ ((u >> 31) & 0x7fffffff));
+    return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
+MOE_DEV double warp_max(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+template <typename F>
+MOE_DEV F warp_add(F v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+MOE_DEV float expo(float v) { return expf(v); }
+MOE_DEV double expo(double v) { return exp(v); }
+
+// Logits as numbers that order: a NaN becomes -inf (never taken). -0 as +0,
+// so that equal values are equal bits.
+MOE_DEV float clean(float r) { return r > -CUDART_INF_F ? r + 0.0f : -CUDART_INF_F; }
+
+struct Params {
+    int T, E, K, G, gs, TG, rank, softmax, renorm;
+    int lg;       // lanes of a group where groups fill whole lanes and lg is a power of two, else 0
+    float scale;
+    long long stride;
+    const float* bias;
+};
+
+template <int VPL, typename T, bool VEC>
+MOE_DEV void load_row(const T* row, int lane, int E, float (&r)[VPL]) {
+    const int e0 = lane * VPL;
+    if constexpr (VEC) {
+        constexpr int B = VPL * sizeof(T) >= 16 ? 16 : VPL * sizeof(T);
+        constexpr int N = B / sizeof(T);
+        if (e0 < E) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += N) {
+                alignas(16) T v[N];
+                if constexpr (B == 16)
+                    *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(row + e0 + i);
+                else if constexpr (B == 8)
+                    *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(row + e0 + i);
+                else if constexpr (B == 4)
+                    *reinterpret_cast<uint32_t*>(v) = *reinterpret_cast<const uint32_t*>(row + e0 + i);
+                else
+                    v[0] = row[e0 + i];
+#pragma unroll
+                for (int j = 0; j < N; ++j) r[i + j] = clean(to_f32(v[j]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) r[i] = -CUDART_INF_F;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) r[i] = e0 + i < E ? clean(to_f32(row[e0 + i])) : -CUDART_INF_F;
+    }
+}
+
+// The two largest of (a1, a2) and (b1, b2).
+template <typename F>
+MOE_DEV void merge2(F& a1, F& a2, F b1, F b2) {
+    const F lo = a1 < b1 ? a1 : b1;
+    a1 = a1 < b1 ? b1 : a1;
+    a2 = a2 < b2 ? b2 : a2;
+    a2 = a2 < lo ? lo : a2;
+}
+
+// Scores and choices of a row in F; m and z: softmax maximum and denominator.
+template <typename F, int VPL>
+MOE_DEV void choices(const Params& p, const float (&r)[VPL], int lane, F (&c)[VPL], float& m, F& z) {
+    const F ninf = -static_cast<F>(CUDART_INF_F);
+    if (p.softmax) {
+        float mx = r[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, r[i]);
+        m = warp_max(mx);
+        F s = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            // equal to the maximum: 1, also where both are infinite
+            c[i] = r[i] == m ? static_cast<F>(1) : expo(static_cast<F>(r[i]) - static_cast<F>(m));
+            if (r[i] == -CUDART_INF_F) c[i] = 0;
+            s += c[i];
+        }
+        z = warp_add(s);
+        if (z == 0) z = 1;
+    } else {
+        m = 0.0f;
+        z = 1;
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane * VPL + i;
+        F s = p.softmax ? c[i] / z : static_cast<F>(1) / (static_cast<F>(1) + expo(-static_cast<F>(r[i])));
+        if (p.bias != nullptr && e < p.E) s += static_cast<F>(__ldg(p.bias + e));
+        c[i] = (r[i] > -CUDART_INF_F && s > ninf) ? s : ninf;
+    }
+}
+
+// Leaves only the experts of the kept groups in c. lo, hi: the lowest kept and
+// the highest dropped group score (ninf: none).
+template <typename F, int VPL>
+MOE_DEV void keep_groups(const Params& p, int lane, F (&c)[VPL], F& lo, F& hi) {
+    const F ninf = -static_cast<F>(CUDART_INF_F);
+    F mine = ninf;  // score of group `lane`
+    if (p.lg) {
+        F a1 = c[0], a2 = ninf;
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) merge2(a1, a2, c[i], ninf);
+        for (int o = 1; o < p.lg; o <<= 1)
+            merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
+        const F g = (p.rank == 2 && a2 > ninf) ? a1 + a2 : a1;
+        mine = __shfl_sync(FULL, g, lane * p.lg & 31);
+        if (lane >= p.G) mine = ninf;
+    } else {
+        for (int g = 0; g < p.G; ++g) {
+            F a1 = ninf, a2 = ninf;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if ((lane * VPL + i) / p.gs == g) merge2(a1, a2, c[i], ninf);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+                merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
+            if (lane == g) mine = (p.rank == 2 && a2 > ninf) ? a1 + a2 : a1;
+        }
+    }
+    int before = 0;  // groups that rank before mine
+    for (int g = 0; g < p.G; ++g) {
+        const F o = __shfl_sync(FULL, mine, g);
+        before += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+    }
+    const bool kept = lane < p.G && before < p.TG;
+    const unsigned keep = __ballot_sync(FULL, kept);
+    lo = -warp_max(kept ? -mine : ninf);
+    hi = warp_max(lane < p.G && !kept ? mine : ninf);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int g = (lane * VPL + i) / p.gs;
+        if (g >= 32 || !((keep >> g) & 1u)) c[i] = ninf;
+    }
+}
+
+// The n largest of c in order; lane k receives the k-th (id -1: none).
+template <typename F, int VPL>
+MOE_DEV void take(F (&c)[VPL], int lane, int n, int& id, F& val) {
+    const F ninf = -static_cast<F>(CUDART_INF_F);
+    id = -1;
+    val = ninf;
+    F best = c[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i)
+        if (c[i] > best) {
+            best = c[i];
+            at = i;
+        }
+    for (int k = 0; k < n; ++k) {
+        const F v = warp_max(best);
+        if (!(v > ninf)) break;
+        const int w = __ffs(__ballot_sync(FULL, best == v)) - 1;
+        const int e = __shfl_sync(FULL, lane * VPL + at, w);
+        if (lane == k) {
+            id = e;
+            val = v;
+        }
+        if (lane == w) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i == at) c[i] = ninf;
+            best = c[0];
+            at = 0;
+#pragma unroll
+            for (int i = 1; i < VPL; ++i)
+                if (c[i] > best) {
+                    best = c[i];
+                    at = i;
+                }
+        }
+    }
+}
+
+// exp(a - b) with the rounding of the difference put back (a - b = d + e).
+MOE_DEV float exp_diff(float a, float b) {
+    const float d = a - b, bv = a - d, e = (a - (d + bv)) + (bv - b);
+    return expf(d) * (1.0f + (isfinite(e) ? e : 0.0f));
+}
+
+// Weight over scale of the selected expert of this lane (r; `there` where the
+// lane has one), and q = s / sum of the selected s. The sum is taken relative
+// to its largest part, so that scores below FP32's range still share it.
+MOE_DEV float selected_score(const Params& p, bool there, float r, float m, float z, float& q) {
+    const float top = warp_max(there ? r : -CUDART_INF_F);
+    float s, part;
+    if (p.softmax) {
+        s = !there ? 0.0f : r == m ? 1.0f / z : exp_diff(r, m) / z;
+        part = !there ? 0.0f : r == top ? 1.0f : exp_diff(r, top);
+    } else {
+        const float base = fminf(top, 0.0f), ex = expf(-fabsf(r)), den = 1.0f / (1.0f + ex);
+        s = !there ? 0.0f : r >= 0.0f ? den : ex * den;
+        part = !there ? 0.0f : r >= 0.0f ? den : (base == 0.0f ? ex : expf(r - base)) * den;
+    }
+    const float sum = warp_add(part);
+    q = there ? part / sum : 0.0f;
+    return s;
+}
+
+template <int VPL, typename T, bool VEC>
+__global__ void __launch_bounds__(32 * WARPS)
+group_route_kernel(Params p, const T* __restrict__ logits, int32_t* __restrict__ idx, float* __restrict__ w) {
+    const int lane = static_cast<int>(lane_id());
+    pdl_wait();
+    pdl_trigger();
+    const int step = gridDim.x * WARPS;
+    float bmax = 0.0f;  // largest |b|: what the choices' additions round by
+    if (p.bias != nullptr) {
+        for (int e = lane; e < p.E; e += 32) bmax = fmaxf(bmax, fabsf(p.bias[e]));
+        bmax = warp_max(bmax);
+    }
+    for (int t = blockIdx.x * WARPS + (threadIdx.x >> 5); t < p.T; t += step) {
+        const T* row = logits + t * p.stride;
+        float r[VPL], c[VPL], m, z;
+        load_row<VPL, T, VEC>(row, lane, p.E, r);
+        choices<float, VPL>(p, r, lane, c, m, z);
+        bool near = false;
+        // How near two FP32 choices may lie before FP64 decides. Without a bias
+        // the errors are relative: 3 units of 2^-23 (exponential, sum, division),
+        // and for a softmax the rounding of its argument, |r - m| 2^-24; the
+        // denominator is common. With one they are absolute: those of the largest
+        // score and half a unit of |b| + s. The bounds cover both sides twice.
+        const float babs = p.softmax ? 0x1p-18f / z + 0x1p-21f * bmax : 0x1p-19f + 0x1p-21f * bmax;
+        if (p.G > 1) {
+            float lo, hi;
+            keep_groups<float, VPL>(p, lane, c, lo, hi);
+            if (hi > -CUDART_INF_F && p.TG < p.G) {
+                const float tol = p.bias != nullptr ? 2.0f * babs : (p.softmax ? 0x1p-17f : 0x1p-19f) * lo;
+                near = !(lo - hi > tol) || (p.bias == nullptr && lo < 1e-20f);
+            }
+        }
+        int id;
+        float val;
+        // one more than K: the rank behind the last taken one
+        take<float, VPL>(c, lane, p.K + 1, id, val);
+        float rk = -CUDART_INF_F;
+        if (id >= 0) rk = clean(to_f32(row[id]));
+        const int id2 = __shfl_down_sync(FULL, id, 1);
+        const float val2 = __shfl_down_sync(FULL, val, 1), rk2 = __shfl_down_sync(FULL, rk, 1);
+        if (lane < p.K && id2 >= 0) {
+            const float spread = p.softmax && isfinite(m - rk2) ? 4.0f + (m - rk2) : 4.0f;
+            const float tol = (p.bias != nullptr ? babs : 0x1p-21f * spread * val) + 1e-36f;
+            if (!(val - val2 > tol)) {
+                // equal inputs are an exact tie: the lower index is first already
+                const bool same = rk == rk2 && (p.bias == nullptr || p.bias[id] == p.bias[id2]);
+                near = near || !same;
+            }
+        }
+        if (__any_sync(FULL, near)) {
+            double cd[VPL], zd, lod, hid, vald;
+            float md;
+            choices<double, VPL>(p, r, lane, cd, md, zd);
+            if (p.G > 1) keep_groups<double, VPL>(p, lane, cd, lod, hid);
+            take<double, VPL>(cd, lane, p.K, id, vald);
+            rk = id >= 0 ? clean(to_f32(row[id])) : -CUDART_INF_F;
+        }
+        const bool there = lane < p.K && id >= 0;
+        float q;
+        const float s = selected_score(p, there, rk, m, z, q);
+        if (lane < p.K) {
+            idx[static_cast<long long>(t) * p.K + lane] = there ? id : -1;
+            w[static_cast<long long>(t) * p.K + lane] = there ? p.scale * (p.renorm ? q : s) : 0.0f;
+        }
+    }
+}
+
+// dL/dr of L = sum dw w with the selection held fixed. With q = s / sum s over
+// the selected and v = sum dw q:
+//   renormalised softmax  dr_k = scale q_k (dw_k - v), zero off the selection
+//   renormalised sigmoid  the same times 1 - s_k
+//   raw sigmoid           dr_k = scale dw_k s_k (1 - s_k)
+//   raw softmax           dr_e = s_e (scale [e taken] dw_e - sum_k scale dw_k s_k)
+// Only the last reads the logits off the selection.
+template <int VPL, typename T, bool VEC>
+__global__ void __launch_bounds__(32 * WARPS)
+group_route_bwd_kernel(Params p, const T* __restrict__ logits, const int32_t* __restrict__ idx,
+                       const float* __restrict__ dw, T* __restrict__ dr) {
+    __shared__ float srow[WARPS][32 * VPL + VPL];
+    const int lane = static_cast<int>(lane_id());
+    float* u = srow[threadIdx.x >> 5];
+    pdl_wait();
+    pdl_trigger();
+    const int step = gridDim.x * WARPS;
+    const bool dense = p.softmax && !p.renorm;
+    for (int t = blockIdx.x * WARPS + (threadIdx.x >> 5); t < p.T; t += step) {
+        const T* row = logits + t * p.stride;
+        float r[VPL], m = 0.0f, z = 1.0f, e[VPL];
+        int id = -1;
+        float g = 0.0f, rk = -CUDART_INF_F;
+        if (lane < p.K) {
+            id = idx[static_cast<long long>(t) * p.K + lane];
+            if (id >= 0 && id < p.E) {
+                rk = clean(to_f32(row[id]));
+                g = p.scale * dw[static_cast<long long>(t) * p.K + lane];
+            }
+        }
+        // a masked expert among the given ids has score 0: no gradient passes
+        const bool there = lane < p.K && id >= 0 && id < p.E && rk > -CUDART_INF_F;
+        if (dense) {
+            load_row<VPL, T, VEC>(row, lane, p.E, r);
+            float mx = r[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, r[i]);
+            m = warp_max(mx);
+            z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                e[i] = r[i] == -CUDART_INF_F ? 0.0f : r[i] == m ? 1.0f : expf(r[i] - m);
+                z += e[i];
+            }
+            z = warp_add(z);
+            if (z == 0.0f) z = 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) u[lane * VPL + i] = 0.0f;
+        float q;
+        const float s = selected_score(p, there, rk, m, z, q);
+        const float v = warp_add(there ? g * (p.renorm ? q : s) : 0.0f);
+        float d = g;
+        if (!dense) {
+            if (p.renorm) d = q * (g - v);
+            if (!p.softmax) {
+                const float ex = expf(-fabsf(rk)), rest = rk >= 0.0f ? ex / (1.0f + ex) : 1.0f / (1.0f + ex);
+                d = (p.renorm ? d : g * s) * rest;
+            }
+        }
+        __syncwarp();
+        if (there) u[id] = d;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int ex = lane * VPL + i;
+            r[i] = u[ex];
+            if (dense) r[i] = e[i] / z * (r[i] - v);
+        }
+        T* out = dr + static_cast<long long>(t) * p.E;
+        if constexpr (VEC) {
+            if (lane * VPL < p.E) {
+                constexpr int B = VPL * sizeof(T) >= 16 ? 16 : VPL * sizeof(T);
+                constexpr int N = B / sizeof(T);
+#pragma unroll
+                for (int i = 0; i < VPL; i += N) {
+                    alignas(16) T o[N];
+#pragma unroll
+                    for (int j = 0; j < N; ++j) o[j] = from_f32<T>(r[i + j]);
+                    T* at = out + lane * VPL + i;
+                    if constexpr (B == 16)
+                        *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(o);
+                    else if constexpr (B == 8)
+                        *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(o);
+                    else if constexpr (B == 4)
+                        *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(o);
+                    else
+                        at[0] = o[0];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (lane * VPL + i < p.E) out[lane * VPL + i] = from_f32<T>(r[i]);
+        }
+        __syncwarp();
+    }
+}
+
+template <int VPL, typename T>
+cudaError_t launch_t(const GroupRouteArgs& a, Params p, bool bwd, cudaStream_t s) {
+    const int want = (a.T + WARPS - 1) / WARPS, cap = num_sms() * 8;
+    const dim3 grid(want < cap ? want : cap), block(32 * WARPS);
+    // vector rows: every lane's run of experts whole and aligned
+    constexpr int B = VPL * static_cast<int>(sizeof(T)) >= 16 ? 16 : VPL * static_cast<int>(sizeof(T));
+    auto even = [&](const void* q, long long st) {
+        return reinterpret_cast<uintptr_t>(q) % B == 0 && st * static_cast<long long>(sizeof(T)) % B == 0;
+    };
+    const bool vec = a.E % VPL == 0 && even(a.logits, a.stride) && (!bwd || even(a.dlogits, a.E));
+    const T* lg = static_cast<const T*>(a.logits);
+    if (!bwd)
+        return vec ? launch_pdl(group_route_kernel<VPL, T, true>, grid, block, 0, s, p, lg, a.idx, a.w)
+                   : launch_pdl(group_route_kernel<VPL, T, false>, grid, block, 0, s, p, lg, a.idx, a.w);
+    const int32_t* ci = a.idx;
+    T* dl = static_cast<T*>(a.dlogits);
+    return vec ? launch_pdl(group_route_bwd_kernel<VPL, T, true>, grid, block, 0, s, p, lg, ci, a.dw, dl)
+               : launch_pdl(group_route_bwd_kernel<VPL, T, false>, grid, block, 0, s, p, lg, ci, a.dw, dl);
+}
+
+template <typename T>
+cudaError_t launch_d(const GroupRouteArgs& a, bool bwd, cudaStream_t s) {
+    Params p{};
+    p.T = a.T;
+    p.E = a.E;
+    p.K = a.K;
+    p.G = a.G;
+    p.gs = a.E / a.G;
+    p.TG = a.TG;
+    p.rank = a.rank;
+    p.softmax = a.softmax;
+    p.renorm = a.renorm;
+    p.scale = a.scale;
+    p.stride = a.stride;
+    p.bias = a.bias;
+    const int vpl = a.E <= 32 ? 1 : a.E <= 64 ? 2 : a.E <= 128 ? 4 : 8;
+    const int lg = p.gs % vpl == 0 ? p.gs / vpl : 0;
+    p.lg = (lg & (lg - 1)) == 0 ? lg : 0;
+    if (vpl == 1) return launch_t<1, T>(a, p, bwd, s);
+    if (vpl == 2) return launch_t<2, T>(a, p, bwd, s);
+    if (vpl == 4) return launch_t<4, T>(a, p, bwd, s);
+    return launch_t<8, T>(a, p, bwd, s);
+}
+
+}  // namespace
+
+cudaError_t launch_group_route(const GroupRouteArgs& a, bool bwd, cudaStream_t s) {
+    switch (a.dtype) {
+        case MOE_BF16: return launch_d<__nv_bfloat16>(a, bwd, s);
+        case MOE_F16: return launch_d<__half>(a, bwd, s);
+        default: return launch_d<float>(a, bwd, s);
+    }
+}
+
+}  // namespace moe

@@ -493,4 +493,66 @@ BwdLayout plan_backward(const moe_config& c);
 moe_status backward_impl(const moe_config& c, const void* x, const moe_weights& w, const float* dout,
                          const moe_grads& g, uint8_t* ws, uint8_t* bws, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Operators around the layer (ops_api.cu holds their entry points)
+// ---------------------------------------------------------------------------
+struct LayerNormArgs {
+    int R, d, dtype;
+    const void* x;
+    long long x_stride;
+    const float* gamma;
+    const float* beta;
+    float eps;
+    void* y;             // forward: y; backward: dx
+    long long y_stride;
+    float* mean_out;     // forward
+    float* rstd_out;
+    const void* dy;      // backward
+    long long dy_stride;
+    const float* mean;
+    const float* rstd;
+    float* dgamma;
+    float* dbeta;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s);
+// Partial rows [2, d] FP32 that the backward's column sums go through.
+int layer_norm_bwd_parts(int R, int d);
+cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a, float* part, cudaStream_t s);
+
+struct GroupRouteArgs {
+    int T, E, K, G, TG, rank, softmax, renorm, dtype;
+    float scale;
+    const void* logits;
+    long long stride;
+    const float* bias;
+    int32_t* idx;       // forward: written; backward: read
+    float* w;           // forward
+    const float* dw;    // backward
+    void* dlogits;
+};
+cudaError_t launch_group_route(const GroupRouteArgs& a, bool bwd, cudaStream_t s);
+
+struct QuantArgs {
+    int R, K, dtype;
+    const void* x;
+    long long x_stride;
+    int8_t* q;
+    float* scale;
+};
+cudaError_t launch_quantize_rows(const QuantArgs& a, cudaStream_t s);
+
+struct Int8Args {
+    int M, Ma, K, N, E, swiglu, out_dtype;
+    long long lda;
+    const int8_t* a;
+    const float* sa;
+    const int8_t* b;
+    const float* sb;
+    const int32_t* offsets;  // NULL: one expert takes every row
+    const int32_t* rows;     // NULL: product row i reads row i of a
+    void* out;
+    int* err;                // NULL: bad row indices are not reported
+};
+cudaError_t launch_int8_vec(const Int8Args& a, cudaStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,188 @@
+// Rows to 8-bit integers with one scale each:
+//   scale = max |x| / 127,  q = x / scale rounded to the nearest integer, ties
+//   to even (the quotient exact, not its FP32 rounding)
+// A row of zeros has scale 0; a row with an infinity or a NaN has q = 0 and
+// scale NaN, which every product of the row then shows.
+//
+// Memory bound: x is read once into registers, by a warp for short rows and by
+// a CTA else, and q written once.
+#include <math_constants.h>
+
+#include "elem.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int REG_MAX_K = 16384;  // 1024 threads x 16 elements
+
+template <int TPR>
+MOE_DEV unsigned row_umax(unsigned v, unsigned* scratch, int& turn) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if constexpr (TPR > 32) {
+        constexpr int W = TPR / 32;
+        unsigned* s = scratch + (turn & 1) * W;
+        ++turn;
+        if (lane_id() == 0) s[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = __reduce_max_sync(0xffffffffu, lane_id() < W ? s[lane_id()] : 0u);
+    }
+    return v;
+}
+
+MOE_DEV unsigned abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// What a row's largest |x| (as bits) makes of its elements.
+struct RowScale {
+    float scale, inv;
+    int mode;  // 0: all zero, 1: FP32 quotient with an exact remainder, 2: FP64 quotient
+    MOE_DEV explicit RowScale(unsigned bits) {
+        if (bits >= 0x7f800000u) {
+            scale = CUDART_NAN_F;
+            inv = 0.0f;
+            mode = 0;
+            return;
+        }
+        scale = __uint_as_float(bits) / 127.0f;
+        // below this the reciprocal or the remainder could leave FP32's normal range
+        mode = scale == 0.0f ? 0 : scale < 1e-30f ? 2 : 1;
+        inv = mode == 1 ? 1.0f / scale : 0.0f;
+    }
+    MOE_DEV int quantize(float x) const {
+        if (mode == 1) {
+            const float t = x * inv;  // off by at most 2^-23 of itself: 2e-5 at 127
+            float q = rintf(t);
+            if (fabsf(t - q) > 0.4999f) {
+                // x - q scale is exact in FP32 (q has 7 bits and the difference is at
+                // most a little over half a step); it says on which side x lies
+                const float rem = fmaf(-q, scale, x), half = 0.5f * scale;
+                const bool odd = (static_cast<int>(q) & 1) != 0;
+                if (rem > half || (rem == half && odd)) q += 1.0f;
+                else if (rem < -half || (rem == -half && odd)) q -= 1.0f;
+            }
+            return static_cast<int>(q);
+        }
+        if (mode == 0) return 0;
+        const double q = rint(static_cast<double>(x) / static_cast<double>(scale));
+        return static_cast<int>(fmin(fmax(q, -127.0), 127.0));
+    }
+};
+
+template <typename T, int VEC, int NV, int TPR>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR)
+quantize_rows_kernel(int R, int K, const T* __restrict__ x, long long xs, int8_t* __restrict__ q,
+                     float* __restrict__ scale) {
+    constexpr int RPC = TPR == 32 ? 4 : 1;
+    __shared__ unsigned scratch[TPR > 32 ? 2 * (TPR / 32) : 1];
+    const int t = TPR == 32 ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
+    const long long step = static_cast<long long>(gridDim.x) * RPC;
+    long long row = static_cast<long long>(blockIdx.x) * RPC + (TPR == 32 ? threadIdx.x >> 5 : 0);
+    int turn = 0;
+    pdl_wait();
+    pdl_trigger();
+    Raw<T, VEC> cur[NV];
+    auto fetch = [&](long long r) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (r < R && c < K)
+                cur[i].load(x + r * xs + c);
+            else
+                cur[i].clear();
+        }
+    };
+    fetch(row);
+    for (; row < R; row += step) {
+        float v[NV][VEC];
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            cur[i].get(v[i]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) m = max(m, abs_bits(v[i][j]));
+        }
+        fetch(row + step);
+        const RowScale rs(row_umax<TPR>(m, scratch, turn));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (c < K) {
+                alignas(8) int8_t o[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) o[j] = static_cast<int8_t>(rs.quantize(v[i][j]));
+                int8_t* at = q + row * K + c;
+                if constexpr (VEC == 8)
+                    *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(o);
+                else if constexpr (VEC == 4)
+                    *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(o);
+                else
+                    at[0] = o[0];
+            }
+        }
+        if (t == 0) scale[row] = rs.scale;
+    }
+}
+
+// Rows longer than the registers hold: two passes, the second from L2.
+template <typename T>
+__global__ void __launch_bounds__(1024)
+quantize_rows_long_kernel(int R, int K, const T* __restrict__ x, long long xs, int8_t* __restrict__ q,
+                          float* __restrict__ scale) {
+    __shared__ unsigned scratch[2 * 32];
+    int turn = 0;
+    pdl_wait();
+    pdl_trigger();
+    for (long long row = blockIdx.x; row < R; row += gridDim.x) {
+        unsigned m = 0;
+        for (int c = threadIdx.x; c < K; c += 1024) m = max(m, abs_bits(to_f32(x[row * xs + c])));
+        const RowScale rs(row_umax<1024>(m, scratch, turn));
+        for (int c = threadIdx.x; c < K; c += 1024)
+            q[row * K + c] = static_cast<int8_t>(rs.quantize(to_f32(x[row * xs + c])));
+        if (threadIdx.x == 0) scale[row] = rs.scale;
+    }
+}
+
+int grid_rows(long long rows, int rpc, int per_sm) {
+    const long long want = (rows + rpc - 1) / rpc, cap = static_cast<long long>(num_sms()) * per_sm;
+    return static_cast<int>(want < cap ? want : cap);
+}
+
+template <typename T, int VEC, int NV, int TPR>
+cudaError_t quant_t(const QuantArgs& a, cudaStream_t s) {
+    const int threads = TPR == 32 ? 128 : TPR;
+    return launch_pdl(quantize_rows_kernel<T, VEC, NV, TPR>, dim3(grid_rows(a.R, TPR == 32 ? 4 : 1, 2048 / threads)),
+                      dim3(threads), 0, s, a.R, a.K, static_cast<const T*>(a.x), a.x_stride, a.q, a.scale);
+}
+
+template <typename T, int VEC>
+cudaError_t quant_v(const QuantArgs& a, cudaStream_t s) {
+    if (a.K <= 32 * 8) return quant_t<T, VEC, 8 / VEC, 32>(a, s);
+    if (a.K <= 32 * 32) return quant_t<T, VEC, 32 / VEC, 32>(a, s);
+    if (a.K <= 128 * 16) return quant_t<T, VEC, 16 / VEC, 128>(a, s);
+    if (a.K <= 256 * 16) return quant_t<T, VEC, 16 / VEC, 256>(a, s);
+    return quant_t<T, VEC, 16 / VEC, 1024>(a, s);
+}
+
+template <typename T>
+cudaError_t quant_d(const QuantArgs& a, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (a.K > REG_MAX_K)
+        return launch_pdl(quantize_rows_long_kernel<T>, dim3(grid_rows(a.R, 1, 2)), dim3(1024), 0, s, a.R, a.K,
+                          static_cast<const T*>(a.x), a.x_stride, a.q, a.scale);
+    const bool vec = a.K % V == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
+                     (a.x_stride * static_cast<long long>(sizeof(T))) % 16 == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.q) & 7u) == 0;
+    return vec ? quant_v<T, V>(a, s) : quant_v<T, 1>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows(const QuantArgs& a, cudaStream_t s) {
+    switch (a.dtype) {
+        case MOE_BF16: return quant_d<__nv_bfloat16>(a, s);
+        case MOE_F16: return quant_d<__half>(a, s);
+        default: return quant_d<float>(a, s);
+    }
+}
+
+}  // namespace moe
