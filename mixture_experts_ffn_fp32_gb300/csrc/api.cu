@@ -60,6 +60,11 @@ static EncodeTiledFn get_encoder() {
 
 bool encode_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides_bytes, const uint32_t* box) {
+    return encode_tmap_typed(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box);
+}
+
+bool encode_tmap_typed(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides_bytes, const uint32_t* box) {
     EncodeTiledFn fn = get_encoder();
     if (!fn) return false;
     cuuint64_t d[5], st[4];
@@ -70,7 +75,7 @@ bool encode_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dim
         es[i] = 1;
     }
     for (int i = 0; i + 1 < rank; ++i) st[i] = strides_bytes[i];
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+    const CUresult r = fn(m, type, static_cast<cuuint32_t>(rank),
                           const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

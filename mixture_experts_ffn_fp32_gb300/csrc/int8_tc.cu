@@ -1,0 +1,574 @@
+// 8-bit expert products on the 5th-generation tensor cores (many rows per
+// expert). y[i, n] = sa[i] sb[e, n] sum_k a[i, k] b[e, n, k], the sum exact.
+//
+// sm_103a's tcgen05 has no integer kind, but 8-bit integers are exact in FP16,
+// their products (below 2^14) and sums of 1024 of them exact in the FP32
+// accumulator. So the reduction runs on kind::f16 in chunks of at most 1024,
+// and each chunk's accumulator is added to 32-bit integers in registers: the
+// whole sum is the integer product's, at the FP16 rate.
+//
+// Roles: output channels are the MMA's M rows, tokens its N columns, one CTA
+// pair (cta_group::2) per tile of 256 channels x 256 tokens. The tokens are
+// widened to FP16 (and gathered) once, by a pass before; the weights stay 8
+// bits in HBM, L2 and shared memory, and four warps widen them on their way
+// into tensor memory, from where the MMA takes its A operand: weights widened
+// into shared memory would add their write and the MMA's read to a shared
+// memory that the copies and the tokens already keep half busy.
+//
+// Warps: 0 copies (TMA), 1 issues MMAs (even CTA), 4-7 widen weights, 8-15
+// hold the integer sums and store. A stage is 128 of the reduction: 16 KB of
+// weights, 32 KB of tokens and 64 columns of tensor memory.
+//
+// Every wait is bounded (common.cuh).
+#include <math_constants.h>
+
+#include "elem.cuh"
+#include "internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int BK = 128;              // reduction per stage
+constexpr int STAGES = 4;
+constexpr int CHUNK_BLOCKS = 8;      // blocks of BK per exact chunk (1024)
+constexpr int CH = 128;              // channels per CTA (MMA rows)
+constexpr int NT = 256;              // tokens per tile (MMA columns of the pair)
+constexpr int W_BYTES = CH * BK;     // 8-bit weights
+constexpr int T_HALF = 128 * 128;    // 64 of the reduction x 128 tokens of FP16
+constexpr int STAGE_BYTES = W_BYTES + 2 * T_HALF;
+constexpr int THREADS = 512;
+constexpr int CONV_WARPS = 4, EPI_WARPS = 8;
+// Registers a thread per warpgroup: copies and MMAs, widening, two of sums
+// (128 of them the integers).
+constexpr int REGS_COPY = 64, REGS_CONV = 80, REGS_EPI = 184;
+constexpr int REGS_SUM = REGS_COPY + REGS_CONV + 2 * REGS_EPI;
+static_assert(REGS_SUM <= 4 * 128, "the shares exceed the launch's registers");
+constexpr int MAXE = 256;
+constexpr int TMEM_COLS = 512;
+constexpr int A_COL = 256;           // tensor-memory columns of the widened weights, 64 per stage
+constexpr int NBARS = 4 * STAGES + 3;
+constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
+constexpr int TAB_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+constexpr int SMEM_BYTES = TAB_OFF + 2 * (MAXE + 1) * 4 + 1024;
+
+struct Int8TcParams {
+    CUtensorMap mapW;   // [E, N, K] 8 bits, boxes of 64 channels x 128
+    CUtensorMap mapT;   // [M, K] FP16, boxes of 128 tokens x 64
+    int M, K, N, E, F;  // F: output channels (N, or N / 2 with SwiGLU)
+    int nt;             // channel tiles of a pair
+    const int32_t* offsets;
+    const float* sa;    // [M], gathered
+    const float* sb;    // [E, N]
+    void* out;
+    int* err;
+    unsigned long long timeout_ns;
+};
+
+// ---------------------------------------------------------------------------
+// tokens: rows gathered and widened to FP16, with their scales
+// ---------------------------------------------------------------------------
+// Four 8-bit integers as two words of FP16 pairs, exactly: v + 128 in the low
+// byte of 1024 + (v + 128), less 1152.
+MOE_DEV void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 k = __half2half2(__ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), k);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), k);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+constexpr int TOK_THREADS = 256;
+
+// One warp per row. Rows from offsets[E] on belong to no expert: their output
+// is zero and nothing reads their tokens.
+template <typename O>
+__global__ void __launch_bounds__(TOK_THREADS)
+int8_tokens_kernel(int M, int Ma, int K, int E, int F, const int8_t* __restrict__ a, long long lda,
+                   const float* __restrict__ sa, const int32_t* __restrict__ offsets,
+                   const int32_t* __restrict__ rows, uint4* __restrict__ tok, float* __restrict__ tsa,
+                   O* __restrict__ out, int* err) {
+    const int lane = static_cast<int>(lane_id());
+    pdl_wait();
+    pdl_trigger();
+    const int covered = offsets != nullptr ? min(max(offsets[E], 0), M) : M;
+    const int step = gridDim.x * (TOK_THREADS / 32);
+    for (int i = blockIdx.x * (TOK_THREADS / 32) + (threadIdx.x >> 5); i < M; i += step) {
+        if (i >= covered) {
+            for (int n = lane; n < F; n += 32) out[static_cast<long long>(i) * F + n] = from_f32<O>(0.0f);
+            continue;
+        }
+        int src = i;
+        bool ok = true;
+        if (rows != nullptr) {
+            src = rows[i];
+            ok = src >= 0 && src < Ma;
+            if (!ok) {
+                if (lane == 0) atomicOr(err, ERRBIT_INDEX);
+                src = 0;
+            }
+        }
+        if (lane == 0) tsa[i] = ok ? sa[src] : CUDART_NAN_F;
+        const uint4* ar = reinterpret_cast<const uint4*>(a + src * lda);
+        uint4* tr = tok + static_cast<long long>(i) * (K / 8);
+        for (int c = lane; c < K / 16; c += 32) {
+            const uint4 v = __ldg(ar + c);
+            uint4 x, y;
+            widen4(v.x, x.x, x.y);
+            widen4(v.y, x.z, x.w);
+            widen4(v.z, y.x, y.y);
+            widen4(v.w, y.z, y.w);
+            tr[2 * c] = x;
+            tr[2 * c + 1] = y;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// tcgen05 pieces of this kernel
+// ---------------------------------------------------------------------------
+// Tensor-memory store, 32 lanes x 32 columns of 32 bits: thread i writes lane
+// base + i.
+MOE_DEV void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Pair MMA with A in tensor memory (each CTA its own 128 rows), FP16 operands.
+MOE_DEV void tc_mma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// FP32 accumulator, FP16 A and B (K-major), M = 256; N is added per tile.
+constexpr uint32_t IDESC0 = (1u << 4) | (static_cast<uint32_t>(256 >> 4) << 24);
+
+template <int N>
+MOE_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+MOE_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+struct Tile {
+    int e, row0, n, f0;  // expert, first product row, rows, first output channel of the pair
+};
+
+// s_tp: tiles before each expert; s_off: its first row. Channel tiles are
+// innermost: neighbouring pairs share a token tile and an expert's weights.
+template <int OUT_CH>
+MOE_DEV Tile tile_of(int u, const Int8TcParams& p, const int* s_tp, const int* s_off) {
+    const int mt = u / p.nt;
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_tp[mid] <= mt) lo = mid;
+        else hi = mid;
+    }
+    Tile t;
+    t.e = lo;
+    t.row0 = s_off[lo] + (mt - s_tp[lo]) * NT;
+    t.n = min(NT, s_off[lo + 1] - t.row0);
+    t.f0 = (u - mt * p.nt) * 2 * OUT_CH;
+    return t;
+}
+
+template <bool SWIGLU, typename O>
+__global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_constant__ Int8TcParams p) {
+    constexpr int OUT_CH = SWIGLU ? CH / 2 : CH;  // output channels per CTA
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + BAR_OFF;
+    auto wfull = [&](int s) { return bar0 + 8u * s; };                  // own weights landed
+    auto tfull = [&](int s) { return bar0 + 8u * (STAGES + s); };       // even CTA: both CTAs' tokens landed
+    auto aready = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // even CTA: both CTAs' weights widened
+    auto empty = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };   // stage and its columns read by the MMAs
+    const uint32_t acc_full = bar0 + 8u * (4 * STAGES), acc_empty = acc_full + 8u, drain_bar = acc_full + 16u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + MISC_OFF + 4);
+    int* s_tp = reinterpret_cast<int*>(smem + TAB_OFF);
+    int* s_off = s_tp + MAXE + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int unit0 = static_cast<int>(blockIdx.x >> 1), ustep = static_cast<int>(gridDim.x >> 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(wfull(s), 1);
+            mbar_init(tfull(s), 1);
+            mbar_init(aready(s), 2 * CONV_WARPS);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 2 * EPI_WARPS);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_map(&p.mapW);
+        tma_prefetch_map(&p.mapT);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    pdl_wait();  // the tokens and their scales
+    pdl_trigger();
+    if (warp == 2) {  // tiles before each expert, from the clamped offsets
+        int before = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            int lo = 0, hi = 0;
+            if (e < p.E) {
+                lo = p.offsets != nullptr ? min(max(p.offsets[e], 0), p.M) : 0;
+                hi = p.offsets != nullptr ? min(max(p.offsets[e + 1], 0), p.M) : p.M;
+                if (hi < lo) hi = lo;
+            }
+            const int c = (hi - lo + NT - 1) / NT;
+            int x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (e < p.E) {
+                s_tp[e] = before + x - c;
+                s_off[e] = lo;
+                if (e == p.E - 1) s_off[p.E] = hi;
+            }
+            before += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) s_tp[p.E] = before;
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int total = s_tp[p.E] * p.nt;
+    const WaitCtx wc{p.err, abort_flag, p.timeout_ns};
+    const int kblocks = (p.K + BK - 1) / BK;
+    const int nchunks0 = (kblocks + CHUNK_BLOCKS - 1) / CHUNK_BLOCKS;
+    const int cblocks = (kblocks + nchunks0 - 1) / nchunks0;   // blocks per chunk, at most 8
+    const int nchunks = (kblocks + cblocks - 1) / cblocks;
+
+    if (warp < 4) {
+        reg_dec<REGS_COPY>();
+        if (warp == 0 && lane == 0) {
+            // ---------------- copies (both CTAs) ----------------
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, last_par = 0;
+            bool ok = true;
+            for (int u = unit0; u < total && ok; u += ustep) {
+                const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
+                const int nh = ((t.n + 15) & ~15) >> 1;  // token columns held by each CTA
+                const int trow = t.row0 + rank * nh;
+                // 64 + 64 channels: a SwiGLU tile's gates and ups, else one run
+                const int c0 = t.f0 + rank * OUT_CH, c1 = SWIGLU ? c0 + p.F : c0 + 64;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!bounded_wait(empty(stage), phase ^ 1u, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sW = sbase + stage * STAGE_BYTES, sT = sW + W_BYTES;
+                    mbar_expect_tx(wfull(stage), W_BYTES);
+                    tma_load_3d(sW, &p.mapW, kb * BK, c0, t.e, wfull(stage));
+                    tma_load_3d(sW + W_BYTES / 2, &p.mapW, kb * BK, c1, t.e, wfull(stage));
+                    const uint32_t tb = map_shared_rank(tfull(stage), 0);
+                    if (rank == 0) mbar_expect_tx(tfull(stage), 4 * T_HALF);
+                    tma_load_2d_pair(sT, &p.mapT, kb * BK, trow, tb);
+                    tma_load_2d_pair(sT + T_HALF, &p.mapT, kb * BK + 64, trow, tb);
+                    issued |= 1u << stage;
+                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // every copy has landed before the CTA leaves: the weights on their own
+            // barrier; the tokens on the even CTA's, or consumed by the MMAs
+            for (int s = 0; s < STAGES; ++s)
+                if ((issued >> s) & 1u) {
+                    bounded_drain(wfull(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
+                    bounded_drain(rank == 0 ? tfull(s) : empty(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
+                }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // ---------------- MMA issuer (even CTA) ----------------
+            int stage = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            const uint64_t bdesc0 = smem_desc_sw128(sbase + W_BYTES, 16, 1024);
+            for (int u = unit0; u < total && ok; u += ustep) {
+                const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
+                const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(((t.n + 15) & ~15) >> 3) << 17);
+                for (int c = 0; c < nchunks && ok; ++c) {
+                    if (!bounded_wait(acc_empty, acc_phase ^ 1u, wc, true)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const int kb1 = min((c + 1) * cblocks, kblocks);
+                    for (int kb = c * cblocks; kb < kb1; ++kb) {
+                        if (!bounded_wait(tfull(stage), phase, wc, true) || !bounded_wait(aready(stage), phase, wc, true)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t bs = bdesc0 + (static_cast<uint64_t>(stage * STAGE_BYTES) >> 4);
+                        const uint32_t at = tmem + A_COL + static_cast<uint32_t>(stage * 64);
+                        const int steps = min(BK, p.K - kb * BK) / 16;
+                        for (int ks = 0; ks < steps; ++ks)
+                            tc_mma_f16_pair_ta(tmem, at + ks * 8, bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16, idesc,
+                                               (kb != c * cblocks || ks != 0) ? 1u : 0u);
+                        tc_commit_pair_mc(empty(stage), 3);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit_pair_mc(acc_full, 3);
+                    acc_phase ^= 1u;
+                }
+            }
+            tc_commit_pair(drain_bar);
+            bounded_drain(drain_bar, 0, p.timeout_ns, p.err);
+        }
+    } else if (warp < 4 + CONV_WARPS) {
+        // ---------------- weights: 8 bits in shared memory to FP16 in tensor memory ----------------
+        reg_dec<REGS_CONV>();
+        const int q = warp & 3;
+        // This thread's tensor-memory lane takes one channel of the stage. SwiGLU: a
+        // quarter's lanes 0-15 are gates, 16-31 the ups of the same channels.
+        const int row = SWIGLU ? (lane < 16 ? 16 * q + lane : 64 + 16 * q + lane - 16) : 32 * q + lane;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = unit0; u < total && ok; u += ustep) {
+            for (int kb = 0; kb < kblocks; ++kb) {
+                int w = 1;
+                if (lane == 0) w = bounded_wait(wfull(stage), phase, wc) ? 1 : 0;
+                if (!__shfl_sync(0xffffffffu, w, 0)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint8_t* wr = smem + stage * STAGE_BYTES + row * BK;
+                const uint32_t at = tmem + A_COL + static_cast<uint32_t>(stage * 64) + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        // 128-byte swizzle: 16-byte chunk j of row r at j ^ (r & 7)
+                        const uint4 v = *reinterpret_cast<const uint4*>(wr + (((4 * h + c) ^ (row & 7)) << 4));
+                        widen4(v.x, r[8 * c], r[8 * c + 1]);
+                        widen4(v.y, r[8 * c + 2], r[8 * c + 3]);
+                        widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
+                        widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
+                    }
+                    tc_st_32x32b_x32(at + 32 * h, r);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(aready(stage));
+                    else mbar_arrive_remote(map_shared_rank(aready(stage), 0));
+                }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ---------------- integer sums and stores ----------------
+        reg_inc<REGS_EPI>();
+        const int q = warp & 3, half = (warp - 8) >> 2;
+        const int c0 = 128 * half;  // this warp's token columns [c0, c0 + 128)
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = unit0; u < total && ok; u += ustep) {
+            const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
+            const uint32_t ta = tmem + static_cast<uint32_t>(c0) + (static_cast<uint32_t>(q * 32) << 16);
+            int acc[128];
+            for (int c = 0; c < nchunks; ++c) {
+                int w = 1;
+                if (lane == 0) w = bounded_wait(acc_full, phase, wc) ? 1 : 0;
+                if (!__shfl_sync(0xffffffffu, w, 0)) {
+                    ok = false;
+                    break;
+                }
+                phase ^= 1u;
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    if (c0 + 16 * g < t.n) {
+                        uint32_t r[16];
+                        tc_ld_32x32b_x16(ta + 16 * g, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int v = __float2int_rn(__uint_as_float(r[i]));
+                            acc[16 * g + i] = c == 0 ? v : acc[16 * g + i] + v;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(acc_empty);
+                    else mbar_arrive_remote(map_shared_rank(acc_empty, 0));
+                }
+            }
+            if (!ok) break;
+            // this lane's channel, its scale, and the tokens' scales (lane l: tokens 32 j + l)
+            const int oc = SWIGLU ? t.f0 + rank * OUT_CH + 16 * q + (lane & 15) : t.f0 + rank * OUT_CH + 32 * q + lane;
+            const bool in = oc < p.F;
+            const int ch = SWIGLU && lane >= 16 ? oc + p.F : oc;
+            const float sb = in ? __ldg(p.sb + static_cast<long long>(t.e) * p.N + ch) : 0.0f;
+            float sa[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int ti = c0 + 32 * j + lane;
+                sa[j] = ti < t.n ? p.sa[t.row0 + ti] : 0.0f;
+            }
+            O* orow = static_cast<O*>(p.out) + static_cast<long long>(t.row0 + c0) * p.F + oc;
+#pragma unroll
+            for (int i = 0; i < 128; i += 2) {
+                if (c0 + i < t.n) {
+                    const float s0 = __shfl_sync(0xffffffffu, sa[i >> 5], i & 31);
+                    const float s1 = __shfl_sync(0xffffffffu, sa[i >> 5], (i & 31) + 1);
+                    const float v0 = static_cast<float>(acc[i]) * s0 * sb, v1 = static_cast<float>(acc[i + 1]) * s1 * sb;
+                    if (SWIGLU) {
+                        // lanes 0-15 finish token i, lanes 16-31 token i + 1
+                        const bool lower = lane < 16;
+                        const float other = __shfl_xor_sync(0xffffffffu, lower ? v1 : v0, 16);
+                        const float g = lower ? v0 : other, up = lower ? other : v1;
+                        const int ti = i + (lower ? 0 : 1);
+                        if (in && c0 + ti < t.n) orow[static_cast<long long>(ti) * p.F] = from_f32<O>(g * sigmoid_f(g) * up);
+                    } else if (in) {
+                        orow[static_cast<long long>(i) * p.F] = from_f32<O>(v0);
+                        if (c0 + i + 1 < t.n) orow[static_cast<long long>(i + 1) * p.F] = from_f32<O>(v1);
+                    }
+                }
+            }
+        }
+    }
+
+    // no CTA of the pair leaves while the other may still touch its shared
+    // memory, barriers or tensor memory
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
+template <bool SWIGLU, typename O>
+int pair_slots(int dev) {
+    static int cache[64] = {};
+    if (dev < 0 || dev >= 64) return 0;
+    if (cache[dev] == 0) {
+        int n = -1;
+        // the warpgroups' register shares are drawn on what the block is launched with
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, int8_tc_kernel<SWIGLU, O>) == cudaSuccess && fa.numRegs * 4 >= REGS_SUM &&
+            cudaFuncSetAttribute(int8_tc_kernel<SWIGLU, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) ==
+                cudaSuccess) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * static_cast<unsigned>(num_sms()));
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = SMEM_BYTES;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int c = 0;
+            if (cudaOccupancyMaxActiveClusters(&c, int8_tc_kernel<SWIGLU, O>, &cfg) == cudaSuccess && c > 0)
+                n = c;
+            else
+                cudaGetLastError();
+        }
+        cache[dev] = n;
+    }
+    return cache[dev] > 0 ? cache[dev] : 0;
+}
+
+template <bool SWIGLU, typename O>
+cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int slots = pair_slots<SWIGLU, O>(dev);
+    if (slots <= 0) return cudaErrorInvalidConfiguration;
+    uint8_t* ws = reinterpret_cast<uint8_t*>(a.err);
+    float* tsa = reinterpret_cast<float*>(ws + 256);
+    uint8_t* tok = ws + int8_tc_tokens_offset(a.M);
+    Int8TcParams p{};
+    p.M = a.M; p.K = a.K; p.N = a.N; p.E = a.E;
+    p.F = SWIGLU ? a.N / 2 : a.N;
+    const int per = 2 * (SWIGLU ? CH / 2 : CH);
+    p.nt = (p.F + per - 1) / per;
+    const uint64_t wd[3] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.E)};
+    const uint64_t wst[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.K) * a.N};
+    const uint32_t wb[3] = {BK, 64, 1};
+    const uint64_t td[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)};
+    const uint64_t tst[1] = {static_cast<uint64_t>(a.K) * 2};
+    const uint32_t tb[2] = {64, 128};
+    if (!encode_tmap_typed(&p.mapW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.b, 3, wd, wst, wb) ||
+        !encode_tmap_typed(&p.mapT, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, tok, 2, td, tst, tb))
+        return cudaErrorInvalidValue;
+    p.offsets = a.offsets;
+    p.sa = tsa; p.sb = a.sb; p.out = a.out;
+    p.err = a.err;
+    p.timeout_ns = wait_timeout_ns();
+    const int warps = TOK_THREADS / 32, cap = num_sms() * 8, want = (a.M + warps - 1) / warps;
+    cudaError_t e = launch_pdl(int8_tokens_kernel<O>, dim3(want < cap ? want : cap), dim3(TOK_THREADS), 0, s, a.M, a.Ma,
+                               a.K, a.E, p.F, a.a, a.lda, a.sa, a.offsets, a.rows, reinterpret_cast<uint4*>(tok), tsa,
+                               static_cast<O*>(a.out), a.err);
+    if (e != cudaSuccess) return e;
+    const long long bound = (static_cast<long long>((a.M + NT - 1) / NT) + (a.E > 1 ? a.E : 0)) * p.nt;
+    const int grid = static_cast<int>(bound < slots ? (bound > 0 ? bound : 1) : slots);
+    return launch_pdl_cluster(int8_tc_kernel<SWIGLU, O>, dim3(2 * static_cast<unsigned>(grid)), dim3(THREADS),
+                              SMEM_BYTES, s, 2, p);
+}
+
+}  // namespace
+
+// Workspace: the error word's 256 bytes, the gathered scales, the tokens.
+size_t int8_tc_tokens_offset(int M) { return 256 + (static_cast<size_t>(M) * 4 + 255) / 256 * 256; }
+size_t int8_tc_workspace(int M, int K) {
+    return int8_tc_tokens_offset(M) + static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
+}
+
+cudaError_t launch_int8_tc(const Int8Args& a, cudaStream_t s) {
+    switch (a.out_dtype) {
+        case MOE_BF16: return a.swiglu ? launch_t<true, __nv_bfloat16>(a, s) : launch_t<false, __nv_bfloat16>(a, s);
+        case MOE_F16: return a.swiglu ? launch_t<true, __half>(a, s) : launch_t<false, __half>(a, s);
+        default: return a.swiglu ? launch_t<true, float>(a, s) : launch_t<false, float>(a, s);
+    }
+}
+
+}  // namespace moe

@@ -376,6 +376,9 @@ cudaError_t launch_decode_fused(const DecodeArgs& a, cudaStream_t s);
 
 bool encode_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                  const uint64_t* strides_bytes, const uint32_t* box);
+// The same for elements of another type.
+bool encode_tmap_typed(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides_bytes, const uint32_t* box);
 
 
 // ---------------------------------------------------------------------------
@@ -554,5 +557,9 @@ struct Int8Args {
     int* err;                // NULL: bad row indices are not reported
 };
 cudaError_t launch_int8_vec(const Int8Args& a, cudaStream_t s);
+// The tensor-core form: a.err points to a workspace of int8_tc_workspace bytes.
+size_t int8_tc_tokens_offset(int M);
+size_t int8_tc_workspace(int M, int K);
+cudaError_t launch_int8_tc(const Int8Args& a, cudaStream_t s);
 
 }  // namespace moe

@@ -163,13 +163,18 @@ moe_status check_int8(const moe_int8_config& c) {
     return MOE_OK;
 }
 
+// Few rows per expert run on the integer dot product, which reads the weights
+// straight into registers; the tensor-core form pays its tile of 256 channels
+// and its tokens' pass whatever the rows.
+bool int8_on_tensor_cores(const moe_int8_config& c) { return c.M >= 16LL * c.E; }
+
 }  // namespace
 
 MOE_API moe_status moe_matmul_int8_workspace_size(const moe_int8_config* cfg, size_t* bytes) {
     if (!cfg || !bytes) return MOE_ERR_INVALID_ARG;
     const moe_status v = check_int8(*cfg);
     if (v != MOE_OK) return v;
-    *bytes = 0;
+    *bytes = int8_on_tensor_cores(*cfg) ? int8_tc_workspace(cfg->M, cfg->K) : 0;
     return MOE_OK;
 }
 
@@ -200,5 +205,6 @@ MOE_API moe_status moe_matmul_int8(const moe_int8_config* cfg, const int8_t* a, 
     g.a = a; g.sa = a_scale; g.b = b; g.sb = b_scale;
     g.offsets = offsets; g.rows = rows; g.out = out;
     g.err = ws && ws_bytes >= 256 ? static_cast<int*>(ws) : nullptr;
-    return cuda_status(launch_int8_vec(g, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return cuda_status(int8_on_tensor_cores(c) ? launch_int8_tc(g, s) : launch_int8_vec(g, s));
 }
