@@ -3,9 +3,12 @@
 //
 // sm_103a's tcgen05 has no integer kind, but 8-bit integers are exact in FP16,
 // their products (below 2^14) and sums of 1024 of them exact in the FP32
-// accumulator. So the reduction runs on kind::f16 in chunks of at most 1024,
-// and each chunk's accumulator is added to 32-bit integers in registers: the
-// whole sum is the integer product's, at the FP16 rate.
+// accumulator. More than that: every partial sum of a row is at most 128 times
+// the row's sum of |a|, so a call whose largest row sum is at most 2^17 (rows
+// quantised by their maximum stay below it up to a few thousand values) runs
+// its whole reduction in one accumulator. Any other call runs in chunks of at
+// most 1024, and each chunk's accumulator is added to 32-bit integers in
+// registers. Either way the sum is the integer product's, at the FP16 rate.
 //
 // Roles: output channels are the MMA's M rows, tokens its N columns, one CTA
 // pair (cta_group::2) per tile of 256 channels x 256 tokens. The tokens are
@@ -15,9 +18,12 @@
 // into shared memory would add their write and the MMA's read to a shared
 // memory that the copies and the tokens already keep half busy.
 //
-// Warps: 0 copies (TMA), 1 issues MMAs (even CTA), 4-7 widen weights, 8-15
-// hold the integer sums and store. A stage is 128 of the reduction: 16 KB of
-// weights, 32 KB of tokens and 64 columns of tensor memory.
+// Warps: 0 copies tokens, 2 weights (TMA), 1 issues MMAs (even CTA), 4-7 widen
+// weights, 8-15 hold the integer sums and store. A stage is 128 of the
+// reduction: 32 KB of tokens and 64 columns of widened weights in tensor
+// memory, which the MMAs free together, and 16 KB of weights in a ring of its
+// own, which the widening frees: weights are in shared memory before their
+// columns are, so that only the widening lies between two uses of a column.
 //
 // Every wait is bounded (common.cuh).
 #include <math_constants.h>
@@ -35,7 +41,10 @@ constexpr int CH = 128;              // channels per CTA (MMA rows)
 constexpr int NT = 256;              // tokens per tile (MMA columns of the pair)
 constexpr int W_BYTES = CH * BK;     // 8-bit weights
 constexpr int T_HALF = 128 * 128;    // 64 of the reduction x 128 tokens of FP16
-constexpr int STAGE_BYTES = W_BYTES + 2 * T_HALF;
+constexpr int T_BYTES = 2 * T_HALF;
+constexpr int WSTAGES = 5;           // stages of the weights' ring
+constexpr int W_OFF = STAGES * T_BYTES;
+constexpr int L1_ONE_CHUNK = 1 << 17;  // row sum of |a| up to which one accumulator is exact
 constexpr int THREADS = 512;
 constexpr int CONV_WARPS = 4, EPI_WARPS = 8;
 // Registers a thread per warpgroup: copies and MMAs, widening, two of sums
@@ -46,11 +55,11 @@ static_assert(REGS_SUM <= 4 * 128, "the shares exceed the launch's registers");
 constexpr int MAXE = 256;
 constexpr int TMEM_COLS = 512;
 constexpr int A_COL = 256;           // tensor-memory columns of the widened weights, 64 per stage
-constexpr int NBARS = 4 * STAGES + 3;
-constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+constexpr int NBARS = 3 * STAGES + 2 * WSTAGES + 3;
+constexpr int BAR_OFF = W_OFF + WSTAGES * W_BYTES;
 constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
 constexpr int TAB_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
-constexpr int SMEM_BYTES = TAB_OFF + 2 * (MAXE + 1) * 4 + 1024;
+constexpr int SMEM_BYTES = TAB_OFF + (2 * (MAXE + 1) + THREADS / 32) * 4 + 1024;
 
 struct Int8TcParams {
     CUtensorMap mapW;   // [E, N, K] 8 bits, boxes of 64 channels x 128
@@ -60,6 +69,8 @@ struct Int8TcParams {
     const int32_t* offsets;
     const float* sa;    // [M], gathered
     const float* sb;    // [E, N]
+    const int* l1;      // [nl1] largest row sum of |a| per CTA of the tokens' pass
+    int nl1;
     void* out;
     int* err;
     unsigned long long timeout_ns;
@@ -82,15 +93,18 @@ MOE_DEV void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
 
 constexpr int TOK_THREADS = 256;
 
-// One warp per row. Rows from offsets[E] on belong to no expert: their output
-// is zero and nothing reads their tokens.
+// One warp per row; l1[CTA] receives the largest sum of |a| of its rows. Rows
+// from offsets[E] on belong to no expert: their output is zero and nothing
+// reads their tokens.
 template <typename O>
 __global__ void __launch_bounds__(TOK_THREADS)
 int8_tokens_kernel(int M, int Ma, int K, int E, int F, const int8_t* __restrict__ a, long long lda,
                    const float* __restrict__ sa, const int32_t* __restrict__ offsets,
                    const int32_t* __restrict__ rows, uint4* __restrict__ tok, float* __restrict__ tsa,
-                   O* __restrict__ out, int* err) {
+                   O* __restrict__ out, int* __restrict__ l1, int* err) {
+    __shared__ unsigned s_l1[TOK_THREADS / 32];
     const int lane = static_cast<int>(lane_id());
+    unsigned most = 0;
     pdl_wait();
     pdl_trigger();
     const int covered = offsets != nullptr ? min(max(offsets[E], 0), M) : M;
@@ -111,18 +125,26 @@ int8_tokens_kernel(int M, int Ma, int K, int E, int F, const int8_t* __restrict_
             }
         }
         if (lane == 0) tsa[i] = ok ? sa[src] : CUDART_NAN_F;
-        const uint4* ar = reinterpret_cast<const uint4*>(a + src * lda);
+        const uint2* ar = reinterpret_cast<const uint2*>(a + src * lda);
         uint4* tr = tok + static_cast<long long>(i) * (K / 8);
-        for (int c = lane; c < K / 16; c += 32) {
-            const uint4 v = __ldg(ar + c);
-            uint4 x, y;
+        unsigned sum = 0;
+#pragma unroll 4
+        for (int c = lane; c < K / 8; c += 32) {
+            const uint2 v = __ldg(ar + c);
+            sum = __dp4a(__vabs4(v.x), 0x01010101u, __dp4a(__vabs4(v.y), 0x01010101u, sum));
+            uint4 x;
             widen4(v.x, x.x, x.y);
             widen4(v.y, x.z, x.w);
-            widen4(v.z, y.x, y.y);
-            widen4(v.w, y.z, y.w);
-            tr[2 * c] = x;
-            tr[2 * c + 1] = y;
+            tr[c] = x;
         }
+        most = max(most, __reduce_add_sync(0xffffffffu, sum));
+    }
+    if (lane == 0) s_l1[threadIdx.x >> 5] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 1; i < TOK_THREADS / 32; ++i) most = max(most, s_l1[i]);
+        l1[blockIdx.x] = static_cast<int>(most);
     }
 }
 
@@ -144,6 +166,9 @@ MOE_DEV void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
 }
 MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// tc_ld_32x32b_x16 into 16 registers of a larger array.
+MOE_DEV void tc_ld_16(uint32_t taddr, uint32_t* r) { tc_ld_32x32b_x16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r)); }
+
 // Pair MMA with A in tensor memory (each CTA its own 128 rows), FP16 operands.
 MOE_DEV void tc_mma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                 uint32_t accumulate) {
@@ -161,6 +186,15 @@ template <int N>
 MOE_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 MOE_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// SiLU's sigmoid in the output's precision: 16-bit outputs take the fast
+// exponential and division, off by (4 + 1.2 |v|) units of 2^-23 at most.
+template <typename O>
+MOE_DEV float epi_sigmoid(float v) {
+    if constexpr (sizeof(O) == 4) return sigmoid_f(v);
+    const float e = __expf(-fabsf(v));
+    return __fdividef(v >= 0.0f ? 1.0f : e, 1.0f + e);
+}
 
 struct Tile {
     int e, row0, n, f0;  // expert, first product row, rows, first output channel of the pair
@@ -193,15 +227,17 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + BAR_OFF;
-    auto wfull = [&](int s) { return bar0 + 8u * s; };                  // own weights landed
-    auto tfull = [&](int s) { return bar0 + 8u * (STAGES + s); };       // even CTA: both CTAs' tokens landed
-    auto aready = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };  // even CTA: both CTAs' weights widened
-    auto empty = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };   // stage and its columns read by the MMAs
-    const uint32_t acc_full = bar0 + 8u * (4 * STAGES), acc_empty = acc_full + 8u, drain_bar = acc_full + 16u;
+    auto tfull = [&](int s) { return bar0 + 8u * s; };                  // even CTA: both CTAs' tokens landed
+    auto aready = [&](int s) { return bar0 + 8u * (STAGES + s); };      // even CTA: both CTAs' weights widened
+    auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };   // tokens and columns read by the MMAs
+    auto wfull = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };   // own weights landed
+    auto wempty = [&](int s) { return bar0 + 8u * (3 * STAGES + WSTAGES + s); };  // and widened
+    const uint32_t acc_full = bar0 + 8u * (3 * STAGES + 2 * WSTAGES), acc_empty = acc_full + 8u, drain_bar = acc_full + 16u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + MISC_OFF + 4);
     int* s_tp = reinterpret_cast<int*>(smem + TAB_OFF);
     int* s_off = s_tp + MAXE + 1;
+    int* s_l1 = s_off + MAXE + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
@@ -209,10 +245,13 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(wfull(s), 1);
             mbar_init(tfull(s), 1);
             mbar_init(aready(s), 2 * CONV_WARPS);
             mbar_init(empty(s), 1);
+        }
+        for (int s = 0; s < WSTAGES; ++s) {
+            mbar_init(wfull(s), 1);
+            mbar_init(wempty(s), CONV_WARPS);
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 2 * EPI_WARPS);
@@ -228,6 +267,10 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
     }
     pdl_wait();  // the tokens and their scales
     pdl_trigger();
+    int l1 = 0;
+    for (int i = threadIdx.x; i < p.nl1; i += THREADS) l1 = max(l1, p.l1[i]);
+    l1 = __reduce_max_sync(0xffffffffu, l1);
+    if (lane == 0) s_l1[warp] = l1;
     if (warp == 2) {  // tiles before each expert, from the clamped offsets
         int before = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -262,14 +305,17 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
     const int total = s_tp[p.E] * p.nt;
     const WaitCtx wc{p.err, abort_flag, p.timeout_ns};
     const int kblocks = (p.K + BK - 1) / BK;
-    const int nchunks0 = (kblocks + CHUNK_BLOCKS - 1) / CHUNK_BLOCKS;
-    const int cblocks = (kblocks + nchunks0 - 1) / nchunks0;   // blocks per chunk, at most 8
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) l1 = max(l1, s_l1[i]);
+    // blocks per chunk: all, or at most 8 and evenly
+    const int nchunks0 = l1 <= L1_ONE_CHUNK ? 1 : (kblocks + CHUNK_BLOCKS - 1) / CHUNK_BLOCKS;
+    const int cblocks = (kblocks + nchunks0 - 1) / nchunks0;
     const int nchunks = (kblocks + cblocks - 1) / cblocks;
 
     if (warp < 4) {
         reg_dec<REGS_COPY>();
         if (warp == 0 && lane == 0) {
-            // ---------------- copies (both CTAs) ----------------
+            // ---------------- tokens (both CTAs) ----------------
             int stage = 0;
             uint32_t phase = 0, issued = 0, last_par = 0;
             bool ok = true;
@@ -277,19 +323,14 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                 const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
                 const int nh = ((t.n + 15) & ~15) >> 1;  // token columns held by each CTA
                 const int trow = t.row0 + rank * nh;
-                // 64 + 64 channels: a SwiGLU tile's gates and ups, else one run
-                const int c0 = t.f0 + rank * OUT_CH, c1 = SWIGLU ? c0 + p.F : c0 + 64;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!bounded_wait(empty(stage), phase ^ 1u, wc)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sW = sbase + stage * STAGE_BYTES, sT = sW + W_BYTES;
-                    mbar_expect_tx(wfull(stage), W_BYTES);
-                    tma_load_3d(sW, &p.mapW, kb * BK, c0, t.e, wfull(stage));
-                    tma_load_3d(sW + W_BYTES / 2, &p.mapW, kb * BK, c1, t.e, wfull(stage));
+                    const uint32_t sT = sbase + stage * T_BYTES;
                     const uint32_t tb = map_shared_rank(tfull(stage), 0);
-                    if (rank == 0) mbar_expect_tx(tfull(stage), 4 * T_HALF);
+                    if (rank == 0) mbar_expect_tx(tfull(stage), 2 * T_BYTES);
                     tma_load_2d_pair(sT, &p.mapT, kb * BK, trow, tb);
                     tma_load_2d_pair(sT + T_HALF, &p.mapT, kb * BK + 64, trow, tb);
                     issued |= 1u << stage;
@@ -300,19 +341,45 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                     }
                 }
             }
-            // every copy has landed before the CTA leaves: the weights on their own
-            // barrier; the tokens on the even CTA's, or consumed by the MMAs
+            // every copy has landed before the CTA leaves: seen on the even CTA's
+            // barrier, or consumed by the MMAs
             for (int s = 0; s < STAGES; ++s)
-                if ((issued >> s) & 1u) {
-                    bounded_drain(wfull(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
+                if ((issued >> s) & 1u)
                     bounded_drain(rank == 0 ? tfull(s) : empty(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
+        } else if (warp == 2 && lane == 0) {
+            // ---------------- weights (both CTAs, each its own channels) ----------------
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, last_par = 0;
+            bool ok = true;
+            for (int u = unit0; u < total && ok; u += ustep) {
+                const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
+                // 64 + 64 channels: a SwiGLU tile's gates and ups, else one run
+                const int c0 = t.f0 + rank * OUT_CH, c1 = SWIGLU ? c0 + p.F : c0 + 64;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!bounded_wait(wempty(stage), phase ^ 1u, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sW = sbase + W_OFF + stage * W_BYTES;
+                    mbar_expect_tx(wfull(stage), W_BYTES);
+                    tma_load_3d(sW, &p.mapW, kb * BK, c0, t.e, wfull(stage));
+                    tma_load_3d(sW + W_BYTES / 2, &p.mapW, kb * BK, c1, t.e, wfull(stage));
+                    issued |= 1u << stage;
+                    last_par = (last_par & ~(1u << stage)) | (phase << stage);
+                    if (++stage == WSTAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
+            }
+            for (int s = 0; s < WSTAGES; ++s)
+                if ((issued >> s) & 1u) bounded_drain(wfull(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
         } else if (warp == 1 && lane == 0 && rank == 0) {
             // ---------------- MMA issuer (even CTA) ----------------
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            const uint64_t bdesc0 = smem_desc_sw128(sbase + W_BYTES, 16, 1024);
+            const uint64_t bdesc0 = smem_desc_sw128(sbase, 16, 1024);
             for (int u = unit0; u < total && ok; u += ustep) {
                 const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
                 const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(((t.n + 15) & ~15) >> 3) << 17);
@@ -329,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t bs = bdesc0 + (static_cast<uint64_t>(stage * STAGE_BYTES) >> 4);
+                        const uint64_t bs = bdesc0 + (static_cast<uint64_t>(stage * T_BYTES) >> 4);
                         const uint32_t at = tmem + A_COL + static_cast<uint32_t>(stage * 64);
                         const int steps = min(BK, p.K - kb * BK) / 16;
                         for (int ks = 0; ks < steps; ++ks)
@@ -356,19 +423,20 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
         // This thread's tensor-memory lane takes one channel of the stage. SwiGLU: a
         // quarter's lanes 0-15 are gates, 16-31 the ups of the same channels.
         const int row = SWIGLU ? (lane < 16 ? 16 * q + lane : 64 + 16 * q + lane - 16) : 32 * q + lane;
-        int stage = 0;
-        uint32_t phase = 0;
+        int stage = 0, ws = 0;
+        uint32_t phase = 0, wphase = 0;
         bool ok = true;
         for (int u = unit0; u < total && ok; u += ustep) {
             for (int kb = 0; kb < kblocks; ++kb) {
                 int w = 1;
-                if (lane == 0) w = bounded_wait(wfull(stage), phase, wc) ? 1 : 0;
+                // the weights are there, and the MMAs have read the columns' last content
+                if (lane == 0) w = bounded_wait(wfull(ws), wphase, wc) && bounded_wait(empty(stage), phase ^ 1u, wc) ? 1 : 0;
                 if (!__shfl_sync(0xffffffffu, w, 0)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint8_t* wr = smem + stage * STAGE_BYTES + row * BK;
+                const uint8_t* wr = smem + W_OFF + ws * W_BYTES + row * BK;
                 const uint32_t at = tmem + A_COL + static_cast<uint32_t>(stage * 64) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -388,8 +456,13 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
+                    mbar_arrive(wempty(ws));
                     if (rank == 0) mbar_arrive(aready(stage));
                     else mbar_arrive_remote(map_shared_rank(aready(stage), 0));
+                }
+                if (++ws == WSTAGES) {
+                    ws = 0;
+                    wphase ^= 1u;
                 }
                 if (++stage == STAGES) {
                     stage = 0;
@@ -407,7 +480,8 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
         for (int u = unit0; u < total && ok; u += ustep) {
             const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
             const uint32_t ta = tmem + static_cast<uint32_t>(c0) + (static_cast<uint32_t>(q * 32) << 16);
-            int acc[128];
+            // one chunk: the FP32 accumulator as it is; several: their integer sum
+            uint32_t acc[128];
             for (int c = 0; c < nchunks; ++c) {
                 int w = 1;
                 if (lane == 0) w = bounded_wait(acc_full, phase, wc) ? 1 : 0;
@@ -417,18 +491,21 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                 }
                 phase ^= 1u;
                 tc_fence_after();
+                if (c == 0) {
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    if (c0 + 16 * g < t.n) {
-                        uint32_t r[16];
-                        tc_ld_32x32b_x16(ta + 16 * g, r);
-                        tc_wait_ld();
+                    for (int g = 0; g < 8; ++g)
+                        if (c0 + 16 * g < t.n) tc_ld_16(ta + 16 * g, acc + 16 * g);
+                    tc_wait_ld();
+                } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int v = __float2int_rn(__uint_as_float(r[i]));
-                            acc[16 * g + i] = c == 0 ? v : acc[16 * g + i] + v;
+                    for (int g = 0; g < 8; ++g)
+                        if (c0 + 16 * g < t.n) {
+                            uint32_t r[16];
+                            tc_ld_16(ta + 16 * g, r);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[16 * g + i] += __float2int_rn(__uint_as_float(r[i]));
                         }
-                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -436,8 +513,16 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                     if (rank == 0) mbar_arrive(acc_empty);
                     else mbar_arrive_remote(map_shared_rank(acc_empty, 0));
                 }
+                if (c == 0 && nchunks > 1) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) acc[i] = __float2int_rn(__uint_as_float(acc[i]));
+                }
             }
             if (!ok) break;
+            if (nchunks > 1) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i) acc[i] = __float_as_uint(static_cast<float>(static_cast<int>(acc[i])));
+            }
             // this lane's channel, its scale, and the tokens' scales (lane l: tokens 32 j + l)
             const int oc = SWIGLU ? t.f0 + rank * OUT_CH + 16 * q + (lane & 15) : t.f0 + rank * OUT_CH + 32 * q + lane;
             const bool in = oc < p.F;
@@ -455,14 +540,14 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                 if (c0 + i < t.n) {
                     const float s0 = __shfl_sync(0xffffffffu, sa[i >> 5], i & 31);
                     const float s1 = __shfl_sync(0xffffffffu, sa[i >> 5], (i & 31) + 1);
-                    const float v0 = static_cast<float>(acc[i]) * s0 * sb, v1 = static_cast<float>(acc[i + 1]) * s1 * sb;
+                    const float v0 = __uint_as_float(acc[i]) * s0 * sb, v1 = __uint_as_float(acc[i + 1]) * s1 * sb;
                     if (SWIGLU) {
                         // lanes 0-15 finish token i, lanes 16-31 token i + 1
                         const bool lower = lane < 16;
                         const float other = __shfl_xor_sync(0xffffffffu, lower ? v1 : v0, 16);
                         const float g = lower ? v0 : other, up = lower ? other : v1;
                         const int ti = i + (lower ? 0 : 1);
-                        if (in && c0 + ti < t.n) orow[static_cast<long long>(ti) * p.F] = from_f32<O>(g * sigmoid_f(g) * up);
+                        if (in && c0 + ti < t.n) orow[static_cast<long long>(ti) * p.F] = from_f32<O>(g * epi_sigmoid<O>(g) * up);
                     } else if (in) {
                         orow[static_cast<long long>(i) * p.F] = from_f32<O>(v0);
                         if (c0 + i + 1 < t.n) orow[static_cast<long long>(i + 1) * p.F] = from_f32<O>(v1);
@@ -483,6 +568,9 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
         tmem_dealloc_pair(tmem, TMEM_COLS);
     }
 }
+
+constexpr size_t L1_BYTES = 8192;  // a word per CTA of the tokens' pass
+size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <bool SWIGLU, typename O>
 int pair_slots(int dev) {
@@ -525,7 +613,8 @@ cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
     if (slots <= 0) return cudaErrorInvalidConfiguration;
     uint8_t* ws = reinterpret_cast<uint8_t*>(a.err);
     float* tsa = reinterpret_cast<float*>(ws + 256);
-    uint8_t* tok = ws + int8_tc_tokens_offset(a.M);
+    int* l1 = reinterpret_cast<int*>(ws + 256 + pad256(static_cast<size_t>(a.M) * 4));
+    uint8_t* tok = reinterpret_cast<uint8_t*>(l1) + L1_BYTES;
     Int8TcParams p{};
     p.M = a.M; p.K = a.K; p.N = a.N; p.E = a.E;
     p.F = SWIGLU ? a.N / 2 : a.N;
@@ -541,13 +630,15 @@ cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
         !encode_tmap_typed(&p.mapT, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, tok, 2, td, tst, tb))
         return cudaErrorInvalidValue;
     p.offsets = a.offsets;
+    const int warps = TOK_THREADS / 32, cap = num_sms() * 8, want = (a.M + warps - 1) / warps;
+    const int tgrid = min(min(want, cap), static_cast<int>(L1_BYTES / 4));
     p.sa = tsa; p.sb = a.sb; p.out = a.out;
+    p.l1 = l1; p.nl1 = tgrid;
     p.err = a.err;
     p.timeout_ns = wait_timeout_ns();
-    const int warps = TOK_THREADS / 32, cap = num_sms() * 8, want = (a.M + warps - 1) / warps;
-    cudaError_t e = launch_pdl(int8_tokens_kernel<O>, dim3(want < cap ? want : cap), dim3(TOK_THREADS), 0, s, a.M, a.Ma,
+    cudaError_t e = launch_pdl(int8_tokens_kernel<O>, dim3(tgrid), dim3(TOK_THREADS), 0, s, a.M, a.Ma,
                                a.K, a.E, p.F, a.a, a.lda, a.sa, a.offsets, a.rows, reinterpret_cast<uint4*>(tok), tsa,
-                               static_cast<O*>(a.out), a.err);
+                               static_cast<O*>(a.out), l1, a.err);
     if (e != cudaSuccess) return e;
     const long long bound = (static_cast<long long>((a.M + NT - 1) / NT) + (a.E > 1 ? a.E : 0)) * p.nt;
     const int grid = static_cast<int>(bound < slots ? (bound > 0 ? bound : 1) : slots);
@@ -557,10 +648,10 @@ cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
 
 }  // namespace
 
-// Workspace: the error word's 256 bytes, the gathered scales, the tokens.
-size_t int8_tc_tokens_offset(int M) { return 256 + (static_cast<size_t>(M) * 4 + 255) / 256 * 256; }
+// Workspace: the error word's 256 bytes, the gathered scales, the tokens'
+// pass's row sums, the tokens.
 size_t int8_tc_workspace(int M, int K) {
-    return int8_tc_tokens_offset(M) + static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
+    return 256 + pad256(static_cast<size_t>(M) * 4) + L1_BYTES + static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
 }
 
 cudaError_t launch_int8_tc(const Int8Args& a, cudaStream_t s) {

@@ -558,7 +558,6 @@ struct Int8Args {
 };
 cudaError_t launch_int8_vec(const Int8Args& a, cudaStream_t s);
 // The tensor-core form: a.err points to a workspace of int8_tc_workspace bytes.
-size_t int8_tc_tokens_offset(int M);
 size_t int8_tc_workspace(int M, int K);
 cudaError_t launch_int8_tc(const Int8Args& a, cudaStream_t s);
 
