@@ -69,6 +69,16 @@ MOE_DEV float warp_sum(float v) {
     return v;
 }
 
+// Sum of the W values (W a power of two, at most 32) that lanes 0 to W - 1
+// hold, the same in every lane and in a fixed order.
+template <int W>
+MOE_DEV float group_sum(float v) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (W < 32) v = __shfl_sync(0xffffffffu, v, 0);
+    return v;
+}
+
 // Sums of a and b over the TPR threads of a row, the same in all of them and
 // in a fixed order. TPR = 32: within the warp. Else over the CTA (TPR
 // threads), through `scratch`, two halves of 2 * TPR / 32 floats used in turn:
@@ -88,9 +98,85 @@ MOE_DEV void row_sum2(float& a, float& b, float* scratch, int& turn) {
         }
         __syncthreads();
         const int l = static_cast<int>(lane_id());
-        a = warp_sum(l < W ? s[l] : 0.0f);
-        b = warp_sum(l < W ? s[W + l] : 0.0f);
+        a = group_sum<W>(l < W ? s[l] : 0.0f);
+        b = group_sum<W>(l < W ? s[W + l] : 0.0f);
     }
 }
+
+// VEC consecutive floats (16-byte aligned where VEC >= 4).
+template <int VEC>
+MOE_DEV void load_f32(const float* p, float (&f)[VEC]) {
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
+            f[i] = v.x;
+            f[i + 1] = v.y;
+            f[i + 2] = v.z;
+            f[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = __ldg(p + i);
+    }
+}
+
+MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+MOE_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// What a thread reads of the rows ahead: its own vectors (NV per row, vector i
+// at column (i * TPR + t) * VEC), copied asynchronously into its own part of
+// shared memory, D rows deep, so that the bytes in flight do not depend on
+// registers and no thread waits for another's copies. Elements that cp.async
+// cannot move (single 16-bit ones) go through registers, one row ahead.
+template <typename T, int VEC, int NV, int TPR, int THREADS, int DEPTH>
+struct RowFetch {
+    static constexpr int BYTES = VEC * static_cast<int>(sizeof(T));
+    static constexpr bool ASYNC = BYTES >= 4;
+    static constexpr int D = ASYNC ? DEPTH : 1;
+    static constexpr int SMEM = ASYNC ? D * NV * THREADS * BYTES : 0;
+    T* slots;
+    const T* base;
+    long long pitch;
+    int d, t;
+    Raw<T, VEC> ahead[ASYNC ? 1 : NV];
+
+    MOE_DEV void init(void* smem, const T* base_, long long pitch_, int d_, int t_) {
+        slots = static_cast<T*>(smem) + threadIdx.x * VEC;
+        base = base_;
+        pitch = pitch_;
+        d = d_;
+        t = t_;
+    }
+    // Starts the copies of `row` into slot s (nothing unless there).
+    MOE_DEV void issue(int s, long long row, bool there) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (there && c < d) {
+                if constexpr (ASYNC) {
+                    T* at = slots + (s * NV + i) * THREADS * VEC;
+                    if constexpr (BYTES == 16) cp_async_16(at, base + row * pitch + c);
+                    else cp_async_4(at, base + row * pitch + c);
+                } else {
+                    ahead[i].load(base + row * pitch + c);
+                }
+            }
+        }
+    }
+    // Vector i of slot s as FP32 (zeros past the row's end).
+    MOE_DEV void get(int s, int i, float (&f)[VEC]) const {
+        const bool in = (i * TPR + t) * VEC < d;
+        Raw<T, VEC> r;
+        r.clear();
+        if constexpr (ASYNC) {
+            if (in) r = *reinterpret_cast<const Raw<T, VEC>*>(slots + (s * NV + i) * THREADS * VEC);
+        } else {
+            if (in) r = ahead[i];
+        }
+        r.get(f);
+    }
+};
 
 }  // namespace moe

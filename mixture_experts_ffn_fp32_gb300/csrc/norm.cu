@@ -8,11 +8,12 @@
 // Both are bound by memory: the forward reads x and writes y, the backward
 // reads x and dy and writes dx, each element once. A row is held in registers
 // by a warp (short rows) or by a CTA, 16 elements a thread, between its
-// reduction and its output.
+// reduction and its output, while the next rows of the CTA travel into shared
+// memory.
 //
-// Statistics are FP32. The forward sums the row, then the row less that mean:
-// the second pass yields the squares and what rounding left in the mean, so a
-// row whose mean is large against its deviation loses nothing.
+// Statistics are FP32. The forward sums the row, then the row less a mean: the
+// second sums yield the squares and what rounding left in the mean, so a row
+// whose mean is large against its deviation loses nothing.
 #include "elem.cuh"
 #include "internal.h"
 
@@ -24,17 +25,92 @@ namespace {
 // registers each, and it spilled).
 constexpr int FWD_MAX_D = 16384;
 constexpr int BWD_MAX_D = 8192;
+// Rows that travel ahead of the one a CTA works on.
+constexpr int FWD_DEPTH = 3;
+constexpr int BWD_DEPTH = 2;
 
 // 1 / sqrt(var + eps); a variance that rounding took below zero is zero, a NaN stays.
 MOE_DEV float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
+// Mean and variance of a row from its threads' NV x VEC values, left as
+// v - m0. A warp takes its own mean, and its sums of the differences and of
+// their squares; the CTA then joins the warps' numbers (m, r, q of n values)
+// behind one sync:
+//   m0 = sum n m / d,  rest = sum (n (m - m0) + r) / d
+//   var = sum (q + 2 (m - m0) r + n (m - m0)^2) / d - rest^2
+// `rest` is what rounding left in m0.
+template <int VEC, int NV, int TPR>
+MOE_DEV void row_moments(float (&v)[NV][VEC], int d, int t, float inv_d, float4* scratch, int& turn, float& m0,
+                         float& rest, float& var) {
+    constexpr int W = TPR / 32;
+    const int w = W == 1 ? 0 : static_cast<int>(threadIdx.x >> 5);
+    float s = 0.0f, n = 0.0f;  // n: the warp's values, cut at d
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        n += static_cast<float>(min(max(d - (i * TPR + w * 32) * VEC, 0), 32 * VEC));
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s += v[i][j];
+    }
+    s = warp_sum(s);
+    const float m = W == 1 ? s * inv_d : (n > 0.0f ? s / n : 0.0f);
+    float r = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const bool in = (i * TPR + t) * VEC < d;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            v[i][j] = in ? v[i][j] - m : 0.0f;
+            r += v[i][j];
+            q += v[i][j] * v[i][j];
+        }
+    }
+    r = warp_sum(r);
+    q = warp_sum(q);
+    if constexpr (W == 1) {
+        m0 = m;
+        rest = r * inv_d;
+        var = q * inv_d - rest * rest;
+    } else {
+        float4* sc = scratch + (turn & 1) * W;  // two turns: see row_sum2
+        ++turn;
+        if (lane_id() == 0) sc[w] = make_float4(m, r, q, n);
+        __syncthreads();
+        const int l = static_cast<int>(lane_id());
+        float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (l < W) e = sc[l];
+        m0 = group_sum<W>(e.w * e.x) * inv_d;
+        const float dm = e.x - m0;
+        rest = group_sum<W>(e.w * dm + e.y) * inv_d;
+        var = group_sum<W>(e.z + 2.0f * dm * e.y + e.w * dm * dm) * inv_d - rest * rest;
+        const float shift = m - m0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[i][j] += shift;
+    }
+}
+
 template <typename T, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR)
+struct Forward {
+    static constexpr int THREADS = TPR == 32 ? 128 : TPR;
+    // CTAs of an SM: as many threads as the registers of a thread's columns leave
+    static constexpr int PER_SM = TPR == 1024 ? 1 : (VEC == 1 || NV * VEC > 16 ? 512 : 768) / THREADS;
+    // gamma and beta stay in registers where a thread has few columns
+    static constexpr bool KEEP = VEC > 1 && NV * VEC <= 16 && TPR < 1024;
+    using Fetch = RowFetch<T, VEC, NV, TPR, THREADS, FWD_DEPTH>;
+};
+
+template <typename T, int VEC, int NV, int TPR>
+__global__ void __launch_bounds__(Forward<T, VEC, NV, TPR>::THREADS, Forward<T, VEC, NV, TPR>::PER_SM)
 layer_norm_kernel(int R, int d, const T* __restrict__ x, long long xs, const float* __restrict__ gamma,
                   const float* __restrict__ beta, float eps, T* __restrict__ y, long long ys,
                   float* __restrict__ mean, float* __restrict__ rstd) {
+    using F = typename Forward<T, VEC, NV, TPR>::Fetch;
+    constexpr int D = F::D;
     constexpr int RPC = TPR == 32 ? 4 : 1;  // rows a CTA works on at a time
-    __shared__ float scratch[TPR > 32 ? 4 * (TPR / 32) : 1];
+    constexpr bool KEEP = Forward<T, VEC, NV, TPR>::KEEP;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float4 scratch[TPR > 32 ? 2 * (TPR / 32) : 1];
     const int t = TPR == 32 ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
     const long long step = static_cast<long long>(gridDim.x) * RPC;
     long long row = static_cast<long long>(blockIdx.x) * RPC + (TPR == 32 ? threadIdx.x >> 5 : 0);
@@ -42,55 +118,49 @@ layer_norm_kernel(int R, int d, const T* __restrict__ x, long long xs, const flo
     int turn = 0;
     pdl_wait();
     pdl_trigger();
-    Raw<T, VEC> cur[NV];
-    auto fetch = [&](long long r) {
+    F in;
+    in.init(smem, x, xs, d, t);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * VEC;
-            if (r < R && c < d)
-                cur[i].load(x + r * xs + c);
-            else
-                cur[i].clear();
+    for (int s = 0; s < D; ++s) {
+        in.issue(s, row + s * step, row + s * step < R);
+        if constexpr (F::ASYNC) cp_async_commit();
+    }
+    float ga[KEEP ? NV : 1][VEC], be[KEEP ? NV : 1][VEC];
+    auto columns = [&](int i, float (&g)[VEC], float (&b)[VEC]) {
+        const int c = (i * TPR + t) * VEC;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            g[j] = 1.0f;
+            b[j] = 0.0f;
         }
+        if (c < d && gamma != nullptr) load_f32<VEC>(gamma + c, g);
+        if (c < d && beta != nullptr) load_f32<VEC>(beta + c, b);
     };
-    fetch(row);
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) columns(i, ga[i], be[i]);
+    }
+    int slot = 0;
     for (; row < R; row += step) {
         float v[NV][VEC];
-        float s = 0.0f, unused = 0.0f;
+        if constexpr (F::ASYNC) cp_async_wait<D - 1>();
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            cur[i].get(v[i]);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) s += v[i][j];
-        }
-        fetch(row + step);  // the next row travels while this one is reduced
-        row_sum2<TPR>(s, unused, scratch, turn);
-        const float m0 = s * inv_d;
-        float r1 = 0.0f, r2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const bool in = (i * TPR + t) * VEC < d;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                v[i][j] = in ? v[i][j] - m0 : 0.0f;
-                r1 += v[i][j];
-                r2 += v[i][j] * v[i][j];
-            }
-        }
-        row_sum2<TPR>(r1, r2, scratch, turn);
-        const float rest = r1 * inv_d;
-        const float rs = rstd_of(r2 * inv_d - rest * rest, eps);
+        for (int i = 0; i < NV; ++i) in.get(slot, i, v[i]);
+        in.issue(slot, row + D * step, row + D * step < R);
+        if constexpr (F::ASYNC) cp_async_commit();
+        if (++slot == D) slot = 0;
+        float m0, rest, var;
+        row_moments<VEC, NV, TPR>(v, d, t, inv_d, scratch, turn, m0, rest, var);
+        const float rs = rstd_of(var, eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VEC;
+            if (!KEEP) columns(i, ga[0], be[0]);
             if (c < d) {
                 float o[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    o[j] = (v[i][j] - rest) * rs;
-                    if (gamma != nullptr) o[j] *= __ldg(gamma + c + j);
-                    if (beta != nullptr) o[j] += __ldg(beta + c + j);
-                }
+                for (int j = 0; j < VEC; ++j)
+                    o[j] = (v[i][j] - rest) * rs * ga[KEEP ? i : 0][j] + be[KEEP ? i : 0][j];
                 Raw<T, VEC> out;
                 out.set(o);
                 out.store(y + row * ys + c);
@@ -141,15 +211,28 @@ layer_norm_long_kernel(int R, int d, const T* __restrict__ x, long long xs, cons
     }
 }
 
+// Threads per row of the backward at width d, and CTAs of them on an SM.
+constexpr int bwd_threads(int d) { return d <= 32 * 8 ? 32 : d <= 128 * 16 ? 128 : d <= 256 * 16 ? 256 : 512; }
+constexpr int bwd_per_sm(int tpr) { return 512 / (tpr == 32 ? 128 : tpr); }
+
+template <typename T, int VEC, int NV, int TPR>
+struct Backward {
+    static constexpr int THREADS = TPR == 32 ? 128 : TPR;
+    using Fetch = RowFetch<T, VEC, NV, TPR, THREADS, BWD_DEPTH>;
+};
+
 // Backward: a CTA walks rows and keeps its threads' columns of dgamma and
 // dbeta in registers; part[cta] receives them, [2, d] FP32 each.
 template <typename T, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR)
+__global__ void __launch_bounds__(Backward<T, VEC, NV, TPR>::THREADS, bwd_per_sm(TPR))
 layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, const T* __restrict__ x, long long xs,
                       const float* __restrict__ mean, const float* __restrict__ rstd,
                       const float* __restrict__ gamma, T* __restrict__ dx, long long dxs,
                       float* __restrict__ part) {
+    using F = typename Backward<T, VEC, NV, TPR>::Fetch;
+    constexpr int D = F::D;
     constexpr int RPC = TPR == 32 ? 4 : 1;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[TPR > 32 ? 4 * (TPR / 32) : 1];
     __shared__ float gather[TPR == 32 ? 2 * NV * VEC * 32 : 1];
     const int t = TPR == 32 ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
@@ -158,45 +241,67 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
     const float inv_d = 1.0f / static_cast<float>(d);
     int turn = 0;
     float dg[NV][VEC] = {}, db[NV][VEC] = {};
+    constexpr bool KEEP = VEC > 1;  // gamma in registers
+    float ga[KEEP ? NV : 1][VEC];
     pdl_wait();
     pdl_trigger();
-    Raw<T, VEC> cx[NV], cy[NV];
-    auto fetch = [&](long long r) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * VEC;
-            if (r < R && c < d) {
-                cx[i].load(x + r * xs + c);
-                cy[i].load(dy + r * dys + c);
-            } else {
-                cx[i].clear();
-                cy[i].clear();
-            }
-        }
+    F fx, fy;
+    fx.init(smem, x, xs, d, t);
+    fy.init(smem + F::SMEM, dy, dys, d, t);
+    auto issue = [&](int s, long long r) {
+        fx.issue(s, r, r < R);
+        fy.issue(s, r, r < R);
+        if constexpr (F::ASYNC) cp_async_commit();
     };
-    fetch(row);
+#pragma unroll
+    for (int s = 0; s < D; ++s) issue(s, row + s * step);
+    auto columns = [&](int i, float (&g)[VEC]) {
+        const int c = (i * TPR + t) * VEC;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) g[j] = 1.0f;
+        if (c < d && gamma != nullptr) load_f32<VEC>(gamma + c, g);
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) columns(i, ga[i]);
+    }
+    float mu = 0.0f, rs = 0.0f;  // of the next row
+    if (row < R) {
+        mu = __ldg(mean + row);
+        rs = __ldg(rstd + row);
+    }
+    int slot = 0;
     for (; row < R; row += step) {
-        const float mu = __ldg(mean + row), rs = __ldg(rstd + row);
         float xh[NV][VEC], g[NV][VEC];
         float s1 = 0.0f, s2 = 0.0f;
+        const float mc = mu, rc = rs;
+        if (row + step < R) {
+            mu = __ldg(mean + row + step);
+            rs = __ldg(rstd + row + step);
+        }
+        if constexpr (F::ASYNC) cp_async_wait<D - 1>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * VEC;
-            cx[i].get(xh[i]);
-            cy[i].get(g[i]);
-            if (c < d) {
+            fx.get(slot, i, xh[i]);
+            fy.get(slot, i, g[i]);
+        }
+        issue(slot, row + D * step);
+        if (++slot == D) slot = 0;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    xh[i][j] = (xh[i][j] - mu) * rs;
-                    dg[i][j] += g[i][j] * xh[i][j];
-                    db[i][j] += g[i][j];
-                    if (gamma != nullptr) g[i][j] *= __ldg(gamma + c + j);
-                    s1 += g[i][j];
-                    s2 += g[i][j] * xh[i][j];
-                }
+        for (int i = 0; i < NV; ++i) {
+            // past the row's end dy is zero; x counts as the mean there
+            const bool in = (i * TPR + t) * VEC < d;
+            if (!KEEP) columns(i, ga[0]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                xh[i][j] = in ? (xh[i][j] - mc) * rc : 0.0f;
+                dg[i][j] += g[i][j] * xh[i][j];
+                db[i][j] += g[i][j];
+                g[i][j] *= ga[KEEP ? i : 0][j];
+                s1 += g[i][j];
+                s2 += g[i][j] * xh[i][j];
             }
         }
-        fetch(row + step);
         row_sum2<TPR>(s1, s2, scratch, turn);
         s1 *= inv_d;
         s2 *= inv_d;
@@ -206,7 +311,7 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
             if (c < d) {
                 float o[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) o[j] = rs * (g[i][j] - s1 - xh[i][j] * s2);
+                for (int j = 0; j < VEC; ++j) o[j] = rc * (g[i][j] - s1 - xh[i][j] * s2);
                 Raw<T, VEC> out;
                 out.set(o);
                 out.store(dx + row * dxs + c);
@@ -304,33 +409,35 @@ layer_norm_bwd_cols_kernel(int R, int d, const T* __restrict__ dy, long long dys
 }
 
 // dgamma, dbeta = the sums of the n partial rows [2, d], each column in a
-// fixed order: 8 threads take every eighth row, then add theirs in order.
-__global__ void __launch_bounds__(256)
+// fixed order: 16 threads take every sixteenth row, eight loads in flight,
+// then theirs are added in order.
+constexpr int COL_ROWS = 16;
+__global__ void __launch_bounds__(32 * COL_ROWS)
 layer_norm_cols_sum_kernel(int n, int d, const float* __restrict__ part, float* __restrict__ dgamma,
                            float* __restrict__ dbeta) {
-    __shared__ float s[8][32];
+    __shared__ float s[COL_ROWS][32];
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + cx;
     pdl_wait();
     pdl_trigger();
     float a = 0.0f;
     if (c < 2 * d) {
-        int r = ry;
-        for (; r + 24 < n; r += 32) {  // four loads in flight
-            const float p0 = part[static_cast<long long>(r) * 2 * d + c];
-            const float p1 = part[static_cast<long long>(r + 8) * 2 * d + c];
-            const float p2 = part[static_cast<long long>(r + 16) * 2 * d + c];
-            const float p3 = part[static_cast<long long>(r + 24) * 2 * d + c];
-            a += (p0 + p1) + (p2 + p3);
+        for (int r0 = ry; r0 < n; r0 += 8 * COL_ROWS) {
+            float p[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = r0 + i * COL_ROWS;
+                p[i] = r < n ? part[static_cast<long long>(r) * 2 * d + c] : 0.0f;
+            }
+            a += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
         }
-        for (; r < n; r += 8) a += part[static_cast<long long>(r) * 2 * d + c];
     }
     s[ry][cx] = a;
     __syncthreads();
     if (ry == 0 && c < 2 * d) {
         float v = s[0][cx];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) v += s[i][cx];
+        for (int i = 1; i < COL_ROWS; ++i) v += s[i][cx];
         if (c < d) {
             if (dgamma != nullptr) dgamma[c] = v;
         } else if (dbeta != nullptr) {
@@ -348,14 +455,26 @@ int grid_rows(long long rows, int rpc, int per_sm) {
     return static_cast<int>(want < cap ? want : cap);
 }
 
-// CTAs of the backward, and so partial rows of its workspace.
-constexpr int BWD_PER_SM = 2;
+// Dynamic shared memory above the default limit has to be asked for, once per
+// kernel and device.
+template <typename K>
+bool allow_smem(K kernel, int bytes, bool (&done)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!done[dev]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+        done[dev] = true;
+    }
+    return true;
+}
 
 template <typename T, int VEC, int NV, int TPR>
 cudaError_t fwd_t(const LayerNormArgs& a, cudaStream_t s) {
-    const int rpc = TPR == 32 ? 4 : 1, threads = TPR == 32 ? 128 : TPR;
-    const int grid = grid_rows(a.R, rpc, 2048 / threads);
-    return launch_pdl(layer_norm_kernel<T, VEC, NV, TPR>, dim3(grid), dim3(threads), 0, s, a.R, a.d,
+    using C = Forward<T, VEC, NV, TPR>;
+    static bool done[64] = {};
+    if (!allow_smem(layer_norm_kernel<T, VEC, NV, TPR>, C::Fetch::SMEM, done)) return cudaErrorInvalidValue;
+    const int grid = grid_rows(a.R, TPR == 32 ? 4 : 1, C::PER_SM);
+    return launch_pdl(layer_norm_kernel<T, VEC, NV, TPR>, dim3(grid), dim3(C::THREADS), C::Fetch::SMEM, s, a.R, a.d,
                       static_cast<const T*>(a.x), a.x_stride, a.gamma, a.beta, a.eps, static_cast<T*>(a.y),
                       a.y_stride, a.mean_out, a.rstd_out);
 }
@@ -377,26 +496,33 @@ cudaError_t fwd_d(const LayerNormArgs& a, cudaStream_t s) {
         return launch_pdl(layer_norm_long_kernel<T>, dim3(grid_rows(a.R, 1, 2)), dim3(1024), 0, s, a.R, a.d,
                           static_cast<const T*>(a.x), a.x_stride, a.gamma, a.beta, a.eps, static_cast<T*>(a.y),
                           a.y_stride, a.mean_out, a.rstd_out);
-    if (a.d % V == 0 && vec_ok(a.x, a.x_stride, sizeof(T)) && vec_ok(a.y, a.y_stride, sizeof(T)))
+    if (a.d % V == 0 && vec_ok(a.x, a.x_stride, sizeof(T)) && vec_ok(a.y, a.y_stride, sizeof(T)) &&
+        vec_ok(a.gamma, 0, 4) && vec_ok(a.beta, 0, 4))
         return fwd_v<T, V>(a, s);
     return fwd_v<T, 1>(a, s);
 }
 
 template <typename T, int VEC, int NV, int TPR>
 cudaError_t bwd_t(const LayerNormArgs& a, int grid, float* part, cudaStream_t s) {
-    const int threads = TPR == 32 ? 128 : TPR;
-    return launch_pdl(layer_norm_bwd_kernel<T, VEC, NV, TPR>, dim3(grid), dim3(threads), 0, s, a.R, a.d,
+    using C = Backward<T, VEC, NV, TPR>;
+    constexpr int SMEM = 2 * C::Fetch::SMEM;
+    static bool done[64] = {};
+    if (!allow_smem(layer_norm_bwd_kernel<T, VEC, NV, TPR>, SMEM, done)) return cudaErrorInvalidValue;
+    return launch_pdl(layer_norm_bwd_kernel<T, VEC, NV, TPR>, dim3(grid), dim3(C::THREADS), SMEM, s, a.R, a.d,
                       static_cast<const T*>(a.dy), a.dy_stride, static_cast<const T*>(a.x), a.x_stride, a.mean,
                       a.rstd, a.gamma, static_cast<T*>(a.y), a.y_stride, part);
 }
 
 template <typename T, int VEC>
 cudaError_t bwd_v(const LayerNormArgs& a, int grid, float* part, cudaStream_t s) {
-    const int d = a.d;
-    if (d <= 32 * 8) return bwd_t<T, VEC, 8 / VEC, 32>(a, grid, part, s);
-    if (d <= 128 * 8) return bwd_t<T, VEC, 8 / VEC, 128>(a, grid, part, s);
-    if (d <= 256 * 16) return bwd_t<T, VEC, 16 / VEC, 256>(a, grid, part, s);
-    return bwd_t<T, VEC, 16 / VEC, 512>(a, grid, part, s);
+    switch (bwd_threads(a.d)) {
+        case 32: return bwd_t<T, VEC, 8 / VEC, 32>(a, grid, part, s);
+        case 128:
+            if (a.d <= 128 * 8) return bwd_t<T, VEC, 8 / VEC, 128>(a, grid, part, s);
+            return bwd_t<T, VEC, 16 / VEC, 128>(a, grid, part, s);
+        case 256: return bwd_t<T, VEC, 16 / VEC, 256>(a, grid, part, s);
+        default: return bwd_t<T, VEC, 16 / VEC, 512>(a, grid, part, s);
+    }
 }
 
 template <typename T>
@@ -413,13 +539,13 @@ cudaError_t bwd_d(const LayerNormArgs& a, float* part, cudaStream_t s) {
                            static_cast<const T*>(a.dy), a.dy_stride, static_cast<const T*>(a.x), a.x_stride,
                            a.mean, a.rstd, part);
     } else if (a.d % V == 0 && vec_ok(a.x, a.x_stride, sizeof(T)) && vec_ok(a.dy, a.dy_stride, sizeof(T)) &&
-               vec_ok(a.y, a.y_stride, sizeof(T))) {
+               vec_ok(a.y, a.y_stride, sizeof(T)) && vec_ok(a.gamma, 0, 4)) {
         e = bwd_v<T, V>(a, n, part, s);
     } else {
         e = bwd_v<T, 1>(a, n, part, s);
     }
     if (e != cudaSuccess || part == nullptr) return e;
-    return launch_pdl(layer_norm_cols_sum_kernel, dim3((2 * a.d + 31) / 32), dim3(256), 0, s, n, a.d,
+    return launch_pdl(layer_norm_cols_sum_kernel, dim3((2 * a.d + 31) / 32), dim3(32 * COL_ROWS), 0, s, n, a.d,
                       static_cast<const float*>(part), a.dgamma, a.dbeta);
 }
 
@@ -427,7 +553,8 @@ cudaError_t bwd_d(const LayerNormArgs& a, float* part, cudaStream_t s) {
 
 int layer_norm_bwd_parts(int R, int d) {
     if (d > BWD_MAX_D) return R < 16 ? R : 16;
-    return grid_rows(R, d <= 256 ? 4 : 1, BWD_PER_SM);
+    const int t = bwd_threads(d);
+    return grid_rows(R, t == 32 ? 4 : 1, bwd_per_sm(t));
 }
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s) {
