@@ -9,6 +9,7 @@ with ``mixture_experts_ffn_fp32_gb300.build.build()``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -549,6 +550,13 @@ def _on(stream, *inputs):
     return _HERE if stream is None else _On(stream, *inputs)
 
 
+def _raw_stream(stream, t) -> int:
+    """The stream's handle, else that of the current stream of t's device (the
+    binding that torch's own generated code uses: torch.cuda.current_stream()
+    takes several microseconds, as long as a small kernel)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
 def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, stream=None) -> dict:
     """moe_layer_norm: x [R, d] (FP32, BF16 or FP16; rows at any pitch), weight and
     bias [d] FP32 or None. Returns y [R, d] in x's type and the FP32 statistics
@@ -560,15 +568,17 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, strea
     if bias is not None:
         _dev(bias, torch.float32, "bias", (d,))
     with _on(stream, x, weight, bias):
-        y = torch.empty((R, d), dtype=x.dtype, device=x.device)
-        st = torch.empty((2, R), dtype=torch.float32, device=x.device)
-        mean, rstd = st.unbind(0)
+        dev = x.device
+        y = torch.empty((R, d), dtype=x.dtype, device=dev)
+        mean = torch.empty((R,), dtype=torch.float32, device=dev)
+        rstd = torch.empty((R,), dtype=torch.float32, device=dev)
         _check(lib().moe_layer_norm(R, d, _DTYPES[x.dtype], x.data_ptr(), xs, _ptr(weight), _ptr(bias), eps,
-                                    y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _stream(stream)),
+                                    y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, x)),
                "moe_layer_norm")
     return {"y": y, "mean": mean, "rstd": rstd}
 
 
+@functools.lru_cache(maxsize=4096)
 def layer_norm_backward_workspace_size(R: int, d: int) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().moe_layer_norm_backward_workspace_size(R, d, ctypes.byref(n)),
@@ -592,15 +602,15 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     with _on(stream, dy, x, mean, rstd, weight, ws):
         out = {"dx": torch.empty((R, d), dtype=x.dtype, device=x.device)}
         if weight_grads:
-            dwb = torch.empty((2, d), dtype=torch.float32, device=x.device)
-            out["dweight"], out["dbias"] = dwb.unbind(0)
+            out["dweight"] = torch.empty((d,), dtype=torch.float32, device=x.device)
+            out["dbias"] = torch.empty((d,), dtype=torch.float32, device=x.device)
             if ws is None:
-                ws = torch.empty(layer_norm_backward_workspace_size(R, d), dtype=torch.uint8, device=x.device)
+                ws = torch.empty((layer_norm_backward_workspace_size(R, d),), dtype=torch.uint8, device=x.device)
         _check(lib().moe_layer_norm_backward(R, d, _DTYPES[x.dtype], dy.data_ptr(), dys, x.data_ptr(), xs,
                                              mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
                                              out["dx"].data_ptr(), d, _ptr(out.get("dweight")),
                                              _ptr(out.get("dbias")), _ptr(ws), 0 if ws is None else ws.numel(),
-                                             _stream(stream)), "moe_layer_norm_backward")
+                                             _raw_stream(stream, x)), "moe_layer_norm_backward")
     return out
 
 
@@ -628,7 +638,7 @@ def group_route(logits: torch.Tensor, K: int, n_groups: int = 1, topk_groups: in
         out = {"idx": torch.empty((T, max(K, 0)), dtype=torch.int32, device=logits.device),
                "w": torch.empty((T, max(K, 0)), dtype=torch.float32, device=logits.device)}
         _check(lib().moe_group_route(ctypes.byref(cfg), logits.data_ptr(), ls, _ptr(bias), out["idx"].data_ptr(),
-                                     out["w"].data_ptr(), _stream(stream)), "moe_group_route")
+                                     out["w"].data_ptr(), _raw_stream(stream, logits)), "moe_group_route")
     return out
 
 
@@ -647,7 +657,7 @@ def group_route_backward(dw: torch.Tensor, idx: torch.Tensor, logits: torch.Tens
     with _on(stream, dw, idx, logits):
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
         _check(lib().moe_group_route_backward(ctypes.byref(cfg), logits.data_ptr(), ls, idx.data_ptr(),
-                                              dw.data_ptr(), out.data_ptr(), _stream(stream)),
+                                              dw.data_ptr(), out.data_ptr(), _raw_stream(stream, logits)),
                "moe_group_route_backward")
     return out
 
@@ -663,18 +673,20 @@ def quantize_rows(x: torch.Tensor, stream=None) -> dict:
         out = {"q": torch.empty((R, K), dtype=torch.int8, device=x.device),
                "scale": torch.empty((R,), dtype=torch.float32, device=x.device)}
         _check(lib().moe_quantize_rows(R, K, _DTYPES[x.dtype], x.data_ptr(), xs, out["q"].data_ptr(),
-                                       out["scale"].data_ptr(), _stream(stream)), "moe_quantize_rows")
+                                       out["scale"].data_ptr(), _raw_stream(stream, x)), "moe_quantize_rows")
     return out
 
 
-def _int8_config(M, Ma, K, N, E, swiglu, out_dtype) -> Int8Config:
+def _int8_config(M, Ma, K, N, E, swiglu, out_dtype) -> tuple:
+    """The fields of an Int8Config."""
     if out_dtype not in _OUT_DTYPES:
         raise ValueError(f"out_dtype must be one of {sorted(_OUT_DTYPES)}, got {out_dtype!r}")
-    return Int8Config(M, Ma, K, N, E, 1 if swiglu else 0, _DTYPES[_OUT_DTYPES[out_dtype]])
+    return M, Ma, K, N, E, 1 if swiglu else 0, _DTYPES[_OUT_DTYPES[out_dtype]]
 
 
-def _int8_ws(cfg) -> int:
-    n = ctypes.c_size_t(0)
+@functools.lru_cache(maxsize=4096)
+def _int8_ws(*shape) -> int:
+    cfg, n = Int8Config(*shape), ctypes.c_size_t(0)
     _check(lib().moe_matmul_int8_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
            "moe_matmul_int8_workspace_size")
     return n.value
@@ -684,7 +696,7 @@ def alloc_int8_workspace(M: int, K: int, N: int, E: int = 1, swiglu: bool = Fals
                          device="cuda") -> torch.Tensor:
     """A workspace for matmul_int8 calls of up to M product rows (its error word
     zeroed; workspace_status reads and clears it)."""
-    n = max(_int8_ws(_int8_config(m, m, K, N, E, swiglu, "f32")) for m in {M, min(M, 1)})
+    n = max(_int8_ws(*_int8_config(m, m, K, N, E, swiglu, "f32")) for m in {M, min(M, 1)})
     ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
@@ -720,14 +732,14 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     cfg = _int8_config(M, Ma, K, N, E, swiglu, out_dtype)
     with _on(stream, a, a_scale, b, b_scale, offsets, rows, ws):
         if ws is None:
-            n = _int8_ws(cfg)
+            n = _int8_ws(*cfg)
             if n:
-                ws = torch.empty(n, dtype=torch.uint8, device=a.device)
+                ws = torch.empty((n,), dtype=torch.uint8, device=a.device)
         out = torch.empty((M, N // 2 if swiglu else N), dtype=_OUT_DTYPES[out_dtype], device=a.device)
-        _check(lib().moe_matmul_int8(ctypes.byref(cfg), a.data_ptr(), a.stride(0) if Ma > 1 else K,
+        _check(lib().moe_matmul_int8(ctypes.byref(Int8Config(*cfg)), a.data_ptr(), a.stride(0) if Ma > 1 else K,
                                      a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),
                                      _ptr(rows), out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
-                                     _stream(stream)), "moe_matmul_int8")
+                                     _raw_stream(stream, a)), "moe_matmul_int8")
     return out
 
 

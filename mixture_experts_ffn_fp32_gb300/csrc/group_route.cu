@@ -97,10 +97,27 @@ MOE_DEV void merge2(F& a1, F& a2, F b1, F b2) {
     a2 = a2 < lo ? lo : a2;
 }
 
+// Sigmoid: FP32 by the fast exponential and division (the error bounds in the
+// kernel count both), FP64 in full.
+MOE_DEV float sigmoid_of(float r) { return __fdividef(1.0f, 1.0f + __expf(-r)); }
+MOE_DEV double sigmoid_of(double r) { return 1.0 / (1.0 + exp(-r)); }
+
+// The biases of a lane's experts (0 without a bias, -inf past the last).
+template <int VPL>
+MOE_DEV void lane_bias(const Params& p, int lane, float (&b)[VPL]) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane * VPL + i;
+        b[i] = e >= p.E ? -CUDART_INF_F : p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
+    }
+}
+
 // Scores and choices of a row in F; m and z: softmax maximum and denominator.
 template <typename F, int VPL>
-MOE_DEV void choices(const Params& p, const float (&r)[VPL], int lane, F (&c)[VPL], float& m, F& z) {
+MOE_DEV void choices(const Params& p, const float (&r)[VPL], const float (&b)[VPL], F (&c)[VPL], float& m, F& z) {
     const F ninf = -static_cast<F>(CUDART_INF_F);
+    m = 0.0f;
+    z = 1;
     if (p.softmax) {
         float mx = r[0];
 #pragma unroll
@@ -116,59 +133,91 @@ MOE_DEV void choices(const Params& p, const float (&r)[VPL], int lane, F (&c)[VP
         }
         z = warp_add(s);
         if (z == 0) z = 1;
+        const F inv = 1 / z;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = sizeof(F) == 8 ? c[i] / z : c[i] * inv;
     } else {
-        m = 0.0f;
-        z = 1;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = sigmoid_of(static_cast<F>(r[i]));
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        F s = p.softmax ? c[i] / z : static_cast<F>(1) / (static_cast<F>(1) + expo(-static_cast<F>(r[i])));
-        if (p.bias != nullptr && e < p.E) s += static_cast<F>(__ldg(p.bias + e));
-        c[i] = (r[i] > -CUDART_INF_F && s > ninf) ? s : ninf;
+        c[i] += static_cast<F>(b[i]);
+        if (!(r[i] > -CUDART_INF_F && c[i] > ninf)) c[i] = ninf;
     }
 }
 
-// Leaves only the experts of the kept groups in c. lo, hi: the lowest kept and
-// the highest dropped group score (ninf: none).
-template <typename F, int VPL>
-MOE_DEV void keep_groups(const Params& p, int lane, F (&c)[VPL], F& lo, F& hi) {
+// Groups that stay, as a mask, from the score of group `lane`; lo, hi: the
+// lowest kept and the highest dropped score (ninf: none).
+template <typename F>
+MOE_DEV unsigned kept_groups(const Params& p, int lane, F mine, F& lo, F& hi) {
     const F ninf = -static_cast<F>(CUDART_INF_F);
-    F mine = ninf;  // score of group `lane`
-    if (p.lg) {
-        F a1 = c[0], a2 = ninf;
-#pragma unroll
-        for (int i = 1; i < VPL; ++i) merge2(a1, a2, c[i], ninf);
-        for (int o = 1; o < p.lg; o <<= 1)
-            merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
-        const F g = (p.rank == 2 && a2 > ninf) ? a1 + a2 : a1;
-        mine = __shfl_sync(FULL, g, lane * p.lg & 31);
-        if (lane >= p.G) mine = ninf;
-    } else {
-        for (int g = 0; g < p.G; ++g) {
-            F a1 = ninf, a2 = ninf;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if ((lane * VPL + i) / p.gs == g) merge2(a1, a2, c[i], ninf);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1)
-                merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
-            if (lane == g) mine = (p.rank == 2 && a2 > ninf) ? a1 + a2 : a1;
-        }
-    }
     int before = 0;  // groups that rank before mine
     for (int g = 0; g < p.G; ++g) {
         const F o = __shfl_sync(FULL, mine, g);
         before += (o > mine || (o == mine && g < lane)) ? 1 : 0;
     }
     const bool kept = lane < p.G && before < p.TG;
-    const unsigned keep = __ballot_sync(FULL, kept);
     lo = -warp_max(kept ? -mine : ninf);
     hi = warp_max(lane < p.G && !kept ? mine : ninf);
+    return __ballot_sync(FULL, kept);
+}
+
+// Groups of any size: each group's two best over the warp in turn. Out of
+// line, so that the group of every expert is not kept in the common path's
+// registers.
+template <typename F, int VPL>
+__device__ __noinline__ void keep_any_groups(const Params* p, F* c, F* bounds) {
+    const F ninf = -static_cast<F>(CUDART_INF_F);
+    const int lane = static_cast<int>(lane_id());
+    F mine = ninf;
+    for (int g = 0; g < p->G; ++g) {
+        F a1 = ninf, a2 = ninf;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if ((lane * VPL + i) / p->gs == g) merge2(a1, a2, c[i], ninf);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+            merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
+        if (lane == g) mine = (p->rank == 2 && a2 > ninf) ? a1 + a2 : a1;
+    }
+    const unsigned keep = kept_groups<F>(*p, lane, mine, bounds[0], bounds[1]);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        const int g = (lane * VPL + i) / p.gs;
+        const int g = (lane * VPL + i) / p->gs;
         if (g >= 32 || !((keep >> g) & 1u)) c[i] = ninf;
+    }
+}
+
+// Leaves only the experts of the kept groups in c.
+template <typename F, int VPL>
+MOE_DEV void keep_groups(const Params& p, int lane, F (&c)[VPL], F& lo, F& hi) {
+    const F ninf = -static_cast<F>(CUDART_INF_F);
+    if (p.lg) {
+        // a lane's experts are one group's, and p.lg lanes (a power of two) make a group
+        F a1 = c[0], a2 = ninf;
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) merge2(a1, a2, c[i], ninf);
+        for (int o = 1; o < p.lg; o <<= 1)
+            merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
+        const F g = (p.rank == 2 && a2 > ninf) ? a1 + a2 : a1;
+        F mine = __shfl_sync(FULL, g, lane * p.lg & 31);
+        if (lane >= p.G) mine = ninf;
+        const unsigned keep = kept_groups<F>(p, lane, mine, lo, hi);
+        const int at = lane / p.lg;
+        if (at >= p.G || !((keep >> at) & 1u)) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) c[i] = ninf;
+        }
+    } else {
+        F t[VPL], bounds[2];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) t[i] = c[i];
+        keep_any_groups<F, VPL>(&p, t, bounds);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = t[i];
+        lo = bounds[0];
+        hi = bounds[1];
     }
 }
 
@@ -236,69 +285,106 @@ MOE_DEV float selected_score(const Params& p, bool there, float r, float m, floa
     return s;
 }
 
+// Ids and weights of token t: lane k holds the k-th id and its logit.
+MOE_DEV void write_token(const Params& p, long long t, int lane, int id, float rk, float m, float z, int32_t* idx,
+                         float* w) {
+    const bool there = lane < p.K && id >= 0;
+    float q;
+    const float s = selected_score(p, there, rk, m, z, q);
+    if (lane < p.K) {
+        idx[t * p.K + lane] = there ? id : -1;
+        w[t * p.K + lane] = there ? p.scale * (p.renorm ? q : s) : 0.0f;
+    }
+}
+
+// A token in FP64: what the rare token needs whose FP32 choices lie within
+// their error. Out of line, so that its registers are not the common path's.
 template <int VPL, typename T, bool VEC>
-__global__ void __launch_bounds__(32 * WARPS)
-group_route_kernel(Params p, const T* __restrict__ logits, int32_t* __restrict__ idx, float* __restrict__ w) {
+__device__ __noinline__ void route_exact(const Params* p, long long t, const T* row, int32_t* idx, float* w) {
+    const int lane = static_cast<int>(lane_id());
+    float r[VPL], b[VPL], m;
+    double c[VPL], z, lo, hi, val;
+    int id;
+    load_row<VPL, T, VEC>(row, lane, p->E, r);
+    lane_bias<VPL>(*p, lane, b);
+    choices<double, VPL>(*p, r, b, c, m, z);
+    if (p->G > 1) keep_groups<double, VPL>(*p, lane, c, lo, hi);
+    take<double, VPL>(c, lane, p->K, id, val);
+    write_token(*p, t, lane, id, id >= 0 ? clean(to_f32(row[id])) : -CUDART_INF_F, m, static_cast<float>(z), idx, w);
+}
+
+template <int VPL, typename T, bool VEC>
+__global__ void __launch_bounds__(32 * WARPS, 4)
+group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logits, int32_t* __restrict__ idx,
+                   float* __restrict__ w) {
     const int lane = static_cast<int>(lane_id());
     pdl_wait();
     pdl_trigger();
     const int step = gridDim.x * WARPS;
-    float bmax = 0.0f;  // largest |b|: what the choices' additions round by
-    if (p.bias != nullptr) {
-        for (int e = lane; e < p.E; e += 32) bmax = fmaxf(bmax, fabsf(p.bias[e]));
-        bmax = warp_max(bmax);
-    }
-    for (int t = blockIdx.x * WARPS + (threadIdx.x >> 5); t < p.T; t += step) {
-        const T* row = logits + t * p.stride;
-        float r[VPL], c[VPL], m, z;
-        load_row<VPL, T, VEC>(row, lane, p.E, r);
-        choices<float, VPL>(p, r, lane, c, m, z);
-        bool near = false;
-        // How near two FP32 choices may lie before FP64 decides. Without a bias
-        // the errors are relative: 3 units of 2^-23 (exponential, sum, division),
-        // and for a softmax the rounding of its argument, |r - m| 2^-24; the
-        // denominator is common. With one they are absolute: those of the largest
-        // score and half a unit of |b| + s. The bounds cover both sides twice.
-        const float babs = p.softmax ? 0x1p-18f / z + 0x1p-21f * bmax : 0x1p-19f + 0x1p-21f * bmax;
-        if (p.G > 1) {
-            float lo, hi;
-            keep_groups<float, VPL>(p, lane, c, lo, hi);
-            if (hi > -CUDART_INF_F && p.TG < p.G) {
-                const float tol = p.bias != nullptr ? 2.0f * babs : (p.softmax ? 0x1p-17f : 0x1p-19f) * lo;
-                near = !(lo - hi > tol) || (p.bias == nullptr && lo < 1e-20f);
+    const int t0 = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    // 32 tokens of the warp at a time; the near ones of them follow, in FP64
+    for (long long tb = t0; tb < p.T; tb += 32LL * step) {
+        unsigned again = 0;
+        float r[VPL], b[VPL];
+        load_row<VPL, T, VEC>(logits + tb * p.stride, lane, p.E, r);
+        lane_bias<VPL>(p, lane, b);
+        // largest |b|: what the choices' additions round by
+        float bmax = 0.0f;
+        if (p.bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (b[i] > -CUDART_INF_F) bmax = fmaxf(bmax, fabsf(b[i]));
+            bmax = warp_max(bmax);
+        }
+        for (int k = 0; k < 32; ++k) {
+            const long long t = tb + static_cast<long long>(k) * step;
+            if (t >= p.T) break;
+            const T* row = logits + t * p.stride;
+            float c[VPL], m, z;
+            choices<float, VPL>(p, r, b, c, m, z);
+            if (t + step < p.T) load_row<VPL, T, VEC>(row + step * p.stride, lane, p.E, r);
+            bool near = false;
+            // How near two FP32 choices may lie before FP64 decides; in units of 2^-23
+            // and for both sides together, twice what they can be off by.
+            // A sigmoid is off by 4 + 1.2 |r| of itself (fast exponential and division),
+            // which is at most 6 where |r| counts; a softmax score by 4 + |r - m| / 2, the
+            // denominator apart, which all scores share. With a bias the bounds are
+            // absolute: the score's, the denominator's error (16) on the largest score, and
+            // the addition's half unit of |b| + s.
+            const float babs = (p.softmax ? 0x1p-18f / z : 0x1p-18f) + 0x1p-21f * bmax;
+            if (p.G > 1) {
+                float lo, hi;
+                keep_groups<float, VPL>(p, lane, c, lo, hi);
+                if (hi > -CUDART_INF_F && p.TG < p.G) {
+                    // without a bias a score names its logit: |r| and |r - m| are below 48 from 1e-20 on
+                    const float tol = p.bias != nullptr ? 2.0f * babs : 0x1p-15f * lo;
+                    near = !(lo - hi > tol) || (p.bias == nullptr && lo < 1e-20f);
+                }
             }
-        }
-        int id;
-        float val;
-        // one more than K: the rank behind the last taken one
-        take<float, VPL>(c, lane, p.K + 1, id, val);
-        float rk = -CUDART_INF_F;
-        if (id >= 0) rk = clean(to_f32(row[id]));
-        const int id2 = __shfl_down_sync(FULL, id, 1);
-        const float val2 = __shfl_down_sync(FULL, val, 1), rk2 = __shfl_down_sync(FULL, rk, 1);
-        if (lane < p.K && id2 >= 0) {
-            const float spread = p.softmax && isfinite(m - rk2) ? 4.0f + (m - rk2) : 4.0f;
-            const float tol = (p.bias != nullptr ? babs : 0x1p-21f * spread * val) + 1e-36f;
-            if (!(val - val2 > tol)) {
-                // equal inputs are an exact tie: the lower index is first already
-                const bool same = rk == rk2 && (p.bias == nullptr || p.bias[id] == p.bias[id2]);
-                near = near || !same;
+            int id;
+            float val;
+            // one more than K: the rank behind the last taken one
+            take<float, VPL>(c, lane, p.K + 1, id, val);
+            float rk = -CUDART_INF_F;
+            if (id >= 0) rk = clean(to_f32(row[id]));
+            const int id2 = __shfl_down_sync(FULL, id, 1);
+            const float val2 = __shfl_down_sync(FULL, val, 1), rk2 = __shfl_down_sync(FULL, rk, 1);
+            if (lane < p.K && id2 >= 0) {
+                const float far = p.softmax ? m - rk2 : fabsf(rk2);
+                const float spread = 4.0f + (isfinite(far) ? far : 0.0f);
+                const float tol = (p.bias != nullptr ? babs : 0x1p-20f * spread * val) + 1e-36f;
+                if (!(val - val2 > tol)) {
+                    // equal inputs are an exact tie: the lower index is first already
+                    const bool same = rk == rk2 && (p.bias == nullptr || p.bias[id] == p.bias[id2]);
+                    near = near || !same;
+                }
             }
+            if (__any_sync(FULL, near)) again |= 1u << k;
+            else write_token(p, t, lane, id, rk, m, z, idx, w);
         }
-        if (__any_sync(FULL, near)) {
-            double cd[VPL], zd, lod, hid, vald;
-            float md;
-            choices<double, VPL>(p, r, lane, cd, md, zd);
-            if (p.G > 1) keep_groups<double, VPL>(p, lane, cd, lod, hid);
-            take<double, VPL>(cd, lane, p.K, id, vald);
-            rk = id >= 0 ? clean(to_f32(row[id])) : -CUDART_INF_F;
-        }
-        const bool there = lane < p.K && id >= 0;
-        float q;
-        const float s = selected_score(p, there, rk, m, z, q);
-        if (lane < p.K) {
-            idx[static_cast<long long>(t) * p.K + lane] = there ? id : -1;
-            w[static_cast<long long>(t) * p.K + lane] = there ? p.scale * (p.renorm ? q : s) : 0.0f;
+        for (; again; again &= again - 1) {
+            const long long t = tb + static_cast<long long>(__ffs(again) - 1) * step;
+            route_exact<VPL, T, VEC>(&p, t, logits + t * p.stride, idx, w);
         }
     }
 }
