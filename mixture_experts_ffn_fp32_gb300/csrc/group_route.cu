@@ -9,8 +9,10 @@
 //
 // Which experts are taken is decided as 64-bit arithmetic decides it, without
 // paying for it: FP32 scores come with an error bound, and only a token whose
-// taken ranks, or the groups on either side of the border, lie within it is
-// ranked again in FP64 (about one token in a thousand on random logits).
+// taken ranks, or the groups on either side of the border, lie within it (about
+// one in five hundred on random logits) takes FP64 scores, and those only for
+// the experts that could be concerned: a warp's FP64 exponential alone is two
+// thousand cycles here.
 //
 // One warp per token, E / 32 consecutive experts a lane; bound by the read of
 // the logits for large batches, by latency below a few thousand tokens.
@@ -22,7 +24,8 @@
 namespace moe {
 namespace {
 
-constexpr int WARPS = 8;
+// Small CTAs, many of them: the rare token that takes FP64 holds up three others.
+constexpr int WARPS = 4;
 constexpr unsigned FULL = 0xffffffffu;
 
 // Largest value over the warp (no NaN among them).
@@ -31,27 +34,19 @@ MOE_DEV float warp_max(float v) {
     const int k = __reduce_max_sync(FULL, u ^ ((u >> 31) & 0x7fffffff));
     return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
 }
-MOE_DEV double warp_max(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(FULL, v, o));
-    return v;
-}
 template <typename F>
 MOE_DEV F warp_add(F v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     return v;
 }
-MOE_DEV float expo(float v) { return expf(v); }
-MOE_DEV double expo(double v) { return exp(v); }
-
 // Logits as numbers that order: a NaN becomes -inf (never taken). -0 as +0,
 // so that equal values are equal bits.
 MOE_DEV float clean(float r) { return r > -CUDART_INF_F ? r + 0.0f : -CUDART_INF_F; }
 
 struct Params {
     int T, E, K, G, gs, TG, rank, softmax, renorm;
-    int lg;       // lanes of a group where groups fill whole lanes and lg is a power of two, else 0
+    int lg, lsh;  // lanes of a group where groups fill whole lanes and lg = 2^lsh is a power of two, else 0
     float scale;
     long long stride;
     const float* bias;
@@ -88,19 +83,27 @@ MOE_DEV void load_row(const T* row, int lane, int E, float (&r)[VPL]) {
     }
 }
 
-// The two largest of (a1, a2) and (b1, b2).
+// The two largest of (a1, a2) and (b1, b2); no NaN among them.
+MOE_DEV float least(float a, float b) { return fminf(a, b); }
+MOE_DEV float most(float a, float b) { return fmaxf(a, b); }
+MOE_DEV long long least(long long a, long long b) { return a < b ? a : b; }
+MOE_DEV long long most(long long a, long long b) { return a < b ? b : a; }
 template <typename F>
 MOE_DEV void merge2(F& a1, F& a2, F b1, F b2) {
-    const F lo = a1 < b1 ? a1 : b1;
-    a1 = a1 < b1 ? b1 : a1;
-    a2 = a2 < b2 ? b2 : a2;
-    a2 = a2 < lo ? lo : a2;
+    const F lo = least(a1, b1);
+    a1 = most(a1, b1);
+    a2 = most(most(a2, b2), lo);
 }
 
-// Sigmoid: FP32 by the fast exponential and division (the error bounds in the
-// kernel count both), FP64 in full.
+// By the fast exponential and division: the error bounds in the kernel count both.
 MOE_DEV float sigmoid_of(float r) { return __fdividef(1.0f, 1.0f + __expf(-r)); }
-MOE_DEV double sigmoid_of(double r) { return 1.0 / (1.0 + exp(-r)); }
+
+// A choice in FP32 from its logit and bias, the same wherever it is computed.
+MOE_DEV float choice(const Params& p, float r, float b, float m, float inv) {
+    const float s = p.softmax ? (r == m ? 1.0f : expf(r - m)) * inv : sigmoid_of(r);
+    const float c = s + b;
+    return (r > -CUDART_INF_F && c > -CUDART_INF_F) ? c : -CUDART_INF_F;
+}
 
 // The biases of a lane's experts (0 without a bias, -inf past the last).
 template <int VPL>
@@ -112,108 +115,128 @@ MOE_DEV void lane_bias(const Params& p, int lane, float (&b)[VPL]) {
     }
 }
 
-// Scores and choices of a row in F; m and z: softmax maximum and denominator.
-template <typename F, int VPL>
-MOE_DEV void choices(const Params& p, const float (&r)[VPL], const float (&b)[VPL], F (&c)[VPL], float& m, F& z) {
-    const F ninf = -static_cast<F>(CUDART_INF_F);
+// Choices of a row; m, z and inv: softmax maximum, denominator and its
+// reciprocal.
+template <int VPL>
+MOE_DEV void choices(const Params& p, const float (&r)[VPL], const float (&b)[VPL], float (&c)[VPL], float& m, float& z,
+                     float& inv) {
     m = 0.0f;
-    z = 1;
+    z = inv = 1.0f;
     if (p.softmax) {
         float mx = r[0];
 #pragma unroll
         for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, r[i]);
         m = warp_max(mx);
-        F s = 0;
+        float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             // equal to the maximum: 1, also where both are infinite
-            c[i] = r[i] == m ? static_cast<F>(1) : expo(static_cast<F>(r[i]) - static_cast<F>(m));
-            if (r[i] == -CUDART_INF_F) c[i] = 0;
-            s += c[i];
+            c[i] = r[i] == m ? 1.0f : expf(r[i] - m);
+            s += r[i] == -CUDART_INF_F ? 0.0f : c[i];
         }
         z = warp_add(s);
-        if (z == 0) z = 1;
-        const F inv = 1 / z;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) c[i] = sizeof(F) == 8 ? c[i] / z : c[i] * inv;
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) c[i] = sigmoid_of(static_cast<F>(r[i]));
+        if (z == 0.0f) z = 1.0f;
+        inv = 1.0f / z;
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        c[i] += static_cast<F>(b[i]);
-        if (!(r[i] > -CUDART_INF_F && c[i] > ninf)) c[i] = ninf;
+        if (p.softmax) {
+            c[i] = c[i] * inv + b[i];
+            if (!(r[i] > -CUDART_INF_F && c[i] > -CUDART_INF_F)) c[i] = -CUDART_INF_F;
+        } else {
+            c[i] = choice(p, r[i], b[i], m, inv);
+        }
     }
 }
 
-// Groups that stay, as a mask, from the score of group `lane`; lo, hi: the
-// lowest kept and the highest dropped score (ninf: none).
+// Groups that stay, as a mask, from the score of group `lane` (none where the
+// group has no expert).
 template <typename F>
-MOE_DEV unsigned kept_groups(const Params& p, int lane, F mine, F& lo, F& hi) {
-    const F ninf = -static_cast<F>(CUDART_INF_F);
+MOE_DEV unsigned kept_groups(const Params& p, int lane, F mine) {
     int before = 0;  // groups that rank before mine
     for (int g = 0; g < p.G; ++g) {
         const F o = __shfl_sync(FULL, mine, g);
         before += (o > mine || (o == mine && g < lane)) ? 1 : 0;
     }
-    const bool kept = lane < p.G && before < p.TG;
-    lo = -warp_max(kept ? -mine : ninf);
-    hi = warp_max(lane < p.G && !kept ? mine : ninf);
-    return __ballot_sync(FULL, kept);
+    return __ballot_sync(FULL, lane < p.G && before < p.TG);
 }
 
-// Groups of any size: each group's two best over the warp in turn. Out of
-// line, so that the group of every expert is not kept in the common path's
-// registers.
+// The two best of each group, in F's order: those of the lane's group in
+// every lane where groups are whole lanes (p.lg), else those of group `lane`.
 template <typename F, int VPL>
-__device__ __noinline__ void keep_any_groups(const Params* p, F* c, F* bounds) {
-    const F ninf = -static_cast<F>(CUDART_INF_F);
-    const int lane = static_cast<int>(lane_id());
-    F mine = ninf;
-    for (int g = 0; g < p->G; ++g) {
-        F a1 = ninf, a2 = ninf;
+MOE_DEV void group_best(const Params& p, int lane, const F (&c)[VPL], F none, F& a1, F& a2) {
+    if (p.lg) {
+        a1 = c[0];
+        a2 = none;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if ((lane * VPL + i) / p->gs == g) merge2(a1, a2, c[i], ninf);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1)
+        for (int i = 1; i < VPL; ++i) merge2(a1, a2, c[i], none);
+        for (int o = 1; o < p.lg; o <<= 1)
             merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
-        if (lane == g) mine = (p->rank == 2 && a2 > ninf) ? a1 + a2 : a1;
+    } else {
+        F m1 = none, m2 = none;
+        for (int g = 0; g < p.G; ++g) {
+            F b1 = none, b2 = none;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if ((lane * VPL + i) / p.gs == g) merge2(b1, b2, c[i], none);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+                merge2(b1, b2, __shfl_xor_sync(FULL, b1, o), __shfl_xor_sync(FULL, b2, o));
+            if (lane == g) {
+                m1 = b1;
+                m2 = b2;
+            }
+        }
+        a1 = m1;
+        a2 = m2;
     }
-    const unsigned keep = kept_groups<F>(*p, lane, mine, bounds[0], bounds[1]);
+}
+
+// Groups of any size. Out of line, so that the group of every expert is not
+// kept in the common path's registers.
+template <int VPL>
+__device__ __noinline__ void keep_any_groups(const Params* p, float* c, float* bounds) {
+    const int lane = static_cast<int>(lane_id());
+    float t[VPL], a1, a2;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) t[i] = c[i];
+    group_best<float, VPL>(*p, lane, t, -CUDART_INF_F, a1, a2);
+    const float mine = (p->rank == 2 && a2 > -CUDART_INF_F) ? a1 + a2 : a1;
+    const unsigned keep = kept_groups<float>(*p, lane, mine);
+    const bool kept = (keep >> lane) & 1u;
+    bounds[0] = -warp_max(kept ? -mine : -CUDART_INF_F);
+    bounds[1] = warp_max(lane < p->G && !kept ? mine : -CUDART_INF_F);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int g = (lane * VPL + i) / p->gs;
-        if (g >= 32 || !((keep >> g) & 1u)) c[i] = ninf;
+        if (g >= 32 || !((keep >> g) & 1u)) c[i] = -CUDART_INF_F;
     }
 }
 
-// Leaves only the experts of the kept groups in c.
-template <typename F, int VPL>
-MOE_DEV void keep_groups(const Params& p, int lane, F (&c)[VPL], F& lo, F& hi) {
-    const F ninf = -static_cast<F>(CUDART_INF_F);
+// Leaves only the experts of the kept groups in c; lo, hi: the lowest kept and
+// the highest dropped score (-inf: none).
+template <int VPL>
+MOE_DEV void keep_groups(const Params& p, int lane, float (&c)[VPL], float& lo, float& hi) {
     if (p.lg) {
-        // a lane's experts are one group's, and p.lg lanes (a power of two) make a group
-        F a1 = c[0], a2 = ninf;
-#pragma unroll
-        for (int i = 1; i < VPL; ++i) merge2(a1, a2, c[i], ninf);
-        for (int o = 1; o < p.lg; o <<= 1)
-            merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
-        const F g = (p.rank == 2 && a2 > ninf) ? a1 + a2 : a1;
-        F mine = __shfl_sync(FULL, g, lane * p.lg & 31);
-        if (lane >= p.G) mine = ninf;
-        const unsigned keep = kept_groups<F>(p, lane, mine, lo, hi);
-        const int at = lane / p.lg;
+        float a1, a2;
+        group_best<float, VPL>(p, lane, c, -CUDART_INF_F, a1, a2);
+        const float g = (p.rank == 2 && a2 > -CUDART_INF_F) ? a1 + a2 : a1;
+        float mine = __shfl_sync(FULL, g, lane * p.lg & 31);
+        if (lane >= p.G) mine = -CUDART_INF_F;
+        const unsigned keep = kept_groups<float>(p, lane, mine);
+        const bool kept = (keep >> lane) & 1u;
+        lo = -warp_max(kept ? -mine : -CUDART_INF_F);
+        hi = warp_max(lane < p.G && !kept ? mine : -CUDART_INF_F);
+        const int at = lane >> p.lsh;
         if (at >= p.G || !((keep >> at) & 1u)) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) c[i] = ninf;
+            for (int i = 0; i < VPL; ++i) c[i] = -CUDART_INF_F;
         }
     } else {
-        F t[VPL], bounds[2];
+        float t[VPL], bounds[2];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) t[i] = c[i];
-        keep_any_groups<F, VPL>(&p, t, bounds);
+        keep_any_groups<VPL>(&p, t, bounds);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) c[i] = t[i];
         lo = bounds[0];
@@ -221,43 +244,74 @@ MOE_DEV void keep_groups(const Params& p, int lane, F (&c)[VPL], F& lo, F& hi) {
     }
 }
 
-// The n largest of c in order; lane k receives the k-th (id -1: none).
-template <typename F, int VPL>
-MOE_DEV void take(F (&c)[VPL], int lane, int n, int& id, F& val) {
-    const F ninf = -static_cast<F>(CUDART_INF_F);
-    id = -1;
-    val = ninf;
-    F best = c[0];
-    int at = 0;
+// Integers that order as the floats do.
+MOE_DEV int order_key(float v) {
+    const int u = __float_as_int(v + 0.0f);  // -0 as +0
+    return u ^ ((u >> 31) & 0x7fffffff);
+}
+MOE_DEV float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+MOE_DEV long long order_key(double v) {
+    const long long u = __double_as_longlong(v + 0.0);
+    return u ^ ((u >> 63) & 0x7fffffffffffffffLL);
+}
+MOE_DEV double key_value(long long k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL)); }
+constexpr long long NONE64 = static_cast<long long>(0x8000000000000000ull);
+
+// Sorts a lane's keys in descending order (Batcher's odd-even merge).
+MOE_DEV void order2(int& a, int& b) {
+    const int hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+template <int VPL>
+MOE_DEV void sort_desc(int (&k)[VPL]) {
+    if constexpr (VPL == 2) {
+        order2(k[0], k[1]);
+    } else if constexpr (VPL == 4 || VPL == 8) {
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-        if (c[i] > best) {
-            best = c[i];
-            at = i;
+        for (int o = 0; o < VPL; o += 4) {
+            order2(k[o], k[o + 1]);
+            order2(k[o + 2], k[o + 3]);
+            order2(k[o], k[o + 2]);
+            order2(k[o + 1], k[o + 3]);
+            order2(k[o + 1], k[o + 2]);
         }
-    for (int k = 0; k < n; ++k) {
-        const F v = warp_max(best);
-        if (!(v > ninf)) break;
-        const int w = __ffs(__ballot_sync(FULL, best == v)) - 1;
-        const int e = __shfl_sync(FULL, lane * VPL + at, w);
-        if (lane == k) {
-            id = e;
-            val = v;
-        }
-        if (lane == w) {
+        if constexpr (VPL == 8) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (i == at) c[i] = ninf;
-            best = c[0];
-            at = 0;
-#pragma unroll
-            for (int i = 1; i < VPL; ++i)
-                if (c[i] > best) {
-                    best = c[i];
-                    at = i;
-                }
+            for (int i = 0; i < 4; ++i) order2(k[i], k[i + 4]);
+            order2(k[2], k[4]);
+            order2(k[3], k[5]);
+            order2(k[1], k[2]);
+            order2(k[3], k[4]);
+            order2(k[5], k[6]);
         }
     }
+}
+
+// The n largest choices, roughly: keys of the choice's upper 24 bits and, below
+// them, 255 less the expert, so that one integer maximum over the warp names
+// the expert and only its lane drops its first. Lane k receives the k-th key
+// (EMPTY: none); the caller puts what the dropped bits leave open in order.
+constexpr int EMPTY = static_cast<int>(0x80000000u);
+template <int VPL>
+MOE_DEV int take_rough(const float (&c)[VPL], int lane, int n) {
+    int k[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        k[i] = c[i] > -CUDART_INF_F ? (order_key(c[i]) & ~255) | (255 - (lane * VPL + i)) : EMPTY;
+    sort_desc<VPL>(k);
+    int key = EMPTY;
+    for (int j = 0; j < n; ++j) {
+        const int v = __reduce_max_sync(FULL, k[0]);
+        if (lane == j) key = v;
+        if (k[0] == v) {
+#pragma unroll
+            for (int i = 0; i + 1 < VPL; ++i) k[i] = k[i + 1];
+            k[VPL - 1] = EMPTY;
+        }
+    }
+    return key;
 }
 
 // exp(a - b) with the rounding of the difference put back (a - b = d + e).
@@ -297,24 +351,127 @@ MOE_DEV void write_token(const Params& p, long long t, int lane, int id, float r
     }
 }
 
-// A token in FP64: what the rare token needs whose FP32 choices lie within
-// their error. Out of line, so that its registers are not the common path's.
+// A token decided in FP64: the rare token whose FP32 choices lie within their
+// error. The choices are 64-bit integers in the doubles' order; those that
+// could be concerned by a decision, `tol` around it, are replaced by exact
+// ones before it is taken. Out of line, so that its registers are not the
+// common path's.
 template <int VPL, typename T, bool VEC>
-__device__ __noinline__ void route_exact(const Params* p, long long t, const T* row, int32_t* idx, float* w) {
+__device__ __noinline__ void route_exact(const Params* pp, long long t, const T* row, float tol, bool groups, int32_t* idx, float* w) {
+    const Params& p = *pp;
     const int lane = static_cast<int>(lane_id());
-    float r[VPL], b[VPL], m;
-    double c[VPL], z, lo, hi, val;
-    int id;
-    load_row<VPL, T, VEC>(row, lane, p->E, r);
-    lane_bias<VPL>(*p, lane, b);
-    choices<double, VPL>(*p, r, b, c, m, z);
-    if (p->G > 1) keep_groups<double, VPL>(*p, lane, c, lo, hi);
-    take<double, VPL>(c, lane, p->K, id, val);
-    write_token(*p, t, lane, id, id >= 0 ? clean(to_f32(row[id])) : -CUDART_INF_F, m, static_cast<float>(z), idx, w);
+    float r[VPL], b[VPL], c[VPL], m, z, inv;
+    load_row<VPL, T, VEC>(row, lane, p.E, r);
+    lane_bias<VPL>(p, lane, b);
+    choices<VPL>(p, r, b, c, m, z, inv);
+    // what two near FP32 choices around v can be apart
+    auto slack = [&](float v) { return p.bias != nullptr ? 4.0f * tol : 0x1p-13f * fabsf(v) + 1e-35f; };
+    // A softmax's denominator is common: without a bias the exponentials decide.
+    double z64 = 1.0;
+    if (p.softmax && p.bias != nullptr) {
+        z64 = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < VPL; ++i) {
+            float ri = r[0];
+#pragma unroll
+            for (int j = 1; j < VPL; ++j)
+                if (j == i) ri = r[j];
+            if (ri > -CUDART_INF_F) z64 += ri == m ? 1.0 : exp(static_cast<double>(ri) - static_cast<double>(m));
+        }
+        z64 = warp_add(z64);
+    }
+    const double unit = p.softmax && p.bias == nullptr ? static_cast<double>(z) : 1.0;  // FP32 choices to that scale
+    long long h[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        h[i] = c[i] > -CUDART_INF_F ? order_key(static_cast<double>(c[i]) * unit) : NONE64;
+    unsigned done = 0;
+    auto make_exact = [&](unsigned need) {
+        need &= ~done;
+        done |= need;
+        while (__any_sync(FULL, need != 0)) {
+            const int at = __ffs(need) - 1;  // -1: nothing left in this lane
+            need &= need - 1;
+            float ri = r[0], bi = b[0];
+#pragma unroll
+            for (int j = 1; j < VPL; ++j)
+                if (j == at) {
+                    ri = r[j];
+                    bi = b[j];
+                }
+            const double x = p.softmax ? static_cast<double>(ri) - static_cast<double>(m) : -static_cast<double>(ri);
+            const double ex = p.softmax && ri == m ? 1.0 : exp(x);
+            const double s = p.softmax ? (p.bias != nullptr ? ex / z64 : ex) : 1.0 / (1.0 + ex);
+            const long long k = order_key(p.bias != nullptr ? s + static_cast<double>(bi) : s);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (j == at) h[j] = k;
+        }
+    };
+    if (p.G > 1) {
+        float f1, f2;
+        group_best<float, VPL>(p, lane, c, -CUDART_INF_F, f1, f2);
+        unsigned need = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int g = min((lane * VPL + i) / p.gs, 31);
+            const float x1 = p.lg ? f1 : __shfl_sync(FULL, f1, g), x2 = p.lg ? f2 : __shfl_sync(FULL, f2, g);
+            const float edge = p.rank == 2 && x2 > -CUDART_INF_F ? x2 : x1;
+            if (c[i] > -CUDART_INF_F && !(c[i] < edge - slack(edge))) need |= 1u << i;
+        }
+        if (groups) make_exact(need);  // else they are clear as they are
+        long long a1, a2;
+        group_best<long long, VPL>(p, lane, h, NONE64, a1, a2);
+        long long g = p.rank == 2 && a2 != NONE64 ? order_key(key_value(a1) + key_value(a2)) : a1;
+        if (p.lg) g = __shfl_sync(FULL, g, lane * p.lg & 31);
+        if (lane >= p.G) g = NONE64;
+        const unsigned keep = kept_groups<long long>(p, lane, g);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int at = (lane * VPL + i) / p.gs;
+            if (at >= p.G || !((keep >> at) & 1u)) {
+                c[i] = -CUDART_INF_F;
+                h[i] = NONE64;
+            }
+        }
+    }
+    {
+        const int kth = __shfl_sync(FULL, take_rough<VPL>(c, lane, p.K), p.K - 1);
+        const float edge = kth == EMPTY ? -CUDART_INF_F : key_value(kth & ~255);
+        unsigned need = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (c[i] > -CUDART_INF_F && !(c[i] < edge - slack(edge) - 0x1p-14f * fabsf(edge))) need |= 1u << i;
+        make_exact(need);
+    }
+    int id = -1;
+    for (int k = 0; k < p.K; ++k) {
+        long long best = h[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < VPL; ++i)
+            if (h[i] > best) {
+                best = h[i];
+                at = i;
+            }
+        const int hi = __reduce_max_sync(FULL, static_cast<int>(best >> 32));
+        const bool top = static_cast<int>(best >> 32) == hi;
+        const unsigned lo = __reduce_max_sync(FULL, top ? static_cast<unsigned>(best) : 0u);
+        const int from = __ffs(__ballot_sync(FULL, top && static_cast<unsigned>(best) == lo)) - 1;
+        if (hi == static_cast<int>(NONE64 >> 32) && lo == 0u) break;
+        const int e = __shfl_sync(FULL, lane * VPL + at, from);
+        if (lane == k) id = e;
+        if (lane == from) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (i == at) h[i] = NONE64;
+        }
+    }
+    write_token(p, t, lane, id, id >= 0 ? clean(to_f32(row[id])) : -CUDART_INF_F, m, z, idx, w);
 }
 
 template <int VPL, typename T, bool VEC>
-__global__ void __launch_bounds__(32 * WARPS, 4)
+__global__ void __launch_bounds__(32 * WARPS, 8)
 group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logits, int32_t* __restrict__ idx,
                    float* __restrict__ w) {
     const int lane = static_cast<int>(lane_id());
@@ -324,7 +481,7 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
     const int t0 = blockIdx.x * WARPS + (threadIdx.x >> 5);
     // 32 tokens of the warp at a time; the near ones of them follow, in FP64
     for (long long tb = t0; tb < p.T; tb += 32LL * step) {
-        unsigned again = 0;
+        unsigned again = 0, groups = 0;  // near tokens, and those near in their groups
         float r[VPL], b[VPL];
         load_row<VPL, T, VEC>(logits + tb * p.stride, lane, p.E, r);
         lane_bias<VPL>(p, lane, b);
@@ -340,10 +497,10 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             const long long t = tb + static_cast<long long>(k) * step;
             if (t >= p.T) break;
             const T* row = logits + t * p.stride;
-            float c[VPL], m, z;
-            choices<float, VPL>(p, r, b, c, m, z);
+            float c[VPL], m, z, inv;
+            choices<VPL>(p, r, b, c, m, z, inv);
             if (t + step < p.T) load_row<VPL, T, VEC>(row + step * p.stride, lane, p.E, r);
-            bool near = false;
+            bool near = false, gnear = false;
             // How near two FP32 choices may lie before FP64 decides; in units of 2^-23
             // and for both sides together, twice what they can be off by.
             // A sigmoid is off by 4 + 1.2 |r| of itself (fast exponential and division),
@@ -354,19 +511,42 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             const float babs = (p.softmax ? 0x1p-18f / z : 0x1p-18f) + 0x1p-21f * bmax;
             if (p.G > 1) {
                 float lo, hi;
-                keep_groups<float, VPL>(p, lane, c, lo, hi);
+                keep_groups<VPL>(p, lane, c, lo, hi);
                 if (hi > -CUDART_INF_F && p.TG < p.G) {
                     // without a bias a score names its logit: |r| and |r - m| are below 48 from 1e-20 on
                     const float tol = p.bias != nullptr ? 2.0f * babs : 0x1p-15f * lo;
-                    near = !(lo - hi > tol) || (p.bias == nullptr && lo < 1e-20f);
+                    gnear = !(lo - hi > tol) || (p.bias == nullptr && lo < 1e-20f);
                 }
             }
-            int id;
-            float val;
-            // one more than K: the rank behind the last taken one
-            take<float, VPL>(c, lane, p.K + 1, id, val);
-            float rk = -CUDART_INF_F;
-            if (id >= 0) rk = clean(to_f32(row[id]));
+            // two more than K: the rank behind the last taken one, and one that bounds the rest
+            const int key = take_rough<VPL>(c, lane, p.K + 2);
+            int id = -1;
+            float rk = -CUDART_INF_F, val = -CUDART_INF_F;
+            if (key != EMPTY) {
+                id = 255 - (key & 255);
+                rk = clean(to_f32(row[id]));
+                val = choice(p, rk, p.bias != nullptr ? __ldg(p.bias + id) : 0.0f, m, inv);
+            }
+            // every expert behind lies at or below the last key with its dropped bits set
+            if (lane > p.K && key != EMPTY) val = key_value(key | 255);
+            const float rest = __shfl_sync(FULL, val, p.K + 1);
+            const float next = __shfl_down_sync(FULL, val, 1);
+            if (__any_sync(FULL, lane < p.K && next > val)) {
+                // ranks that the dropped bits had out of order
+                int rank = 0;
+                for (int j = 0; j <= p.K; ++j) {
+                    const float o = __shfl_sync(FULL, val, j);
+                    const int oid = __shfl_sync(FULL, id, j);
+                    rank += (o > val || (o == val && oid < id)) ? 1 : 0;
+                }
+                if (lane > p.K || id < 0) rank = lane;
+                int src = lane;
+                for (int j = 0; j <= p.K; ++j)
+                    if (__shfl_sync(FULL, rank, j) == lane) src = j;
+                id = __shfl_sync(FULL, id, src);
+                rk = __shfl_sync(FULL, rk, src);
+                val = __shfl_sync(FULL, val, src);
+            }
             const int id2 = __shfl_down_sync(FULL, id, 1);
             const float val2 = __shfl_down_sync(FULL, val, 1), rk2 = __shfl_down_sync(FULL, rk, 1);
             if (lane < p.K && id2 >= 0) {
@@ -375,16 +555,18 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
                 const float tol = (p.bias != nullptr ? babs : 0x1p-20f * spread * val) + 1e-36f;
                 if (!(val - val2 > tol)) {
                     // equal inputs are an exact tie: the lower index is first already
-                    const bool same = rk == rk2 && (p.bias == nullptr || p.bias[id] == p.bias[id2]);
-                    near = near || !same;
+                    near = near || !(rk == rk2 && (p.bias == nullptr || p.bias[id] == p.bias[id2]));
                 }
+                if (lane == p.K - 1 && rest > -CUDART_INF_F && !(val - rest > tol)) near = true;
             }
-            if (__any_sync(FULL, near)) again |= 1u << k;
+            if (__any_sync(FULL, gnear)) groups |= 1u << k;
+            if (__any_sync(FULL, near || gnear)) again |= 1u << k;
             else write_token(p, t, lane, id, rk, m, z, idx, w);
         }
         for (; again; again &= again - 1) {
-            const long long t = tb + static_cast<long long>(__ffs(again) - 1) * step;
-            route_exact<VPL, T, VEC>(&p, t, logits + t * p.stride, idx, w);
+            const int k = __ffs(again) - 1;
+            const long long t = tb + static_cast<long long>(k) * step;
+            route_exact<VPL, T, VEC>(&p, t, logits + t * p.stride, 0x1p-18f + 0x1p-21f * bmax, (groups >> k) & 1u, idx, w);
         }
     }
 }
@@ -490,7 +672,7 @@ group_route_bwd_kernel(Params p, const T* __restrict__ logits, const int32_t* __
 
 template <int VPL, typename T>
 cudaError_t launch_t(const GroupRouteArgs& a, Params p, bool bwd, cudaStream_t s) {
-    const int want = (a.T + WARPS - 1) / WARPS, cap = num_sms() * 8;
+    const int want = (a.T + WARPS - 1) / WARPS, cap = num_sms() * (bwd ? 16 : 32);
     const dim3 grid(want < cap ? want : cap), block(32 * WARPS);
     // vector rows: every lane's run of experts whole and aligned
     constexpr int B = VPL * static_cast<int>(sizeof(T)) >= 16 ? 16 : VPL * static_cast<int>(sizeof(T));
@@ -526,6 +708,7 @@ cudaError_t launch_d(const GroupRouteArgs& a, bool bwd, cudaStream_t s) {
     const int vpl = a.E <= 32 ? 1 : a.E <= 64 ? 2 : a.E <= 128 ? 4 : 8;
     const int lg = p.gs % vpl == 0 ? p.gs / vpl : 0;
     p.lg = (lg & (lg - 1)) == 0 ? lg : 0;
+    while (p.lg >> (p.lsh + 1)) ++p.lsh;
     if (vpl == 1) return launch_t<1, T>(a, p, bwd, s);
     if (vpl == 2) return launch_t<2, T>(a, p, bwd, s);
     if (vpl == 4) return launch_t<4, T>(a, p, bwd, s);
