@@ -40,9 +40,8 @@ MOE_DEV F warp_add(F v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     return v;
 }
-// Logits as numbers that order: a NaN becomes -inf (never taken). -0 as +0,
-// so that equal values are equal bits.
-MOE_DEV float clean(float r) { return r > -CUDART_INF_F ? r + 0.0f : -CUDART_INF_F; }
+// A NaN becomes -inf: never taken.
+MOE_DEV float clean(float r) { return fmaxf(r, -CUDART_INF_F); }
 
 struct Params {
     int T, E, K, G, gs, TG, rank, softmax, renorm;
@@ -95,23 +94,30 @@ MOE_DEV void merge2(F& a1, F& a2, F b1, F b2) {
     a2 = most(most(a2, b2), lo);
 }
 
-// By the fast exponential and division: the error bounds in the kernel count both.
-MOE_DEV float sigmoid_of(float r) { return __fdividef(1.0f, 1.0f + __expf(-r)); }
-
-// A choice in FP32 from its logit and bias, the same wherever it is computed.
-MOE_DEV float choice(const Params& p, float r, float b, float m, float inv) {
-    const float s = p.softmax ? (r == m ? 1.0f : expf(r - m)) * inv : sigmoid_of(r);
-    const float c = s + b;
-    return (r > -CUDART_INF_F && c > -CUDART_INF_F) ? c : -CUDART_INF_F;
+// 1 / (1 + 2^(-r log2 e)) on the special-function unit; the error bounds in the
+// kernel count it. Beyond 87 it is 0 or 1.
+MOE_DEV float sigmoid_of(float r) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(r * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
 }
 
-// The biases of a lane's experts (0 without a bias, -inf past the last).
-template <int VPL>
+// A choice in FP32 from its logit and bias (no NaN), the same wherever it is
+// computed.
+MOE_DEV float choice(const Params& p, float r, float b, float m, float inv) {
+    const float s = p.softmax ? __fmul_rn(r == m ? 1.0f : expf(r - m), inv) : sigmoid_of(r);
+    return __fadd_rn(s, r > -CUDART_INF_F ? b : -CUDART_INF_F);
+}
+
+// The biases of a lane's experts (0 without a bias, -inf for a NaN and past the last).
+template <int VPL, bool VEC>
 MOE_DEV void lane_bias(const Params& p, int lane, float (&b)[VPL]) {
+    if (p.bias == nullptr) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        b[i] = e >= p.E ? -CUDART_INF_F : p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
+        for (int i = 0; i < VPL; ++i) b[i] = lane * VPL + i < p.E ? 0.0f : -CUDART_INF_F;
+    } else {
+        load_row<VPL, float, VEC>(p.bias, lane, p.E, b);
     }
 }
 
@@ -141,8 +147,7 @@ MOE_DEV void choices(const Params& p, const float (&r)[VPL], const float (&b)[VP
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         if (p.softmax) {
-            c[i] = c[i] * inv + b[i];
-            if (!(r[i] > -CUDART_INF_F && c[i] > -CUDART_INF_F)) c[i] = -CUDART_INF_F;
+            c[i] = __fadd_rn(__fmul_rn(c[i], inv), r[i] > -CUDART_INF_F ? b[i] : -CUDART_INF_F);
         } else {
             c[i] = choice(p, r[i], b[i], m, inv);
         }
@@ -206,6 +211,7 @@ __device__ __noinline__ void keep_any_groups(const Params* p, float* c, float* b
     const bool kept = (keep >> lane) & 1u;
     bounds[0] = -warp_max(kept ? -mine : -CUDART_INF_F);
     bounds[1] = warp_max(lane < p->G && !kept ? mine : -CUDART_INF_F);
+    bounds[2] = warp_max((a1 > -CUDART_INF_F ? fabsf(a1) : 0.0f) + (a2 > -CUDART_INF_F ? fabsf(a2) : 0.0f));
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int g = (lane * VPL + i) / p->gs;
@@ -214,9 +220,10 @@ __device__ __noinline__ void keep_any_groups(const Params* p, float* c, float* b
 }
 
 // Leaves only the experts of the kept groups in c; lo, hi: the lowest kept and
-// the highest dropped score (-inf: none).
+// the highest dropped score (-inf: none); mag: the largest |a| + |b| of a
+// group's two best.
 template <int VPL>
-MOE_DEV void keep_groups(const Params& p, int lane, float (&c)[VPL], float& lo, float& hi) {
+MOE_DEV void keep_groups(const Params& p, int lane, float (&c)[VPL], float& lo, float& hi, float& mag) {
     if (p.lg) {
         float a1, a2;
         group_best<float, VPL>(p, lane, c, -CUDART_INF_F, a1, a2);
@@ -227,13 +234,14 @@ MOE_DEV void keep_groups(const Params& p, int lane, float (&c)[VPL], float& lo, 
         const bool kept = (keep >> lane) & 1u;
         lo = -warp_max(kept ? -mine : -CUDART_INF_F);
         hi = warp_max(lane < p.G && !kept ? mine : -CUDART_INF_F);
+        mag = warp_max((a1 > -CUDART_INF_F ? fabsf(a1) : 0.0f) + (a2 > -CUDART_INF_F ? fabsf(a2) : 0.0f));
         const int at = lane >> p.lsh;
         if (at >= p.G || !((keep >> at) & 1u)) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i) c[i] = -CUDART_INF_F;
         }
     } else {
-        float t[VPL], bounds[2];
+        float t[VPL], bounds[3];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) t[i] = c[i];
         keep_any_groups<VPL>(&p, t, bounds);
@@ -241,6 +249,7 @@ MOE_DEV void keep_groups(const Params& p, int lane, float (&c)[VPL], float& lo, 
         for (int i = 0; i < VPL; ++i) c[i] = t[i];
         lo = bounds[0];
         hi = bounds[1];
+        mag = bounds[2];
     }
 }
 
@@ -292,14 +301,17 @@ MOE_DEV void sort_desc(int (&k)[VPL]) {
 // The n largest choices, roughly: keys of the choice's upper 24 bits and, below
 // them, 255 less the expert, so that one integer maximum over the warp names
 // the expert and only its lane drops its first. Lane k receives the k-th key
-// (EMPTY: none); the caller puts what the dropped bits leave open in order.
-constexpr int EMPTY = static_cast<int>(0x80000000u);
+// (below FIRST, which -inf and the lanes past n are: none); the caller puts
+// what the dropped bits leave open in order.
+constexpr int EMPTY = static_cast<int>(0x80000000u), FIRST = static_cast<int>(0x80800000u);
 template <int VPL>
 MOE_DEV int take_rough(const float (&c)[VPL], int lane, int n) {
     int k[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        k[i] = c[i] > -CUDART_INF_F ? (order_key(c[i]) & ~255) | (255 - (lane * VPL + i)) : EMPTY;
+    for (int i = 0; i < VPL; ++i) {
+        const int u = __float_as_int(c[i]);
+        k[i] = ((u ^ ((u >> 31) & 0x7fffffff)) & ~255) | (255 - (lane * VPL + i));
+    }
     sort_desc<VPL>(k);
     int key = EMPTY;
     for (int j = 0; j < n; ++j) {
@@ -352,20 +364,19 @@ MOE_DEV void write_token(const Params& p, long long t, int lane, int id, float r
 }
 
 // A token decided in FP64: the rare token whose FP32 choices lie within their
-// error. The choices are 64-bit integers in the doubles' order; those that
-// could be concerned by a decision, `tol` around it, are replaced by exact
-// ones before it is taken. Out of line, so that its registers are not the
+// error. The choices are 64-bit integers in the doubles' order; those that a
+// decision could concern are replaced by exact ones before it is taken. Out of line, so that its registers are not the
 // common path's.
 template <int VPL, typename T, bool VEC>
-__device__ __noinline__ void route_exact(const Params* pp, long long t, const T* row, float tol, bool groups, int32_t* idx, float* w) {
+__device__ __noinline__ void route_exact(const Params* pp, long long t, const T* row, bool groups, int32_t* idx, float* w) {
     const Params& p = *pp;
     const int lane = static_cast<int>(lane_id());
     float r[VPL], b[VPL], c[VPL], m, z, inv;
     load_row<VPL, T, VEC>(row, lane, p.E, r);
-    lane_bias<VPL>(p, lane, b);
+    lane_bias<VPL, VEC>(p, lane, b);
     choices<VPL>(p, r, b, c, m, z, inv);
     // what two near FP32 choices around v can be apart
-    auto slack = [&](float v) { return p.bias != nullptr ? 4.0f * tol : 0x1p-13f * fabsf(v) + 1e-35f; };
+    auto slack = [&](float v) { return (p.bias != nullptr ? 0x1p-16f : 0.0f) + 0x1p-13f * fabsf(v) + 1e-35f; };
     // A softmax's denominator is common: without a bias the exponentials decide.
     double z64 = 1.0;
     if (p.softmax && p.bias != nullptr) {
@@ -436,12 +447,20 @@ __device__ __noinline__ void route_exact(const Params* pp, long long t, const T*
         }
     }
     {
-        const int kth = __shfl_sync(FULL, take_rough<VPL>(c, lane, p.K), p.K - 1);
-        const float edge = kth == EMPTY ? -CUDART_INF_F : key_value(kth & ~255);
+        // near a taken rank other than its own, or near the last
+        const int key = take_rough<VPL>(c, lane, p.K);
+        const float v = key >= FIRST ? key_value(key & ~255) : -CUDART_INF_F;
+        const float last = __shfl_sync(FULL, v, p.K - 1);
+        int n[VPL] = {};
+        for (int k = 0; k < p.K; ++k) {
+            const float vk = __shfl_sync(FULL, v, k), sk = 2.0f * slack(vk);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) n[i] += fabsf(c[i] - vk) <= sk || c[i] == vk ? 1 : 0;
+        }
         unsigned need = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (c[i] > -CUDART_INF_F && !(c[i] < edge - slack(edge) - 0x1p-14f * fabsf(edge))) need |= 1u << i;
+            if (c[i] > -CUDART_INF_F && (n[i] >= 2 || fabsf(c[i] - last) <= 2.0f * slack(last) || c[i] == last)) need |= 1u << i;
         make_exact(need);
     }
     int id = -1;
@@ -484,15 +503,7 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
         unsigned again = 0, groups = 0;  // near tokens, and those near in their groups
         float r[VPL], b[VPL];
         load_row<VPL, T, VEC>(logits + tb * p.stride, lane, p.E, r);
-        lane_bias<VPL>(p, lane, b);
-        // largest |b|: what the choices' additions round by
-        float bmax = 0.0f;
-        if (p.bias != nullptr) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (b[i] > -CUDART_INF_F) bmax = fmaxf(bmax, fabsf(b[i]));
-            bmax = warp_max(bmax);
-        }
+        lane_bias<VPL, VEC>(p, lane, b);
         for (int k = 0; k < 32; ++k) {
             const long long t = tb + static_cast<long long>(k) * step;
             if (t >= p.T) break;
@@ -501,20 +512,19 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             choices<VPL>(p, r, b, c, m, z, inv);
             if (t + step < p.T) load_row<VPL, T, VEC>(row + step * p.stride, lane, p.E, r);
             bool near = false, gnear = false;
-            // How near two FP32 choices may lie before FP64 decides; in units of 2^-23
-            // and for both sides together, twice what they can be off by.
-            // A sigmoid is off by 4 + 1.2 |r| of itself (fast exponential and division),
-            // which is at most 6 where |r| counts; a softmax score by 4 + |r - m| / 2, the
-            // denominator apart, which all scores share. With a bias the bounds are
-            // absolute: the score's, the denominator's error (16) on the largest score, and
-            // the addition's half unit of |b| + s.
-            const float babs = (p.softmax ? 0x1p-18f / z : 0x1p-18f) + 0x1p-21f * bmax;
+            // How near two FP32 choices may lie before FP64 decides: in units of 2^-23 and
+            // for both sides together, twice what they can be off by. A sigmoid is off by
+            // 4 + 1.2 |r| of itself (special functions, argument), which is at most 6 of the
+            // largest score; a softmax score by 4 + |r - m| / 2, the denominator apart, which
+            // all scores share. With a bias the bounds are absolute: the score's, the
+            // denominator's error (16) on the largest score, and half a unit of the choice.
+            const float sabs = p.softmax ? 0x1p-18f * inv : 0x1p-18f;
             if (p.G > 1) {
-                float lo, hi;
-                keep_groups<VPL>(p, lane, c, lo, hi);
+                float lo, hi, mag;
+                keep_groups<VPL>(p, lane, c, lo, hi, mag);
                 if (hi > -CUDART_INF_F && p.TG < p.G) {
                     // without a bias a score names its logit: |r| and |r - m| are below 48 from 1e-20 on
-                    const float tol = p.bias != nullptr ? 2.0f * babs : 0x1p-15f * lo;
+                    const float tol = p.bias != nullptr ? 2.0f * sabs + 0x1p-21f * mag : 0x1p-15f * lo;
                     gnear = !(lo - hi > tol) || (p.bias == nullptr && lo < 1e-20f);
                 }
             }
@@ -522,13 +532,13 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             const int key = take_rough<VPL>(c, lane, p.K + 2);
             int id = -1;
             float rk = -CUDART_INF_F, val = -CUDART_INF_F;
-            if (key != EMPTY) {
+            if (key >= FIRST) {
                 id = 255 - (key & 255);
                 rk = clean(to_f32(row[id]));
                 val = choice(p, rk, p.bias != nullptr ? __ldg(p.bias + id) : 0.0f, m, inv);
             }
             // every expert behind lies at or below the last key with its dropped bits set
-            if (lane > p.K && key != EMPTY) val = key_value(key | 255);
+            if (lane > p.K && key >= FIRST) val = key_value(key | 255);
             const float rest = __shfl_sync(FULL, val, p.K + 1);
             const float next = __shfl_down_sync(FULL, val, 1);
             if (__any_sync(FULL, lane < p.K && next > val)) {
@@ -552,7 +562,7 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             if (lane < p.K && id2 >= 0) {
                 const float far = p.softmax ? m - rk2 : fabsf(rk2);
                 const float spread = 4.0f + (isfinite(far) ? far : 0.0f);
-                const float tol = (p.bias != nullptr ? babs : 0x1p-20f * spread * val) + 1e-36f;
+                const float tol = (p.bias != nullptr ? sabs + 0x1p-21f * fabsf(val) : 0x1p-20f * spread * val) + 1e-36f;
                 if (!(val - val2 > tol)) {
                     // equal inputs are an exact tie: the lower index is first already
                     near = near || !(rk == rk2 && (p.bias == nullptr || p.bias[id] == p.bias[id2]));
@@ -566,7 +576,7 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
         for (; again; again &= again - 1) {
             const int k = __ffs(again) - 1;
             const long long t = tb + static_cast<long long>(k) * step;
-            route_exact<VPL, T, VEC>(&p, t, logits + t * p.stride, 0x1p-18f + 0x1p-21f * bmax, (groups >> k) & 1u, idx, w);
+            route_exact<VPL, T, VEC>(&p, t, logits + t * p.stride, (groups >> k) & 1u, idx, w);
         }
     }
 }
@@ -679,7 +689,8 @@ cudaError_t launch_t(const GroupRouteArgs& a, Params p, bool bwd, cudaStream_t s
     auto even = [&](const void* q, long long st) {
         return reinterpret_cast<uintptr_t>(q) % B == 0 && st * static_cast<long long>(sizeof(T)) % B == 0;
     };
-    const bool vec = a.E % VPL == 0 && even(a.logits, a.stride) && (!bwd || even(a.dlogits, a.E));
+    const bool vec = a.E % VPL == 0 && even(a.logits, a.stride) && (!bwd || even(a.dlogits, a.E)) &&
+                     reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     const T* lg = static_cast<const T*>(a.logits);
     if (!bwd)
         return vec ? launch_pdl(group_route_kernel<VPL, T, true>, grid, block, 0, s, p, lg, a.idx, a.w)
