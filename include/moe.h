@@ -432,7 +432,7 @@ typedef struct moe_int8_config {
     int32_t out_dtype;  /* moe_dtype of out */
 } moe_int8_config;
 
-/* Bytes of workspace moe_matmul_int8 needs for cfg; 0: ws may be NULL. */
+/* Bytes of workspace moe_matmul_int8 needs for cfg (0 for M = 0). */
 moe_status moe_matmul_int8_workspace_size(const moe_int8_config* cfg, size_t* bytes);
 
 /* 8-bit products with a scale per row of a and per channel of b, grouped by
@@ -447,10 +447,14 @@ moe_status moe_matmul_int8_workspace_size(const moe_int8_config* cfg, size_t* by
  *   int32 or NULL (moe_dispatch's sorted_token); out [M, N or N/2].
  *   a, b, out 16-byte aligned, ws 256-byte aligned.
  * Rows from offsets[E] on are written as zeros. Offsets are clamped to
- * [0, M]; a row index outside [0, Ma) makes its product row NaN and, where
- * the workspace has 256 bytes or more, sets MOE_ERR_DEVICE_INDEX in its
- * error word. The call adds to that word and never clears it: have it zeroed
- * before the first call, moe_workspace_status reads and clears it. */
+ * [0, M]; a row index outside [0, Ma) makes its product row NaN and sets
+ * MOE_ERR_DEVICE_INDEX in the workspace's error word. The call adds to that
+ * word and never clears it: have it zeroed before the first call,
+ * moe_workspace_status reads and clears it.
+ *   The form is chosen from the rows per expert; the environment variable
+ * MOE_INT8_FORM, read at each call, overrides it for tests and tuning ("vec":
+ * integer dot products; "small", "wide": tensor cores, tiles of up to 32 or
+ * 256 rows). The sums are exact in every form; the scales round alike. */
 moe_status moe_matmul_int8(const moe_int8_config* cfg, const int8_t* a, int64_t a_stride,
                            const float* a_scale, const int8_t* b, const float* b_scale,
                            const int32_t* offsets, const int32_t* rows, void* out, void* ws,

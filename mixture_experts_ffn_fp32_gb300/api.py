@@ -696,7 +696,7 @@ def alloc_int8_workspace(M: int, K: int, N: int, E: int = 1, swiglu: bool = Fals
                          device="cuda") -> torch.Tensor:
     """A workspace for matmul_int8 calls of up to M product rows (its error word
     zeroed; workspace_status reads and clears it)."""
-    n = max(_int8_ws(*_int8_config(m, m, K, N, E, swiglu, "f32")) for m in {M, min(M, 1)})
+    n = _int8_ws(*_int8_config(M, M, K, N, E, swiglu, "f32"))
     ws = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
@@ -732,9 +732,7 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     cfg = _int8_config(M, Ma, K, N, E, swiglu, out_dtype)
     with _on(stream, a, a_scale, b, b_scale, offsets, rows, ws):
         if ws is None:
-            n = _int8_ws(*cfg)
-            if n:
-                ws = torch.empty((n,), dtype=torch.uint8, device=a.device)
+            ws = torch.empty((_int8_ws(*cfg),), dtype=torch.uint8, device=a.device)
         out = torch.empty((M, N // 2 if swiglu else N), dtype=_OUT_DTYPES[out_dtype], device=a.device)
         _check(lib().moe_matmul_int8(ctypes.byref(Int8Config(*cfg)), a.data_ptr(), a.stride(0) if Ma > 1 else K,
                                      a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),

@@ -11,15 +11,16 @@
 // registers. Either way the sum is the integer product's, at the FP16 rate.
 //
 // Roles: output channels are the MMA's M rows, tokens its N columns, one CTA
-// pair (cta_group::2) per tile of 256 channels x 256 tokens. The tokens are
+// pair (cta_group::2) per tile of 256 channels x 256 tokens (or 32, see Form). The tokens are
 // widened to FP16 (and gathered) once, by a pass before; the weights stay 8
 // bits in HBM, L2 and shared memory, and four warps widen them on their way
 // into tensor memory, from where the MMA takes its A operand: weights widened
 // into shared memory would add their write and the MMA's read to a shared
 // memory that the copies and the tokens already keep half busy.
 //
-// Warps: 0 copies tokens, 2 weights (TMA), 1 issues MMAs (even CTA), 4-7 widen
-// weights, 8-15 hold the integer sums and store. A stage is 128 of the
+// Warps: 0 copies tokens, 2 weights (TMA), 1 issues MMAs (even CTA), 4-7 (and
+// 12-15 with few tokens) widen weights, 8-15 (8-11) hold the integer sums and
+// store. A stage is 128 of the
 // reduction: 32 KB of tokens and 64 columns of widened weights in tensor
 // memory, which the MMAs free together, and 16 KB of weights in a ring of its
 // own, which the widening frees: weights are in shared memory before their
@@ -35,35 +36,51 @@ namespace moe {
 namespace {
 
 constexpr int BK = 128;              // reduction per stage
-constexpr int STAGES = 4;
 constexpr int CHUNK_BLOCKS = 8;      // blocks of BK per exact chunk (1024)
-constexpr int CH = 128;              // channels per CTA (MMA rows)
-constexpr int NT = 256;              // tokens per tile (MMA columns of the pair)
-constexpr int W_BYTES = CH * BK;     // 8-bit weights
-constexpr int T_HALF = 128 * 128;    // 64 of the reduction x 128 tokens of FP16
-constexpr int T_BYTES = 2 * T_HALF;
-constexpr int WSTAGES = 5;           // stages of the weights' ring
-constexpr int W_OFF = STAGES * T_BYTES;
 constexpr int L1_ONE_CHUNK = 1 << 17;  // row sum of |a| up to which one accumulator is exact
+constexpr int CH = 128;              // channels per CTA (MMA rows)
+constexpr int W_BYTES = CH * BK;     // a stage's 8-bit weights
 constexpr int THREADS = 512;
-constexpr int CONV_WARPS = 4, EPI_WARPS = 8;
-// Registers a thread per warpgroup: copies and MMAs, widening, two of sums
-// (128 of them the integers).
-constexpr int REGS_COPY = 64, REGS_CONV = 80, REGS_EPI = 184;
-constexpr int REGS_SUM = REGS_COPY + REGS_CONV + 2 * REGS_EPI;
-static_assert(REGS_SUM <= 4 * 128, "the shares exceed the launch's registers");
+constexpr int CONV_WARPS = 4;        // warps that widen one stage
 constexpr int MAXE = 256;
 constexpr int TMEM_COLS = 512;
-constexpr int A_COL = 256;           // tensor-memory columns of the widened weights, 64 per stage
-constexpr int NBARS = 3 * STAGES + 2 * WSTAGES + 3;
-constexpr int BAR_OFF = W_OFF + WSTAGES * W_BYTES;
-constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
-constexpr int TAB_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
-constexpr int SMEM_BYTES = TAB_OFF + (2 * (MAXE + 1) + THREADS / 32) * 4 + 1024;
+
+// A form: tiles of up to NT tokens (MMA columns of the pair).
+//   256: compute-bound; one team of widening warps, two of sums (128 integers a thread).
+//   32: bound by the weights' bytes; single CTAs (a pair's MMA takes about 160
+//       cycles however few its columns), deep weights' ring, two teams of widening
+//       warps in turn (one takes 850 cycles a stage, HBM delivers one in 700),
+//       one of sums.
+template <int NT>
+struct Form {
+    static constexpr bool WIDE = NT > 32;  // CTA pairs, each CTA half of the tokens
+    static constexpr int CTAS = WIDE ? 2 : 1;
+    static constexpr int T_HALF = NT / CTAS * 128;  // 64 of the reduction x this CTA's tokens of FP16
+    static constexpr int T_BYTES = 2 * T_HALF;
+    static constexpr int STAGES = WIDE ? 4 : 7;    // of tokens and of widened weights (64 columns each)
+    static constexpr int WSTAGES = WIDE ? 5 : 10;  // of weights
+    static constexpr int A_COL = NT;               // tensor-memory columns: accumulator, then widened weights
+    static constexpr int TEAMS = WIDE ? 1 : 2;
+    static constexpr int EPI_WARPS = WIDE ? 8 : 4;
+    static constexpr int EPI_TOK = WIDE ? NT / 2 : NT;  // tokens of an epilogue warp
+    // Registers a thread per warpgroup: copies and MMAs, widening, two of sums
+    // (or one and the second widening team, where the launch's split is kept).
+    static constexpr int REGS_COPY = 64, REGS_CONV = 80, REGS_EPI = 184;
+    static constexpr int REGS_SUM = REGS_COPY + REGS_CONV + 2 * REGS_EPI;
+    static constexpr int W_OFF = STAGES * T_BYTES;
+    static constexpr int NBARS = 3 * STAGES + 2 * WSTAGES + 3;
+    static constexpr int BAR_OFF = W_OFF + WSTAGES * W_BYTES;
+    static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
+    static constexpr int TAB_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
+    static constexpr int SMEM_BYTES = TAB_OFF + (2 * (MAXE + 1) + THREADS / 32) * 4 + 1024;
+    static_assert(A_COL + 64 * STAGES <= TMEM_COLS, "tensor memory");
+    static_assert(REGS_SUM <= 4 * 128, "the shares exceed the launch's registers");
+    static_assert(T_HALF % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory");
+};
 
 struct Int8TcParams {
     CUtensorMap mapW;   // [E, N, K] 8 bits, boxes of 64 channels x 128
-    CUtensorMap mapT;   // [M, K] FP16, boxes of 128 tokens x 64
+    CUtensorMap mapT;   // [M, K] FP16, boxes of a CTA's tokens x 64
     int M, K, N, E, F;  // F: output channels (N, or N / 2 with SwiGLU)
     int nt;             // channel tiles of a pair
     const int32_t* offsets;
@@ -179,8 +196,16 @@ MOE_DEV void tc_mma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// FP32 accumulator, FP16 A and B (K-major), M = 256; N is added per tile.
-constexpr uint32_t IDESC0 = (1u << 4) | (static_cast<uint32_t>(256 >> 4) << 24);
+MOE_DEV void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// FP32 accumulator, FP16 A and B (K-major), M = 128 per CTA; N is added per tile.
+constexpr uint32_t idesc0(int ctas) { return (1u << 4) | (static_cast<uint32_t>(ctas * CH >> 4) << 24); }
 
 template <int N>
 MOE_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -210,7 +235,7 @@ struct Tile {
 
 // s_tp: tiles before each expert; s_off: its first row. Channel tiles are
 // innermost: neighbouring pairs share a token tile and an expert's weights.
-template <int OUT_CH>
+template <int TILE_CH, int NT>
 MOE_DEV Tile tile_of(int u, const Int8TcParams& p, const int* s_tp, const int* s_off) {
     const int mt = u / p.nt;
     int lo = 0, hi = p.E;
@@ -223,38 +248,41 @@ MOE_DEV Tile tile_of(int u, const Int8TcParams& p, const int* s_tp, const int* s
     t.e = lo;
     t.row0 = s_off[lo] + (mt - s_tp[lo]) * NT;
     t.n = min(NT, s_off[lo + 1] - t.row0);
-    t.f0 = (u - mt * p.nt) * 2 * OUT_CH;
+    t.f0 = (u - mt * p.nt) * TILE_CH;
     return t;
 }
 
-template <bool SWIGLU, typename O>
+template <int NT, bool SWIGLU, typename O>
 __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_constant__ Int8TcParams p) {
+    using G = Form<NT>;
+    constexpr int STAGES = G::STAGES, WSTAGES = G::WSTAGES, T_BYTES = G::T_BYTES, T_HALF = G::T_HALF;
     constexpr int OUT_CH = SWIGLU ? CH / 2 : CH;  // output channels per CTA
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t bar0 = sbase + BAR_OFF;
+    const uint32_t bar0 = sbase + G::BAR_OFF;
     auto tfull = [&](int s) { return bar0 + 8u * s; };                  // even CTA: both CTAs' tokens landed
     auto aready = [&](int s) { return bar0 + 8u * (STAGES + s); };      // even CTA: both CTAs' weights widened
     auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };   // tokens and columns read by the MMAs
     auto wfull = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };   // own weights landed
     auto wempty = [&](int s) { return bar0 + 8u * (3 * STAGES + WSTAGES + s); };  // and widened
     const uint32_t acc_full = bar0 + 8u * (3 * STAGES + 2 * WSTAGES), acc_empty = acc_full + 8u, drain_bar = acc_full + 16u;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + MISC_OFF);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + MISC_OFF + 4);
-    int* s_tp = reinterpret_cast<int*>(smem + TAB_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::MISC_OFF + 4);
+    int* s_tp = reinterpret_cast<int*>(smem + G::TAB_OFF);
     int* s_off = s_tp + MAXE + 1;
     int* s_l1 = s_off + MAXE + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = static_cast<int>(cluster_ctarank());
-    const int unit0 = static_cast<int>(blockIdx.x >> 1), ustep = static_cast<int>(gridDim.x >> 1);
+    constexpr bool PAIR = G::CTAS == 2;
+    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const int unit0 = static_cast<int>(blockIdx.x) / G::CTAS, ustep = static_cast<int>(gridDim.x) / G::CTAS;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(tfull(s), 1);
-            mbar_init(aready(s), 2 * CONV_WARPS);
+            mbar_init(aready(s), G::CTAS * CONV_WARPS);
             mbar_init(empty(s), 1);
         }
         for (int s = 0; s < WSTAGES; ++s) {
@@ -262,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             mbar_init(wempty(s), CONV_WARPS);
         }
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 2 * EPI_WARPS);
+        mbar_init(acc_empty, G::CTAS * G::EPI_WARPS);
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
@@ -270,8 +298,13 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
         tma_prefetch_map(&p.mapT);
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
-        tmem_relinquish_pair();
+        if (PAIR) {
+            tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+            tmem_relinquish();
+        }
     }
     pdl_wait();  // the tokens and their scales
     pdl_trigger();
@@ -307,7 +340,8 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();
+    if (PAIR) cluster_sync();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int total = s_tp[p.E] * p.nt;
@@ -321,15 +355,15 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
     const int nchunks = (kblocks + cblocks - 1) / cblocks;
 
     if (warp < 4) {
-        reg_dec<REGS_COPY>();
+        if (G::WIDE) reg_dec<G::REGS_COPY>();
         if (warp == 0 && lane == 0) {
             // ---------------- tokens (both CTAs) ----------------
             int stage = 0;
             uint32_t phase = 0, issued = 0, last_par = 0;
             bool ok = true;
             for (int u = unit0; u < total && ok; u += ustep) {
-                const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
-                const int nh = ((t.n + 15) & ~15) >> 1;  // token columns held by each CTA
+                const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
+                const int nh = ((t.n + 15) & ~15) / G::CTAS;  // token columns held by each CTA
                 const int trow = t.row0 + rank * nh;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!bounded_wait(empty(stage), phase ^ 1u, wc)) {
@@ -337,10 +371,15 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                         break;
                     }
                     const uint32_t sT = sbase + stage * T_BYTES;
-                    const uint32_t tb = map_shared_rank(tfull(stage), 0);
-                    if (rank == 0) mbar_expect_tx(tfull(stage), 2 * T_BYTES);
-                    tma_load_2d_pair(sT, &p.mapT, kb * BK, trow, tb);
-                    tma_load_2d_pair(sT + T_HALF, &p.mapT, kb * BK + 64, trow, tb);
+                    if (rank == 0) mbar_expect_tx(tfull(stage), G::CTAS * T_BYTES);
+                    if (PAIR) {
+                        const uint32_t tb = map_shared_rank(tfull(stage), 0);
+                        tma_load_2d_pair(sT, &p.mapT, kb * BK, trow, tb);
+                        tma_load_2d_pair(sT + T_HALF, &p.mapT, kb * BK + 64, trow, tb);
+                    } else {
+                        tma_load_2d(sT, &p.mapT, kb * BK, trow, tfull(stage));
+                        tma_load_2d(sT + T_HALF, &p.mapT, kb * BK + 64, trow, tfull(stage));
+                    }
                     issued |= 1u << stage;
                     last_par = (last_par & ~(1u << stage)) | (phase << stage);
                     if (++stage == STAGES) {
@@ -360,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             uint32_t phase = 0, issued = 0, last_par = 0;
             bool ok = true;
             for (int u = unit0; u < total && ok; u += ustep) {
-                const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
+                const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
                 // 64 + 64 channels: a SwiGLU tile's gates and ups, else one run
                 const int c0 = t.f0 + rank * OUT_CH, c1 = SWIGLU ? c0 + p.F : c0 + 64;
                 for (int kb = 0; kb < kblocks; ++kb) {
@@ -368,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                         ok = false;
                         break;
                     }
-                    const uint32_t sW = sbase + W_OFF + stage * W_BYTES;
+                    const uint32_t sW = sbase + G::W_OFF + stage * W_BYTES;
                     mbar_expect_tx(wfull(stage), W_BYTES);
                     tma_load_3d(sW, &p.mapW, kb * BK, c0, t.e, wfull(stage));
                     tma_load_3d(sW + W_BYTES / 2, &p.mapW, kb * BK, c1, t.e, wfull(stage));
@@ -389,53 +428,62 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             bool ok = true;
             const uint64_t bdesc0 = smem_desc_sw128(sbase, 16, 1024);
             for (int u = unit0; u < total && ok; u += ustep) {
-                const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
-                const uint32_t idesc = IDESC0 | (static_cast<uint32_t>(((t.n + 15) & ~15) >> 3) << 17);
+                const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
+                const uint32_t idesc = idesc0(G::CTAS) | (static_cast<uint32_t>(((t.n + 15) & ~15) >> 3) << 17);
                 for (int c = 0; c < nchunks && ok; ++c) {
-                    if (!bounded_wait(acc_empty, acc_phase ^ 1u, wc, true)) {
+                    if (!bounded_wait(acc_empty, acc_phase ^ 1u, wc, PAIR)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const int kb1 = min((c + 1) * cblocks, kblocks);
                     for (int kb = c * cblocks; kb < kb1; ++kb) {
-                        if (!bounded_wait(tfull(stage), phase, wc, true) || !bounded_wait(aready(stage), phase, wc, true)) {
+                        if (!bounded_wait(tfull(stage), phase, wc, PAIR) || !bounded_wait(aready(stage), phase, wc, PAIR)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint64_t bs = bdesc0 + (static_cast<uint64_t>(stage * T_BYTES) >> 4);
-                        const uint32_t at = tmem + A_COL + static_cast<uint32_t>(stage * 64);
+                        const uint32_t at = tmem + G::A_COL + static_cast<uint32_t>(stage * 64);
                         const int steps = min(BK, p.K - kb * BK) / 16;
-                        for (int ks = 0; ks < steps; ++ks)
-                            tc_mma_f16_pair_ta(tmem, at + ks * 8, bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16, idesc,
-                                               (kb != c * cblocks || ks != 0) ? 1u : 0u);
-                        tc_commit_pair_mc(empty(stage), 3);
+                        for (int ks = 0; ks < steps; ++ks) {
+                            const uint64_t bd = bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16;
+                            const uint32_t add = (kb != c * cblocks || ks != 0) ? 1u : 0u;
+                            if (PAIR) tc_mma_f16_pair_ta(tmem, at + ks * 8, bd, idesc, add);
+                            else tc_mma_f16_ta(tmem, at + ks * 8, bd, idesc, add);
+                        }
+                        if (PAIR) tc_commit_pair_mc(empty(stage), 3);
+                        else tc_commit(empty(stage));
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (!ok) break;
-                    tc_commit_pair_mc(acc_full, 3);
+                    if (PAIR) tc_commit_pair_mc(acc_full, 3);
+                    else tc_commit(acc_full);
                     acc_phase ^= 1u;
                 }
             }
-            tc_commit_pair(drain_bar);
+            if (PAIR) tc_commit_pair(drain_bar);
+            else tc_commit(drain_bar);
             bounded_drain(drain_bar, 0, p.timeout_ns, p.err);
         }
-    } else if (warp < 4 + CONV_WARPS) {
+    } else if (warp < 4 + CONV_WARPS || (G::TEAMS == 2 && warp >= 12)) {
         // ---------------- weights: 8 bits in shared memory to FP16 in tensor memory ----------------
-        reg_dec<REGS_CONV>();
+        if (G::WIDE) reg_dec<G::REGS_CONV>();
+        const int team = warp >= 12 ? 1 : 0;
         const int q = warp & 3;
         // This thread's tensor-memory lane takes one channel of the stage. SwiGLU: a
         // quarter's lanes 0-15 are gates, 16-31 the ups of the same channels.
         const int row = SWIGLU ? (lane < 16 ? 16 * q + lane : 64 + 16 * q + lane - 16) : 32 * q + lane;
-        int stage = 0, ws = 0;
+        // teams take the stages in turn, across tiles
+        int stage = team, ws = team, turn = 0;
         uint32_t phase = 0, wphase = 0;
         bool ok = true;
         for (int u = unit0; u < total && ok; u += ustep) {
             for (int kb = 0; kb < kblocks; ++kb) {
+                if (G::TEAMS == 2 && (turn++ & 1) != team) continue;
                 int w = 1;
                 // the weights are there, and the MMAs have read the columns' last content
                 if (lane == 0) w = bounded_wait(wfull(ws), wphase, wc) && bounded_wait(empty(stage), phase ^ 1u, wc) ? 1 : 0;
@@ -444,8 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                     break;
                 }
                 tc_fence_after();
-                const uint8_t* wr = smem + W_OFF + ws * W_BYTES + row * BK;
-                const uint32_t at = tmem + A_COL + static_cast<uint32_t>(stage * 64) + (static_cast<uint32_t>(q * 32) << 16);
+                const uint8_t* wr = smem + G::W_OFF + ws * W_BYTES + row * BK;
+                const uint32_t at = tmem + G::A_COL + static_cast<uint32_t>(stage * 64) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t r[32];
@@ -468,28 +516,31 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                     if (rank == 0) mbar_arrive(aready(stage));
                     else mbar_arrive_peer(map_shared_rank(aready(stage), 0));
                 }
-                if (++ws == WSTAGES) {
-                    ws = 0;
+                ws += G::TEAMS;
+                if (ws >= WSTAGES) {
+                    ws -= WSTAGES;
                     wphase ^= 1u;
                 }
-                if (++stage == STAGES) {
-                    stage = 0;
+                stage += G::TEAMS;
+                if (stage >= STAGES) {
+                    stage -= STAGES;
                     phase ^= 1u;
                 }
             }
         }
     } else {
         // ---------------- integer sums and stores ----------------
-        reg_inc<REGS_EPI>();
-        const int q = warp & 3, half = (warp - 8) >> 2;
-        const int c0 = 128 * half;  // this warp's token columns [c0, c0 + 128)
+        if (G::WIDE) reg_inc<G::REGS_EPI>();
+        constexpr int TOK = G::EPI_TOK;
+        const int q = warp & 3;
+        const int c0 = TOK * ((warp - 8) >> 2);  // this warp's token columns [c0, c0 + TOK)
         uint32_t phase = 0;
         bool ok = true;
         for (int u = unit0; u < total && ok; u += ustep) {
-            const Tile t = tile_of<OUT_CH>(u, p, s_tp, s_off);
+            const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
             const uint32_t ta = tmem + static_cast<uint32_t>(c0) + (static_cast<uint32_t>(q * 32) << 16);
             // one chunk: the FP32 accumulator as it is; several: their integer sum
-            uint32_t acc[128];
+            uint32_t acc[TOK];
             for (int c = 0; c < nchunks; ++c) {
                 int w = 1;
                 if (lane == 0) w = bounded_wait(acc_full, phase, wc) ? 1 : 0;
@@ -501,12 +552,12 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                 tc_fence_after();
                 if (c == 0) {
 #pragma unroll
-                    for (int g = 0; g < 8; ++g)
+                    for (int g = 0; g < TOK / 16; ++g)
                         if (c0 + 16 * g < t.n) tc_ld_16(ta + 16 * g, acc + 16 * g);
                     tc_wait_ld();
                 } else {
 #pragma unroll
-                    for (int g = 0; g < 8; ++g)
+                    for (int g = 0; g < TOK / 16; ++g)
                         if (c0 + 16 * g < t.n) {
                             uint32_t r[16];
                             tc_ld_16(ta + 16 * g, r);
@@ -523,28 +574,28 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                 }
                 if (c == 0 && nchunks > 1) {
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) acc[i] = __float2int_rn(__uint_as_float(acc[i]));
+                    for (int i = 0; i < TOK; ++i) acc[i] = __float2int_rn(__uint_as_float(acc[i]));
                 }
             }
             if (!ok) break;
             if (nchunks > 1) {
 #pragma unroll
-                for (int i = 0; i < 128; ++i) acc[i] = __float_as_uint(static_cast<float>(static_cast<int>(acc[i])));
+                for (int i = 0; i < TOK; ++i) acc[i] = __float_as_uint(static_cast<float>(static_cast<int>(acc[i])));
             }
             // this lane's channel, its scale, and the tokens' scales (lane l: tokens 32 j + l)
             const int oc = SWIGLU ? t.f0 + rank * OUT_CH + 16 * q + (lane & 15) : t.f0 + rank * OUT_CH + 32 * q + lane;
             const bool in = oc < p.F;
             const int ch = SWIGLU && lane >= 16 ? oc + p.F : oc;
             const float sb = in ? __ldg(p.sb + static_cast<long long>(t.e) * p.N + ch) : 0.0f;
-            float sa[4];
+            float sa[TOK / 32];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < TOK / 32; ++j) {
                 const int ti = c0 + 32 * j + lane;
                 sa[j] = ti < t.n ? p.sa[t.row0 + ti] : 0.0f;
             }
             O* orow = static_cast<O*>(p.out) + static_cast<long long>(t.row0 + c0) * p.F + oc;
 #pragma unroll
-            for (int i = 0; i < 128; i += 2) {
+            for (int i = 0; i < TOK; i += 2) {
                 if (c0 + i < t.n) {
                     const float s0 = __shfl_sync(0xffffffffu, sa[i >> 5], i & 31);
                     const float s1 = __shfl_sync(0xffffffffu, sa[i >> 5], (i & 31) + 1);
@@ -569,32 +620,37 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
     // memory, barriers or tensor memory
     __syncwarp();
     tc_fence_before();
-    cluster_sync();
+    if (PAIR) cluster_sync();
+    else __syncthreads();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc_pair(tmem, TMEM_COLS);
+        if (PAIR) tmem_dealloc_pair(tmem, TMEM_COLS);
+        else tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
 constexpr size_t L1_BYTES = 8192;  // a word per CTA of the tokens' pass
 size_t pad256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <bool SWIGLU, typename O>
-int pair_slots(int dev) {
+template <int NT, bool SWIGLU, typename O>
+int cta_slots(int dev) {  // CTAs, or pairs, that are resident at once
+    using G = Form<NT>;
     static int cache[64] = {};
     if (dev < 0 || dev >= 64) return 0;
     if (cache[dev] == 0) {
         int n = -1;
         // the warpgroups' register shares are drawn on what the block is launched with
         cudaFuncAttributes fa{};
-        if (cudaFuncGetAttributes(&fa, int8_tc_kernel<SWIGLU, O>) == cudaSuccess && fa.numRegs * 4 >= REGS_SUM &&
-            cudaFuncSetAttribute(int8_tc_kernel<SWIGLU, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES) ==
+        if (cudaFuncGetAttributes(&fa, int8_tc_kernel<NT, SWIGLU, O>) == cudaSuccess &&
+            (!G::WIDE || fa.numRegs * 4 >= G::REGS_SUM) &&
+            cudaFuncSetAttribute(int8_tc_kernel<NT, SWIGLU, O>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM_BYTES) ==
                 cudaSuccess) {
+            if (G::CTAS == 1) return cache[dev] = num_sms();  // a CTA's shared memory fills an SM
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(2 * static_cast<unsigned>(num_sms()));
             cfg.blockDim = dim3(THREADS);
-            cfg.dynamicSmemBytes = SMEM_BYTES;
+            cfg.dynamicSmemBytes = G::SMEM_BYTES;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
             attr[0].val.clusterDim.x = 2;
@@ -603,7 +659,7 @@ int pair_slots(int dev) {
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int c = 0;
-            if (cudaOccupancyMaxActiveClusters(&c, int8_tc_kernel<SWIGLU, O>, &cfg) == cudaSuccess && c > 0)
+            if (cudaOccupancyMaxActiveClusters(&c, int8_tc_kernel<NT, SWIGLU, O>, &cfg) == cudaSuccess && c > 0)
                 n = c;
             else
                 cudaGetLastError();
@@ -613,11 +669,11 @@ int pair_slots(int dev) {
     return cache[dev] > 0 ? cache[dev] : 0;
 }
 
-template <bool SWIGLU, typename O>
+template <int NT, bool SWIGLU, typename O>
 cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
-    const int slots = pair_slots<SWIGLU, O>(dev);
+    const int slots = cta_slots<NT, SWIGLU, O>(dev);
     if (slots <= 0) return cudaErrorInvalidConfiguration;
     uint8_t* ws = reinterpret_cast<uint8_t*>(a.err);
     float* tsa = reinterpret_cast<float*>(ws + 256);
@@ -626,14 +682,15 @@ cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
     Int8TcParams p{};
     p.M = a.M; p.K = a.K; p.N = a.N; p.E = a.E;
     p.F = SWIGLU ? a.N / 2 : a.N;
-    const int per = 2 * (SWIGLU ? CH / 2 : CH);
+    constexpr int CTAS = Form<NT>::CTAS;
+    const int per = CTAS * (SWIGLU ? CH / 2 : CH);
     p.nt = (p.F + per - 1) / per;
     const uint64_t wd[3] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.E)};
     const uint64_t wst[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.K) * a.N};
     const uint32_t wb[3] = {BK, 64, 1};
     const uint64_t td[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)};
     const uint64_t tst[1] = {static_cast<uint64_t>(a.K) * 2};
-    const uint32_t tb[2] = {64, 128};
+    const uint32_t tb[2] = {64, NT / CTAS};
     if (!encode_tmap_typed(&p.mapW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.b, 3, wd, wst, wb) ||
         !encode_tmap_typed(&p.mapT, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, tok, 2, td, tst, tb))
         return cudaErrorInvalidValue;
@@ -648,10 +705,13 @@ cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
                                a.K, a.E, p.F, a.a, a.lda, a.sa, a.offsets, a.rows, reinterpret_cast<uint4*>(tok), tsa,
                                static_cast<O*>(a.out), l1, a.err);
     if (e != cudaSuccess) return e;
-    const long long bound = (static_cast<long long>((a.M + NT - 1) / NT) + (a.E > 1 ? a.E : 0)) * p.nt;
+    // tiles: whole ones, and a part for each expert that has rows
+    const long long bound = (static_cast<long long>((a.M + NT - 1) / NT) + (a.E > 1 ? (a.E < a.M ? a.E : a.M) : 0)) * p.nt;
     const int grid = static_cast<int>(bound < slots ? (bound > 0 ? bound : 1) : slots);
-    return launch_pdl_cluster(int8_tc_kernel<SWIGLU, O>, dim3(2 * static_cast<unsigned>(grid)), dim3(THREADS),
-                              SMEM_BYTES, s, 2, p);
+    if (CTAS == 1)
+        return launch_pdl(int8_tc_kernel<NT, SWIGLU, O>, dim3(grid), dim3(THREADS), Form<NT>::SMEM_BYTES, s, p);
+    return launch_pdl_cluster(int8_tc_kernel<NT, SWIGLU, O>, dim3(2 * static_cast<unsigned>(grid)), dim3(THREADS),
+                              Form<NT>::SMEM_BYTES, s, 2, p);
 }
 
 }  // namespace
@@ -662,12 +722,17 @@ size_t int8_tc_workspace(int M, int K) {
     return 256 + pad256(static_cast<size_t>(M) * 4) + L1_BYTES + static_cast<size_t>(M) * static_cast<size_t>(K) * 2;
 }
 
-cudaError_t launch_int8_tc(const Int8Args& a, cudaStream_t s) {
+template <int NT>
+static cudaError_t launch_form(const Int8Args& a, cudaStream_t s) {
     switch (a.out_dtype) {
-        case MOE_BF16: return a.swiglu ? launch_t<true, __nv_bfloat16>(a, s) : launch_t<false, __nv_bfloat16>(a, s);
-        case MOE_F16: return a.swiglu ? launch_t<true, __half>(a, s) : launch_t<false, __half>(a, s);
-        default: return a.swiglu ? launch_t<true, float>(a, s) : launch_t<false, float>(a, s);
+        case MOE_BF16: return a.swiglu ? launch_t<NT, true, __nv_bfloat16>(a, s) : launch_t<NT, false, __nv_bfloat16>(a, s);
+        case MOE_F16: return a.swiglu ? launch_t<NT, true, __half>(a, s) : launch_t<NT, false, __half>(a, s);
+        default: return a.swiglu ? launch_t<NT, true, float>(a, s) : launch_t<NT, false, float>(a, s);
     }
+}
+
+cudaError_t launch_int8_tc(const Int8Args& a, bool wide, cudaStream_t s) {
+    return wide ? launch_form<256>(a, s) : launch_form<32>(a, s);
 }
 
 }  // namespace moe

@@ -52,7 +52,7 @@ MOE_DEV void block(const VecParams& p, int e, int n0, int i0, int nrows, int lan
             src = p.rows[src];
             ok = src >= 0 && src < p.Ma;
             if (!ok) {
-                if (p.err != nullptr && lane == 0) atomicOr(p.err, ERRBIT_INDEX);
+                if (lane == 0) atomicOr(p.err, ERRBIT_INDEX);
                 src = 0;
             }
         }

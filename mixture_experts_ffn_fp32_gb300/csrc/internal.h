@@ -554,11 +554,12 @@ struct Int8Args {
     const int32_t* offsets;  // NULL: one expert takes every row
     const int32_t* rows;     // NULL: product row i reads row i of a
     void* out;
-    int* err;                // NULL: bad row indices are not reported
+    int* err;                // the workspace, its error word first
 };
 cudaError_t launch_int8_vec(const Int8Args& a, cudaStream_t s);
-// The tensor-core form: a.err points to a workspace of int8_tc_workspace bytes.
+// The tensor-core forms (tiles of 256 tokens, or of 32): a.err points to a
+// workspace of int8_tc_workspace bytes.
 size_t int8_tc_workspace(int M, int K);
-cudaError_t launch_int8_tc(const Int8Args& a, cudaStream_t s);
+cudaError_t launch_int8_tc(const Int8Args& a, bool wide, cudaStream_t s);
 
 }  // namespace moe

@@ -1,6 +1,8 @@
 // C entry points of the operators around the layer (declared in
 // include/moe.h): layer norm, group-limited routing, row quantisation and the
 // 8-bit expert products. Host-side validation, then the launchers.
+#include <stdlib.h>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -164,9 +166,19 @@ moe_status check_int8(const moe_int8_config& c) {
 }
 
 // Few rows per expert run on the integer dot product, which reads the weights
-// straight into registers; the tensor-core form pays its tile of 256 channels
-// and its tokens' pass whatever the rows.
-bool int8_on_tensor_cores(const moe_int8_config& c) { return c.M >= 16LL * c.E; }
+// straight into registers; the tensor-core forms pay their tile of 256
+// channels and their tokens' pass whatever the rows. MOE_INT8_FORM overrides
+// the choice for tests and tuning.
+enum Int8Form { INT8_VEC, INT8_SMALL, INT8_WIDE };
+Int8Form int8_form(const moe_int8_config& c) {
+    if (const char* e = getenv("MOE_INT8_FORM")) {
+        if (e[0] == 'v') return INT8_VEC;
+        if (e[0] == 's') return INT8_SMALL;
+        if (e[0] == 'w') return INT8_WIDE;
+    }
+    if (c.M < 2LL * c.E) return INT8_VEC;
+    return c.M <= 32LL * c.E ? INT8_SMALL : INT8_WIDE;
+}
 
 }  // namespace
 
@@ -174,7 +186,7 @@ MOE_API moe_status moe_matmul_int8_workspace_size(const moe_int8_config* cfg, si
     if (!cfg || !bytes) return MOE_ERR_INVALID_ARG;
     const moe_status v = check_int8(*cfg);
     if (v != MOE_OK) return v;
-    *bytes = int8_on_tensor_cores(*cfg) ? int8_tc_workspace(cfg->M, cfg->K) : 0;
+    *bytes = cfg->M == 0 ? 0 : int8_tc_workspace(cfg->M, cfg->K);  // whichever form the call takes
     return MOE_OK;
 }
 
@@ -196,15 +208,15 @@ MOE_API moe_status moe_matmul_int8(const moe_int8_config* cfg, const int8_t* a, 
         return MOE_ERR_INVALID_ARG;
     size_t need = 0;
     moe_matmul_int8_workspace_size(cfg, &need);
-    if (need > 0 && !ws) return MOE_ERR_INVALID_ARG;
-    if (ws && !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     Int8Args g{};
     g.M = c.M; g.Ma = c.Ma; g.K = c.K; g.N = c.N; g.E = c.E; g.swiglu = c.swiglu; g.out_dtype = c.out_dtype;
     g.lda = a_stride;
     g.a = a; g.sa = a_scale; g.b = b; g.sb = b_scale;
     g.offsets = offsets; g.rows = rows; g.out = out;
-    g.err = ws && ws_bytes >= 256 ? static_cast<int*>(ws) : nullptr;
+    g.err = static_cast<int*>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return cuda_status(int8_on_tensor_cores(c) ? launch_int8_tc(g, s) : launch_int8_vec(g, s));
+    const Int8Form f = int8_form(c);
+    return cuda_status(f == INT8_VEC ? launch_int8_vec(g, s) : launch_int8_tc(g, f == INT8_WIDE, s));
 }

@@ -141,6 +141,22 @@ def test_gathered_rows(A, shape):
     check(A, a, sa, b, sb, sp, rows, True, "f32")
 
 
+@pytest.mark.parametrize("form", ["vec", "small", "wide"])
+@pytest.mark.parametrize("shape", [(1, 1, 16, 2), (33, 1, 1040, 258), (70, 3, 256, 514), (300, 5, 2048, 136),
+                                   (90, 40, 4096, 64), (700, 2, 640, 1030)], ids=str)
+def test_every_form(A, monkeypatch, shape, form):
+    """Each form at any number of rows, plain and SwiGLU, gathered and not."""
+    monkeypatch.setenv("MOE_INT8_FORM", form)
+    M, E, K, N = shape
+    a, b = ints(M, K, seed=M + 1), ints(E, N, K, seed=N + 1)
+    sa = 0.5 + torch.rand(M, generator=gen(31), device="cuda")
+    sb = (0.5 + torch.rand(E, N, generator=gen(32), device="cuda")) / (5000 * K ** 0.5)
+    sp = None if E == 1 else splits_of(E, M, M + 2)
+    rows = torch.randint(0, M, (M,), generator=gen(33), device="cuda").to(torch.int32)
+    check(A, a, sa, b, sb, sp, None, False, "f32")
+    check(A, a, sa, b, sb, sp, rows, True, "bf16")
+
+
 @pytest.mark.parametrize("M", [1, 6, 200, 700])
 @pytest.mark.parametrize("av,bv", [(127, 127), (-128, -128), (-128, 127), (101, 127)])
 def test_extreme_sums_are_exact(A, M, av, bv):

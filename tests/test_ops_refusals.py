@@ -100,10 +100,11 @@ def test_matmul_int8(A):
     for kw in (dict(M=-1), dict(Ma=-1), dict(K=0), dict(N=0), dict(E=0), dict(swiglu=2), dict(swiglu=1, N=33),
                dict(out_dtype=3), dict(off=None), dict(Ma=7), dict(Ma=0, rows=P), dict(a=None), dict(sa=None),
                dict(b=None), dict(sb=None), dict(out=None), dict(st=48), dict(st=72), dict(a=P + 8), dict(b=P + 8),
-               dict(out=P + 8), dict(off=P + 2), dict(rows=P + 1), dict(ws=P + 16)):
+               dict(out=P + 8), dict(off=P + 2), dict(rows=P + 1), dict(ws=P + 16), dict(ws=None)):
         assert call(**kw) == A.MOE_ERR_INVALID_ARG, kw
     for kw in (dict(K=72, st=80), dict(E=257), dict(K=1 << 18, st=1 << 18)):
         assert call(**kw) == A.MOE_ERR_UNSUPPORTED, kw
+    assert call(n=256) == A.MOE_ERR_WORKSPACE
     assert call(M=0, a=None, out=None) == A.MOE_OK
     n = ctypes.c_size_t()
     assert L.moe_matmul_int8_workspace_size(ctypes.byref(A.Int8Config(**{**base, "K": 40})), ctypes.byref(n)) == \
