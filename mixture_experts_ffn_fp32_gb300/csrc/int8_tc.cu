@@ -186,23 +186,59 @@ MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "m
 // tc_ld_32x32b_x16 into 16 registers of a larger array.
 MOE_DEV void tc_ld_16(uint32_t taddr, uint32_t* r) { tc_ld_32x32b_x16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r)); }
 
-// Pair MMA with A in tensor memory (each CTA its own 128 rows), FP16 operands.
-MOE_DEV void tc_mma_f16_pair_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                uint32_t accumulate) {
+// The issuing warp stays whole: every lane runs its loop, so that descriptors
+// and addresses are warp-uniform, and the tensor instructions are predicated
+// on the elected lane. (One lane in a branch of its own took 140 cycles an
+// MMA, whatever its size, moving the operands to uniform registers.)
+MOE_DEV uint32_t elect_one() {
+    uint32_t e;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(e));
+    return e;
 }
-MOE_DEV void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+
+// MMA with A in tensor memory (of a pair: each CTA its own 128 rows), FP16
+// operands, by the elected lane.
+template <bool PAIR>
+MOE_DEV void tc_mma_f16_ta(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                           uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 e, %5, 0;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 e, %5, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+            : "memory");
+}
+// Arrive on `bar` (of a pair: in both CTAs) once the elected lane's MMAs are done.
+template <bool PAIR>
+MOE_DEV void tc_commit_elected(uint32_t elected, uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred e;\n\t"
+            "setp.ne.b32 e, %2, 0;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3)), "r"(elected)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e;\n\t"
+            "setp.ne.b32 e, %1, 0;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
+            "r"(elected)
+            : "memory");
 }
 // FP32 accumulator, FP16 A and B (K-major), M = 128 per CTA; N is added per tile.
 constexpr uint32_t idesc0(int ctas) { return (1u << 4) | (static_cast<uint32_t>(ctas * CH >> 4) << 24); }
@@ -421,53 +457,60 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             }
             for (int s = 0; s < WSTAGES; ++s)
                 if ((issued >> s) & 1u) bounded_drain(wfull(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            // ---------------- MMA issuer (even CTA) ----------------
+        } else if (warp == 1 && rank == 0) {
+            // ---------------- MMA issuer (one warp; even CTA of a pair) ----------------
+            const uint32_t elected = elect_one();
+            const uint32_t d_tmem = __shfl_sync(0xffffffffu, tmem, 0);
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, bounded_wait(bar, parity, wc, PAIR)) != 0;
+            };
             const uint64_t bdesc0 = smem_desc_sw128(sbase, 16, 1024);
             for (int u = unit0; u < total && ok; u += ustep) {
                 const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
                 const uint32_t idesc = idesc0(G::CTAS) | (static_cast<uint32_t>(((t.n + 15) & ~15) >> 3) << 17);
                 for (int c = 0; c < nchunks && ok; ++c) {
-                    if (!bounded_wait(acc_empty, acc_phase ^ 1u, wc, PAIR)) {
+                    if (!wait(acc_empty, acc_phase ^ 1u)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const int kb1 = min((c + 1) * cblocks, kblocks);
                     for (int kb = c * cblocks; kb < kb1; ++kb) {
-                        if (!bounded_wait(tfull(stage), phase, wc, PAIR) || !bounded_wait(aready(stage), phase, wc, PAIR)) {
+                        if (!wait(tfull(stage), phase) || !wait(aready(stage), phase)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint64_t bs = bdesc0 + (static_cast<uint64_t>(stage * T_BYTES) >> 4);
-                        const uint32_t at = tmem + G::A_COL + static_cast<uint32_t>(stage * 64);
+                        const uint32_t at = d_tmem + G::A_COL + static_cast<uint32_t>(stage * 64);
+                        const uint32_t first = kb == c * cblocks ? 0u : 1u;
                         const int steps = min(BK, p.K - kb * BK) / 16;
-                        for (int ks = 0; ks < steps; ++ks) {
-                            const uint64_t bd = bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16;
-                            const uint32_t add = (kb != c * cblocks || ks != 0) ? 1u : 0u;
-                            if (PAIR) tc_mma_f16_pair_ta(tmem, at + ks * 8, bd, idesc, add);
-                            else tc_mma_f16_ta(tmem, at + ks * 8, bd, idesc, add);
-                        }
-                        if (PAIR) tc_commit_pair_mc(empty(stage), 3);
-                        else tc_commit(empty(stage));
+#pragma unroll
+                        for (int ks = 0; ks < BK / 16; ++ks)
+                            if (ks < steps)
+                                tc_mma_f16_ta<PAIR>(elected, d_tmem, at + ks * 8,
+                                                    bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16, idesc, ks ? 1u : first);
+                        tc_commit_elected<PAIR>(elected, empty(stage));
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (!ok) break;
-                    if (PAIR) tc_commit_pair_mc(acc_full, 3);
-                    else tc_commit(acc_full);
+                    tc_commit_elected<PAIR>(elected, acc_full);
                     acc_phase ^= 1u;
                 }
             }
-            if (PAIR) tc_commit_pair(drain_bar);
-            else tc_commit(drain_bar);
-            bounded_drain(drain_bar, 0, p.timeout_ns, p.err);
+            // the MMAs in flight are done before the CTA leaves
+            __syncwarp();
+            if (elected) {
+                if (PAIR) tc_commit_pair(drain_bar);
+                else tc_commit(drain_bar);
+                bounded_drain(drain_bar, 0, p.timeout_ns, p.err);
+            }
         }
     } else if (warp < 4 + CONV_WARPS || (G::TEAMS == 2 && warp >= 12)) {
         // ---------------- weights: 8 bits in shared memory to FP16 in tensor memory ----------------
