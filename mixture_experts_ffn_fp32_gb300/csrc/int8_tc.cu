@@ -68,7 +68,7 @@ struct Form {
     static constexpr int REGS_COPY = 64, REGS_CONV = 80, REGS_EPI = 184;
     static constexpr int REGS_SUM = REGS_COPY + REGS_CONV + 2 * REGS_EPI;
     static constexpr int W_OFF = STAGES * T_BYTES;
-    static constexpr int NBARS = 3 * STAGES + 2 * WSTAGES + 3;
+    static constexpr int NBARS = 2 * STAGES + 2 * WSTAGES + 3;
     static constexpr int BAR_OFF = W_OFF + WSTAGES * W_BYTES;
     static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
     static constexpr int TAB_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
@@ -200,6 +200,33 @@ MOE_DEV uint32_t elect_one() {
     return e;
 }
 
+// Whether the phase of `bar` with parity `parity` is complete, without waiting.
+template <bool CLUSTER>
+MOE_DEV bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    return ok != 0;
+}
+// bounded_wait by every lane of a warp, with one outcome.
+MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, bool cluster = false) {
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, w, cluster)) != 0;
+}
+
 // MMA with A in tensor memory (of a pair: each CTA its own 128 rows), FP16
 // operands, by the elected lane.
 template <bool PAIR>
@@ -298,12 +325,12 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + G::BAR_OFF;
-    auto tfull = [&](int s) { return bar0 + 8u * s; };                  // even CTA: both CTAs' tokens landed
-    auto aready = [&](int s) { return bar0 + 8u * (STAGES + s); };      // even CTA: both CTAs' weights widened
-    auto empty = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };   // tokens and columns read by the MMAs
-    auto wfull = [&](int s) { return bar0 + 8u * (3 * STAGES + s); };   // own weights landed
-    auto wempty = [&](int s) { return bar0 + 8u * (3 * STAGES + WSTAGES + s); };  // and widened
-    const uint32_t acc_full = bar0 + 8u * (3 * STAGES + 2 * WSTAGES), acc_empty = acc_full + 8u, drain_bar = acc_full + 16u;
+    // ready (even CTA): both CTAs' tokens landed and their weights are widened
+    auto ready = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };       // tokens and columns read by the MMAs
+    auto wfull = [&](int s) { return bar0 + 8u * (2 * STAGES + s); };   // own weights landed
+    auto wempty = [&](int s) { return bar0 + 8u * (2 * STAGES + WSTAGES + s); };  // and widened
+    const uint32_t acc_full = bar0 + 8u * (2 * STAGES + 2 * WSTAGES), acc_empty = acc_full + 8u, drain_bar = acc_full + 16u;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + G::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::MISC_OFF + 4);
     int* s_tp = reinterpret_cast<int*>(smem + G::TAB_OFF);
@@ -317,8 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(tfull(s), 1);
-            mbar_init(aready(s), G::CTAS * CONV_WARPS);
+            mbar_init(ready(s), 1 + G::CTAS * CONV_WARPS);
             mbar_init(empty(s), 1);
         }
         for (int s = 0; s < WSTAGES; ++s) {
@@ -407,14 +433,14 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                         break;
                     }
                     const uint32_t sT = sbase + stage * T_BYTES;
-                    if (rank == 0) mbar_expect_tx(tfull(stage), G::CTAS * T_BYTES);
+                    if (rank == 0) mbar_expect_tx(ready(stage), G::CTAS * T_BYTES);
                     if (PAIR) {
-                        const uint32_t tb = map_shared_rank(tfull(stage), 0);
+                        const uint32_t tb = map_shared_rank(ready(stage), 0);
                         tma_load_2d_pair(sT, &p.mapT, kb * BK, trow, tb);
                         tma_load_2d_pair(sT + T_HALF, &p.mapT, kb * BK + 64, trow, tb);
                     } else {
-                        tma_load_2d(sT, &p.mapT, kb * BK, trow, tfull(stage));
-                        tma_load_2d(sT + T_HALF, &p.mapT, kb * BK + 64, trow, tfull(stage));
+                        tma_load_2d(sT, &p.mapT, kb * BK, trow, ready(stage));
+                        tma_load_2d(sT + T_HALF, &p.mapT, kb * BK + 64, trow, ready(stage));
                     }
                     issued |= 1u << stage;
                     last_par = (last_par & ~(1u << stage)) | (phase << stage);
@@ -428,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             // barrier, or consumed by the MMAs
             for (int s = 0; s < STAGES; ++s)
                 if ((issued >> s) & 1u)
-                    bounded_drain(rank == 0 ? tfull(s) : empty(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
+                    bounded_drain(rank == 0 ? ready(s) : empty(s), (last_par >> s) & 1u, p.timeout_ns, p.err);
         } else if (warp == 2 && lane == 0) {
             // ---------------- weights (both CTAs, each its own channels) ----------------
             int stage = 0;
@@ -464,26 +490,27 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, bounded_wait(bar, parity, wc, PAIR)) != 0;
-            };
+            bool peek = false;  // the stage was seen ready while the one before it was issued
             const uint64_t bdesc0 = smem_desc_sw128(sbase, 16, 1024);
             for (int u = unit0; u < total && ok; u += ustep) {
                 const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
                 const uint32_t idesc = idesc0(G::CTAS) | (static_cast<uint32_t>(((t.n + 15) & ~15) >> 3) << 17);
                 for (int c = 0; c < nchunks && ok; ++c) {
-                    if (!wait(acc_empty, acc_phase ^ 1u)) {
+                    if (!warp_wait(acc_empty, acc_phase ^ 1u, wc, PAIR)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const int kb1 = min((c + 1) * cblocks, kblocks);
                     for (int kb = c * cblocks; kb < kb1; ++kb) {
-                        if (!wait(tfull(stage), phase) || !wait(aready(stage), phase)) {
+                        if (!__all_sync(0xffffffffu, peek) && !warp_wait(ready(stage), phase, wc, PAIR)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
+                        const int next = stage + 1 == STAGES ? 0 : stage + 1;
+                        const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+                        peek = mbar_test<PAIR>(ready(next), next_phase);
                         const uint64_t bs = bdesc0 + (static_cast<uint64_t>(stage * T_BYTES) >> 4);
                         const uint32_t at = d_tmem + G::A_COL + static_cast<uint32_t>(stage * 64);
                         const uint32_t first = kb == c * cblocks ? 0u : 1u;
@@ -494,10 +521,8 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                                 tc_mma_f16_ta<PAIR>(elected, d_tmem, at + ks * 8,
                                                     bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16, idesc, ks ? 1u : first);
                         tc_commit_elected<PAIR>(elected, empty(stage));
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                        stage = next;
+                        phase = next_phase;
                     }
                     if (!ok) break;
                     tc_commit_elected<PAIR>(elected, acc_full);
@@ -527,14 +552,12 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
         for (int u = unit0; u < total && ok; u += ustep) {
             for (int kb = 0; kb < kblocks; ++kb) {
                 if (G::TEAMS == 2 && (turn++ & 1) != team) continue;
-                int w = 1;
-                // the weights are there, and the MMAs have read the columns' last content
-                if (lane == 0) w = bounded_wait(wfull(ws), wphase, wc) && bounded_wait(empty(stage), phase ^ 1u, wc) ? 1 : 0;
-                if (!__shfl_sync(0xffffffffu, w, 0)) {
+                // the weights are there ...
+                if (!warp_wait(wfull(ws), wphase, wc)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
+                bool free = mbar_test<false>(empty(stage), phase ^ 1u);
                 const uint8_t* wr = smem + G::W_OFF + ws * W_BYTES + row * BK;
                 const uint32_t at = tmem + G::A_COL + static_cast<uint32_t>(stage * 64) + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
@@ -549,15 +572,23 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                         widen4(v.z, r[8 * c + 4], r[8 * c + 5]);
                         widen4(v.w, r[8 * c + 6], r[8 * c + 7]);
                     }
+                    if (h == 0) {  // ... and the MMAs have read the columns' last content
+                        if (!__all_sync(0xffffffffu, free)) free = warp_wait(empty(stage), phase ^ 1u, wc);
+                        tc_fence_after();
+                    }
                     tc_st_32x32b_x32(at + 32 * h, r);
+                }
+                if (!free) {
+                    ok = false;
+                    break;
                 }
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(wempty(ws));
-                    if (rank == 0) mbar_arrive(aready(stage));
-                    else mbar_arrive_peer(map_shared_rank(aready(stage), 0));
+                    if (rank == 0) mbar_arrive(ready(stage));
+                    else mbar_arrive_peer(map_shared_rank(ready(stage), 0));
                 }
                 ws += G::TEAMS;
                 if (ws >= WSTAGES) {
@@ -585,9 +616,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             // one chunk: the FP32 accumulator as it is; several: their integer sum
             uint32_t acc[TOK];
             for (int c = 0; c < nchunks; ++c) {
-                int w = 1;
-                if (lane == 0) w = bounded_wait(acc_full, phase, wc) ? 1 : 0;
-                if (!__shfl_sync(0xffffffffu, w, 0)) {
+                if (!warp_wait(acc_full, phase, wc)) {
                     ok = false;
                     break;
                 }
