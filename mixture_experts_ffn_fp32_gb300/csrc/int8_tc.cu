@@ -666,22 +666,34 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                 sa[j] = ti < t.n ? p.sa[t.row0 + ti] : 0.0f;
             }
             O* orow = static_cast<O*>(p.out) + static_cast<long long>(t.row0 + c0) * p.F + oc;
+            const int upper = lane >> 4;
+            // eight tokens at a time, so that their chains overlap
 #pragma unroll
-            for (int i = 0; i < TOK; i += 2) {
-                if (c0 + i < t.n) {
-                    const float s0 = __shfl_sync(0xffffffffu, sa[i >> 5], i & 31);
-                    const float s1 = __shfl_sync(0xffffffffu, sa[i >> 5], (i & 31) + 1);
-                    const float v0 = __uint_as_float(acc[i]) * s0 * sb, v1 = __uint_as_float(acc[i + 1]) * s1 * sb;
-                    if (SWIGLU) {
-                        // lanes 0-15 finish token i, lanes 16-31 token i + 1
-                        const bool lower = lane < 16;
-                        const float other = __shfl_xor_sync(0xffffffffu, lower ? v1 : v0, 16);
-                        const float g = lower ? v0 : other, up = lower ? other : v1;
-                        const int ti = i + (lower ? 0 : 1);
-                        if (in && c0 + ti < t.n) orow[static_cast<long long>(ti) * p.F] = from_f32<O>(g * epi_sigmoid<O>(g) * up);
-                    } else if (in) {
-                        orow[static_cast<long long>(i) * p.F] = from_f32<O>(v0);
-                        if (c0 + i + 1 < t.n) orow[static_cast<long long>(i + 1) * p.F] = from_f32<O>(v1);
+            for (int i = 0; i < TOK; i += 8) {
+                if (c0 + i >= t.n) break;
+                if constexpr (SWIGLU) {
+                    // lanes 0-15 hold gates and finish the even tokens, lanes 16-31 ups and the odd
+                    float g[4], up[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float a = __uint_as_float(acc[i + 2 * k]) * sb, b = __uint_as_float(acc[i + 2 * k + 1]) * sb;
+                        const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+                        const float st = __shfl_sync(0xffffffffu, sa[i >> 5], ((i + 2 * k) & 31) + upper);
+                        g[k] = (upper ? other : a) * st;
+                        up[k] = (upper ? b : other) * st;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int ti = i + 2 * k + upper;
+                        const O h = from_f32<O>(g[k] * epi_sigmoid<O>(g[k]) * up[k]);
+                        if (in && c0 + ti < t.n) orow[static_cast<long long>(ti) * p.F] = h;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float st = __shfl_sync(0xffffffffu, sa[i >> 5], (i + k) & 31);
+                        const O h = from_f32<O>(__uint_as_float(acc[i + k]) * sb * st);
+                        if (in && c0 + i + k < t.n) orow[static_cast<long long>(i + k) * p.F] = h;
                     }
                 }
             }
