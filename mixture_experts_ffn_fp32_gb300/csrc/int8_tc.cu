@@ -486,23 +486,26 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
         } else if (warp == 1 && rank == 0) {
             // ---------------- MMA issuer (one warp; even CTA of a pair) ----------------
             const uint32_t elected = elect_one();
-            const uint32_t d_tmem = __shfl_sync(0xffffffffu, tmem, 0);
+            // warp reductions put what came from memory into uniform registers
+            const uint32_t d_tmem = __reduce_max_sync(0xffffffffu, tmem);
+            const int units = __reduce_max_sync(0xffffffffu, total);
+            const int nch = __reduce_max_sync(0xffffffffu, nchunks), cbl = __reduce_max_sync(0xffffffffu, cblocks);
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             bool peek = false;  // the stage was seen ready while the one before it was issued
             const uint64_t bdesc0 = smem_desc_sw128(sbase, 16, 1024);
-            for (int u = unit0; u < total && ok; u += ustep) {
-                const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
-                const uint32_t idesc = idesc0(G::CTAS) | (static_cast<uint32_t>(((t.n + 15) & ~15) >> 3) << 17);
-                for (int c = 0; c < nchunks && ok; ++c) {
+            for (int u = unit0; u < units && ok; u += ustep) {
+                const int n = __reduce_max_sync(0xffffffffu, (tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off)).n);
+                const uint32_t idesc = idesc0(G::CTAS) | (static_cast<uint32_t>(((n + 15) & ~15) >> 3) << 17);
+                for (int c = 0; c < nch && ok; ++c) {
                     if (!warp_wait(acc_empty, acc_phase ^ 1u, wc, PAIR)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const int kb1 = min((c + 1) * cblocks, kblocks);
-                    for (int kb = c * cblocks; kb < kb1; ++kb) {
+                    const int kb1 = min((c + 1) * cbl, kblocks);
+                    for (int kb = c * cbl; kb < kb1; ++kb) {
                         if (!__all_sync(0xffffffffu, peek) && !warp_wait(ready(stage), phase, wc, PAIR)) {
                             ok = false;
                             break;
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                         peek = mbar_test<PAIR>(ready(next), next_phase);
                         const uint64_t bs = bdesc0 + (static_cast<uint64_t>(stage * T_BYTES) >> 4);
                         const uint32_t at = d_tmem + G::A_COL + static_cast<uint32_t>(stage * 64);
-                        const uint32_t first = kb == c * cblocks ? 0u : 1u;
+                        const uint32_t first = kb == c * cbl ? 0u : 1u;
                         const int steps = min(BK, p.K - kb * BK) / 16;
 #pragma unroll
                         for (int ks = 0; ks < BK / 16; ++ks)
