@@ -187,9 +187,9 @@ MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "m
 MOE_DEV void tc_ld_16(uint32_t taddr, uint32_t* r) { tc_ld_32x32b_x16(taddr, *reinterpret_cast<uint32_t(*)[16]>(r)); }
 
 // The issuing warp stays whole: every lane runs its loop, so that descriptors
-// and addresses are warp-uniform, and the tensor instructions are predicated
-// on the elected lane. (One lane in a branch of its own took 140 cycles an
-// MMA, whatever its size, moving the operands to uniform registers.)
+// and addresses are warp-uniform, and only the tensor instructions are the
+// elected lane's. (A loop of one lane took 140 cycles an MMA, whatever its
+// size, moving the operands to uniform registers.)
 MOE_DEV uint32_t elect_one() {
     uint32_t e;
     asm volatile(
@@ -228,44 +228,29 @@ MOE_DEV bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, bool clu
 }
 
 // MMA with A in tensor memory (of a pair: each CTA its own 128 rows), FP16
-// operands, by the elected lane.
+// operands.
 template <bool PAIR>
-MOE_DEV void tc_mma_f16_ta(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                           uint32_t accumulate) {
+MOE_DEV void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     if constexpr (PAIR)
         asm volatile(
-            "{\n\t.reg .pred p, e;\n\t"
+            "{\n\t.reg .pred p;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "setp.ne.b32 e, %5, 0;\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p, e;\n\t"
+            "{\n\t.reg .pred p;\n\t"
             "setp.ne.b32 p, %4, 0;\n\t"
-            "setp.ne.b32 e, %5, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+            "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
             : "memory");
 }
-// Arrive on `bar` (of a pair: in both CTAs) once the elected lane's MMAs are done.
+// Arrive on `bar` (of a pair: in both CTAs) once this thread's MMAs are done.
 template <bool PAIR>
-MOE_DEV void tc_commit_elected(uint32_t elected, uint32_t bar) {
-    if constexpr (PAIR)
-        asm volatile(
-            "{\n\t.reg .pred e;\n\t"
-            "setp.ne.b32 e, %2, 0;\n\t"
-            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
-            "h"(static_cast<uint16_t>(3)), "r"(elected)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred e;\n\t"
-            "setp.ne.b32 e, %1, 0;\n\t"
-            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
-            "r"(elected)
-            : "memory");
+MOE_DEV void tc_commit_to(uint32_t bar) {
+    if constexpr (PAIR) tc_commit_pair_mc(bar, 3);
+    else tc_commit(bar);
 }
 // FP32 accumulator, FP16 A and B (K-major), M = 128 per CTA; N is added per tile.
 constexpr uint32_t idesc0(int ctas) { return (1u << 4) | (static_cast<uint32_t>(ctas * CH >> 4) << 24); }
@@ -518,17 +503,21 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                         const uint32_t at = d_tmem + G::A_COL + static_cast<uint32_t>(stage * 64);
                         const uint32_t first = kb == c * cbl ? 0u : 1u;
                         const int steps = min(BK, p.K - kb * BK) / 16;
+                        if (elected) {
 #pragma unroll
-                        for (int ks = 0; ks < BK / 16; ++ks)
-                            if (ks < steps)
-                                tc_mma_f16_ta<PAIR>(elected, d_tmem, at + ks * 8,
-                                                    bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16, idesc, ks ? 1u : first);
-                        tc_commit_elected<PAIR>(elected, empty(stage));
+                            for (int ks = 0; ks < BK / 16; ++ks)
+                                if (ks < steps)
+                                    tc_mma_f16_ta<PAIR>(d_tmem, at + ks * 8, bs + ((ks >> 2) * T_HALF + (ks & 3) * 32) / 16,
+                                                        idesc, ks ? 1u : first);
+                            tc_commit_to<PAIR>(empty(stage));
+                        }
+                        __syncwarp();
                         stage = next;
                         phase = next_phase;
                     }
                     if (!ok) break;
-                    tc_commit_elected<PAIR>(elected, acc_full);
+                    if (elected) tc_commit_to<PAIR>(acc_full);
+                    __syncwarp();
                     acc_phase ^= 1u;
                 }
             }
