@@ -165,10 +165,16 @@ moe_status check_int8(const moe_int8_config& c) {
     return MOE_OK;
 }
 
-// Few rows per expert run on the integer dot product, which reads the weights
-// straight into registers; the tensor-core forms pay their tile of 256
-// channels and their tokens' pass whatever the rows. MOE_INT8_FORM overrides
-// the choice for tests and tuning.
+// The form of a product, from sizes alone. MOE_INT8_FORM overrides the choice
+// for tests and tuning.
+//   Integer dot products while the whole product is small: they have no tokens'
+//   pass and spread over channels (us, dot products against tiles of 32: one row,
+//   4096 x 2048, 8 : 25; 8 rows, 4096 x 4096, 14 : 29; 32 rows of 8 experts,
+//   2048 x 2048, 23 : 23; 32 rows, 4096 x 4096, 33 : 29; 32 rows of 256 experts,
+//   4096 x 4096, 180 : 121).
+//   Tiles of 32 rows while they hold an expert's (against 256: 4 rows each of 256
+//   experts, 643 : 1040; 32 each of 8, 2048 x 2048, 27 : 25; 64 each, 33 : 27;
+//   128 rows of one, whose 32 channel tiles are more than the pairs' 16, 29 : 35).
 enum Int8Form { INT8_VEC, INT8_SMALL, INT8_WIDE };
 Int8Form int8_form(const moe_int8_config& c) {
     if (const char* e = getenv("MOE_INT8_FORM")) {
@@ -176,8 +182,8 @@ Int8Form int8_form(const moe_int8_config& c) {
         if (e[0] == 's') return INT8_SMALL;
         if (e[0] == 'w') return INT8_WIDE;
     }
-    if (c.M < 2LL * c.E) return INT8_VEC;
-    return c.M <= 32LL * c.E ? INT8_SMALL : INT8_WIDE;
+    if (static_cast<double>(c.M) * c.N * c.K <= 134217728.0) return INT8_VEC;
+    return c.M <= 32LL * c.E || c.M <= 128 ? INT8_SMALL : INT8_WIDE;
 }
 
 }  // namespace
