@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "internal.h"
 
 namespace moe {
 
@@ -178,5 +179,24 @@ struct RowFetch {
         r.get(f);
     }
 };
+
+// CTAs for `rows` rows, rpc of them at a time, at most per_sm on an SM.
+inline int grid_rows(long long rows, int rpc, int per_sm) {
+    const long long want = (rows + rpc - 1) / rpc, cap = static_cast<long long>(num_sms()) * per_sm;
+    return static_cast<int>(want < cap ? want : cap);
+}
+
+// Dynamic shared memory above the default limit has to be asked for, once per
+// kernel and device.
+template <typename K>
+inline bool allow_smem(K kernel, int bytes, bool (&done)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (!done[dev]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+        done[dev] = true;
+    }
+    return true;
+}
 
 }  // namespace moe

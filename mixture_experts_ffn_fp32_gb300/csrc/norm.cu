@@ -450,24 +450,6 @@ bool vec_ok(const void* p, long long stride, int esz) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * esz) % 16 == 0;
 }
 
-int grid_rows(long long rows, int rpc, int per_sm) {
-    const long long want = (rows + rpc - 1) / rpc, cap = static_cast<long long>(num_sms()) * per_sm;
-    return static_cast<int>(want < cap ? want : cap);
-}
-
-// Dynamic shared memory above the default limit has to be asked for, once per
-// kernel and device.
-template <typename K>
-bool allow_smem(K kernel, int bytes, bool (&done)[64]) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    if (!done[dev]) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-        done[dev] = true;
-    }
-    return true;
-}
-
 template <typename T, int VEC, int NV, int TPR>
 cudaError_t fwd_t(const LayerNormArgs& a, cudaStream_t s) {
     using C = Forward<T, VEC, NV, TPR>;

@@ -5,7 +5,8 @@
 // scale NaN, which every product of the row then shows.
 //
 // Memory bound: x is read once into registers, by a warp for short rows and by
-// a CTA else, and q written once.
+// a CTA else, while the CTA's next rows travel into shared memory, and q is
+// written once.
 #include <math_constants.h>
 
 #include "elem.cuh"
@@ -15,6 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int REG_MAX_K = 16384;  // 1024 threads x 16 elements
+constexpr int DEPTH = 2;          // rows that travel ahead
 
 template <int TPR>
 MOE_DEV unsigned row_umax(unsigned v, unsigned* scratch, int& turn) {
@@ -68,8 +70,37 @@ struct RowScale {
     }
 };
 
+// VEC quotients as bytes. Adding 1.5 2^23 leaves the rounded integer in a
+// float's low bits; what lies within 1e-4 of a half step, or has no FP32
+// quotient, is decided one by one.
+template <int VEC>
+MOE_DEV void quantize_vec(const RowScale& rs, const float (&v)[VEC], uint32_t (&b)[VEC]) {
+    constexpr float MAGIC = 12582912.0f;
+    bool edge = rs.mode != 1;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        const float t = v[j] * rs.inv, y = __fadd_rn(t, MAGIC), q = __fadd_rn(y, -MAGIC);
+        edge = edge || fabsf(t - q) > 0.4999f;
+        b[j] = __float_as_uint(y);
+    }
+    if (edge) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) b[j] = static_cast<uint32_t>(rs.quantize(v[j]));
+    }
+}
+MOE_DEV uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
 template <typename T, int VEC, int NV, int TPR>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR)
+struct Quant {
+    static constexpr int THREADS = TPR == 32 ? 128 : TPR;
+    static constexpr int PER_SM = TPR == 1024 ? 1 : (VEC == 1 || NV * VEC > 16 ? 768 : 1024) / THREADS;
+    using Fetch = RowFetch<T, VEC, NV, TPR, THREADS, DEPTH>;
+};
+
+template <typename T, int VEC, int NV, int TPR>
+__global__ void __launch_bounds__(Quant<T, VEC, NV, TPR>::THREADS, Quant<T, VEC, NV, TPR>::PER_SM)
 quantize_rows_kernel(int R, int K, const T* __restrict__ x, long long xs, int8_t* __restrict__ q,
                      float* __restrict__ scale) {
     constexpr int RPC = TPR == 32 ? 4 : 1;
@@ -80,43 +111,44 @@ quantize_rows_kernel(int R, int K, const T* __restrict__ x, long long xs, int8_t
     int turn = 0;
     pdl_wait();
     pdl_trigger();
-    Raw<T, VEC> cur[NV];
-    auto fetch = [&](long long r) {
+    using F = typename Quant<T, VEC, NV, TPR>::Fetch;
+    constexpr int D = F::D;
+    extern __shared__ __align__(16) uint8_t smem[];
+    F in;
+    in.init(smem, x, xs, K, t);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + t) * VEC;
-            if (r < R && c < K)
-                cur[i].load(x + r * xs + c);
-            else
-                cur[i].clear();
-        }
-    };
-    fetch(row);
+    for (int s = 0; s < D; ++s) {
+        in.issue(s, row + s * step, row + s * step < R);
+        if constexpr (F::ASYNC) cp_async_commit();
+    }
+    int slot = 0;
     for (; row < R; row += step) {
         float v[NV][VEC];
         unsigned m = 0;
+        if constexpr (F::ASYNC) cp_async_wait<D - 1>();
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            cur[i].get(v[i]);
+            in.get(slot, i, v[i]);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) m = max(m, abs_bits(v[i][j]));
         }
-        fetch(row + step);
+        in.issue(slot, row + D * step, row + D * step < R);
+        if constexpr (F::ASYNC) cp_async_commit();
+        if (++slot == D) slot = 0;
         const RowScale rs(row_umax<TPR>(m, scratch, turn));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VEC;
             if (c < K) {
-                alignas(8) int8_t o[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) o[j] = static_cast<int8_t>(rs.quantize(v[i][j]));
+                uint32_t b[VEC];
+                quantize_vec<VEC>(rs, v[i], b);
                 int8_t* at = q + row * K + c;
                 if constexpr (VEC == 8)
-                    *reinterpret_cast<uint2*>(at) = *reinterpret_cast<const uint2*>(o);
+                    *reinterpret_cast<uint2*>(at) = make_uint2(pack4(b[0], b[1], b[2], b[3]), pack4(b[4], b[5], b[6], b[7]));
                 else if constexpr (VEC == 4)
-                    *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(o);
+                    *reinterpret_cast<uint32_t*>(at) = pack4(b[0], b[1], b[2], b[3]);
                 else
-                    at[0] = o[0];
+                    at[0] = static_cast<int8_t>(b[0]);
             }
         }
         if (t == 0) scale[row] = rs.scale;
@@ -142,16 +174,13 @@ quantize_rows_long_kernel(int R, int K, const T* __restrict__ x, long long xs, i
     }
 }
 
-int grid_rows(long long rows, int rpc, int per_sm) {
-    const long long want = (rows + rpc - 1) / rpc, cap = static_cast<long long>(num_sms()) * per_sm;
-    return static_cast<int>(want < cap ? want : cap);
-}
-
 template <typename T, int VEC, int NV, int TPR>
 cudaError_t quant_t(const QuantArgs& a, cudaStream_t s) {
-    const int threads = TPR == 32 ? 128 : TPR;
-    return launch_pdl(quantize_rows_kernel<T, VEC, NV, TPR>, dim3(grid_rows(a.R, TPR == 32 ? 4 : 1, 2048 / threads)),
-                      dim3(threads), 0, s, a.R, a.K, static_cast<const T*>(a.x), a.x_stride, a.q, a.scale);
+    using C = Quant<T, VEC, NV, TPR>;
+    static bool done[64] = {};
+    if (!allow_smem(quantize_rows_kernel<T, VEC, NV, TPR>, C::Fetch::SMEM, done)) return cudaErrorInvalidValue;
+    return launch_pdl(quantize_rows_kernel<T, VEC, NV, TPR>, dim3(grid_rows(a.R, TPR == 32 ? 4 : 1, C::PER_SM)),
+                      dim3(C::THREADS), C::Fetch::SMEM, s, a.R, a.K, static_cast<const T*>(a.x), a.x_stride, a.q, a.scale);
 }
 
 template <typename T, int VEC>
