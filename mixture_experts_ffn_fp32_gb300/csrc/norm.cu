@@ -409,9 +409,9 @@ layer_norm_bwd_cols_kernel(int R, int d, const T* __restrict__ dy, long long dys
 }
 
 // dgamma, dbeta = the sums of the n partial rows [2, d], each column in a
-// fixed order: 16 threads take every sixteenth row, eight loads in flight,
-// then theirs are added in order.
-constexpr int COL_ROWS = 16;
+// fixed order: 32 threads take every 32nd row, ten loads in flight (the rows
+// of two CTAs an SM in one go), then theirs are added in order.
+constexpr int COL_ROWS = 32;
 __global__ void __launch_bounds__(32 * COL_ROWS)
 layer_norm_cols_sum_kernel(int n, int d, const float* __restrict__ part, float* __restrict__ dgamma,
                            float* __restrict__ dbeta) {
@@ -422,14 +422,14 @@ layer_norm_cols_sum_kernel(int n, int d, const float* __restrict__ part, float* 
     pdl_trigger();
     float a = 0.0f;
     if (c < 2 * d) {
-        for (int r0 = ry; r0 < n; r0 += 8 * COL_ROWS) {
-            float p[8];
+        for (int r0 = ry; r0 < n; r0 += 10 * COL_ROWS) {
+            float p[10];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 10; ++i) {
                 const int r = r0 + i * COL_ROWS;
                 p[i] = r < n ? part[static_cast<long long>(r) * 2 * d + c] : 0.0f;
             }
-            a += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+            a += (((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]))) + (p[8] + p[9]);
         }
     }
     s[ry][cx] = a;
