@@ -104,6 +104,38 @@ MOE_DEV void row_sum2(float& a, float& b, float* scratch, int& turn) {
     }
 }
 
+// Two FP32 values in a register pair; the packed operations do both at the
+// issue of one.
+struct F2 {
+    unsigned long long v;
+};
+MOE_DEV F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+MOE_DEV void unpack(F2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+MOE_DEV float both(F2 p) {
+    float a, b;
+    unpack(p, a, b);
+    return a + b;
+}
+MOE_DEV F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+MOE_DEV F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+MOE_DEV F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // VEC consecutive floats (16-byte aligned where VEC >= 4).
 template <int VEC>
 MOE_DEV void load_f32(const float* p, float (&f)[VEC]) {
@@ -165,6 +197,14 @@ struct RowFetch {
                 }
             }
         }
+    }
+    // Slot s as FP32 pairs, vectors one after the other (zeros past the row's end).
+    MOE_DEV void pairs(int s, F2 (&p)[NV * VEC / 2]) const {
+        float f[NV][VEC];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) get(s, i, f[i]);
+#pragma unroll
+        for (int k = 0; k < NV * VEC / 2; ++k) p[k] = f2(f[2 * k / VEC][2 * k % VEC], f[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
     }
     // Vector i of slot s as FP32 (zeros past the row's end).
     MOE_DEV void get(int s, int i, float (&f)[VEC]) const {

@@ -32,43 +32,41 @@ constexpr int BWD_DEPTH = 2;
 // 1 / sqrt(var + eps); a variance that rounding took below zero is zero, a NaN stays.
 MOE_DEV float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
-// Mean and variance of a row from its threads' NV x VEC values, left as
-// v - m0. A warp takes its own mean, and its sums of the differences and of
-// their squares; the CTA then joins the warps' numbers (m, r, q of n values)
+// Mean and variance of a row from its threads' NV x VEC values (in pairs), left
+// as v - m, m a mean the warp took of its own. Its sums of the differences and of
+// their squares follow, and the CTA joins the warps' numbers (m, r, q of n values)
 // behind one sync:
 //   m0 = sum n m / d,  rest = sum (n (m - m0) + r) / d
 //   var = sum (q + 2 (m - m0) r + n (m - m0)^2) / d - rest^2
-// `rest` is what rounding left in m0.
+// `rest` is what rounding left in m0; shift = m - (m0 + rest).
 template <int VEC, int NV, int TPR>
-MOE_DEV void row_moments(float (&v)[NV][VEC], int d, int t, float inv_d, float4* scratch, int& turn, float& m0,
-                         float& rest, float& var) {
-    constexpr int W = TPR / 32;
+MOE_DEV void row_moments(F2 (&v)[NV * VEC / 2], int d, int t, float inv_d, float4* scratch, int& turn, float& mean,
+                         float& shift, float& var) {
+    constexpr int W = TPR / 32, N2 = NV * VEC / 2;
     const int w = W == 1 ? 0 : static_cast<int>(threadIdx.x >> 5);
-    float s = 0.0f, n = 0.0f;  // n: the warp's values, cut at d
+    float n = 0.0f;  // the warp's values, cut at d
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        n += static_cast<float>(min(max(d - (i * TPR + w * 32) * VEC, 0), 32 * VEC));
+    for (int i = 0; i < NV; ++i) n += static_cast<float>(min(max(d - (i * TPR + w * 32) * VEC, 0), 32 * VEC));
+    F2 s2 = v[0];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s += v[i][j];
-    }
-    s = warp_sum(s);
+    for (int k = 1; k < N2; ++k) s2 = add2(s2, v[k]);
+    const float s = warp_sum(both(s2));
     const float m = W == 1 ? s * inv_d : (n > 0.0f ? s / n : 0.0f);
-    float r = 0.0f, q = 0.0f;
+    F2 r2 = f2(0.0f, 0.0f), q2 = r2;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool in = (i * TPR + t) * VEC < d;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            v[i][j] = in ? v[i][j] - m : 0.0f;
-            r += v[i][j];
-            q += v[i][j] * v[i][j];
-        }
+    for (int k = 0; k < N2; ++k) {
+        // zeros past the end stay zeros
+        const float ma = (2 * k / VEC * TPR + t) * VEC < d ? -m : 0.0f;
+        const float mb = VEC > 1 ? ma : ((2 * k + 1) * TPR + t < d ? -m : 0.0f);
+        v[k] = add2(v[k], f2(ma, mb));
+        r2 = add2(r2, v[k]);
+        q2 = fma2(v[k], v[k], q2);
     }
-    r = warp_sum(r);
-    q = warp_sum(q);
+    const float r = warp_sum(both(r2)), q = warp_sum(both(q2));
     if constexpr (W == 1) {
-        m0 = m;
-        rest = r * inv_d;
+        const float rest = r * inv_d;
+        mean = m + rest;
+        shift = -rest;
         var = q * inv_d - rest * rest;
     } else {
         float4* sc = scratch + (turn & 1) * W;  // two turns: see row_sum2
@@ -78,15 +76,12 @@ MOE_DEV void row_moments(float (&v)[NV][VEC], int d, int t, float inv_d, float4*
         const int l = static_cast<int>(lane_id());
         float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (l < W) e = sc[l];
-        m0 = group_sum<W>(e.w * e.x) * inv_d;
+        const float m0 = group_sum<W>(e.w * e.x) * inv_d;
         const float dm = e.x - m0;
-        rest = group_sum<W>(e.w * dm + e.y) * inv_d;
+        const float rest = group_sum<W>(e.w * dm + e.y) * inv_d;
         var = group_sum<W>(e.z + 2.0f * dm * e.y + e.w * dm * dm) * inv_d - rest * rest;
-        const float shift = m - m0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) v[i][j] += shift;
+        mean = m0 + rest;
+        shift = (m - m0) - rest;
     }
 }
 
@@ -125,49 +120,59 @@ layer_norm_kernel(int R, int d, const T* __restrict__ x, long long xs, const flo
         in.issue(s, row + s * step, row + s * step < R);
         if constexpr (F::ASYNC) cp_async_commit();
     }
-    float ga[KEEP ? NV : 1][VEC], be[KEEP ? NV : 1][VEC];
-    auto columns = [&](int i, float (&g)[VEC], float (&b)[VEC]) {
-        const int c = (i * TPR + t) * VEC;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            g[j] = 1.0f;
-            b[j] = 0.0f;
-        }
-        if (c < d && gamma != nullptr) load_f32<VEC>(gamma + c, g);
-        if (c < d && beta != nullptr) load_f32<VEC>(beta + c, b);
-    };
-    if constexpr (KEEP) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) columns(i, ga[i], be[i]);
-    }
-    int slot = 0;
-    for (; row < R; row += step) {
-        float v[NV][VEC];
-        if constexpr (F::ASYNC) cp_async_wait<D - 1>();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) in.get(slot, i, v[i]);
-        in.issue(slot, row + D * step, row + D * step < R);
-        if constexpr (F::ASYNC) cp_async_commit();
-        if (++slot == D) slot = 0;
-        float m0, rest, var;
-        row_moments<VEC, NV, TPR>(v, d, t, inv_d, scratch, turn, m0, rest, var);
-        const float rs = rstd_of(var, eps);
+    constexpr int N2 = NV * VEC / 2;
+    F2 ga[N2], be[N2];
+    auto columns = [&] {
+        float g[NV][VEC], b[NV][VEC];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VEC;
-            if (!KEEP) columns(i, ga[0], be[0]);
-            if (c < d) {
-                float o[VEC];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    o[j] = (v[i][j] - rest) * rs * ga[KEEP ? i : 0][j] + be[KEEP ? i : 0][j];
+            for (int j = 0; j < VEC; ++j) {
+                g[i][j] = 1.0f;
+                b[i][j] = 0.0f;
+            }
+            if (c < d && gamma != nullptr) load_f32<VEC>(gamma + c, g[i]);
+            if (c < d && beta != nullptr) load_f32<VEC>(beta + c, b[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < N2; ++k) {
+            constexpr int V = VEC;
+            ga[k] = f2(g[2 * k / V][2 * k % V], g[(2 * k + 1) / V][(2 * k + 1) % V]);
+            be[k] = f2(b[2 * k / V][2 * k % V], b[(2 * k + 1) / V][(2 * k + 1) % V]);
+        }
+    };
+    if constexpr (KEEP) columns();
+    int slot = 0;
+    for (; row < R; row += step) {
+        F2 v[N2];
+        if constexpr (F::ASYNC) cp_async_wait<D - 1>();
+        in.pairs(slot, v);
+        in.issue(slot, row + D * step, row + D * step < R);
+        if constexpr (F::ASYNC) cp_async_commit();
+        if (++slot == D) slot = 0;
+        float m, shift, var;
+        row_moments<VEC, NV, TPR>(v, d, t, inv_d, scratch, turn, m, shift, var);
+        const float rs = rstd_of(var, eps);
+        if constexpr (!KEEP) columns();
+        const F2 sh2 = f2(shift, shift), rs2 = f2(rs, rs);
+        float o[NV][VEC];
+#pragma unroll
+        for (int k = 0; k < N2; ++k) {
+            const F2 y2 = fma2(mul2(add2(v[k], sh2), rs2), ga[k], be[k]);
+            unpack(y2, o[2 * k / VEC][2 * k % VEC], o[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (c < d) {
                 Raw<T, VEC> out;
-                out.set(o);
+                out.set(o[i]);
                 out.store(y + row * ys + c);
             }
         }
         if (t == 0) {
-            if (mean != nullptr) mean[row] = m0 + rest;
+            if (mean != nullptr) mean[row] = m;
             if (rstd != nullptr) rstd[row] = rs;
         }
     }
@@ -240,9 +245,11 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
     long long row = static_cast<long long>(blockIdx.x) * RPC + (TPR == 32 ? threadIdx.x >> 5 : 0);
     const float inv_d = 1.0f / static_cast<float>(d);
     int turn = 0;
-    float dg[NV][VEC] = {}, db[NV][VEC] = {};
+    constexpr int N2 = NV * VEC / 2;
     constexpr bool KEEP = VEC > 1;  // gamma in registers
-    float ga[KEEP ? NV : 1][VEC];
+    F2 dg2[N2], db2[N2], ga[N2];
+#pragma unroll
+    for (int k = 0; k < N2; ++k) dg2[k] = db2[k] = f2(0.0f, 0.0f);
     pdl_wait();
     pdl_trigger();
     F fx, fy;
@@ -255,16 +262,19 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
     };
 #pragma unroll
     for (int s = 0; s < D; ++s) issue(s, row + s * step);
-    auto columns = [&](int i, float (&g)[VEC]) {
-        const int c = (i * TPR + t) * VEC;
+    auto columns = [&] {
+        float g[NV][VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) g[j] = 1.0f;
-        if (c < d && gamma != nullptr) load_f32<VEC>(gamma + c, g);
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) g[i][j] = 1.0f;
+            if (c < d && gamma != nullptr) load_f32<VEC>(gamma + c, g[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < N2; ++k) ga[k] = f2(g[2 * k / VEC][2 * k % VEC], g[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
     };
-    if constexpr (KEEP) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) columns(i, ga[i]);
-    }
+    if constexpr (KEEP) columns();
     float mu = 0.0f, rs = 0.0f;  // of the next row
     if (row < R) {
         mu = __ldg(mean + row);
@@ -272,51 +282,56 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
     }
     int slot = 0;
     for (; row < R; row += step) {
-        float xh[NV][VEC], g[NV][VEC];
-        float s1 = 0.0f, s2 = 0.0f;
+        F2 xh[N2], g[N2];
         const float mc = mu, rc = rs;
         if (row + step < R) {
             mu = __ldg(mean + row + step);
             rs = __ldg(rstd + row + step);
         }
         if constexpr (F::ASYNC) cp_async_wait<D - 1>();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            fx.get(slot, i, xh[i]);
-            fy.get(slot, i, g[i]);
-        }
+        fx.pairs(slot, xh);
+        fy.pairs(slot, g);
         issue(slot, row + D * step);
         if (++slot == D) slot = 0;
+        if constexpr (!KEEP) columns();
+        const F2 nm = f2(-mc, -mc), rc2 = f2(rc, rc);
+        F2 a1 = f2(0.0f, 0.0f), a2 = a1;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            // past the row's end dy is zero; x counts as the mean there
-            const bool in = (i * TPR + t) * VEC < d;
-            if (!KEEP) columns(i, ga[0]);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                xh[i][j] = in ? (xh[i][j] - mc) * rc : 0.0f;
-                dg[i][j] += g[i][j] * xh[i][j];
-                db[i][j] += g[i][j];
-                g[i][j] *= ga[KEEP ? i : 0][j];
-                s1 += g[i][j];
-                s2 += g[i][j] * xh[i][j];
-            }
+        for (int k = 0; k < N2; ++k) {
+            // past the row's end dy is zero, and with it every term
+            xh[k] = mul2(add2(xh[k], nm), rc2);
+            dg2[k] = fma2(g[k], xh[k], dg2[k]);
+            db2[k] = add2(db2[k], g[k]);
+            g[k] = mul2(g[k], ga[k]);
+            a1 = add2(a1, g[k]);
+            a2 = fma2(g[k], xh[k], a2);
         }
+        float s1 = both(a1), s2 = both(a2);
         row_sum2<TPR>(s1, s2, scratch, turn);
-        s1 *= inv_d;
-        s2 *= inv_d;
+        s1 *= -inv_d;
+        s2 *= -inv_d;
+        const F2 n1 = f2(s1, s1), n2 = f2(s2, s2);
+        float o[NV][VEC];
+#pragma unroll
+        for (int k = 0; k < N2; ++k) {
+            const F2 x2 = mul2(fma2(xh[k], n2, add2(g[k], n1)), rc2);
+            unpack(x2, o[2 * k / VEC][2 * k % VEC], o[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VEC;
             if (c < d) {
-                float o[VEC];
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) o[j] = rc * (g[i][j] - s1 - xh[i][j] * s2);
                 Raw<T, VEC> out;
-                out.set(o);
+                out.set(o[i]);
                 out.store(dx + row * dxs + c);
             }
         }
+    }
+    float dg[NV][VEC], db[NV][VEC];
+#pragma unroll
+    for (int k = 0; k < N2; ++k) {
+        unpack(dg2[k], dg[2 * k / VEC][2 * k % VEC], dg[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
+        unpack(db2[k], db[2 * k / VEC][2 * k % VEC], db[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
     }
     if (part == nullptr) return;
     float* pg = part + static_cast<long long>(blockIdx.x) * 2 * d;
