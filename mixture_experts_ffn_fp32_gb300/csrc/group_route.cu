@@ -219,45 +219,26 @@ __device__ __noinline__ void keep_any_groups(const Params* p, float* c, float* b
     }
 }
 
-// Leaves only the experts of the kept groups in c; lo, hi: the lowest kept and
-// the highest dropped score (-inf: none); mag: the largest |a| + |b| of a
-// group's two best.
+// The groups to keep, as a mask (p.lg); lo, hi: the lowest kept and the highest
+// dropped score (-inf: none); mag: the largest |a| + |b| of a group's two best;
+// mine: the score of the lane's group, a2 its second best.
 template <int VPL>
-MOE_DEV void keep_groups(const Params& p, int lane, float (&c)[VPL], float& lo, float& hi, float& mag) {
-    if (p.lg) {
-        float a1, a2;
-        group_best<float, VPL>(p, lane, c, -CUDART_INF_F, a1, a2);
-        const float g = (p.rank == 2 && a2 > -CUDART_INF_F) ? a1 + a2 : a1;
-        float mine = __shfl_sync(FULL, g, lane * p.lg & 31);
-        if (lane >= p.G) mine = -CUDART_INF_F;
-        const unsigned keep = kept_groups<float>(p, lane, mine);
-        const bool kept = (keep >> lane) & 1u;
-        lo = -warp_max(kept ? -mine : -CUDART_INF_F);
-        hi = warp_max(lane < p.G && !kept ? mine : -CUDART_INF_F);
-        mag = warp_max((a1 > -CUDART_INF_F ? fabsf(a1) : 0.0f) + (a2 > -CUDART_INF_F ? fabsf(a2) : 0.0f));
-        const int at = lane >> p.lsh;
-        if (at >= p.G || !((keep >> at) & 1u)) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) c[i] = -CUDART_INF_F;
-        }
-    } else {
-        float t[VPL], bounds[3];
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) t[i] = c[i];
-        keep_any_groups<VPL>(&p, t, bounds);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) c[i] = t[i];
-        lo = bounds[0];
-        hi = bounds[1];
-        mag = bounds[2];
-    }
+MOE_DEV unsigned choose_groups(const Params& p, int lane, const float (&c)[VPL], float& lo, float& hi, float& mag,
+                               float& mine, float& a2) {
+    float a1;
+    group_best<float, VPL>(p, lane, c, -CUDART_INF_F, a1, a2);
+    mine = (p.rank == 2 && a2 > -CUDART_INF_F) ? a1 + a2 : a1;
+    float of = __shfl_sync(FULL, mine, lane * p.lg & 31);  // of group `lane`
+    if (lane >= p.G) of = -CUDART_INF_F;
+    const unsigned keep = kept_groups<float>(p, lane, of);
+    const bool kept = (keep >> lane) & 1u;
+    lo = -warp_max(kept ? -of : -CUDART_INF_F);
+    hi = warp_max(lane < p.G && !kept ? of : -CUDART_INF_F);
+    mag = warp_max((a1 > -CUDART_INF_F ? fabsf(a1) : 0.0f) + (a2 > -CUDART_INF_F ? fabsf(a2) : 0.0f));
+    return keep;
 }
 
-// Integers that order as the floats do.
-MOE_DEV int order_key(float v) {
-    const int u = __float_as_int(v + 0.0f);  // -0 as +0
-    return u ^ ((u >> 31) & 0x7fffffff);
-}
+// Integers that order as the floats do, and back.
 MOE_DEV float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
 MOE_DEV long long order_key(double v) {
@@ -266,6 +247,20 @@ MOE_DEV long long order_key(double v) {
 }
 MOE_DEV double key_value(long long k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL)); }
 constexpr long long NONE64 = static_cast<long long>(0x8000000000000000ull);
+
+// Scores rise with their logits: without a bias the logits rank.
+template <int VPL>
+MOE_DEV void logits_rank(const float (&r)[VPL], float (&c)[VPL]) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = c[i] > -CUDART_INF_F ? r[i] : -CUDART_INF_F;
+}
+
+// How far apart two logits a >= b must be for FP64 to tell their scores apart
+// (infinite where it may not: sigmoids near 1, scores below its range).
+MOE_DEV float logit_slack(const Params& p, float m, float a, float b) {
+    if (p.softmax) return m - b < 690.0f ? 1e-11f : CUDART_INF_F;
+    return b > -690.0f && a < 80.0f ? 1e-11f + 4e-16f * __expf(a) : CUDART_INF_F;
+}
 
 // Sorts a lane's keys in descending order (Batcher's odd-even merge).
 MOE_DEV void order2(int& a, int& b) {
@@ -363,12 +358,71 @@ MOE_DEV void write_token(const Params& p, long long t, int lane, int id, float r
     }
 }
 
+// An exact score plus bias: what FP64 makes of a logit (a softmax's without its
+// denominator, which is common where there is no bias).
+__device__ __noinline__ double exact_choice(int softmax, float r, float m, float b) {
+    const double ex = exp(softmax ? static_cast<double>(r) - static_cast<double>(m) : -static_cast<double>(r));
+    return (softmax ? (r == m ? 1.0 : ex) : 1.0 / (1.0 + ex)) + static_cast<double>(b);
+}
+
+// The groups to keep where some scores lie within `tol` of the border: those
+// groups' best experts get FP64 scores, one a lane. False: a lane holds several
+// candidates for its group's best, or a softmax with a bias.
+template <int VPL>
+__device__ __noinline__ bool choose_groups_exact(const Params* pp, const float* r, const float* b, const float* c, float m,
+                                                 float mine, float a2, float lo, float hi, float tol, unsigned* keep) {
+    const Params& p = *pp;
+    if (p.softmax && p.bias != nullptr) return false;
+    const int lane = static_cast<int>(lane_id());
+    const bool near = mine > -CUDART_INF_F && mine >= lo - 2.0f * tol && mine <= hi + 2.0f * tol;
+    const bool pair = p.rank == 2 && a2 > -CUDART_INF_F;
+    const float edge = pair ? a2 : mine;
+    int n = 0;
+    float ri = 0.0f, bi = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+        if (near && c[i] > -CUDART_INF_F && c[i] >= edge - 2.0f * tol) {
+            ++n;
+            ri = r[i];
+            bi = p.bias != nullptr ? b[i] : 0.0f;
+        }
+    int all = n;
+    for (int o = 1; o < p.lg; o <<= 1) all += __shfl_xor_sync(FULL, all, o);
+    if (__any_sync(FULL, n > 1 || (near && all != (pair ? 2 : 1)))) return false;
+    double x = n ? exact_choice(p.softmax, ri, m, bi) : 0.0;
+    for (int o = 1; o < p.lg; o <<= 1) x += __shfl_xor_sync(FULL, x, o);
+    // the others lie clear on either side: kept above all, or behind all
+    const long long key = near ? order_key(x) : mine > hi ? 0x7fffffffffffffffLL : mine > -CUDART_INF_F ? NONE64 + 1 : NONE64;
+    long long of = __shfl_sync(FULL, key, lane * p.lg & 31);
+    if (lane >= p.G) of = NONE64;
+    *keep = kept_groups<long long>(p, lane, of);
+    return true;
+}
+
+// Puts the K + 1 first ranks (lanes 0 to K) in their exact order: some are close,
+// but none behind them is. One FP64 score a lane.
+__device__ __noinline__ void order_exact(const Params& p, int lane, float m, float b, int& id, float& rk) {
+    long long key = NONE64;
+    if (lane <= p.K && id >= 0) key = order_key(exact_choice(p.softmax, rk, m, b));
+    int rank = 0, src = lane;
+    for (int j = 0; j <= p.K; ++j) {
+        const long long o = __shfl_sync(FULL, key, j);
+        const int oid = __shfl_sync(FULL, id, j);
+        rank += (o > key || (o == key && oid < id)) ? 1 : 0;
+    }
+    if (key == NONE64) rank = lane;
+    for (int j = 0; j <= p.K; ++j)
+        if (__shfl_sync(FULL, rank, j) == lane) src = j;
+    id = __shfl_sync(FULL, id, src);
+    rk = __shfl_sync(FULL, rk, src);
+}
+
 // A token decided in FP64: the rare token whose FP32 choices lie within their
 // error. The choices are 64-bit integers in the doubles' order; those that a
 // decision could concern are replaced by exact ones before it is taken. Out of line, so that its registers are not the
 // common path's.
 template <int VPL, typename T, bool VEC>
-__device__ __noinline__ void route_exact(const Params* pp, long long t, const T* row, bool groups, int32_t* idx, float* w) {
+__device__ __noinline__ void route_exact(const Params* pp, long long t, const T* row, int32_t* idx, float* w) {
     const Params& p = *pp;
     const int lane = static_cast<int>(lane_id());
     float r[VPL], b[VPL], c[VPL], m, z, inv;
@@ -430,7 +484,7 @@ __device__ __noinline__ void route_exact(const Params* pp, long long t, const T*
             const float edge = p.rank == 2 && x2 > -CUDART_INF_F ? x2 : x1;
             if (c[i] > -CUDART_INF_F && !(c[i] < edge - slack(edge))) need |= 1u << i;
         }
-        if (groups) make_exact(need);  // else they are clear as they are
+        make_exact(need);
         long long a1, a2;
         group_best<long long, VPL>(p, lane, h, NONE64, a1, a2);
         long long g = p.rank == 2 && a2 != NONE64 ? order_key(key_value(a1) + key_value(a2)) : a1;
@@ -498,9 +552,10 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
     pdl_trigger();
     const int step = gridDim.x * WARPS;
     const int t0 = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    const bool by_logit = p.bias == nullptr;
     // 32 tokens of the warp at a time; the near ones of them follow, in FP64
     for (long long tb = t0; tb < p.T; tb += 32LL * step) {
-        unsigned again = 0, groups = 0;  // near tokens, and those near in their groups
+        unsigned again = 0;  // tokens that FP32 and the short resolutions left open
         float r[VPL], b[VPL];
         load_row<VPL, T, VEC>(logits + tb * p.stride, lane, p.E, r);
         lane_bias<VPL, VEC>(p, lane, b);
@@ -510,24 +565,57 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             const T* row = logits + t * p.stride;
             float c[VPL], m, z, inv;
             choices<VPL>(p, r, b, c, m, z, inv);
-            if (t + step < p.T) load_row<VPL, T, VEC>(row + step * p.stride, lane, p.E, r);
-            bool near = false, gnear = false;
-            // How near two FP32 choices may lie before FP64 decides: in units of 2^-23 and
-            // for both sides together, twice what they can be off by. A sigmoid is off by
-            // 4 + 1.2 |r| of itself (special functions, argument), which is at most 6 of the
-            // largest score; a softmax score by 4 + |r - m| / 2, the denominator apart, which
-            // all scores share. With a bias the bounds are absolute: the score's, the
-            // denominator's error (16) on the largest score, and half a unit of the choice.
-            const float sabs = p.softmax ? 0x1p-18f * inv : 0x1p-18f;
+            bool near = false, gnear = false, close = false;
+            // How near two FP32 choices may lie before FP64 decides, both sides' errors
+            // together and not quite twice what they can be. A sigmoid: 4.4 units of 2^-24
+            // (exponential 2^-22 of itself and 1.5 |r| 2^-24 of its argument, both times
+            // s (1 - s); sum, reciprocal); a softmax score: 22 + |r - m| units of itself,
+            // at most 23 of the largest; the bias's addition: one unit of the choice.
+            const float sabs = p.softmax ? 0x1p-18f * inv : 0x1p-20f;
+            const bool ranked = by_logit && (p.G == 1 || p.rank == 1);
+            if (ranked) logits_rank<VPL>(r, c);
             if (p.G > 1) {
-                float lo, hi, mag;
-                keep_groups<VPL>(p, lane, c, lo, hi, mag);
+                float lo, hi, mag, mine, a2;
+                unsigned keep = 0;
+                if (p.lg) {
+                    keep = choose_groups<VPL>(p, lane, c, lo, hi, mag, mine, a2);
+                } else {
+                    float tmp[VPL], bounds[3];
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) tmp[i] = c[i];
+                    keep_any_groups<VPL>(&p, tmp, bounds);
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) c[i] = tmp[i];
+                    lo = bounds[0];
+                    hi = bounds[1];
+                    mag = bounds[2];
+                }
                 if (hi > -CUDART_INF_F && p.TG < p.G) {
                     // without a bias a score names its logit: |r| and |r - m| are below 48 from 1e-20 on
-                    const float tol = p.bias != nullptr ? 2.0f * sabs + 0x1p-21f * mag : 0x1p-15f * lo;
-                    gnear = !(lo - hi > tol) || (p.bias == nullptr && lo < 1e-20f);
+                    const float tol = ranked ? (lo == hi ? 0.0f : logit_slack(p, m, lo, hi))
+                                      : p.bias != nullptr ? 2.0f * sabs + 0x1p-22f * mag : 0x1p-15f * lo;
+                    gnear = ranked ? !(lo - hi >= tol) : !(lo - hi > tol) || (by_logit && lo < 1e-20f);
+                    if (gnear && p.lg && !ranked && isfinite(tol) && !(by_logit && lo < 1e-20f)) {
+                        float tr[VPL], tb[VPL], tc[VPL];
+#pragma unroll
+                        for (int i = 0; i < VPL; ++i) {
+                            tr[i] = r[i];
+                            tb[i] = b[i];
+                            tc[i] = c[i];
+                        }
+                        gnear = !choose_groups_exact<VPL>(&p, tr, tb, tc, m, mine, a2, lo, hi, tol, &keep);
+                    }
+                }
+                if (p.lg) {
+                    const int at = lane >> p.lsh;
+                    if (at >= p.G || !((keep >> at) & 1u)) {
+#pragma unroll
+                        for (int i = 0; i < VPL; ++i) c[i] = -CUDART_INF_F;
+                    }
                 }
             }
+            if (by_logit && !ranked) logits_rank<VPL>(r, c);
+            if (t + step < p.T) load_row<VPL, T, VEC>(row + step * p.stride, lane, p.E, r);
             // two more than K: the rank behind the last taken one, and one that bounds the rest
             const int key = take_rough<VPL>(c, lane, p.K + 2);
             int id = -1;
@@ -535,7 +623,7 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             if (key >= FIRST) {
                 id = 255 - (key & 255);
                 rk = clean(to_f32(row[id]));
-                val = choice(p, rk, p.bias != nullptr ? __ldg(p.bias + id) : 0.0f, m, inv);
+                val = by_logit ? rk : choice(p, rk, __ldg(p.bias + id), m, inv);
             }
             // every expert behind lies at or below the last key with its dropped bits set
             if (lane > p.K && key >= FIRST) val = key_value(key | 255);
@@ -560,23 +648,22 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             const int id2 = __shfl_down_sync(FULL, id, 1);
             const float val2 = __shfl_down_sync(FULL, val, 1), rk2 = __shfl_down_sync(FULL, rk, 1);
             if (lane < p.K && id2 >= 0) {
-                const float far = p.softmax ? m - rk2 : fabsf(rk2);
-                const float spread = 4.0f + (isfinite(far) ? far : 0.0f);
-                const float tol = (p.bias != nullptr ? sabs + 0x1p-21f * fabsf(val) : 0x1p-20f * spread * val) + 1e-36f;
-                if (!(val - val2 > tol)) {
-                    // equal inputs are an exact tie: the lower index is first already
-                    near = near || !(rk == rk2 && (p.bias == nullptr || p.bias[id] == p.bias[id2]));
-                }
-                if (lane == p.K - 1 && rest > -CUDART_INF_F && !(val - rest > tol)) near = true;
+                const float tol = by_logit ? logit_slack(p, m, val, val2) : sabs + 0x1p-22f * fabsf(val);
+                // equal inputs are an exact tie: the lower index is first already
+                if (!(val - val2 > tol)) close = !(rk == rk2 && (by_logit || p.bias[id] == p.bias[id2]));
+                near = lane == p.K - 1 && rest > -CUDART_INF_F && !(val - rest > tol);
             }
-            if (__any_sync(FULL, gnear)) groups |= 1u << k;
-            if (__any_sync(FULL, near || gnear)) again |= 1u << k;
+            near = near || gnear;
+            if (__any_sync(FULL, close)) {
+                if (__any_sync(FULL, near) || (p.softmax && !by_logit)) near = true;
+                else order_exact(p, lane, m, by_logit || id < 0 ? 0.0f : p.bias[id], id, rk);
+            }
+            if (__any_sync(FULL, near)) again |= 1u << k;
             else write_token(p, t, lane, id, rk, m, z, idx, w);
         }
         for (; again; again &= again - 1) {
-            const int k = __ffs(again) - 1;
-            const long long t = tb + static_cast<long long>(k) * step;
-            route_exact<VPL, T, VEC>(&p, t, logits + t * p.stride, (groups >> k) & 1u, idx, w);
+            const long long t = tb + static_cast<long long>(__ffs(again) - 1) * step;
+            route_exact<VPL, T, VEC>(&p, t, logits + t * p.stride, idx, w);
         }
     }
 }

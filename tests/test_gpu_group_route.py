@@ -210,3 +210,25 @@ def test_backward_skips_foreign_ids(A):
     for i, e in ((0, 0), (2, 3), (3, 15), (3, 2)):
         want[i, e] = s[i, e] * (1 - s[i, e])
     assert ((got.double() - want).abs() <= 1e-6).all()
+
+
+def test_logits_that_float64_scores_cannot_tell_apart(A):
+    """Sigmoids that round to the same float64 (logits above 20), scores below its
+    range, and logits within 1e-12: equal there, so the lowest index is taken."""
+    E = 32
+    base = torch.tensor([0.0, 5.0, 15.0, 21.0, 25.0, 33.0, 40.0, 85.0, -30.0, -600.0, -720.0, -1000.0], device="cuda")
+    r = base[:, None].repeat(1, E)
+    up = torch.arange(E, device="cuda") % 5
+    for _ in range(4):
+        r = torch.where(up[None] > 0, torch.nextafter(r, torch.full_like(r, 1e4)), r)
+        up = up - 1
+    tiny = torch.zeros(2, E, device="cuda")
+    tiny[0, 7], tiny[1, 9] = 1e-30, 1e-9
+    r = torch.cat([r, tiny])
+    top = r.clone()
+    top[:, 3] = 90.0  # softmax maximum far above the others
+    for score in ("sigmoid", "softmax"):
+        for x in (r, top):
+            check(A, x, 6, 1, 1, None, score)
+            check(A, x, 6, 4, 2, None, score, rank=1)
+            check(A, x, 6, 4, 2, None, score, rank=2)
