@@ -206,8 +206,8 @@ struct RowFetch {
 #pragma unroll
         for (int k = 0; k < NV * VEC / 2; ++k) p[k] = f2(f[2 * k / VEC][2 * k % VEC], f[(2 * k + 1) / VEC][(2 * k + 1) % VEC]);
     }
-    // Vector i of slot s as FP32 (zeros past the row's end).
-    MOE_DEV void get(int s, int i, float (&f)[VEC]) const {
+    // Vector i of slot s as loaded, or as FP32 (zeros past the row's end).
+    MOE_DEV Raw<T, VEC> raw(int s, int i) const {
         const bool in = (i * TPR + t) * VEC < d;
         Raw<T, VEC> r;
         r.clear();
@@ -216,9 +216,30 @@ struct RowFetch {
         } else {
             if (in) r = ahead[i];
         }
-        r.get(f);
+        return r;
     }
+    MOE_DEV void get(int s, int i, float (&f)[VEC]) const { raw(s, i).get(f); }
 };
+
+// How the row kernels lay rows over threads: TPR threads a row, up to a warp
+// several rows to a CTA of 128.
+template <int TPR>
+struct RowThreads {
+    static constexpr int THREADS = TPR <= 32 ? 128 : TPR;
+    static constexpr int ROWS = THREADS / TPR;      // rows a CTA works on at a time
+    MOE_DEV static int col() { return static_cast<int>(threadIdx.x) % TPR; }
+    MOE_DEV static int row() { return static_cast<int>(threadIdx.x) / TPR; }
+    // the first of the rows that the warp (or the CTA) works on together, from this thread's
+    MOE_DEV static long long first(long long row) { return TPR < 32 ? row - static_cast<int>(lane_id()) / TPR : row; }
+};
+
+// Sum over the TPR <= 32 threads of a row, the same in all of them.
+template <int TPR>
+MOE_DEV float seg_sum(float v) {
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 
 // CTAs for `rows` rows, rpc of them at a time, at most per_sm on an SM.
 inline int grid_rows(long long rows, int rpc, int per_sm) {

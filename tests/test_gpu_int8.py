@@ -45,6 +45,19 @@ def test_quantize_rows(A, shape, dt):
     assert torch.equal(got["scale"], scale) and torch.equal(got["q"], q)
 
 
+@pytest.mark.parametrize("dt", list(DT))
+def test_quantize_coarse_values(A, dt):
+    """Few significant bits: quotients on half steps, and next to them by the
+    scale's own rounding, in every row."""
+    x = torch.randint(-64, 65, (300, 1000), generator=gen(40), device="cuda").float() * \
+        2.0 ** torch.randint(-20, 20, (300, 1), generator=gen(41), device="cuda")
+    x[:, 0] = x.abs().amax(1) * (1 + torch.arange(300, device="cuda") % 4 * 0.25)
+    x = x.to(DT[dt])
+    got = A.quantize_rows(x)
+    q, scale = R.quantize_rows(x)
+    assert torch.equal(got["scale"].nan_to_num(-1), scale.nan_to_num(-1)) and torch.equal(got["q"], q)
+
+
 def test_quantize_half_steps(A):
     """Quotients on and next to half steps: x = scale (n + 1/2) exactly, and one unit off."""
     n = torch.arange(-127, 127, device="cuda", dtype=torch.float32) + 0.5
