@@ -58,10 +58,19 @@ struct Raw<T, 1> {
 };
 
 // sigmoid(v) = exp(v) / (1 + exp(v)) below zero, where exp(-v) would leave
-// FP32's range while v sigmoid(v) is still in it.
+// FP32's range while v sigmoid(v) is still in it. On the special-function
+// unit: the argument |v| log2(e) keeps what its rounding lost (and what log2(e)
+// itself does), so that the result is off by 4 units of 2^-23 at any v.
 MOE_DEV float sigmoid_f(float v) {
-    const float e = expf(-fabsf(v));
-    return (v >= 0.0f ? 1.0f : e) / (1.0f + e);
+    constexpr double LOG2E = 1.4426950408889634;
+    constexpr float HI = static_cast<float>(LOG2E), LO = static_cast<float>(LOG2E - static_cast<double>(HI));
+    const float a = fminf(fabsf(v), 150.0f), t = a * -HI;  // below 2^-150 is zero
+    const float lost = fmaf(a, -LO, fmaf(a, -HI, -t));
+    float e, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = fmaf(e, lost * 0.6931471805599453f, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return (v >= 0.0f ? 1.0f : e) * r;
 }
 
 MOE_DEV float warp_sum(float v) {

@@ -19,7 +19,7 @@ constexpr int WARPS = 8;
 constexpr int NC = 4;  // weight rows per warp
 
 struct VecParams {
-    int M, Ma, K, N, E;
+    int M, Ma, K, N, E, slots;  // slots: experts that can have rows
     long long lda;
     const int8_t* a;
     const float* sa;
@@ -114,20 +114,37 @@ int8_vec_kernel(const VecParams p) {
     pdl_wait();
     pdl_trigger();
     if (n0 >= F) return;
-    const int e = static_cast<int>(blockIdx.y);
-    if (e == p.E) {  // rows that no expert covers
+    if (static_cast<int>(blockIdx.y) == p.slots) {  // rows that no expert covers
         const int lo = min(max(p.offsets[p.E], 0), p.M);
-        for (int i = lo; i < p.M; ++i)
+        for (int i = lo + blockIdx.z; i < p.M; i += gridDim.z)
             if (lane < NO && n0 + lane < F)
                 static_cast<O*>(p.out)[static_cast<long long>(i) * F + n0 + lane] = from_f32<O>(0.0f);
         return;
     }
-    int lo = 0, hi = p.M;
+    int e = 0, lo = 0, hi = p.M;
     if (p.offsets != nullptr) {
-        lo = min(max(p.offsets[e], 0), p.M);
-        hi = min(max(p.offsets[e + 1], lo), p.M);
+        // the blockIdx.y-th expert that has rows
+        int before = 0;
+        e = -1;
+        for (int e0 = 0; e0 < p.E && e < 0; e0 += 32) {
+            int a = 0, b = 0;
+            if (e0 + lane < p.E) {
+                a = min(max(p.offsets[e0 + lane], 0), p.M);
+                b = min(max(p.offsets[e0 + lane + 1], a), p.M);
+            }
+            const unsigned some = __ballot_sync(0xffffffffu, b > a);
+            const int want = static_cast<int>(blockIdx.y) - before;
+            if (want < __popc(some)) {
+                const int at = static_cast<int>(__fns(some, 0, want + 1));
+                e = e0 + at;
+                lo = __shfl_sync(0xffffffffu, a, at);
+                hi = __shfl_sync(0xffffffffu, b, at);
+            }
+            before += __popc(some);
+        }
+        if (e < 0) return;
     }
-    for (int i = lo; i < hi; i += 8) {
+    for (int i = lo + 8 * blockIdx.z; i < hi; i += 8 * gridDim.z) {
         const int n = min(8, hi - i);
         if (n == 1) block<1, SWIGLU, O>(p, e, n0, i, n, lane);
         else if (n == 2) block<2, SWIGLU, O>(p, e, n0, i, n, lane);
@@ -139,9 +156,14 @@ int8_vec_kernel(const VecParams p) {
 template <bool SWIGLU, typename O>
 cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
     const int F = SWIGLU ? a.N / 2 : a.N, per = WARPS * (SWIGLU ? NC / 2 : NC);
-    VecParams p{a.M, a.Ma, a.K, a.N, a.E, a.lda, a.a, a.sa, a.b, a.sb, a.offsets, a.rows, a.out, a.err};
-    return launch_pdl(int8_vec_kernel<SWIGLU, O>, dim3((F + per - 1) / per, a.E + (a.offsets != nullptr ? 1 : 0)),
-                      dim3(32 * WARPS), 0, s, p);
+    const int slots = a.E < a.M ? a.E : a.M, gx = (F + per - 1) / per;
+    VecParams p{a.M, a.Ma, a.K, a.N, a.E, slots, a.lda, a.a, a.sa, a.b, a.sb, a.offsets, a.rows, a.out, a.err};
+    // An expert's rows go over several CTAs, eight at a time, as far as that fills the SMs.
+    const long long ctas = static_cast<long long>(gx) * slots;
+    const int most = (a.M + 7) / 8, want = static_cast<int>((4LL * num_sms() + ctas - 1) / ctas);
+    const int z = want < 1 ? 1 : want < most ? want : most;
+    return launch_pdl(int8_vec_kernel<SWIGLU, O>, dim3(gx, slots + (a.offsets != nullptr ? 1 : 0), z), dim3(32 * WARPS),
+                      0, s, p);
 }
 
 }  // namespace

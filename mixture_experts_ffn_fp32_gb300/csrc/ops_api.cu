@@ -182,7 +182,8 @@ Int8Form int8_form(const moe_int8_config& c) {
         if (e[0] == 's') return INT8_SMALL;
         if (e[0] == 'w') return INT8_WIDE;
     }
-    if (static_cast<double>(c.M) * c.N * c.K <= 134217728.0) return INT8_VEC;
+    // (a warp walks its expert's rows eight at a time: few of them)
+    if (c.M <= 32LL * c.E && static_cast<double>(c.M) * c.N * c.K <= 134217728.0) return INT8_VEC;
     return c.M <= 32LL * c.E || c.M <= 128 ? INT8_SMALL : INT8_WIDE;
 }
 
