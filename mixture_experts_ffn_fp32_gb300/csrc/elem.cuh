@@ -79,6 +79,14 @@ MOE_DEV float warp_sum(float v) {
     return v;
 }
 
+// Sum over the TPR <= 32 threads of a row, the same in all of them.
+template <int TPR>
+MOE_DEV float seg_sum(float v) {
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // Sum of the W values (W a power of two, at most 32) that lanes 0 to W - 1
 // hold, the same in every lane and in a fixed order.
 template <int W>
@@ -90,13 +98,13 @@ MOE_DEV float group_sum(float v) {
 }
 
 // Sums of a and b over the TPR threads of a row, the same in all of them and
-// in a fixed order. TPR = 32: within the warp. Else over the CTA (TPR
+// in a fixed order. TPR <= 32: within the warp. Else over the CTA (TPR
 // threads), through `scratch`, two halves of 2 * TPR / 32 floats used in turn:
 // the sync of one call orders the reads of the call before last.
 template <int TPR>
 MOE_DEV void row_sum2(float& a, float& b, float* scratch, int& turn) {
-    a = warp_sum(a);
-    b = warp_sum(b);
+    a = seg_sum<(TPR < 32 ? TPR : 32)>(a);
+    b = seg_sum<(TPR < 32 ? TPR : 32)>(b);
     if constexpr (TPR > 32) {
         constexpr int W = TPR / 32;
         float* s = scratch + (turn & 1) * 2 * W;
@@ -241,14 +249,6 @@ struct RowThreads {
     // the first of the rows that the warp (or the CTA) works on together, from this thread's
     MOE_DEV static long long first(long long row) { return TPR < 32 ? row - static_cast<int>(lane_id()) / TPR : row; }
 };
-
-// Sum over the TPR <= 32 threads of a row, the same in all of them.
-template <int TPR>
-MOE_DEV float seg_sum(float v) {
-#pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 
 // CTAs for `rows` rows, rpc of them at a time, at most per_sm on an SM.
 inline int grid_rows(long long rows, int rpc, int per_sm) {

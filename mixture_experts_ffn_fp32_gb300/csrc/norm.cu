@@ -218,12 +218,12 @@ layer_norm_long_kernel(int R, int d, const T* __restrict__ x, long long xs, cons
 }
 
 // Threads per row of the backward at width d, and CTAs of them on an SM.
-constexpr int bwd_threads(int d) { return d <= 32 * 8 ? 32 : d <= 128 * 16 ? 128 : d <= 256 * 16 ? 256 : 512; }
-constexpr int bwd_per_sm(int tpr) { return 512 / (tpr == 32 ? 128 : tpr); }
+constexpr int bwd_threads(int d) { return d <= 8 * 8 ? 8 : d <= 32 * 8 ? 32 : d <= 128 * 16 ? 128 : d <= 256 * 16 ? 256 : 512; }
+constexpr int bwd_per_sm(int tpr) { return 512 / (tpr <= 32 ? 128 : tpr); }
 
 template <typename T, int VEC, int NV, int TPR>
 struct Backward {
-    static constexpr int THREADS = TPR == 32 ? 128 : TPR;
+    static constexpr int THREADS = RowThreads<TPR>::THREADS;
     using Fetch = RowFetch<T, VEC, NV, TPR, THREADS, BWD_DEPTH>;
 };
 
@@ -237,13 +237,13 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
                       float* __restrict__ part) {
     using F = typename Backward<T, VEC, NV, TPR>::Fetch;
     constexpr int D = F::D;
-    constexpr int RPC = TPR == 32 ? 4 : 1;
+    using L = RowThreads<TPR>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[TPR > 32 ? 4 * (TPR / 32) : 1];
-    __shared__ float gather[TPR == 32 ? 2 * NV * VEC * 32 : 1];
-    const int t = TPR == 32 ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
-    const long long step = static_cast<long long>(gridDim.x) * RPC;
-    long long row = static_cast<long long>(blockIdx.x) * RPC + (TPR == 32 ? threadIdx.x >> 5 : 0);
+    __shared__ float gather[TPR <= 32 ? 2 * NV * VEC * TPR : 1];
+    const int t = L::col();
+    const long long step = static_cast<long long>(gridDim.x) * L::ROWS;
+    long long row = static_cast<long long>(blockIdx.x) * L::ROWS + L::row();
     const float inv_d = 1.0f / static_cast<float>(d);
     int turn = 0;
     constexpr int N2 = NV * VEC / 2;
@@ -282,7 +282,7 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
         rs = __ldg(rstd + row);
     }
     int slot = 0;
-    for (; row < R; row += step) {
+    for (; L::first(row) < R; row += step) {
         F2 xh[N2], g[N2];
         const float mc = mu, rc = rs;
         if (row + step < R) {
@@ -292,6 +292,10 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
         if constexpr (F::ASYNC) cp_async_wait<D - 1>();
         fx.pairs(slot, xh);
         fy.pairs(slot, g);
+        if (TPR < 32 && row >= R) {  // of a warp whose other rows are there
+#pragma unroll
+            for (int k = 0; k < N2; ++k) xh[k] = g[k] = f2(0.0f, 0.0f);
+        }
         issue(slot, row + D * step);
         if (++slot == D) slot = 0;
         if constexpr (!KEEP) columns();
@@ -321,7 +325,7 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (i * TPR + t) * VEC;
-            if (c < d) {
+            if (c < d && row < R) {
                 Raw<T, VEC> out;
                 out.set(o[i]);
                 out.store(dx + row * dxs + c);
@@ -336,31 +340,31 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
     }
     if (part == nullptr) return;
     float* pg = part + static_cast<long long>(blockIdx.x) * 2 * d;
-    if constexpr (TPR == 32) {
-        // the CTA's four rows in flight: one after the other into shared memory
+    if constexpr (TPR <= 32) {
+        // the CTA's rows in flight: one after the other into shared memory
         constexpr int N = NV * VEC;
-        for (int w = 0; w < RPC; ++w) {
-            if (static_cast<int>(threadIdx.x >> 5) == w) {
+        for (int w = 0; w < L::ROWS; ++w) {
+            if (L::row() == w) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
-                        const int a = (i * VEC + j) * 32 + t;
+                        const int a = (i * VEC + j) * TPR + t;
                         gather[a] = (w ? gather[a] : 0.0f) + dg[i][j];
-                        gather[N * 32 + a] = (w ? gather[N * 32 + a] : 0.0f) + db[i][j];
+                        gather[N * TPR + a] = (w ? gather[N * TPR + a] : 0.0f) + db[i][j];
                     }
             }
             __syncthreads();
         }
-        if (threadIdx.x < 32) {
+        if (threadIdx.x < TPR) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    const int c = (i * 32 + t) * VEC + j, a = (i * VEC + j) * 32 + t;
+                    const int c = (i * TPR + t) * VEC + j, a = (i * VEC + j) * TPR + t;
                     if (c < d) {
                         pg[c] = gather[a];
-                        pg[d + c] = gather[N * 32 + a];
+                        pg[d + c] = gather[N * TPR + a];
                     }
                 }
         }
@@ -517,6 +521,7 @@ cudaError_t bwd_t(const LayerNormArgs& a, int grid, float* part, cudaStream_t s)
 template <typename T, int VEC>
 cudaError_t bwd_v(const LayerNormArgs& a, int grid, float* part, cudaStream_t s) {
     switch (bwd_threads(a.d)) {
+        case 8: return bwd_t<T, VEC, 8 / VEC, 8>(a, grid, part, s);
         case 32: return bwd_t<T, VEC, 8 / VEC, 32>(a, grid, part, s);
         case 128:
             if (a.d <= 128 * 8) return bwd_t<T, VEC, 8 / VEC, 128>(a, grid, part, s);
@@ -555,7 +560,7 @@ cudaError_t bwd_d(const LayerNormArgs& a, float* part, cudaStream_t s) {
 int layer_norm_bwd_parts(int R, int d) {
     if (d > BWD_MAX_D) return R < 16 ? R : 16;
     const int t = bwd_threads(d);
-    return grid_rows(R, t == 32 ? 4 : 1, bwd_per_sm(t));
+    return grid_rows(R, t <= 32 ? 128 / t : 1, bwd_per_sm(t));
 }
 
 cudaError_t launch_layer_norm(const LayerNormArgs& a, cudaStream_t s) {

@@ -36,7 +36,8 @@ def ints(*shape, seed=0, lo=-128, hi=128):
 
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("shape", [(1, 1, 0), (3, 16, 0), (70, 96, 0), (33, 250, 3), (64, 1000, 0), (9, 1411, 5),
-                                   (40, 2048, 0), (17, 4096, 8), (3, 8200, 0), (2, 20000, 1)], ids=str)
+                                   (40, 2048, 0), (17, 4096, 8), (3, 8200, 0), (2, 20000, 1), (5001, 64, 0), (333, 128, 8),
+                                   (700, 100, 3), (9, 8192, 0)], ids=str)
 def test_quantize_rows(A, shape, dt):
     n, k, pad = shape
     x = (rand(n, k + pad, seed=k) * 3).to(DT[dt])[:, :k]

@@ -27,7 +27,9 @@ def rand(shape, seed, scale=1.0, dtype=torch.float32, pad=0):
 # width, odd widths, unaligned pitches, rows past the register forms
 SHAPES = [(1, 1, 0), (7, 1, 3), (1, 64, 0), (33, 100, 0), (65, 256, 8), (130, 257, 0), (300, 1000, 24), (64, 1024, 0),
           (19, 1411, 5), (128, 2048, 0), (1000, 2048, 1), (128, 4096, 0), (5, 8191, 0), (9, 8192, 0), (3, 12288, 0),
-          (4, 16384, 0), (2, 20001, 0), (5, 16392, 0)]
+          (4, 16384, 0), (2, 20001, 0), (5, 16392, 0),
+          # several rows a warp, the last warps part empty
+          (9000, 16, 0), (5001, 33, 3), (3003, 64, 8), (4097, 128, 0), (2049, 72, 0)]
 
 
 def check_forward(x, w, b, eps, got):
