@@ -14,8 +14,12 @@
 // the experts that could be concerned: a warp's FP64 exponential alone is two
 // thousand cycles here.
 //
-// One warp per token, E / 32 consecutive experts a lane; bound by the read of
-// the logits for large batches, by latency below a few thousand tokens.
+// One warp per token, E / 32 consecutive experts a lane: scores, the groups'
+// two best by shuffles, then the lanes' sorted keys popped by one integer
+// maximum over the warp a rank. Bound by instructions (about 900 a token) and,
+// below a few thousand tokens, by the latency of that chain. Measured: 16384 x
+// 256 sigmoid, 8 groups, bias 23 us (3 us of it for the reads at the copy rate);
+// 128 tokens 6 us; the gradient of a raw softmax, 16384 x 256, 13 us (its bytes: 5).
 #include <math_constants.h>
 
 #include "elem.cuh"

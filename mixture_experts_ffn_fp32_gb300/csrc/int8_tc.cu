@@ -26,6 +26,15 @@
 // own, which the widening frees: weights are in shared memory before their
 // columns are, so that only the widening lies between two uses of a column.
 //
+// Measured (one GB300; 1866 TFLOP/s BF16 and 6.8 TB/s by the libraries' product and
+// copy): 16384 x 4096 x 4096 268 us without the tokens' pass (2.05 P operations/s: small
+// integers in FP16 draw less power than random BF16); 131072 gathered rows of 64 experts,
+// 2048 x 2816 SwiGLU, 790 us (1.9 P), the tensor pipe active 81 %; there the widening (1110
+// cycles a stage of 1024 MMA cycles) and the last waves bind. 1024 rows of 256 experts,
+// 4096 x 4096: 615 us, 6.8 TB/s of weights. The tokens' pass writes two bytes an
+// element, 110 us for the 131072 rows: the rate at which this memory takes writes
+// alone (a fill of as many bytes takes 141 us).
+//
 // Every wait is bounded (common.cuh).
 #include <math_constants.h>
 

@@ -6,7 +6,11 @@
 // A warp takes four output channels (SwiGLU: two and their partners) and up to
 // eight rows of one expert and walks the whole reduction, 512 values a step:
 // the weights, which bound the product, are read once per eight rows, straight
-// into registers, and each 16 bytes of them feed 4 dot products per row.
+// into registers, and each 16 bytes of them feed 4 dot products per row. The
+// grid covers as many experts as can have rows, and where that leaves SMs idle
+// an expert's rows beyond eight go to further CTAs. Measured: one row, 4096 x
+// 2048, 5.5 us (1.5 TB/s of weights: one round of loads and its latency); 8 rows,
+// 4096 x 4096, 11 us; from 32 rows on the dot products bind (35 T operations/s).
 #include <math_constants.h>
 
 #include "elem.cuh"

@@ -14,6 +14,14 @@
 // Statistics are FP32. The forward sums the row, then the row less a mean: the
 // second sums yield the squares and what rounding left in the mean, so a row
 // whose mean is large against its deviation loses nothing.
+//
+// Measured (one GB300, 6.8 TB/s copy rate, caches cold): forward, 16384 x 2048
+// BF16 26 us (5.2 TB/s), 8192 x 4096 FP32 5.5 TB/s; backward, 8192 x 4096 BF16
+// 41 us and 5 for the column sums (4.9 TB/s), FP32 5.5 TB/s, 5003 x 1411 FP32
+// unaligned 23 + 5 us. BF16 rows are held back by instructions (unpacking, and
+// the products in FP32): packed FP32 pairs took 29 us to 26 and 45 to 41; more
+// rows ahead or more CTAs do not help (35 us with 1216 CTAs, each of which reads
+// gamma and beta again). Few rows are latency: 128 x 4096 4 us.
 #include "elem.cuh"
 #include "internal.h"
 
