@@ -499,19 +499,22 @@ def _rows(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or t.size(1) < 1:
-        raise ValueError(f"{name} must be a [rows, n] tensor with n >= 1, got {tuple(t.shape)}")
+    have = t.shape
+    if len(have) != 2 or have[1] < 1:
+        raise ValueError(f"{name} must be a [rows, n] tensor with n >= 1, got {tuple(have)}")
     if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype or 'float32, bfloat16 or float16'}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.size(1) > 1 and t.stride(1) != 1:
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} has shape {tuple(have)}, expected {tuple(shape)}")
+    R, n = have
+    pitch, inner = t.stride()
+    if inner != 1 and n > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if t.size(0) > 1:
-        if t.stride(0) < t.size(1):
-            raise ValueError(f"{name}'s rows must not overlap")
-        return t.stride(0)
-    return t.size(1)
+    if R <= 1:
+        return n
+    if pitch < n:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return pitch
 
 
 class _On:
@@ -614,11 +617,19 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _struct(kind, *fields):
+    """A reference to a config that the library only reads (building one takes as
+    long as a small kernel)."""
+    return ctypes.byref(kind(*fields))
+
+
 def _group_config(logits, K, n_groups, topk_groups, group_rank, score, renormalize, scale):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
-    return GroupRouteConfig(logits.size(0), logits.size(1), K, n_groups, topk_groups, group_rank, SCORES[score],
-                            1 if renormalize else 0, scale, _DTYPES[logits.dtype])
+    T, E = logits.shape
+    return _struct(GroupRouteConfig, T, E, K, n_groups, topk_groups, group_rank, SCORES[score],
+                   1 if renormalize else 0, scale, _DTYPES[logits.dtype])
 
 
 def group_route(logits: torch.Tensor, K: int, n_groups: int = 1, topk_groups: int = 1, bias=None,
@@ -637,7 +648,7 @@ def group_route(logits: torch.Tensor, K: int, n_groups: int = 1, topk_groups: in
     with _on(stream, logits, bias):
         out = {"idx": torch.empty((T, max(K, 0)), dtype=torch.int32, device=logits.device),
                "w": torch.empty((T, max(K, 0)), dtype=torch.float32, device=logits.device)}
-        _check(lib().moe_group_route(ctypes.byref(cfg), logits.data_ptr(), ls, _ptr(bias), out["idx"].data_ptr(),
+        _check(lib().moe_group_route(cfg, logits.data_ptr(), ls, _ptr(bias), out["idx"].data_ptr(),
                                      out["w"].data_ptr(), _raw_stream(stream, logits)), "moe_group_route")
     return out
 
@@ -656,7 +667,7 @@ def group_route_backward(dw: torch.Tensor, idx: torch.Tensor, logits: torch.Tens
     cfg = _group_config(logits, K, 1, 1, 1, score, renormalize, scale)
     with _on(stream, dw, idx, logits):
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        _check(lib().moe_group_route_backward(ctypes.byref(cfg), logits.data_ptr(), ls, idx.data_ptr(),
+        _check(lib().moe_group_route_backward(cfg, logits.data_ptr(), ls, idx.data_ptr(),
                                               dw.data_ptr(), out.data_ptr(), _raw_stream(stream, logits)),
                "moe_group_route_backward")
     return out
@@ -686,8 +697,8 @@ def _int8_config(M, Ma, K, N, E, swiglu, out_dtype) -> tuple:
 
 @functools.lru_cache(maxsize=4096)
 def _int8_ws(*shape) -> int:
-    cfg, n = Int8Config(*shape), ctypes.c_size_t(0)
-    _check(lib().moe_matmul_int8_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_matmul_int8_workspace_size(_struct(Int8Config, *shape), ctypes.byref(n)),
            "moe_matmul_int8_workspace_size")
     return n.value
 
@@ -734,7 +745,7 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
         if ws is None:
             ws = torch.empty((_int8_ws(*cfg),), dtype=torch.uint8, device=a.device)
         out = torch.empty((M, N // 2 if swiglu else N), dtype=_OUT_DTYPES[out_dtype], device=a.device)
-        _check(lib().moe_matmul_int8(ctypes.byref(Int8Config(*cfg)), a.data_ptr(), a.stride(0) if Ma > 1 else K,
+        _check(lib().moe_matmul_int8(_struct(Int8Config, *cfg), a.data_ptr(), a.stride(0) if Ma > 1 else K,
                                      a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),
                                      _ptr(rows), out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
                                      _raw_stream(stream, a)), "moe_matmul_int8")
