@@ -378,15 +378,13 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const int c = (i * TPR + t) * VEC + j;
-                if (c < d) {
-                    pg[c] = dg[i][j];
-                    pg[d + c] = db[i][j];
-                }
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (c < d) {  // 16-byte stores (4-byte ones, a sector each: 41 us for 33)
+                store_f32<VEC>(pg + c, dg[i]);
+                store_f32<VEC>(pg + d + c, db[i]);
             }
+        }
     }
 }
 

@@ -171,9 +171,9 @@ moe_status check_int8(const moe_int8_config& c) {
 //   pass and spread over channels (us, dot products against tiles of 32: one row,
 //   4096 x 2048, 8 : 25; 8 rows, 4096 x 4096, 14 : 29; 32 rows of 8 experts,
 //   2048 x 2048, 23 : 23; 32 rows, 4096 x 4096, 33 : 29; 32 rows of 256 experts,
-//   4096 x 4096, 180 : 121).
+//   4096 x 4096, 117 : 119).
 //   Tiles of 32 rows while they hold an expert's (against 256: 4 rows each of 256
-//   experts, 643 : 1040; 32 each of 8, 2048 x 2048, 27 : 25; 64 each, 33 : 27;
+//   experts, 570 : 729; 32 each of 8, 2048 x 2048, 27 : 25; 64 each, 33 : 27;
 //   128 rows of one, whose 32 channel tiles are more than the pairs' 16, 29 : 35).
 enum Int8Form { INT8_VEC, INT8_SMALL, INT8_WIDE };
 Int8Form int8_form(const moe_int8_config& c) {
