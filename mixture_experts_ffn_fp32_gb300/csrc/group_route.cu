@@ -252,11 +252,12 @@ MOE_DEV long long order_key(double v) {
 MOE_DEV double key_value(long long k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffLL)); }
 constexpr long long NONE64 = static_cast<long long>(0x8000000000000000ull);
 
-// Scores rise with their logits: without a bias the logits rank.
+// Scores rise with their logits: without a bias the logits rank (the sum turns
+// -0 into 0, which it equals but whose bits lie below).
 template <int VPL>
 MOE_DEV void logits_rank(const float (&r)[VPL], float (&c)[VPL]) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) c[i] = c[i] > -CUDART_INF_F ? r[i] : -CUDART_INF_F;
+    for (int i = 0; i < VPL; ++i) c[i] = c[i] > -CUDART_INF_F ? __fadd_rn(r[i], 0.0f) : -CUDART_INF_F;
 }
 
 // How far apart two logits a >= b must be for FP64 to tell their scores apart
@@ -629,8 +630,10 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
                 rk = clean(to_f32(row[id]));
                 val = by_logit ? rk : choice(p, rk, __ldg(p.bias + id), m, inv);
             }
-            // every expert behind lies at or below the last key with its dropped bits set
-            if (lane > p.K && key >= FIRST) val = key_value(key | 255);
+            // every expert behind lies at or below the last key with its dropped bits set;
+            // a key drops nothing of a 16-bit logit
+            const bool whole = by_logit && sizeof(T) == 2;
+            if (!whole && lane > p.K && key >= FIRST) val = key_value(key | 255);
             const float rest = __shfl_sync(FULL, val, p.K + 1);
             const float next = __shfl_down_sync(FULL, val, 1);
             if (__any_sync(FULL, lane < p.K && next > val)) {
@@ -656,6 +659,8 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
                 // equal inputs are an exact tie: the lower index is first already
                 if (!(val - val2 > tol)) close = !(rk == rk2 && (by_logit || p.bias[id] == p.bias[id2]));
                 near = lane == p.K - 1 && rest > -CUDART_INF_F && !(val - rest > tol);
+                // whole keys rank equal logits; the next lower one is a step of the type below, and clear
+                if (whole && rest == val && tol <= 0x1p-12f * fabsf(val)) near = false;
             }
             near = near || gnear;
             if (__any_sync(FULL, close)) {

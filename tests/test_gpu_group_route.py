@@ -232,3 +232,25 @@ def test_logits_that_float64_scores_cannot_tell_apart(A):
             check(A, x, 6, 1, 1, None, score)
             check(A, x, 6, 4, 2, None, score, rank=1)
             check(A, x, 6, 4, 2, None, score, rank=2)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_zeros_of_both_signs_are_equal(A, score, dt):
+    sign = torch.where(rand(64, 256, seed=7) > 0, 1.0, -1.0)
+    r = (0.0 * sign).to(DT[dt])
+    r[:, 200] = -1.0
+    for G, TG, rank in [(1, 1, 2), (8, 3, 1), (8, 3, 2)]:
+        got = check(A, r, 8, G, TG, None, score, rank)
+        assert torch.equal(got["idx"].cpu(), torch.arange(8, dtype=torch.int32).expand(64, 8))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("step", [0.5, 2.0 ** -7, 2.0 ** -24])
+def test_ties_of_coarse_logits(A, score, dt, step):
+    """Runs of equal logits across the last rank, next to others a step away."""
+    r = (torch.round(2.0 * rand(300, 96, seed=11)) * step).to(DT[dt])
+    r[150:] += torch.tensor(1.5, dtype=DT[dt], device="cuda")
+    for G, TG, rank in [(1, 1, 2), (6, 2, 1), (6, 2, 2)]:
+        check(A, r, 5, G, TG, None, score, rank)
