@@ -371,8 +371,8 @@ __device__ __noinline__ double exact_choice(int softmax, float r, float m, float
 }
 
 // The groups to keep where some scores lie within `tol` of the border: those
-// groups' best experts get FP64 scores, one a lane. False: a lane holds several
-// candidates for its group's best, or a softmax with a bias.
+// groups' best experts get FP64 scores. False: there are several candidates for
+// a group's best, or a softmax with a bias.
 template <int VPL>
 __device__ __noinline__ bool choose_groups_exact(const Params* pp, const float* r, const float* b, const float* c, float m,
                                                  float mine, float a2, float lo, float hi, float tol, unsigned* keep) {
@@ -383,18 +383,21 @@ __device__ __noinline__ bool choose_groups_exact(const Params* pp, const float* 
     const bool pair = p.rank == 2 && a2 > -CUDART_INF_F;
     const float edge = pair ? a2 : mine;
     int n = 0;
-    float ri = 0.0f, bi = 0.0f;
+    float ri = 0.0f, bi = 0.0f, rj = 0.0f, bj = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
         if (near && c[i] > -CUDART_INF_F && c[i] >= edge - 2.0f * tol) {
             ++n;
+            rj = ri;
+            bj = bi;
             ri = r[i];
             bi = p.bias != nullptr ? b[i] : 0.0f;
         }
     int all = n;
     for (int o = 1; o < p.lg; o <<= 1) all += __shfl_xor_sync(FULL, all, o);
-    if (__any_sync(FULL, n > 1 || (near && all != (pair ? 2 : 1)))) return false;
+    if (__any_sync(FULL, near && all != (pair ? 2 : 1))) return false;
     double x = n ? exact_choice(p.softmax, ri, m, bi) : 0.0;
+    if (__any_sync(FULL, n > 1)) x += n > 1 ? exact_choice(p.softmax, rj, m, bj) : 0.0;  // both in one lane
     for (int o = 1; o < p.lg; o <<= 1) x += __shfl_xor_sync(FULL, x, o);
     // the others lie clear on either side: kept above all, or behind all
     const long long key = near ? order_key(x) : mine > hi ? 0x7fffffffffffffffLL : mine > -CUDART_INF_F ? NONE64 + 1 : NONE64;

@@ -254,3 +254,19 @@ def test_ties_of_coarse_logits(A, score, dt, step):
     r[150:] += torch.tensor(1.5, dtype=DT[dt], device="cuda")
     for G, TG, rank in [(1, 1, 2), (6, 2, 1), (6, 2, 2)]:
         check(A, r, 5, G, TG, None, score, rank)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("at", [(3, 5), (3, 20), (3, 5, 6), (0, 8, 31)], ids=str)
+def test_group_sums_next_to_each_other(A, score, biased, at):
+    """Groups whose two best sum to nearly the same, wherever in the group they
+    are, with a third best next to the second."""
+    T, G, n = 200, 8, 32
+    r = -3.0 + 0.5 * rand(T, G, n, seed=21)
+    ulps = torch.randint(-3, 4, (T, G, len(at)), generator=torch.Generator(device="cuda").manual_seed(22),
+                         device="cuda")
+    best = 2.0 + 0.5 * rand(T, 1, 1, seed=23) - torch.tensor([0.0, 0.25, 0.25], device="cuda")[:len(at)]
+    r[:, :, list(at)] = best * (1 + ulps * 2.0 ** -23)
+    bias = 0.1 * rand(1, n, seed=24).expand(G, n).reshape(-1).contiguous() if biased else None
+    check(A, r.reshape(T, G * n), 8, G, 3, bias, score, rank=2)
