@@ -49,7 +49,10 @@ MOE_DEV float clean(float r) { return fmaxf(r, -CUDART_INF_F); }
 
 struct Params {
     int T, E, K, G, gs, TG, rank, softmax, renorm;
-    int lg, lsh;  // lanes of a group where groups fill whole lanes and lg = 2^lsh is a power of two, else 0
+    // lg = 2^lsh lanes a group: those that hold its experts where groups fill whole
+    // lanes (whole), else as many as 32 lanes give G groups
+    int lg, lsh, whole;
+    int per_group;  // 2^16 / gs, rounded up: expert e < 256 is in group e per_group / 2^16
     float scale;
     long long stride;
     const float* bias;
@@ -171,10 +174,10 @@ MOE_DEV unsigned kept_groups(const Params& p, int lane, F mine) {
 }
 
 // The two best of each group, in F's order: those of the lane's group in
-// every lane where groups are whole lanes (p.lg), else those of group `lane`.
+// every lane where groups are whole lanes, else those of group `lane`.
 template <typename F, int VPL>
 MOE_DEV void group_best(const Params& p, int lane, const F (&c)[VPL], F none, F& a1, F& a2) {
-    if (p.lg) {
+    if (p.whole) {
         a1 = c[0];
         a2 = none;
 #pragma unroll
@@ -201,38 +204,43 @@ MOE_DEV void group_best(const Params& p, int lane, const F (&c)[VPL], F none, F&
     }
 }
 
-// Groups of any size. Out of line, so that the group of every expert is not
-// kept in the common path's registers.
+// The two best of a group of any size, in every lane of the group: from a copy
+// in shared memory, every lg-th expert a lane. Out of line, as few routings have
+// groups that do not fill lanes.
 template <int VPL>
-__device__ __noinline__ void keep_any_groups(const Params* p, float* c, float* bounds) {
-    const int lane = static_cast<int>(lane_id());
-    float t[VPL], a1, a2;
+__device__ __noinline__ float2 any_group_best(const Params* pp, const float* c, float* copy) {
+    const Params& p = *pp;
+    const int lane = static_cast<int>(lane_id()), g = lane >> p.lsh;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) t[i] = c[i];
-    group_best<float, VPL>(*p, lane, t, -CUDART_INF_F, a1, a2);
-    const float mine = (p->rank == 2 && a2 > -CUDART_INF_F) ? a1 + a2 : a1;
-    const unsigned keep = kept_groups<float>(*p, lane, mine);
-    const bool kept = (keep >> lane) & 1u;
-    bounds[0] = -warp_max(kept ? -mine : -CUDART_INF_F);
-    bounds[1] = warp_max(lane < p->G && !kept ? mine : -CUDART_INF_F);
-    bounds[2] = warp_max((a1 > -CUDART_INF_F ? fabsf(a1) : 0.0f) + (a2 > -CUDART_INF_F ? fabsf(a2) : 0.0f));
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int g = (lane * VPL + i) / p->gs;
-        if (g >= 32 || !((keep >> g) & 1u)) c[i] = -CUDART_INF_F;
-    }
+    for (int i = 0; i < VPL; ++i) copy[lane * VPL + i] = c[i];
+    __syncwarp();
+    float a1 = -CUDART_INF_F, a2 = a1;
+    if (g < p.G)
+        for (int j = lane & (p.lg - 1); j < p.gs; j += p.lg) merge2(a1, a2, copy[g * p.gs + j], -CUDART_INF_F);
+    for (int o = 1; o < p.lg; o <<= 1) merge2(a1, a2, __shfl_xor_sync(FULL, a1, o), __shfl_xor_sync(FULL, a2, o));
+    __syncwarp();
+    return make_float2(a1, a2);
 }
 
-// The groups to keep, as a mask (p.lg); lo, hi: the lowest kept and the highest
+// The groups to keep, as a mask; lo, hi: the lowest kept and the highest
 // dropped score (-inf: none); mag: the largest |a| + |b| of a group's two best;
 // mine: the score of the lane's group, a2 its second best.
 template <int VPL>
-MOE_DEV unsigned choose_groups(const Params& p, int lane, const float (&c)[VPL], float& lo, float& hi, float& mag,
-                               float& mine, float& a2) {
+MOE_DEV unsigned choose_groups(const Params& p, int lane, const float (&c)[VPL], float* copy, float& lo, float& hi,
+                               float& mag, float& mine, float& a2) {
     float a1;
-    group_best<float, VPL>(p, lane, c, -CUDART_INF_F, a1, a2);
+    if (p.whole) {
+        group_best<float, VPL>(p, lane, c, -CUDART_INF_F, a1, a2);
+    } else {
+        float tmp[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) tmp[i] = c[i];
+        const float2 best = any_group_best<VPL>(&p, tmp, copy);
+        a1 = best.x;
+        a2 = best.y;
+    }
     mine = (p.rank == 2 && a2 > -CUDART_INF_F) ? a1 + a2 : a1;
-    float of = __shfl_sync(FULL, mine, lane * p.lg & 31);  // of group `lane`
+    float of = __shfl_sync(FULL, mine, lane << p.lsh & 31);  // of group `lane`
     if (lane >= p.G) of = -CUDART_INF_F;
     const unsigned keep = kept_groups<float>(p, lane, of);
     const bool kept = (keep >> lane) & 1u;
@@ -373,25 +381,29 @@ __device__ __noinline__ double exact_choice(int softmax, float r, float m, float
 // The groups to keep where some scores lie within `tol` of the border: those
 // groups' best experts get FP64 scores. False: there are several candidates for
 // a group's best, or a softmax with a bias.
-template <int VPL>
-__device__ __noinline__ bool choose_groups_exact(const Params* pp, const float* r, const float* b, const float* c, float m,
-                                                 float mine, float a2, float lo, float hi, float tol, unsigned* keep) {
+template <typename T>
+__device__ __noinline__ bool choose_groups_exact(const Params* pp, const T* row, float m, float inv, float mine, float a2,
+                                                 float lo, float hi, float tol, unsigned* keep) {
     const Params& p = *pp;
     if (p.softmax && p.bias != nullptr) return false;
-    const int lane = static_cast<int>(lane_id());
+    const int lane = static_cast<int>(lane_id()), g = lane >> p.lsh;
     const bool near = mine > -CUDART_INF_F && mine >= lo - 2.0f * tol && mine <= hi + 2.0f * tol;
     const bool pair = p.rank == 2 && a2 > -CUDART_INF_F;
     const float edge = pair ? a2 : mine;
     int n = 0;
     float ri = 0.0f, bi = 0.0f, rj = 0.0f, bj = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        if (near && c[i] > -CUDART_INF_F && c[i] >= edge - 2.0f * tol) {
-            ++n;
-            rj = ri;
-            bj = bi;
-            ri = r[i];
-            bi = p.bias != nullptr ? b[i] : 0.0f;
+    if (near)  // which lane of the group looks at which expert does not matter
+        for (int j = lane & (p.lg - 1); j < p.gs; j += p.lg) {
+            const int e = g * p.gs + j;
+            const float r = clean(to_f32(row[e])), b = p.bias != nullptr ? clean(p.bias[e]) : 0.0f;
+            const float c = choice(p, r, b, m, inv);
+            if (c > -CUDART_INF_F && c >= edge - 2.0f * tol) {
+                ++n;
+                rj = ri;
+                bj = bi;
+                ri = r;
+                bi = b;
+            }
         }
     int all = n;
     for (int o = 1; o < p.lg; o <<= 1) all += __shfl_xor_sync(FULL, all, o);
@@ -401,7 +413,7 @@ __device__ __noinline__ bool choose_groups_exact(const Params* pp, const float* 
     for (int o = 1; o < p.lg; o <<= 1) x += __shfl_xor_sync(FULL, x, o);
     // the others lie clear on either side: kept above all, or behind all
     const long long key = near ? order_key(x) : mine > hi ? 0x7fffffffffffffffLL : mine > -CUDART_INF_F ? NONE64 + 1 : NONE64;
-    long long of = __shfl_sync(FULL, key, lane * p.lg & 31);
+    long long of = __shfl_sync(FULL, key, lane << p.lsh & 31);
     if (lane >= p.G) of = NONE64;
     *keep = kept_groups<long long>(p, lane, of);
     return true;
@@ -488,7 +500,7 @@ __device__ __noinline__ void route_exact(const Params* pp, long long t, const T*
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             const int g = min((lane * VPL + i) / p.gs, 31);
-            const float x1 = p.lg ? f1 : __shfl_sync(FULL, f1, g), x2 = p.lg ? f2 : __shfl_sync(FULL, f2, g);
+            const float x1 = p.whole ? f1 : __shfl_sync(FULL, f1, g), x2 = p.whole ? f2 : __shfl_sync(FULL, f2, g);
             const float edge = p.rank == 2 && x2 > -CUDART_INF_F ? x2 : x1;
             if (c[i] > -CUDART_INF_F && !(c[i] < edge - slack(edge))) need |= 1u << i;
         }
@@ -496,7 +508,7 @@ __device__ __noinline__ void route_exact(const Params* pp, long long t, const T*
         long long a1, a2;
         group_best<long long, VPL>(p, lane, h, NONE64, a1, a2);
         long long g = p.rank == 2 && a2 != NONE64 ? order_key(key_value(a1) + key_value(a2)) : a1;
-        if (p.lg) g = __shfl_sync(FULL, g, lane * p.lg & 31);
+        if (p.whole) g = __shfl_sync(FULL, g, lane << p.lsh & 31);
         if (lane >= p.G) g = NONE64;
         const unsigned keep = kept_groups<long long>(p, lane, g);
 #pragma unroll
@@ -555,7 +567,9 @@ template <int VPL, typename T, bool VEC>
 __global__ void __launch_bounds__(32 * WARPS, 8)
 group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logits, int32_t* __restrict__ idx,
                    float* __restrict__ w) {
+    __shared__ float copies[WARPS][32 * VPL];
     const int lane = static_cast<int>(lane_id());
+    float* copy = copies[threadIdx.x >> 5];
     pdl_wait();
     pdl_trigger();
     const int step = gridDim.x * WARPS;
@@ -584,42 +598,25 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
             if (ranked) logits_rank<VPL>(r, c);
             if (p.G > 1) {
                 float lo, hi, mag, mine, a2;
-                unsigned keep = 0;
-                if (p.lg) {
-                    keep = choose_groups<VPL>(p, lane, c, lo, hi, mag, mine, a2);
-                } else {
-                    float tmp[VPL], bounds[3];
-#pragma unroll
-                    for (int i = 0; i < VPL; ++i) tmp[i] = c[i];
-                    keep_any_groups<VPL>(&p, tmp, bounds);
-#pragma unroll
-                    for (int i = 0; i < VPL; ++i) c[i] = tmp[i];
-                    lo = bounds[0];
-                    hi = bounds[1];
-                    mag = bounds[2];
-                }
+                unsigned keep = choose_groups<VPL>(p, lane, c, copy, lo, hi, mag, mine, a2);
                 if (hi > -CUDART_INF_F && p.TG < p.G) {
                     // without a bias a score names its logit: |r| and |r - m| are below 48 from 1e-20 on
                     const float tol = ranked ? (lo == hi ? 0.0f : logit_slack(p, m, lo, hi))
                                       : p.bias != nullptr ? 2.0f * sabs + 0x1p-22f * mag : 0x1p-15f * lo;
                     gnear = ranked ? !(lo - hi >= tol) : !(lo - hi > tol) || (by_logit && lo < 1e-20f);
-                    if (gnear && p.lg && !ranked && isfinite(tol) && !(by_logit && lo < 1e-20f)) {
-                        float tr[VPL], tb[VPL], tc[VPL];
-#pragma unroll
-                        for (int i = 0; i < VPL; ++i) {
-                            tr[i] = r[i];
-                            tb[i] = b[i];
-                            tc[i] = c[i];
-                        }
-                        gnear = !choose_groups_exact<VPL>(&p, tr, tb, tc, m, mine, a2, lo, hi, tol, &keep);
-                    }
+                    if (gnear && !ranked && isfinite(tol) && !(by_logit && lo < 1e-20f))
+                        gnear = !choose_groups_exact<T>(&p, row, m, inv, mine, a2, lo, hi, tol, &keep);
                 }
-                if (p.lg) {
+                if (p.whole) {
                     const int at = lane >> p.lsh;
                     if (at >= p.G || !((keep >> at) & 1u)) {
 #pragma unroll
                         for (int i = 0; i < VPL; ++i) c[i] = -CUDART_INF_F;
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i)
+                        if (!((keep >> ((lane * VPL + i) * p.per_group >> 16 & 31)) & 1u)) c[i] = -CUDART_INF_F;
                 }
             }
             if (by_logit && !ranked) logits_rank<VPL>(r, c);
@@ -817,8 +814,10 @@ cudaError_t launch_d(const GroupRouteArgs& a, bool bwd, cudaStream_t s) {
     p.bias = a.bias;
     const int vpl = a.E <= 32 ? 1 : a.E <= 64 ? 2 : a.E <= 128 ? 4 : 8;
     const int lg = p.gs % vpl == 0 ? p.gs / vpl : 0;
-    p.lg = (lg & (lg - 1)) == 0 ? lg : 0;
-    while (p.lg >> (p.lsh + 1)) ++p.lsh;
+    p.whole = lg > 0 && (lg & (lg - 1)) == 0;
+    while ((p.whole ? lg : 32 / p.G) >> (p.lsh + 1)) ++p.lsh;
+    p.lg = 1 << p.lsh;
+    p.per_group = (65536 + p.gs - 1) / p.gs;
     if (vpl == 1) return launch_t<1, T>(a, p, bwd, s);
     if (vpl == 2) return launch_t<2, T>(a, p, bwd, s);
     if (vpl == 4) return launch_t<4, T>(a, p, bwd, s);
