@@ -87,12 +87,13 @@ MOE_DEV float seg_sum(float v) {
     return v;
 }
 
-// Sum of the W values (W a power of two, at most 32) that lanes 0 to W - 1
-// hold, the same in every lane and in a fixed order.
+// Sum of the W <= 32 values that lanes 0 to W - 1 hold (the lanes behind: 0), the
+// same in every lane and in a fixed order.
 template <int W>
 MOE_DEV float group_sum(float v) {
+    constexpr int P = W > 16 ? 32 : W > 8 ? 16 : W > 4 ? 8 : W > 2 ? 4 : W;
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = P / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (W < 32) v = __shfl_sync(0xffffffffu, v, 0);
     return v;
 }

@@ -47,6 +47,13 @@ def test_quantize_rows(A, shape, dt):
 
 
 @pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("shape", [(900, 1280, 0), (700, 1536, 3), (600, 2560, 8), (31, 2561, 0), (400, 5120, 0),
+                                   (65, 6144, 1)], ids=str)
+def test_quantize_three_quarter_widths(A, shape, dt):
+    test_quantize_rows(A, shape, dt)
+
+
+@pytest.mark.parametrize("dt", list(DT))
 def test_quantize_coarse_values(A, dt):
     """Few significant bits: quotients on half steps, and next to them by the
     scale's own rounding, in every row."""

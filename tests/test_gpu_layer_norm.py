@@ -172,3 +172,15 @@ def test_stream_and_graph(A):
     want = A.layer_norm(dy)
     wb = A.layer_norm_backward(x, dy, want["mean"], want["rstd"])
     assert torch.equal(f["y"], want["y"]) and all(torch.equal(b[k], wb[k]) for k in wb)
+
+
+# CTAs of three quarters of a power of two, whole and part full, several rows each
+THREE_QUARTERS = [(40, 1280, 0), (1301, 1536, 8), (1001, 2560, 0), (700, 2561, 1), (505, 5120, 8), (161, 5121, 0),
+                  (320, 6144, 0)]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("shape", THREE_QUARTERS, ids=str)
+def test_three_quarter_widths(A, shape, dt):
+    test_forward(A, shape, dt)
+    test_backward(A, shape, dt)
