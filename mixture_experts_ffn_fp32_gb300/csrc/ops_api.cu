@@ -1,6 +1,7 @@
 // C entry points of the operators around the layer (declared in
 // include/moe.h): layer norm, group-limited routing, row quantisation and the
 // 8-bit expert products. Host-side validation, then the launchers.
+#include <math.h>
 #include <stdlib.h>
 
 #include "common.cuh"
@@ -172,9 +173,13 @@ moe_status check_int8(const moe_int8_config& c) {
 //   4096 x 2048, 8 : 25; 8 rows, 4096 x 4096, 14 : 29; 32 rows of 8 experts,
 //   2048 x 2048, 23 : 23; 32 rows, 4096 x 4096, 33 : 29; 32 rows of 256 experts,
 //   4096 x 4096, 117 : 119).
-//   Tiles of 32 rows while they hold an expert's (against 256: 4 rows each of 256
-//   experts, 570 : 729; 32 each of 8, 2048 x 2048, 27 : 25; 64 each, 33 : 27;
-//   128 rows of one, whose 32 channel tiles are more than the pairs' 16, 29 : 35).
+//   Tiles of 32 rows while they hold an expert's (against 256: 2 rows each of 256
+//   experts, 4096 x 4096, 571 : 701; 4 each, 645 : 787).
+//   Else the form whose waves take less: one of 32-row tiles on every SM takes 1.2 us
+//   and 3.2 ns a reduction step, one of 256-row tiles on the pairs 3 us and 4.5 ns, and
+//   4 us more to begin (tiles of 32 against 256: 801 rows, 368 x 574, 12 : 18; 128 rows,
+//   4096 x 4096, 29 : 35; 4096 x 16384, 66 : 39; 160 rows, 8192 x 2048, 47 : 61;
+//   4000 rows, 256 x 1024, 20 : 18; 10676 rows of 4, 3440 x 245, 80 : 51).
 enum Int8Form { INT8_VEC, INT8_SMALL, INT8_WIDE };
 Int8Form int8_form(const moe_int8_config& c) {
     if (const char* e = getenv("MOE_INT8_FORM")) {
@@ -184,7 +189,15 @@ Int8Form int8_form(const moe_int8_config& c) {
     }
     // (a warp walks its expert's rows eight at a time: few of them)
     if (c.M <= 32LL * c.E && static_cast<double>(c.M) * c.N * c.K <= 134217728.0) return INT8_VEC;
-    return c.M <= 32LL * c.E || c.M <= 128 ? INT8_SMALL : INT8_WIDE;
+    if (c.M <= 32LL * c.E) return INT8_SMALL;
+    const int F = c.swiglu ? c.N / 2 : c.N, sms = num_sms();
+    // us of tiles of `rows` rows and `chans` outputs, at most one part full an expert
+    auto waves = [&](int rows, int chans, int at_a_time, double us, double us_per_k) {
+        const double tiles = ((c.M + rows - 1) / rows + (c.E > 1 ? c.E : 0)) * static_cast<double>((F + chans - 1) / chans);
+        return ceil(tiles / at_a_time) * (us + us_per_k * c.K);
+    };
+    const double small = waves(32, c.swiglu ? 64 : 128, sms, 1.2, 3.2e-3);
+    return small <= 4.0 + waves(256, c.swiglu ? 128 : 256, sms / 2, 3.0, 4.5e-3) ? INT8_SMALL : INT8_WIDE;
 }
 
 }  // namespace
