@@ -98,7 +98,11 @@ template <typename T, int VEC, int NV, int TPR>
 struct Forward {
     static constexpr int THREADS = RowThreads<TPR>::THREADS;
     // CTAs of an SM: as many threads as the registers of a thread's columns leave
-    static constexpr int PER_SM = TPR == 1024 ? 1 : (VEC == 1 || TPR == 512 || NV * VEC > 16 ? 512 : 768) / THREADS;
+    static constexpr int PER_SM = (TPR == 1024 ? 1024
+                                   : NV * VEC <= 4 ? 1536
+                                   : NV * VEC <= 8 ? 1024
+                                   : VEC == 1 || TPR == 512 || NV * VEC > 16 ? 512
+                                                                            : 768) / THREADS;
     // gamma and beta stay in registers where a thread has few columns
     static constexpr bool KEEP = VEC > 1 && NV * VEC <= 16 && TPR < 1024;
     using Fetch = RowFetch<T, VEC, NV, TPR, THREADS, FWD_DEPTH>;
@@ -225,11 +229,13 @@ layer_norm_long_kernel(int R, int d, const T* __restrict__ x, long long xs, cons
     }
 }
 
-// Threads per row of the backward at width d, and CTAs of them on an SM. (192 and
-// 384 leave fewer threads without columns; BF16 rows of 2560, 5120, 100 MB: 70 -> 66,
-// 74 -> 70 us. 96 gained nothing, and three CTAs of 192 spilled: 96 us.)
+// Threads per row of the backward at width d, and CTAs of them on an SM. (16
+// threads for rows to 128, 32 of 16 columns to 512: 100000 BF16 rows of 128 39 -> 29 us,
+// 34605 of 320 43 -> 25. 192 and 384 leave fewer threads without columns; BF16 rows of
+// 2560, 5120, 100 MB: 70 -> 66, 74 -> 70 us. 96 gained nothing, and three CTAs of 192
+// spilled: 96 us.)
 constexpr int bwd_threads(int d) {
-    return d <= 8 * 8 ? 8 : d <= 32 * 8 ? 32 : d <= 128 * 16 ? 128 : d <= 192 * 16 ? 192 : d <= 256 * 16 ? 256 : d <= 384 * 16 ? 384 : 512;
+    return d <= 8 * 8 ? 8 : d <= 16 * 8 ? 16 : d <= 32 * 16 ? 32 : d <= 128 * 16 ? 128 : d <= 192 * 16 ? 192 : d <= 256 * 16 ? 256 : d <= 384 * 16 ? 384 : 512;
 }
 constexpr int bwd_per_sm(int tpr) { return 512 / (tpr <= 32 ? 128 : tpr); }
 
@@ -494,10 +500,26 @@ cudaError_t fwd_t(const LayerNormArgs& a, cudaStream_t s) {
 template <typename T, int VEC>
 cudaError_t fwd_v(const LayerNormArgs& a, cudaStream_t s) {
     const int d = a.d;
-    if (d <= 8 * 16) return fwd_t<T, VEC, 16 / VEC, 8>(a, s);
+    // short rows: few columns a thread, or many would have none (us, against 16 columns of 8 or
+    // 32 threads: 961280 BF16 rows of 16 at an odd pitch 158 -> 55, 143974 of 160 45 -> 27,
+    // 51456 FP16 of 163 37 -> 22)
+    if constexpr (VEC == 1) {
+        if (d <= 8 * 4) return fwd_t<T, 1, 4, 8>(a, s);
+        if (d <= 16 * 4) return fwd_t<T, 1, 4, 16>(a, s);
+        if (d <= 16 * 8) return fwd_t<T, 1, 8, 16>(a, s);
+        if (d <= 32 * 8) return fwd_t<T, 1, 8, 32>(a, s);
+    } else {
+        if (d <= 8 * 8) return fwd_t<T, VEC, 8 / VEC, 8>(a, s);
+        if (d <= 8 * 16) return fwd_t<T, VEC, 16 / VEC, 8>(a, s);
+        if (d <= 16 * 16) return fwd_t<T, VEC, 16 / VEC, 16>(a, s);
+    }
     if (d <= 32 * 16) return fwd_t<T, VEC, 16 / VEC, 32>(a, s);
     // a warp without a sync beats a CTA of four (32768 rows of 1024, BF16: 33 against 39 us)
-    if (d <= 32 * 32 && VEC > 1) return fwd_t<T, VEC, 32 / VEC, 32>(a, s);
+    if constexpr (VEC > 1) {
+        if (d <= 32 * 32) return fwd_t<T, VEC, 32 / VEC, 32>(a, s);
+    } else {
+        if (d <= 128 * 8) return fwd_t<T, 1, 8, 128>(a, s);
+    }
     // CTAs of three quarters beside those of powers of two: fewer threads without columns,
     // and at 384 threads two CTAs an SM for one (BF16 rows of 2560, 5120, 100 MB: 61 -> 49,
     // 68 -> 51 us)
@@ -537,8 +559,14 @@ cudaError_t bwd_t(const LayerNormArgs& a, int grid, float* part, cudaStream_t s)
 template <typename T, int VEC>
 cudaError_t bwd_v(const LayerNormArgs& a, int grid, float* part, cudaStream_t s) {
     switch (bwd_threads(a.d)) {
-        case 8: return bwd_t<T, VEC, 8 / VEC, 8>(a, grid, part, s);
-        case 32: return bwd_t<T, VEC, 8 / VEC, 32>(a, grid, part, s);
+        case 8:
+            if constexpr (VEC == 1)
+                if (a.d <= 8 * 4) return bwd_t<T, 1, 4, 8>(a, grid, part, s);
+            return bwd_t<T, VEC, 8 / VEC, 8>(a, grid, part, s);
+        case 16: return bwd_t<T, VEC, 8 / VEC, 16>(a, grid, part, s);
+        case 32:
+            if (a.d <= 32 * 8) return bwd_t<T, VEC, 8 / VEC, 32>(a, grid, part, s);
+            return bwd_t<T, VEC, 16 / VEC, 32>(a, grid, part, s);
         case 128:
             if (a.d <= 128 * 8) return bwd_t<T, VEC, 8 / VEC, 128>(a, grid, part, s);
             return bwd_t<T, VEC, 16 / VEC, 128>(a, grid, part, s);
