@@ -7,10 +7,11 @@
 // eight rows of one expert and walks the whole reduction, 512 values a step:
 // the weights, which bound the product, are read once per eight rows, straight
 // into registers, and each 16 bytes of them feed 4 dot products per row. The
-// grid covers as many experts as can have rows, and where that leaves SMs idle
-// an expert's rows beyond eight go to further CTAs. Measured: one row, 4096 x
-// 2048, 5.5 us (1.5 TB/s of weights: one round of loads and its latency); 8 rows,
-// 4096 x 4096, 11 us; from 32 rows on the dot products bind (35 T operations/s).
+// grid covers as many experts as can have rows; where that leaves SMs idle CTAs
+// have fewer warps, and an expert's rows beyond eight go to further CTAs.
+// Measured: one row, 4096 x 2048, 5.5 us (1.5 TB/s of weights: one round of loads
+// and its latency); 64 rows of 256 experts, 4096 x 4096, 150 us (6.3 TB/s); from 32
+// rows of one expert on the dot products bind (40 T operations/s).
 #include <math_constants.h>
 
 #include "elem.cuh"
@@ -40,11 +41,14 @@ MOE_DEV void block(const VecParams& p, int e, int n0, int i0, int nrows, int lan
     const int F = SWIGLU ? p.N / 2 : p.N;
     constexpr int NO = SWIGLU ? NC / 2 : NC;  // outputs per row
     const int8_t* wr[NC];
+    float sb[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
         int n = SWIGLU ? n0 + (j >> 1) + (j & 1) * F : n0 + j;
         n = min(n, p.N - 1);  // channels past the end are read from the last and not stored
-        wr[j] = p.b + (static_cast<long long>(e) * p.N + n) * p.K;
+        const long long at = static_cast<long long>(e) * p.N + n;
+        wr[j] = p.b + at * p.K;
+        sb[j] = p.sb[at];
     }
     const int8_t* ar[RB];
     float sa[RB];
@@ -64,6 +68,10 @@ MOE_DEV void block(const VecParams& p, int e, int n0, int i0, int nrows, int lan
         sa[r] = ok ? p.sa[src] : CUDART_NAN_F;
     }
     int acc[RB][NC] = {};
+    // Bytes in flight for one row or two; for more, registers that leave room for a second
+    // CTA (all four forms unrolled: 207 registers; 32 rows of 256 experts 111 -> 90 us,
+    // 128 of 64, 65 -> 49, one row as before; 8 rows, 4096 x 4096, 12 -> 16).
+#pragma unroll (RB == 1 ? 4 : RB == 2 ? 2 : 1)
     for (int k = lane * 16; k < p.K; k += 512) {
         int4 w[NC], x[RB];
 #pragma unroll
@@ -84,12 +92,6 @@ MOE_DEV void block(const VecParams& p, int e, int n0, int i0, int nrows, int lan
     for (int r = 0; r < RB; ++r)
 #pragma unroll
         for (int j = 0; j < NC; ++j) acc[r][j] = __reduce_add_sync(0xffffffffu, acc[r][j]);
-    float sb[NC];
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-        int n = SWIGLU ? n0 + (j >> 1) + (j & 1) * F : n0 + j;
-        sb[j] = p.sb[static_cast<long long>(e) * p.N + min(n, p.N - 1)];
-    }
     // lane r * NO + j stores output j of row r
 #pragma unroll
     for (int r = 0; r < RB; ++r)
@@ -114,7 +116,7 @@ int8_vec_kernel(const VecParams p) {
     const int lane = static_cast<int>(lane_id());
     const int F = SWIGLU ? p.N / 2 : p.N;
     constexpr int NO = SWIGLU ? NC / 2 : NC;
-    const int n0 = (blockIdx.x * WARPS + (threadIdx.x >> 5)) * NO;
+    const int n0 = static_cast<int>(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * NO;
     pdl_wait();
     pdl_trigger();
     if (n0 >= F) return;
@@ -139,7 +141,8 @@ int8_vec_kernel(const VecParams p) {
             const unsigned some = __ballot_sync(0xffffffffu, b > a);
             const int want = static_cast<int>(blockIdx.y) - before;
             if (want < __popc(some)) {
-                const int at = static_cast<int>(__fns(some, 0, want + 1));
+                const bool mine = b > a && __popc(some & ((1u << lane) - 1)) == want;
+                const int at = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
                 e = e0 + at;
                 lo = __shfl_sync(0xffffffffu, a, at);
                 hi = __shfl_sync(0xffffffffu, b, at);
@@ -159,14 +162,17 @@ int8_vec_kernel(const VecParams p) {
 
 template <bool SWIGLU, typename O>
 cudaError_t launch_t(const Int8Args& a, cudaStream_t s) {
-    const int F = SWIGLU ? a.N / 2 : a.N, per = WARPS * (SWIGLU ? NC / 2 : NC);
-    const int slots = a.E < a.M ? a.E : a.M, gx = (F + per - 1) / per;
+    const int F = SWIGLU ? a.N / 2 : a.N, slots = a.E < a.M ? a.E : a.M;
+    auto channel_ctas = [&](int w) { return (F + w * (SWIGLU ? NC / 2 : NC) - 1) / (w * (SWIGLU ? NC / 2 : NC)); };
+    int warps = WARPS;
+    while (warps > 2 && static_cast<long long>(channel_ctas(warps)) * slots < num_sms()) warps /= 2;
+    const int gx = channel_ctas(warps);
     VecParams p{a.M, a.Ma, a.K, a.N, a.E, slots, a.lda, a.a, a.sa, a.b, a.sb, a.offsets, a.rows, a.out, a.err};
     // An expert's rows go over several CTAs, eight at a time, as far as that fills the SMs.
     const long long ctas = static_cast<long long>(gx) * slots;
     const int most = (a.M + 7) / 8, want = static_cast<int>((4LL * num_sms() + ctas - 1) / ctas);
     const int z = want < 1 ? 1 : want < most ? want : most;
-    return launch_pdl(int8_vec_kernel<SWIGLU, O>, dim3(gx, slots + (a.offsets != nullptr ? 1 : 0), z), dim3(32 * WARPS),
+    return launch_pdl(int8_vec_kernel<SWIGLU, O>, dim3(gx, slots + (a.offsets != nullptr ? 1 : 0), z), dim3(32 * warps),
                       0, s, p);
 }
 

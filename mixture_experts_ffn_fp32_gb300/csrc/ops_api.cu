@@ -168,11 +168,12 @@ moe_status check_int8(const moe_int8_config& c) {
 
 // The form of a product, from sizes alone. MOE_INT8_FORM overrides the choice
 // for tests and tuning.
-//   Integer dot products while the whole product is small: they have no tokens'
-//   pass and spread over channels (us, dot products against tiles of 32: one row,
-//   4096 x 2048, 8 : 25; 8 rows, 4096 x 4096, 14 : 29; 32 rows of 8 experts,
-//   2048 x 2048, 23 : 23; 32 rows, 4096 x 4096, 33 : 29; 32 rows of 256 experts,
-//   4096 x 4096, 117 : 119).
+//   Integer dot products while the whole product is small, or few experts have rows:
+//   they have no tokens' pass and spread over channels (us, dot products against tiles
+//   of 32: one row, 4096 x 2048, 8 : 25; 16 rows, 4096 x 4096, 16 : 29; 16 rows,
+//   4096 x 16384, 45 : 33; 128 rows of 64 experts, 2048 x 1408, 49 : 47; 64 rows of 256
+//   experts, 4096 x 4096, 150 : 174; 128, 279 : 291; 256, 469 : 434). A step of their
+//   reduction is 512 values, whatever part of it is there.
 //   Tiles of 32 rows while they hold an expert's (against 256: 2 rows each of 256
 //   experts, 4096 x 4096, 571 : 701; 4 each, 645 : 787).
 //   Else the form whose waves take less: one of 32-row tiles on every SM takes 1.2 us
@@ -187,8 +188,8 @@ Int8Form int8_form(const moe_int8_config& c) {
         if (e[0] == 's') return INT8_SMALL;
         if (e[0] == 'w') return INT8_WIDE;
     }
-    // (a warp walks its expert's rows eight at a time: few of them)
-    if (c.M <= 32LL * c.E && static_cast<double>(c.M) * c.N * c.K <= 134217728.0) return INT8_VEC;
+    const double steps = static_cast<double>(c.M) * c.N * ((c.K + 511) / 512 * 512);
+    if (c.M <= 32LL * c.E && (2LL * c.M <= c.E || steps <= 268435456.0)) return INT8_VEC;
     if (c.M <= 32LL * c.E) return INT8_SMALL;
     const int F = c.swiglu ? c.N / 2 : c.N, sms = num_sms();
     // us of tiles of `rows` rows and `chans` outputs, at most one part full an expert
