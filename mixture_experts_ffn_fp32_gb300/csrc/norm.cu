@@ -508,6 +508,7 @@ cudaError_t fwd_v(const LayerNormArgs& a, cudaStream_t s) {
         if (d <= 16 * 4) return fwd_t<T, 1, 4, 16>(a, s);
         if (d <= 16 * 8) return fwd_t<T, 1, 8, 16>(a, s);
         if (d <= 32 * 8) return fwd_t<T, 1, 8, 32>(a, s);
+        if (d <= 32 * 12) return fwd_t<T, 1, 12, 32>(a, s);
     } else {
         if (d <= 8 * 8) return fwd_t<T, VEC, 8 / VEC, 8>(a, s);
         if (d <= 8 * 16) return fwd_t<T, VEC, 16 / VEC, 8>(a, s);
@@ -566,9 +567,14 @@ cudaError_t bwd_v(const LayerNormArgs& a, int grid, float* part, cudaStream_t s)
         case 16: return bwd_t<T, VEC, 8 / VEC, 16>(a, grid, part, s);
         case 32:
             if (a.d <= 32 * 8) return bwd_t<T, VEC, 8 / VEC, 32>(a, grid, part, s);
+            // elements one by one: as few columns a thread as there are (17835 FP32 rows of 1411 80 -> 72 us)
+            if constexpr (VEC == 1)
+                if (a.d <= 32 * 12) return bwd_t<T, 1, 12, 32>(a, grid, part, s);
             return bwd_t<T, VEC, 16 / VEC, 32>(a, grid, part, s);
         case 128:
             if (a.d <= 128 * 8) return bwd_t<T, VEC, 8 / VEC, 128>(a, grid, part, s);
+            if constexpr (VEC == 1)
+                if (a.d <= 128 * 12) return bwd_t<T, 1, 12, 128>(a, grid, part, s);
             return bwd_t<T, VEC, 16 / VEC, 128>(a, grid, part, s);
         case 192: return bwd_t<T, VEC, 16 / VEC, 192>(a, grid, part, s);
         case 256: return bwd_t<T, VEC, 16 / VEC, 256>(a, grid, part, s);

@@ -186,8 +186,9 @@ def test_three_quarter_widths(A, shape, dt):
     test_backward(A, shape, dt)
 
 
-# 4, 8 and 16 columns a thread, 8 to 128 threads a row; rows that end inside a warp's
-SHORT_ROWS = [(9001, 26, 0), (4100, 17, 3), (1, 2, 0), (6007, 47, 0), (3003, 114, 8), (2050, 99, 1), (5146, 163, 0),
+# 4 to 16 columns a thread, 8 to 128 threads a row; rows that end inside a warp's
+SHORT_ROWS = [(5003, 1411, 5), (3000, 1100, 3), (2900, 257, 0), (777, 384, 3),
+              (9001, 26, 0), (4100, 17, 3), (1, 2, 0), (6007, 47, 0), (3003, 114, 8), (2050, 99, 1), (5146, 163, 0),
               (2500, 160, 0), (3460, 320, 0), (1501, 333, 0), (900, 576, 3), (1001, 777, 0)]
 
 
