@@ -12,14 +12,16 @@
 // taken ranks, or the groups on either side of the border, lie within it (about
 // one in five hundred on random logits) takes FP64 scores, and those only for
 // the experts that could be concerned: a warp's FP64 exponential alone is two
-// thousand cycles here.
+// thousand cycles here, and a token all of whose choices took one held up the
+// whole batch for 10 us.
 //
 // One warp per token, E / 32 consecutive experts a lane: scores, the groups'
 // two best by shuffles, then the lanes' sorted keys popped by one integer
 // maximum over the warp a rank. Bound by instructions (about 900 a token) and,
 // below a few thousand tokens, by the latency of that chain. Measured: 16384 x
 // 256 sigmoid, 8 groups, bias 23 us (3 us of it for the reads at the copy rate);
-// 128 tokens 6 us; the gradient of a raw softmax, 16384 x 256, 13 us (its bytes: 5).
+// 128 tokens 6 us; 10007 x 96 softmax of BF16 logits 13.5 us; groups of 9 experts,
+// which fill no lanes, 7711 x 144, 22 us; the gradient of a raw softmax, 16384 x 256, 13 us (its bytes: 5).
 #include <math_constants.h>
 
 #include "elem.cuh"

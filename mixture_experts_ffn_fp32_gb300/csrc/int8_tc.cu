@@ -21,8 +21,7 @@
 // Warps: 0 copies tokens, 2 weights (TMA), 1 issues MMAs (even CTA), 4-7 (and
 // 12-15 with few tokens) widen weights, 8-15 (8-11) hold the integer sums and
 // store. A stage is 128 of the
-// reduction: 32 KB of tokens and 64 columns of widened weights in tensor
-// memory, which the MMAs free together, and 16 KB of weights in a ring of its
+// reduction: 32 KB of tokens and 64 columns of widened weights in tensor memory, which the MMAs free together, and 16 KB of weights in a ring of its
 // own, which the widening frees: weights are in shared memory before their
 // columns are, so that only the widening lies between two uses of a column.
 //
@@ -32,7 +31,7 @@
 // 2048 x 2816 SwiGLU, 790 us (1.9 P), the tensor pipe active 81 %; there the widening (1110
 // cycles a stage of 1024 MMA cycles) and the last waves bind. 1024 rows of 256 experts,
 // 4096 x 4096: 615 us, 6.8 TB/s of weights. The tokens' pass writes two bytes an
-// element, 110 us for the 131072 rows: the rate at which this memory takes writes
+// element, 108 us for the 131072 rows: the rate at which this memory takes writes
 // alone (a fill of as many bytes takes 141 us).
 //
 // Every wait is bounded (common.cuh).
@@ -133,17 +132,19 @@ int8_tokens_kernel(int M, int Ma, int K, int E, int F, const int8_t* __restrict_
     unsigned most = 0;
     pdl_wait();
     pdl_trigger();
-    const int covered = offsets != nullptr ? min(max(offsets[E], 0), M) : M;
     const int step = gridDim.x * (TOK_THREADS / 32);
-    for (int i = blockIdx.x * (TOK_THREADS / 32) + (threadIdx.x >> 5); i < M; i += step) {
+    int i = blockIdx.x * (TOK_THREADS / 32) + (threadIdx.x >> 5);
+    int row = rows != nullptr && i < M ? rows[i] : i;  // of the next turn
+    const int covered = offsets != nullptr ? min(max(offsets[E], 0), M) : M;
+    for (; i < M; i += step) {
+        int src = row;
+        row = rows != nullptr && i + step < M ? rows[i + step] : i + step;
         if (i >= covered) {
             for (int n = lane; n < F; n += 32) out[static_cast<long long>(i) * F + n] = from_f32<O>(0.0f);
             continue;
         }
-        int src = i;
         bool ok = true;
         if (rows != nullptr) {
-            src = rows[i];
             ok = src >= 0 && src < Ma;
             if (!ok) {
                 if (lane == 0) atomicOr(err, ERRBIT_INDEX);

@@ -7,8 +7,8 @@
 //
 // Both are bound by memory: the forward reads x and writes y, the backward
 // reads x and dy and writes dx, each element once. A row is held in registers
-// by a warp (short rows) or by a CTA, 16 elements a thread, between its
-// reduction and its output, while the next rows of the CTA travel into shared
+// by part of a warp (short rows) or by a CTA, up to 16 elements a thread, between
+// its reduction and its output, while the next rows of the CTA travel into shared
 // memory.
 //
 // Statistics are FP32. The forward sums the row, then the row less a mean: the
@@ -17,9 +17,10 @@
 //
 // Measured (one GB300, 6.8 TB/s copy rate, caches cold): forward, 16384 x 2048
 // BF16 26 us (5.2 TB/s), 8192 x 4096 FP32 5.5 TB/s; backward, 8192 x 4096 BF16
-// 41 us and 5 for the column sums (4.9 TB/s), FP32 5.5 TB/s, 5003 x 1411 FP32
-// unaligned 23 + 5 us. BF16 rows are held back by instructions (unpacking, and
-// the products in FP32): packed FP32 pairs took 29 us to 26 and 45 to 41; more
+// 33 us and 5 for the column sums (6.1 TB/s; 41 before the CTAs' partial sums
+// were stored 16 bytes at a time), 5003 x 1411 FP32 unaligned 19 + 5 us. BF16
+// rows are held back by instructions (unpacking, and the products in FP32):
+// packed FP32 pairs took 29 us to 26 forward and 45 to 41 backward; more
 // rows ahead or more CTAs do not help (35 us with 1216 CTAs, each of which reads
 // gamma and beta again). Few rows are latency: 128 x 4096 4 us.
 #include "elem.cuh"
