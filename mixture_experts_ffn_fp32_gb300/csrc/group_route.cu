@@ -632,10 +632,10 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
                 rk = clean(to_f32(row[id]));
                 val = by_logit ? rk : choice(p, rk, __ldg(p.bias + id), m, inv);
             }
-            // every expert behind lies at or below the last key with its dropped bits set;
-            // a key drops nothing of a 16-bit logit
+            // every expert behind lies at or below the last key with its dropped bits set (an
+            // infinity stays one); a key drops nothing of a 16-bit logit
             const bool whole = by_logit && sizeof(T) == 2;
-            if (!whole && lane > p.K && key >= FIRST) val = key_value(key | 255);
+            if (!whole && lane > p.K && key >= FIRST) val = key_value(min(key | 255, 0x7f800000));
             const float rest = __shfl_sync(FULL, val, p.K + 1);
             const float next = __shfl_down_sync(FULL, val, 1);
             if (__any_sync(FULL, lane < p.K && next > val)) {
@@ -661,8 +661,9 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
                 // equal inputs are an exact tie: the lower index is first already
                 if (!(val - val2 > tol)) close = !(rk == rk2 && (by_logit || p.bias[id] == p.bias[id2]));
                 near = lane == p.K - 1 && rest > -CUDART_INF_F && !(val - rest > tol);
-                // whole keys rank equal logits; the next lower one is a step of the type below, and clear
-                if (whole && rest == val && tol <= 0x1p-12f * fabsf(val)) near = false;
+                // whole keys rank equal logits; the next lower one is a step of the type below, and
+                // clear (not below an infinity, whose sigmoid large logits have in FP64 too)
+                if (whole && rest == val && val < CUDART_INF_F && tol <= 0x1p-12f * fabsf(val)) near = false;
             }
             near = near || gnear;
             if (__any_sync(FULL, close)) {
