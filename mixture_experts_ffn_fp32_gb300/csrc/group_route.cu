@@ -277,6 +277,19 @@ MOE_DEV float logit_slack(const Params& p, float m, float a, float b) {
     return b > -690.0f && a < 80.0f ? 1e-11f + 4e-16f * __expf(a) : CUDART_INF_F;
 }
 
+// Groups ranked by their best logits tie exactly at the border, at `tie`: whether
+// FP64 could take a group above or below for equal to them too. `mine`: the score of
+// the lane's group.
+__device__ __noinline__ bool tied_border_near(const Params* pp, float m, float mine, float tie) {
+    const Params& p = *pp;
+    const int lane = static_cast<int>(lane_id());
+    float of = __shfl_sync(FULL, mine, lane << p.lsh & 31);  // of group `lane`
+    if (lane >= p.G) of = -CUDART_INF_F;
+    const float up = -warp_max(of > tie ? -of : -CUDART_INF_F), down = warp_max(of < tie ? of : -CUDART_INF_F);
+    return (__any_sync(FULL, of > tie) && !(up - tie > logit_slack(p, m, up, tie))) ||
+           (down > -CUDART_INF_F && !(tie - down > logit_slack(p, m, tie, down)));
+}
+
 // Sorts a lane's keys in descending order (Batcher's odd-even merge).
 MOE_DEV void order2(int& a, int& b) {
     const int hi = max(a, b);
@@ -603,9 +616,13 @@ group_route_kernel(const __grid_constant__ Params p, const T* __restrict__ logit
                 unsigned keep = choose_groups<VPL>(p, lane, c, copy, lo, hi, mag, mine, a2);
                 if (hi > -CUDART_INF_F && p.TG < p.G) {
                     // without a bias a score names its logit: |r| and |r - m| are below 48 from 1e-20 on
-                    const float tol = ranked ? (lo == hi ? 0.0f : logit_slack(p, m, lo, hi))
+                    const float tol = ranked ? logit_slack(p, m, lo, hi)
                                       : p.bias != nullptr ? 2.0f * sabs + 0x1p-22f * mag : 0x1p-15f * lo;
-                    gnear = ranked ? !(lo - hi >= tol) : !(lo - hi > tol) || (by_logit && lo < 1e-20f);
+                    gnear = !(lo - hi > tol) || (by_logit && !ranked && lo < 1e-20f);
+                    // an exact tie: the lower index stays, unless FP64 knows more equals (not where
+                    // even the type's next value is clear)
+                    constexpr float STEP = sizeof(T) == 2 ? 0x1p-12f : 0x1p-25f;
+                    if (ranked && lo == hi) gnear = !(tol <= STEP * fabsf(lo) && lo < CUDART_INF_F) && tied_border_near(&p, m, mine, lo);
                     if (gnear && !ranked && isfinite(tol) && !(by_logit && lo < 1e-20f))
                         gnear = !choose_groups_exact<T>(&p, row, m, inv, mine, a2, lo, hi, tol, &keep);
                 }
