@@ -41,6 +41,9 @@ constexpr int BWD_DEPTH = 2;
 // 1 / sqrt(var + eps); a variance that rounding took below zero is zero, a NaN stays.
 MOE_DEV float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
+// A mean and what rounding left in it, which is no number where the mean is infinite.
+MOE_DEV float joined(float m, float rest) { return rest == rest ? m + rest : m; }
+
 // Mean and variance of a row from its threads' NV x VEC values (in pairs), left
 // as v - m, m a mean the warp took of its own. Its sums of the differences and of
 // their squares follow, and the CTA joins the warps' numbers (m, r, q of n values)
@@ -75,7 +78,7 @@ MOE_DEV void row_moments(F2 (&v)[NV * VEC / 2], int d, int t, float inv_d, float
     const float r = seg_sum<S>(both(r2)), q = seg_sum<S>(both(q2));
     if constexpr (W == 1) {
         const float rest = r * inv_d;
-        mean = m + rest;
+        mean = joined(m, rest);
         shift = -rest;
         var = q * inv_d - rest * rest;
     } else {
@@ -90,7 +93,7 @@ MOE_DEV void row_moments(F2 (&v)[NV * VEC / 2], int d, int t, float inv_d, float
         const float dm = e.x - m0;
         const float rest = group_sum<W>(e.w * dm + e.y) * inv_d;
         var = group_sum<W>(e.z + 2.0f * dm * e.y + e.w * dm * dm) * inv_d - rest * rest;
-        mean = m0 + rest;
+        mean = joined(m0, rest);
         shift = (m - m0) - rest;
     }
 }
@@ -224,7 +227,7 @@ layer_norm_long_kernel(int R, int d, const T* __restrict__ x, long long xs, cons
             y[row * ys + c] = from_f32<T>(o);
         }
         if (threadIdx.x == 0) {
-            if (mean != nullptr) mean[row] = m0 + rest;
+            if (mean != nullptr) mean[row] = joined(m0, rest);
             if (rstd != nullptr) rstd[row] = rs;
         }
     }
