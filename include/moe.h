@@ -454,7 +454,8 @@ moe_status moe_matmul_int8_workspace_size(const moe_int8_config* cfg, size_t* by
  *   The form is chosen from the rows per expert; the environment variable
  * MOE_INT8_FORM, read at each call, overrides it for tests and tuning ("vec":
  * integer dot products; "small", "wide": tensor cores, tiles of up to 32 or
- * 256 rows). The sums are exact in every form; the scales round alike. */
+ * 256 rows). The sums are exact in every form, and what follows them (the row's
+ * scale, the channel's, SiLU) is the same arithmetic: equal outputs bit for bit. */
 moe_status moe_matmul_int8(const moe_int8_config* cfg, const int8_t* a, int64_t a_stride,
                            const float* a_scale, const int8_t* b, const float* b_scale,
                            const int32_t* offsets, const int32_t* rows, void* out, void* ws,

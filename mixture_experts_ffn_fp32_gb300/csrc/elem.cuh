@@ -60,7 +60,8 @@ struct Raw<T, 1> {
 // sigmoid(v) = exp(v) / (1 + exp(v)) below zero, where exp(-v) would leave
 // FP32's range while v sigmoid(v) is still in it. On the special-function
 // unit: the argument |v| log2(e) keeps what its rounding lost (and what log2(e)
-// itself does), so that the result is off by 4 units of 2^-23 at any v.
+// itself does), so that the result is off by 4 units of 2^-23 down to v = -87, and
+// below that, where it is subnormal, by a unit of 2^-149 besides.
 MOE_DEV float sigmoid_f(float v) {
     constexpr double LOG2E = 1.4426950408889634;
     constexpr float HI = static_cast<float>(LOG2E), LO = static_cast<float>(LOG2E - static_cast<double>(HI));
@@ -71,6 +72,16 @@ MOE_DEV float sigmoid_f(float v) {
     e = fmaf(e, lost * 0.6931471805599453f, e);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return (v >= 0.0f ? 1.0f : e) * r;
+}
+
+// SiLU's sigmoid in the output's precision: 16-bit outputs take the fast
+// exponential and division, off by (4 + 1.2 |v|) units of 2^-23 at most down to
+// v = -87 (8-bit gate/up product of 131072 rows 1012 us with the other one, 992 with this).
+template <typename O>
+MOE_DEV float sigmoid_to(float v) {
+    if constexpr (sizeof(O) == 4) return sigmoid_f(v);
+    const float e = __expf(-fabsf(v));
+    return __fdividef(v >= 0.0f ? 1.0f : e, 1.0f + e);
 }
 
 MOE_DEV float warp_sum(float v) {

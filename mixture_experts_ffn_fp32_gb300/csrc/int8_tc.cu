@@ -270,15 +270,6 @@ MOE_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n
 template <int N>
 MOE_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// SiLU's sigmoid in the output's precision: 16-bit outputs take the fast
-// exponential and division, off by (4 + 1.2 |v|) units of 2^-23 at most.
-template <typename O>
-MOE_DEV float epi_sigmoid(float v) {
-    if constexpr (sizeof(O) == 4) return sigmoid_f(v);
-    const float e = __expf(-fabsf(v));
-    return __fdividef(v >= 0.0f ? 1.0f : e, 1.0f + e);
-}
-
 // Arrive on an mbarrier of the other CTA, for what tensor memory holds: the
 // tcgen05 wait and fence before it order that, so the arrival carries the
 // default (CTA) release. A cluster-scope release waits for every access of the
@@ -661,6 +652,9 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
             const bool in = oc < p.F;
             const int ch = SWIGLU && lane >= 16 ? oc + p.F : oc;
             const float sb = in ? __ldg(p.sb + static_cast<long long>(t.e) * p.N + ch) : 0.0f;
+            // SwiGLU: lane l + 16 holds the up of lane l's gate
+            const float sb2 = SWIGLU ? __shfl_xor_sync(0xffffffffu, sb, 16) : 0.0f;
+            const float sbg = lane >> 4 ? sb2 : sb, sbu = lane >> 4 ? sb : sb2;
             float sa[TOK / 32];
 #pragma unroll
             for (int j = 0; j < TOK / 32; ++j) {
@@ -678,23 +672,23 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                     float g[4], up[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float a = __uint_as_float(acc[i + 2 * k]) * sb, b = __uint_as_float(acc[i + 2 * k + 1]) * sb;
+                        const float a = __uint_as_float(acc[i + 2 * k]), b = __uint_as_float(acc[i + 2 * k + 1]);
                         const float other = __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
                         const float st = __shfl_sync(0xffffffffu, sa[i >> 5], ((i + 2 * k) & 31) + upper);
-                        g[k] = (upper ? other : a) * st;
-                        up[k] = (upper ? b : other) * st;
+                        g[k] = (upper ? other : a) * st * sbg;
+                        up[k] = (upper ? b : other) * st * sbu;
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int ti = i + 2 * k + upper;
-                        const O h = from_f32<O>(g[k] * epi_sigmoid<O>(g[k]) * up[k]);
+                        const O h = from_f32<O>(g[k] * sigmoid_to<O>(g[k]) * up[k]);
                         if (in && c0 + ti < t.n) orow[static_cast<long long>(ti) * p.F] = h;
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const float st = __shfl_sync(0xffffffffu, sa[i >> 5], (i + k) & 31);
-                        const O h = from_f32<O>(__uint_as_float(acc[i + k]) * sb * st);
+                        const O h = from_f32<O>(__uint_as_float(acc[i + k]) * st * sb);
                         if (in && c0 + i + k < t.n) orow[static_cast<long long>(i + k) * p.F] = h;
                     }
                 }

@@ -102,7 +102,7 @@ MOE_DEV void block(const VecParams& p, int e, int n0, int i0, int nrows, int lan
             if (SWIGLU) {
                 const float g = static_cast<float>(acc[r][2 * j]) * sa[r] * sb[2 * j];
                 const float u = static_cast<float>(acc[r][2 * j + 1]) * sa[r] * sb[2 * j + 1];
-                v = g * sigmoid_f(g) * u;
+                v = g * sigmoid_to<O>(g) * u;
             } else {
                 v = static_cast<float>(acc[r][j]) * sa[r] * sb[j];
             }
