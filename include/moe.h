@@ -448,9 +448,10 @@ moe_status moe_matmul_int8_workspace_size(const moe_int8_config* cfg, size_t* by
  *   a, b, out 16-byte aligned, ws 256-byte aligned.
  * Rows from offsets[E] on are written as zeros. Offsets are clamped to
  * [0, M]; a row index outside [0, Ma) makes its product row NaN and sets
- * MOE_ERR_DEVICE_INDEX in the workspace's error word. The call adds to that
- * word and never clears it: have it zeroed before the first call,
- * moe_workspace_status reads and clears it.
+ * MOE_ERR_DEVICE_INDEX in the workspace's error word; a bounded device wait
+ * that runs out makes the outputs that are not stored yet NaN and sets
+ * MOE_ERR_TIMEOUT. The call adds to that word and never clears it: have it
+ * zeroed before the first call, moe_workspace_status reads and clears it.
  *   The form is chosen from the rows per expert; the environment variable
  * MOE_INT8_FORM, read at each call, overrides it for tests and tuning ("vec":
  * integer dot products; "small", "wide": tensor cores, tiles of up to 32 or

@@ -729,8 +729,9 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     and rows [M] int32 as dispatch's offsets and sorted_token (None: one expert
     takes every row; rows of a in order). With swiglu the channels of an
     expert are its gates, then its ups, and the output is SiLU(gate) * up.
-    Returns out [M, N] ([M, N / 2] with swiglu). ws: see alloc_int8_workspace
-    (allocated when None)."""
+    Returns out [M, N] ([M, N / 2] with swiglu). ws: see alloc_int8_workspace. When
+    None one is allocated for the call and its error word is not read: a bad row
+    index, or a device wait that ran out, then shows by the NaNs it leaves alone."""
     if a.dim() != 2 or b.dim() != 3 or not a.is_cuda or a.dtype != torch.int8:
         raise ValueError("a must be a [Ma, K] int8 CUDA tensor and b [E, N, K]")
     E, N, K = b.shape

@@ -80,7 +80,7 @@ struct Form {
     static constexpr int BAR_OFF = W_OFF + WSTAGES * W_BYTES;
     static constexpr int MISC_OFF = BAR_OFF + 8 * NBARS;
     static constexpr int TAB_OFF = (MISC_OFF + 16 + 15) / 16 * 16;
-    static constexpr int SMEM_BYTES = TAB_OFF + (2 * (MAXE + 1) + THREADS / 32) * 4 + 1024;
+    static constexpr int SMEM_BYTES = TAB_OFF + (2 * (MAXE + 1) + 2 * (THREADS / 32)) * 4 + 1024;
     static_assert(A_COL + 64 * STAGES <= TMEM_COLS, "tensor memory");
     static_assert(REGS_SUM <= 4 * 128, "the shares exceed the launch's registers");
     static_assert(T_HALF % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory");
@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
     int* s_tp = reinterpret_cast<int*>(smem + G::TAB_OFF);
     int* s_off = s_tp + MAXE + 1;
     int* s_l1 = s_off + MAXE + 1;
+    int* s_left = s_l1 + THREADS / 32;  // an epilogue warp's first tile that it did not store
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr bool PAIR = G::CTAS == 2;
@@ -571,11 +572,11 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                     }
                     tc_st_32x32b_x32(at + 32 * h, r);
                 }
+                tc_wait_st();
                 if (!free) {
                     ok = false;
                     break;
                 }
-                tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -603,7 +604,8 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
         const int c0 = TOK * ((warp - 8) >> 2);  // this warp's token columns [c0, c0 + TOK)
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = unit0; u < total && ok; u += ustep) {
+        int u = unit0;
+        for (; u < total; u += ustep) {
             const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
             const uint32_t ta = tmem + static_cast<uint32_t>(c0) + (static_cast<uint32_t>(q * 32) << 16);
             // one chunk: the FP32 accumulator as it is; several: their integer sum
@@ -693,6 +695,22 @@ __global__ void __launch_bounds__(THREADS, 1) int8_tc_kernel(const __grid_consta
                     }
                 }
             }
+        }
+        if (lane == 0) s_left[warp] = u;
+    }
+
+    // A wait ran out: tiles that are not stored become NaN, so that it shows also where
+    // nobody reads the error word.
+    __syncwarp();
+    if (*abort_flag && warp >= 8 && warp < 8 + G::EPI_WARPS) {
+        const int c0 = G::EPI_TOK * ((warp - 8) >> 2);
+        for (int u = s_left[warp]; u < total; u += ustep) {
+            const Tile t = tile_of<G::CTAS * OUT_CH, NT>(u, p, s_tp, s_off);
+            const int oc = t.f0 + rank * OUT_CH + (SWIGLU ? 16 * (warp & 3) + (lane & 15) : 32 * (warp & 3) + lane);
+            if (oc >= p.F) continue;
+            O* orow = static_cast<O*>(p.out) + static_cast<long long>(t.row0 + c0) * p.F + oc;
+            for (int i = SWIGLU ? lane >> 4 : 0; i < min(G::EPI_TOK, t.n - c0); i += SWIGLU ? 2 : 1)
+                orow[static_cast<long long>(i) * p.F] = from_f32<O>(CUDART_NAN_F);
         }
     }
 
