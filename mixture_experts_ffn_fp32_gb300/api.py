@@ -211,16 +211,18 @@ def alloc_workspace(spec: LayerSpec, device="cuda") -> torch.Tensor:
     return torch.empty(workspace_size(spec), dtype=torch.uint8, device=device)
 
 
-def _dev(t, dtype, name, shape=None):
+def _dev(t, dtype, name, shape=None, here=None):
     if t is None:
         raise ValueError(f"{name} is required")
-    if not t.is_cuda:
+    if here is not None:
+        _at(t, name, here)
+    elif not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
@@ -489,8 +491,20 @@ def workspace_status(ws: torch.Tensor, stream=None) -> int:
 # ---------------------------------------------------------------------------
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _OUT_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _here(stream) -> int:
+    """The device a call runs on: the current one, or the given stream's. Its outputs
+    will be there, its kernels launch there, and its tensors have to be there."""
+    return _current_device() if stream is None else stream.device_index
+
+
+def _at(t, name, here):
+    if t.get_device() != here:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{here}")
 
 
 def _rows(t, name, dtype=None, shape=None):
@@ -562,11 +576,11 @@ def _on(stream, *inputs):
     return _HERE if stream is None else _On(stream, *inputs)
 
 
-def _raw_stream(stream, t) -> int:
-    """The stream's handle, else that of the current stream of t's device (the
-    binding that torch's own generated code uses: torch.cuda.current_stream()
-    takes several microseconds, as long as a small kernel)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _raw_stream(stream, here) -> int:
+    """The stream's handle, else that of the device's current stream (the binding
+    that torch's own generated code uses: torch.cuda.current_stream() takes several
+    microseconds, as long as a small kernel)."""
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
 
 
 def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, stream=None) -> dict:
@@ -574,17 +588,19 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, strea
     bias [d] FP32 or None. Returns y [R, d] in x's type and the FP32 statistics
     mean and rstd [R] that the backward takes."""
     xs = _rows(x, "x")
+    here = _here(stream)
+    _at(x, "x", here)
     R, d = x.shape
     if weight is not None:
-        _dev(weight, torch.float32, "weight", (d,))
+        _dev(weight, torch.float32, "weight", (d,), here)
     if bias is not None:
-        _dev(bias, torch.float32, "bias", (d,))
+        _dev(bias, torch.float32, "bias", (d,), here)
     with _on(stream, x, weight, bias):
         y = _empty(x.dtype, R, d)
         mean = _empty(torch.float32, R)
         rstd = _empty(torch.float32, R)
         _check(lib().moe_layer_norm(R, d, _DTYPES[x.dtype], x.data_ptr(), xs, _ptr(weight), _ptr(bias), eps,
-                                    y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, x)),
+                                    y.data_ptr(), d, mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, here)),
                "moe_layer_norm")
     return {"y": y, "mean": mean, "rstd": rstd}
 
@@ -604,12 +620,17 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     dweight and dbias [d] FP32, given layer_norm's mean and rstd. ws: uint8 of
     layer_norm_backward_workspace_size(R, d) bytes (allocated when None)."""
     xs = _rows(x, "x")
+    here = _here(stream)
+    _at(x, "x", here)
     R, d = x.shape
     dys = _rows(dy, "dy", x.dtype, x.shape)
-    _dev(mean, torch.float32, "mean", (R,))
-    _dev(rstd, torch.float32, "rstd", (R,))
+    _at(dy, "dy", here)
+    _dev(mean, torch.float32, "mean", (R,), here)
+    _dev(rstd, torch.float32, "rstd", (R,), here)
     if weight is not None:
-        _dev(weight, torch.float32, "weight", (d,))
+        _dev(weight, torch.float32, "weight", (d,), here)
+    if ws is not None:
+        _at(ws, "ws", here)
     with _on(stream, dy, x, mean, rstd, weight, ws):
         out = {"dx": _empty(x.dtype, R, d)}
         if weight_grads:
@@ -621,7 +642,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
                                              mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
                                              out["dx"].data_ptr(), d, _ptr(out.get("dweight")),
                                              _ptr(out.get("dbias")), _ptr(ws), 0 if ws is None else ws.numel(),
-                                             _raw_stream(stream, x)), "moe_layer_norm_backward")
+                                             _raw_stream(stream, here)), "moe_layer_norm_backward")
     return out
 
 
@@ -649,15 +670,17 @@ def group_route(logits: torch.Tensor, K: int, n_groups: int = 1, topk_groups: in
     best. Experts whose logit is -inf are never taken; slots that stay empty
     hold id -1, weight 0. Returns idx [T, K] int32 and w [T, K] FP32."""
     ls = _rows(logits, "logits")
+    here = _here(stream)
+    _at(logits, "logits", here)
     T, E = logits.shape
     if bias is not None:
-        _dev(bias, torch.float32, "bias", (E,))
+        _dev(bias, torch.float32, "bias", (E,), here)
     cfg = _group_config(logits, K, n_groups, topk_groups, group_rank, score, renormalize, scale)
     with _on(stream, logits, bias):
         out = {"idx": _empty(torch.int32, T, max(K, 0)),
                "w": _empty(torch.float32, T, max(K, 0))}
         _check(lib().moe_group_route(cfg, logits.data_ptr(), ls, _ptr(bias), out["idx"].data_ptr(),
-                                     out["w"].data_ptr(), _raw_stream(stream, logits)), "moe_group_route")
+                                     out["w"].data_ptr(), _raw_stream(stream, here)), "moe_group_route")
     return out
 
 
@@ -666,17 +689,19 @@ def group_route_backward(dw: torch.Tensor, idx: torch.Tensor, logits: torch.Tens
     """moe_group_route_backward: the gradient with respect to the logits (their
     type) of sum(dw * w), the selection idx held fixed."""
     ls = _rows(logits, "logits")
+    here = _here(stream)
+    _at(logits, "logits", here)
     T, E = logits.shape
     if idx.dim() != 2:
         raise ValueError(f"idx must be [T, K], got {tuple(idx.shape)}")
     K = idx.size(1)
-    _dev(idx, torch.int32, "idx", (T, K))
-    _dev(dw, torch.float32, "dw", (T, K))
+    _dev(idx, torch.int32, "idx", (T, K), here)
+    _dev(dw, torch.float32, "dw", (T, K), here)
     cfg = _group_config(logits, K, 1, 1, 1, score, renormalize, scale)
     with _on(stream, dw, idx, logits):
         out = _empty(logits.dtype, T, E)
         _check(lib().moe_group_route_backward(cfg, logits.data_ptr(), ls, idx.data_ptr(),
-                                              dw.data_ptr(), out.data_ptr(), _raw_stream(stream, logits)),
+                                              dw.data_ptr(), out.data_ptr(), _raw_stream(stream, here)),
                "moe_group_route_backward")
     return out
 
@@ -687,12 +712,14 @@ def quantize_rows(x: torch.Tensor, stream=None) -> dict:
     out for matmul_int8 by quantising the rows of their transpose:
     ``quantize_rows(W.transpose(1, 2).reshape(E * N, K))``."""
     xs = _rows(x, "x")
+    here = _here(stream)
+    _at(x, "x", here)
     R, K = x.shape
     with _on(stream, x):
         out = {"q": _empty(torch.int8, R, K),
                "scale": _empty(torch.float32, R)}
         _check(lib().moe_quantize_rows(R, K, _DTYPES[x.dtype], x.data_ptr(), xs, out["q"].data_ptr(),
-                                       out["scale"].data_ptr(), _raw_stream(stream, x)), "moe_quantize_rows")
+                                       out["scale"].data_ptr(), _raw_stream(stream, here)), "moe_quantize_rows")
     return out
 
 
@@ -738,18 +765,22 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
     Ma = a.size(0)
     if a.size(1) != K or (K > 1 and a.stride(1) != 1):
         raise ValueError(f"a must have contiguous rows of {K} elements, got {tuple(a.shape)}")
-    _dev(b, torch.int8, "b")
-    _dev(a_scale, torch.float32, "a_scale", (Ma,))
-    _dev(b_scale, torch.float32, "b_scale", (E, N))
+    here = _here(stream)
+    _at(a, "a", here)
+    _dev(b, torch.int8, "b", None, here)
+    _dev(a_scale, torch.float32, "a_scale", (Ma,), here)
+    _dev(b_scale, torch.float32, "b_scale", (E, N), here)
     if offsets is not None:
-        _dev(offsets, torch.int32, "offsets", (E + 1,))
+        _dev(offsets, torch.int32, "offsets", (E + 1,), here)
     M = Ma
     if rows is not None:
         if rows.dim() != 1:
             raise ValueError(f"rows must be [M], got {tuple(rows.shape)}")
-        _dev(rows, torch.int32, "rows")
+        _dev(rows, torch.int32, "rows", None, here)
         M = rows.size(0)
     cfg = _int8_config(M, Ma, K, N, E, swiglu, out_dtype)
+    if ws is not None:
+        _at(ws, "ws", here)
     with _on(stream, a, a_scale, b, b_scale, offsets, rows, ws):
         if ws is None:
             ws = _empty(torch.uint8, _int8_ws(*cfg))
@@ -757,7 +788,7 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
         _check(lib().moe_matmul_int8(_struct(Int8Config, *cfg), a.data_ptr(), a.stride(0) if Ma > 1 else K,
                                      a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),
                                      _ptr(rows), out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
-                                     _raw_stream(stream, a)), "moe_matmul_int8")
+                                     _raw_stream(stream, here)), "moe_matmul_int8")
     return out
 
 
