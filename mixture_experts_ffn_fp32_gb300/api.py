@@ -491,9 +491,27 @@ def workspace_status(ws: torch.Tensor, stream=None) -> int:
 # ---------------------------------------------------------------------------
 
 _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _OUT_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _internal(path, public):
+    """A binding that torch's own generated code uses, or, in a torch without it, the
+    public function that does the same at more host time."""
+    f = torch._C
+    for name in path.split("."):
+        f = getattr(f, name, None)
+    return public if f is None else f
+
+
+# An uninitialised CUDA tensor of the current device: a third less host time than
+# torch.empty, of which a call has three. torch.cuda.current_stream() takes several
+# microseconds, as long as a small kernel.
+_empty_strided = _internal("_dynamo.guards._empty_strided_cuda",
+                           lambda size, stride, dtype: torch.empty_strided(size, stride, dtype=dtype, device="cuda"))
+_current_device = _internal("_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = _internal("_cuda_getCurrentRawStream",
+                                lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _here(stream) -> int:
@@ -530,10 +548,6 @@ def _rows(t, name, dtype=None, shape=None):
         raise ValueError(f"{name}'s rows must not overlap")
     return pitch
 
-
-# Uninitialised CUDA tensors of the current device, as torch's own generated code
-# makes them: a third less host time than torch.empty, of which a call has three.
-_empty_strided = torch._C._dynamo.guards._empty_strided_cuda
 
 
 def _empty(dtype, n, m=None):
@@ -577,10 +591,8 @@ def _on(stream, *inputs):
 
 
 def _raw_stream(stream, here) -> int:
-    """The stream's handle, else that of the device's current stream (the binding
-    that torch's own generated code uses: torch.cuda.current_stream() takes several
-    microseconds, as long as a small kernel)."""
-    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+    """The stream's handle, else that of the device's current stream."""
+    return _current_raw_stream(here) if stream is None else stream.cuda_stream
 
 
 def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-5, stream=None) -> dict:
