@@ -670,7 +670,7 @@ def _group_config(logits, K, n_groups, topk_groups, group_rank, score, renormali
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
     T, E = logits.shape
     return _struct(GroupRouteConfig, T, E, K, n_groups, topk_groups, group_rank, SCORES[score],
-                   1 if renormalize else 0, scale, _DTYPES[logits.dtype])
+                   1 if renormalize else 0, float(scale), _DTYPES[logits.dtype])
 
 
 def group_route(logits: torch.Tensor, K: int, n_groups: int = 1, topk_groups: int = 1, bias=None,
