@@ -84,12 +84,6 @@ MOE_DEV float sigmoid_to(float v) {
     return __fdividef(v >= 0.0f ? 1.0f : e, 1.0f + e);
 }
 
-MOE_DEV float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 // Sum over the TPR <= 32 threads of a row, the same in all of them.
 template <int TPR>
 MOE_DEV float seg_sum(float v) {

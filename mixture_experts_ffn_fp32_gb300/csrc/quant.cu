@@ -237,14 +237,21 @@ cudaError_t quant_v(const QuantArgs& a, cudaStream_t s) {
     if (a.K <= 32 * 16) return quant_t<T, VEC, 16 / VEC, 32>(a, s);
     // a warp without a sync beats a CTA of four (32768 rows of 1024, BF16: 19 against 26 us);
     // with 64 elements a lane it no longer does (16384 of 2048: 23 against 21 us)
-    if (a.K <= 32 * 32 && VEC > 1) return quant_t<T, VEC, 32 / VEC, 32>(a, s);
-    if (a.K <= 128 * 8) return quant_t<T, VEC, 8 / VEC, 128>(a, s);
-    // three quarters of those for 16-bit rows (BF16 of 2560, 100 MB: 43 -> 39 us; FP32 of 2880: 29 -> 37)
-    if (a.K <= 96 * 16 && SHORT) return quant_t<T, VEC, 16 / VEC, 96>(a, s);
+    if constexpr (VEC > 1) {
+        if (a.K <= 32 * 32) return quant_t<T, VEC, 32 / VEC, 32>(a, s);
+    } else {
+        if (a.K <= 128 * 8) return quant_t<T, 1, 8, 128>(a, s);
+    }
+    // three quarters of those of powers of two for 16-bit rows (BF16 of 2560, 100 MB: 43 -> 39
+    // us; FP32 of 2880: 29 -> 37)
+    if constexpr (SHORT)
+        if (a.K <= 96 * 16) return quant_t<T, VEC, 16 / VEC, 96>(a, s);
     if (a.K <= 128 * 16) return quant_t<T, VEC, 16 / VEC, 128>(a, s);
-    if (a.K <= 192 * 16 && SHORT) return quant_t<T, VEC, 16 / VEC, 192>(a, s);
+    if constexpr (SHORT)
+        if (a.K <= 192 * 16) return quant_t<T, VEC, 16 / VEC, 192>(a, s);
     if (a.K <= 256 * 16) return quant_t<T, VEC, 16 / VEC, 256>(a, s);
-    if (a.K <= 384 * 16 && SHORT) return quant_t<T, VEC, 16 / VEC, 384>(a, s);
+    if constexpr (SHORT)
+        if (a.K <= 384 * 16) return quant_t<T, VEC, 16 / VEC, 384>(a, s);
     if (a.K <= 512 * 16) return quant_t<T, VEC, 16 / VEC, 512>(a, s);
     return quant_t<T, VEC, 16 / VEC, 1024>(a, s);
 }
