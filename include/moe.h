@@ -396,7 +396,8 @@ typedef struct moe_group_route_config {
 /* Group-limited routing of T rows of E logits: choices c = s + bias, the
  * topk_groups best groups, the K largest c among their experts, weights from
  * the uncorrected s. Equal values rank the lower index first; what is taken
- * is what 64-bit arithmetic on the given logits and bias takes. An expert
+ * is what 64-bit arithmetic on the given logits and bias takes (of a softmax
+ * without a bias on its exponentials, whose denominator is common). An expert
  * whose logit or choice is -inf or NaN is never taken: masked experts, and
  * rows that are masked whole, need no other form. Slots without an expert
  * hold id -1 and weight 0 (moe_dispatch skips them and reports

@@ -17,11 +17,16 @@
 //
 // One warp per token, E / 32 consecutive experts a lane: scores, the groups'
 // two best by shuffles, then the lanes' sorted keys popped by one integer
-// maximum over the warp a rank. Bound by instructions (about 900 a token) and,
-// below a few thousand tokens, by the latency of that chain. Measured: 16384 x
-// 256 sigmoid, 8 groups, bias 23 us (3 us of it for the reads at the copy rate);
-// 128 tokens 6 us; 10007 x 96 softmax of BF16 logits 13.5 us; groups of 9 experts,
-// which fill no lanes, 7711 x 144, 22 us; the gradient of a raw softmax, 16384 x 256, 13 us (its bytes: 5).
+// maximum over the warp a rank. Bound by instructions (1020 a token of 256 experts,
+// 75 of them accesses to registers spilled at the 64 a thread that eight CTAs an SM
+// leave; 69 % of the issue slots busy) and, below a few thousand tokens, by the
+// latency of that chain. Measured, alone with cold caches: 16384 x 256 sigmoid, 8
+// groups, bias 23-28 us, 21 among other calls (3 us of it for the reads at the copy
+// rate); 128 tokens 6 us (4 among others); 10007 x 96 softmax of BF16 logits 13.5-16 us;
+// groups of 9 experts, which fill no lanes, 7711 x 144, 22 us. The gradient of a raw
+// softmax, 16384 x 256: 13-15 us, 11-12 among others (its bytes: 5); of the other forms,
+// which read the taken logits alone, 7.7 among others (its bytes: 2.7). It takes 565
+// instructions a token in 67 % of the issue slots, and waits for its loads most.
 #include <math_constants.h>
 
 #include "elem.cuh"

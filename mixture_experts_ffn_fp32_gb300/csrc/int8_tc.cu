@@ -25,7 +25,7 @@
 // own, which the widening frees: weights are in shared memory before their
 // columns are, so that only the widening lies between two uses of a column.
 //
-// Measured (one GB300; 1866 TFLOP/s BF16 and 6.8 TB/s by the libraries' product and
+// Measured (one GB300; 1912 TFLOP/s BF16 and 6.8 TB/s by the libraries' product and
 // copy): 16384 x 4096 x 4096 268 us without the tokens' pass (2.05 P operations/s: small
 // integers in FP16 draw less power than random BF16); 131072 gathered rows of 64 experts,
 // 2048 x 2816 SwiGLU, 790 us (1.9 P), the tensor pipe active 81 %; there the widening (1110

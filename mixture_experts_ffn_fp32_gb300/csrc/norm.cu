@@ -7,9 +7,9 @@
 //
 // Both are bound by memory: the forward reads x and writes y, the backward
 // reads x and dy and writes dx, each element once. A row is held in registers
-// by part of a warp (short rows) or by a CTA, up to 16 elements a thread, between
-// its reduction and its output, while the next rows of the CTA travel into shared
-// memory.
+// by part of a warp (short rows) or by a CTA, up to 16 elements a thread (32 where
+// a warp holds a row of up to 1024 in the forward), between its reduction and its
+// output, while the next rows of the CTA travel into shared memory.
 //
 // Statistics are FP32. The forward sums the row, then the row less a mean: the
 // second sums yield the squares and what rounding left in the mean, so a row
@@ -19,10 +19,13 @@
 // BF16 26 us (5.2 TB/s), 8192 x 4096 FP32 5.5 TB/s; backward, 8192 x 4096 BF16
 // 33 us and 5 for the column sums (6.1 TB/s; 41 before the CTAs' partial sums
 // were stored 16 bytes at a time), 5003 x 1411 FP32 unaligned 19 + 5 us. BF16
-// rows are held back by instructions (unpacking, and the products in FP32):
-// packed FP32 pairs took 29 us to 26 forward and 45 to 41 backward; more
-// rows ahead or more CTAs do not help (35 us with 1216 CTAs, each of which reads
-// gamma and beta again). Few rows are latency: 128 x 4096 4 us.
+// rows are held back by instructions and their latencies: 1200 a row of 2048 forward
+// keep 65 % of the issue slots busy and 2290 a row of 4096 backward 50 %, and the
+// commonest waits are for shuffles and shared memory. Packed FP32 pairs took 29 us to
+// 26 forward and 45 to 41 backward; more rows ahead or more CTAs do not help (35 us with
+// 1216 CTAs, each of which reads gamma and beta again). Few rows are latency: 128 x 4096
+// 4 us. Rows that registers do not hold are read two or three times, element by element:
+// 4096 x 20480 BF16 forward 136 us (2.5 TB/s), 8192 x 12288 backward 363 us (1.7 TB/s).
 #include "elem.cuh"
 #include "internal.h"
 
@@ -571,13 +574,13 @@ cudaError_t bwd_v(const LayerNormArgs& a, int grid, float* part, cudaStream_t s)
         case 16: return bwd_t<T, VEC, 8 / VEC, 16>(a, grid, part, s);
         case 32:
             if (a.d <= 32 * 8) return bwd_t<T, VEC, 8 / VEC, 32>(a, grid, part, s);
-            // elements one by one: as few columns a thread as there are (17835 FP32 rows of 1411 80 -> 72 us)
+            // elements one by one: as few columns a thread as there are
             if constexpr (VEC == 1)
                 if (a.d <= 32 * 12) return bwd_t<T, 1, 12, 32>(a, grid, part, s);
             return bwd_t<T, VEC, 16 / VEC, 32>(a, grid, part, s);
         case 128:
             if (a.d <= 128 * 8) return bwd_t<T, VEC, 8 / VEC, 128>(a, grid, part, s);
-            if constexpr (VEC == 1)
+            if constexpr (VEC == 1)  // 17835 FP32 rows of 1411 80 -> 72 us
                 if (a.d <= 128 * 12) return bwd_t<T, 1, 12, 128>(a, grid, part, s);
             return bwd_t<T, VEC, 16 / VEC, 128>(a, grid, part, s);
         case 192: return bwd_t<T, VEC, 16 / VEC, 192>(a, grid, part, s);

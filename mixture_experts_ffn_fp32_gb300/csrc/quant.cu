@@ -6,9 +6,11 @@
 //
 // Memory bound: x is read once into registers, by a warp for short rows and by
 // a CTA else, while the CTA's next rows travel into shared memory, and q is
-// written once. Measured: 16384 x 2048 BF16 21 us (4.9 TB/s of 6.8), FP32 5.5
-// TB/s; BF16 is held back by the instructions of exact rounding (33 us when a
-// branch sorted out what lies next to half steps: BF16 rows are full of it).
+// written once. Measured, among other calls: 16384 x 2048 BF16 21 us (4.7 TB/s of
+// 6.8; 24 alone with cold caches), FP32 32 us (5.3 TB/s); BF16 is held back by the
+// instructions of exact rounding, 1100 a row, which keep 74 % of the issue slots busy
+// (33 us when a branch sorted out what lies next to half steps: BF16 rows are full of
+// it). Rows past 16384 are read twice, element by element: 4096 x 20480 BF16 124 us.
 #include <math_constants.h>
 
 #include "elem.cuh"
