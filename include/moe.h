@@ -463,6 +463,107 @@ moe_status moe_matmul_int8(const moe_int8_config* cfg, const int8_t* a, int64_t 
                            const int32_t* offsets, const int32_t* rows, void* out, void* ws,
                            size_t ws_bytes, void* stream);
 
+typedef enum moe_norm_kind {
+    MOE_NORM_LAYER = 0,  /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) */
+    MOE_NORM_RMS = 1     /* v / sqrt(mean(v^2) + eps) */
+} moe_norm_kind;
+
+typedef enum moe_gate_shape {
+    MOE_GATE_NONE = 0,     /* 1 */
+    MOE_GATE_CHANNEL = 1,  /* [d] FP32 */
+    MOE_GATE_ELEMENT = 2   /* [R, d] of the rows' type, at any pitch */
+} moe_gate_shape;
+
+typedef struct moe_block_norm_config {
+    int32_t R;      /* rows, >= 0 */
+    int32_t d;      /* width, at most 2^24 */
+    int32_t dtype;  /* moe_dtype of all [R, d] operands */
+    int32_t kind;   /* moe_norm_kind, of both norms */
+    int32_t post;   /* 0 or 1: the block's output is normalised */
+    int32_t gate;   /* moe_gate_shape */
+    float alpha;    /* residual scale */
+    float eps;      /* >= 0 */
+} moe_block_norm_config;
+
+/* The norms on both sides of a block, fused with its gate and the residual:
+ *     z  = post ? Norm(y; post_w, post_b) : y       y: the block's output
+ *     x' = alpha x + gate z                         the new residual stream
+ *     n  = Norm(x'; w, b)                           the next block's input
+ * with Norm(v; w, b) = (v - mu) rstd w + b, statistics and arithmetic in FP32,
+ * x' and n rounded once each (n is taken of x' before its rounding).
+ *   x, y [R, d]. y NULL: no block in front, x' = x, n = Norm(x); then post and
+ *   gate are 0 and out is NULL. Vectors [d] are FP32; post_w, w may be NULL
+ *   (1), post_b, b too (0; always with MOE_NORM_RMS). gate NULL exactly with
+ *   MOE_GATE_NONE.
+ *   out [R, d]: x'. n [R, d] or NULL: no norm follows (w and b NULL).
+ *   stats: what the backward takes, or NULL. RMS [2, R] FP32: rstd of y, of
+ *   x'; layer [4, R]: mean and rstd of y, mean and rstd of x'. A norm that the
+ *   call does not take has mean 0 and rstd 1. */
+moe_status moe_block_norm(const moe_block_norm_config* cfg, const void* x, int64_t x_stride, const void* y,
+                          int64_t y_stride, const void* gate, int64_t gate_stride, const float* post_w,
+                          const float* post_b, const float* w, const float* b, void* out, void* n,
+                          float* stats, void* stream);
+
+/* Bytes of workspace moe_block_norm_backward needs where it returns a
+ * parameter's gradient (the columns' sums). */
+moe_status moe_block_norm_backward_workspace_size(const moe_block_norm_config* cfg, size_t* bytes);
+
+/* Gradients of L = sum(dn n) + sum(dxo x') given the forward's y, gate,
+ * vectors and stats and, as x, its x' (y NULL: its x). With h = dn w,
+ * xh = (x' - mu) rstd, yh = (y - mu_y) rstd_y ([.]: layer norm alone):
+ *     t  = dxo + rstd (h - [mean(h)] - xh mean(h xh)),   dx = alpha t (y NULL: t)
+ *     dgate = t z, summed over the rows of a MOE_GATE_CHANNEL
+ *     k  = t gate post_w,  dy = rstd_y (k - [mean(k)] - yh mean(k yh))
+ *                          (post = 0: t gate)
+ *     dpost_w = sum_rows t gate yh, dpost_b = sum_rows t gate,
+ *     dw = sum_rows dn xh, db = sum_rows dn
+ *   dn or dxo may be NULL, not both; without dn w, dw and db are NULL. dx, dy
+ *   and an element's dgate [R, d] contiguous, of dtype; dy NULL exactly where
+ *   y is. Vectors' gradients [d] FP32, each may be NULL, overwritten (zeros for
+ *   R = 0). An element's dgate may be NULL. ws: 16-byte aligned, needed where a
+ *   vector's gradient is asked for. Fixed order of sums: bit-reproducible. */
+moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void* x, int64_t x_stride,
+                                   const void* y, int64_t y_stride, const void* gate, int64_t gate_stride,
+                                   const float* post_w, const float* post_b, const float* w,
+                                   const float* stats, const void* dn, int64_t dn_stride, const void* dxo,
+                                   int64_t dxo_stride, void* dx, void* dy, void* dgate, float* dpost_w,
+                                   float* dpost_b, float* dw, float* db, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+typedef struct moe_adapter_config {
+    int32_t T;          /* rows, >= 0, at most 2^24 */
+    int32_t d;          /* input width */
+    int32_t N;          /* output width */
+    int32_t r;          /* rank (smaller ones padded with zeros), 1..256 */
+    int32_t E;          /* adapters, 1..1024 */
+    int32_t dtype;      /* moe_dtype of x, a and b */
+    int32_t out_dtype;  /* moe_dtype of base and out: dtype or MOE_F32 */
+} moe_adapter_config;
+
+/* Bytes of workspace moe_adapter_add needs for cfg (0 for T = 0). */
+moe_status moe_adapter_add_workspace_size(const moe_adapter_config* cfg, size_t* bytes);
+
+/* Low-rank adapters of many requests beside a shared projection, whose result
+ * is base:
+ *     out[t] = base[t] + scale[e] (x[t] a[e]^T) b[e]^T,   e the adapter of row t
+ * FP32 sums, both products; out rounded once. Rows are grouped by adapter:
+ * those of adapter e are rows[offsets[e]] .. rows[offsets[e + 1] - 1], and rows
+ * from position offsets[E] on have none: out[t] = base[t].
+ *   x [T, d], a [E, r, d], b [E, N, r] (contiguous); scale [E] FP32 or NULL (1);
+ *   offsets [E + 1] int32, ascending from 0, at most T; rows [T] int32, each row
+ *   once, or NULL (row i at position i); base, out [T, N] at any pitch, base NULL:
+ *   zeros. out may be base (the same pointer and pitch: rows without an adapter are
+ *   left as they are), else overlaps no input. moe_dispatch with K = 1 and E + 1
+ *   experts, the last for rows without an adapter, gives offsets and rows.
+ * ws: 256-byte aligned. Offsets are clamped to [0, T]; a row index outside
+ * [0, T) is skipped and sets MOE_ERR_DEVICE_INDEX in the workspace's error word,
+ * which the call adds to and never clears; a row that no position names is not
+ * written, and what a row named twice holds is not specified. */
+moe_status moe_adapter_add(const moe_adapter_config* cfg, const void* x, int64_t x_stride, const void* a,
+                           const void* b, const float* scale, const int32_t* offsets, const int32_t* rows,
+                           const void* base, int64_t base_stride, void* out, int64_t out_stride, void* ws,
+                           size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then reads and clears the device-side error word of
  * the workspace: MOE_OK, MOE_ERR_TIMEOUT (a bounded device wait ran out and
  * its kernel stopped early; outputs of that call are invalid) or

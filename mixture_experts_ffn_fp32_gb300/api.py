@@ -71,6 +71,15 @@ class Int8Config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("M", "Ma", "K", "N", "E", "swiglu", "out_dtype")]
 
 
+class BlockNormConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "d", "dtype", "kind", "post", "gate")] + \
+        [("alpha", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class AdapterConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "N", "r", "E", "dtype", "out_dtype")]
+
+
 _lib = None
 
 
@@ -117,6 +126,17 @@ def lib() -> ctypes.CDLL:
                                                               ctypes.POINTER(sz)]),
             "moe_matmul_int8": (ctypes.c_int, [ctypes.POINTER(Int8Config), vp, i64, vp, vp, vp, vp, vp,
                                                vp, vp, sz, vp]),
+            "moe_block_norm": (ctypes.c_int, [ctypes.POINTER(BlockNormConfig), vp, i64, vp, i64, vp, i64, vp, vp,
+                                              vp, vp, vp, vp, vp, vp]),
+            "moe_block_norm_backward_workspace_size": (ctypes.c_int, [ctypes.POINTER(BlockNormConfig),
+                                                                      ctypes.POINTER(sz)]),
+            "moe_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(BlockNormConfig), vp, i64, vp, i64, vp, i64,
+                                                       vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp,
+                                                       vp, vp, sz, vp]),
+            "moe_adapter_add_workspace_size": (ctypes.c_int, [ctypes.POINTER(AdapterConfig),
+                                                              ctypes.POINTER(sz)]),
+            "moe_adapter_add": (ctypes.c_int, [ctypes.POINTER(AdapterConfig), vp, i64, vp, vp, vp, vp, vp, vp,
+                                               i64, vp, i64, vp, sz, vp]),
             "moe_timing_begin": (ctypes.c_int, [i32, ctypes.c_uint32]),
             "moe_timing_end": (ctypes.c_int, [ctypes.POINTER(ctypes.c_float), i32,
                                               ctypes.POINTER(i32), ctypes.POINTER(i32)]),
@@ -801,6 +821,228 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
                                      a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),
                                      _ptr(rows), out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
                                      _raw_stream(stream, here)), "moe_matmul_int8")
+    return out
+
+
+NORMS = {"layer": 0, "rms": 1}
+_GATE_NONE, _GATE_CHANNEL, _GATE_ELEMENT = range(3)
+
+
+def _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here):
+    """The checks that both directions share: pitches of x, y and gate, the gate's shape and whether y is normalised."""
+    if kind not in NORMS:
+        raise ValueError(f"kind must be one of {sorted(NORMS)}, got {kind!r}")
+    xs = _rows(x, "x")
+    _at(x, "x", here)
+    d = x.size(1)
+    ys = gs = 0
+    shape = _GATE_NONE
+    if y is None:
+        if gate is not None:
+            raise ValueError("a gate needs y")
+        post = False
+    else:
+        ys = _rows(y, "y", x.dtype, x.shape)
+        _at(y, "y", here)
+        if gate is not None:
+            if gate.dim() == 1:
+                shape = _GATE_CHANNEL
+                _dev(gate, torch.float32, "gate", (d,), here)
+            else:
+                shape = _GATE_ELEMENT
+                gs = _rows(gate, "gate", x.dtype, x.shape)
+                _at(gate, "gate", here)
+    if not post and (post_weight is not None or post_bias is not None):
+        raise ValueError("post_weight and post_bias need a norm of y")
+    if post_weight is not None:
+        _dev(post_weight, torch.float32, "post_weight", (d,), here)
+    if post_bias is not None:
+        if kind == "rms":
+            raise ValueError("an RMS norm has no bias")
+        _dev(post_bias, torch.float32, "post_bias", (d,), here)
+    return xs, ys, gs, shape, 1 if post else 0
+
+
+def block_norm(x: torch.Tensor, y=None, weight=None, bias=None, post_weight=None, post_bias=None, gate=None,
+               alpha: float = 1.0, kind: str = "rms", post: bool = True, norm: bool = True, eps: float = 1e-5,
+               stats: bool = True, stream=None) -> dict:
+    """moe_block_norm: the norms on both sides of a block, fused with its gate and
+    the residual. x [R, d] the residual stream, y [R, d] the block's output (FP32,
+    BF16 or FP16; rows at any pitch):
+
+        z = Norm(y; post_weight, post_bias) (y itself with post=False)
+        x' = alpha x + gate z,   n = Norm(x'; weight, bias)
+
+    kind "rms" or "layer" (which alone takes biases); gate None, [d] FP32 or [R, d]
+    in x's type; vectors [d] FP32 or None. Returns x (x'), n and, with stats, the
+    FP32 statistics that the backward takes. y None: n = Norm(x) alone, no x.
+    norm=False: no norm follows, no n."""
+    here = _here(stream)
+    xs, ys, gs, shape, post = _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here)
+    R, d = x.shape
+    if y is None and not norm:
+        raise ValueError("norm=False needs y")
+    if not norm and (weight is not None or bias is not None):
+        raise ValueError("weight and bias need a norm")
+    if weight is not None:
+        _dev(weight, torch.float32, "weight", (d,), here)
+    if bias is not None:
+        if kind == "rms":
+            raise ValueError("an RMS norm has no bias")
+        _dev(bias, torch.float32, "bias", (d,), here)
+    cfg = _struct(BlockNormConfig, R, d, _DTYPES[x.dtype], NORMS[kind], post, shape, float(alpha), float(eps))
+    out = {}
+    with _on(stream, x, y, weight, bias, post_weight, post_bias, gate):
+        if y is not None:
+            out["x"] = _empty(x.dtype, R, d)
+        if norm:
+            out["n"] = _empty(x.dtype, R, d)
+        if stats:
+            out["stats"] = _empty(torch.float32, 2 if kind == "rms" else 4, R)
+        _check(lib().moe_block_norm(cfg, x.data_ptr(), xs, _ptr(y), ys, _ptr(gate), gs, _ptr(post_weight),
+                                    _ptr(post_bias), _ptr(weight), _ptr(bias), _ptr(out.get("x")),
+                                    _ptr(out.get("n")), _ptr(out.get("stats")), _raw_stream(stream, here)),
+               "moe_block_norm")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def block_norm_backward_workspace_size(R: int, d: int, kind: str = "rms") -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_block_norm_backward_workspace_size(
+        _struct(BlockNormConfig, R, d, MOE_F32, NORMS[kind], 0, 0, 1.0, 0.0), ctypes.byref(n)),
+        "moe_block_norm_backward_workspace_size")
+    return n.value
+
+
+def block_norm_backward(x: torch.Tensor, stats: torch.Tensor, y=None, dn=None, dx=None, weight=None,
+                        post_weight=None, post_bias=None, gate=None, alpha: float = 1.0, kind: str = "rms",
+                        post: bool = True, weight_grads: bool = True, ws: torch.Tensor | None = None,
+                        stream=None) -> dict:
+    """moe_block_norm_backward: gradients of sum(dn * n) + sum(dx * x'), either of dn
+    and dx (rows at any pitch) None for none. x: the forward's result x' (its input x
+    where y is None); stats, y, the gate and the vectors as in the forward. Returns dx
+    and, with y, dy in x's type; of an element-wise gate dgate too; with weight_grads,
+    FP32, dgate of a gate [d], dpost_weight where y is normalised, dweight with dn,
+    and for layer norms dpost_bias and dbias. ws: uint8 of
+    block_norm_backward_workspace_size(R, d, kind) bytes (allocated when None)."""
+    here = _here(stream)
+    xs, ys, gs, shape, post = _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here)
+    R, d = x.shape
+    layer = kind == "layer"
+    if dn is None and dx is None:
+        raise ValueError("dn or dx is required")
+    dns = dxs = 0
+    if dn is not None:
+        dns = _rows(dn, "dn", x.dtype, x.shape)
+        _at(dn, "dn", here)
+    elif weight is not None:
+        raise ValueError("weight needs dn")
+    if dx is not None:
+        dxs = _rows(dx, "dx", x.dtype, x.shape)
+        _at(dx, "dx", here)
+    _dev(stats, torch.float32, "stats", (4 if layer else 2, R), here)
+    if weight is not None:
+        _dev(weight, torch.float32, "weight", (d,), here)
+    if ws is not None:
+        _at(ws, "ws", here)
+    cfg = _struct(BlockNormConfig, R, d, _DTYPES[x.dtype], NORMS[kind], post, shape, float(alpha), 0.0)
+    out = {}
+    with _on(stream, x, stats, y, dn, dx, weight, post_weight, post_bias, gate, ws):
+        out["dx"] = _empty(x.dtype, R, d)
+        if y is not None:
+            out["dy"] = _empty(x.dtype, R, d)
+        if shape == _GATE_ELEMENT:
+            out["dgate"] = _empty(x.dtype, R, d)
+        if weight_grads:
+            names = (["dgate"] if shape == _GATE_CHANNEL else []) + (["dpost_weight"] if post else []) + \
+                (["dpost_bias"] if post and layer else []) + (["dweight"] if dn is not None else []) + \
+                (["dbias"] if dn is not None and layer else [])
+            for name in names:
+                out[name] = _empty(torch.float32, d)
+            if names and ws is None:
+                ws = _empty(torch.uint8, block_norm_backward_workspace_size(R, d, kind))
+        _check(lib().moe_block_norm_backward(
+            cfg, x.data_ptr(), xs, _ptr(y), ys, _ptr(gate), gs, _ptr(post_weight), _ptr(post_bias), _ptr(weight),
+            stats.data_ptr(), _ptr(dn), dns, _ptr(dx), dxs, out["dx"].data_ptr(), _ptr(out.get("dy")),
+            _ptr(out.get("dgate")), _ptr(out.get("dpost_weight")), _ptr(out.get("dpost_bias")),
+            _ptr(out.get("dweight")), _ptr(out.get("dbias")), _ptr(ws), 0 if ws is None else ws.numel(),
+            _raw_stream(stream, here)), "moe_block_norm_backward")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _adapter_ws(*shape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_adapter_add_workspace_size(_struct(AdapterConfig, *shape), ctypes.byref(n)),
+           "moe_adapter_add_workspace_size")
+    return n.value
+
+
+def alloc_adapter_workspace(T: int, d: int, N: int, r: int, E: int, dtype=torch.bfloat16, device="cuda") -> torch.Tensor:
+    """A workspace for adapter_add calls of up to T rows with these sizes (its error
+    word zeroed; workspace_status reads and clears it)."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    ws = torch.empty(max(_adapter_ws(T, d, N, r, E, _DTYPES[dtype], MOE_F32), 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def adapter_add(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor, rows=None,
+                scale=None, out=None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """moe_adapter_add: low-rank adapters of many requests beside a shared projection,
+    whose result is base [T, N] (None: zeros):
+
+        out[t] = base[t] + scale[e] (x[t] a[e].T) b[e].T,   e the adapter of row t
+
+    x [T, d], a [E, r, d], b [E, N, r] of one type (FP32, BF16, FP16; smaller ranks
+    padded with zeros), scale [E] FP32 or None; base in x's type or FP32. Rows are
+    grouped by adapter: rows [T] int32 names each row once (None: in order), those of
+    adapter e at positions offsets[e] to offsets[e + 1] (int32 [E + 1]); rows from
+    offsets[E] on have no adapter. ``dispatch`` of the rows' adapter ids with K = 1 and
+    E + 1 experts, the last for rows without one, gives both (its offsets without the
+    last entry, its sorted_token). out: [T, N] to write, or base itself for an update in
+    place (allocated when None). ws: see alloc_adapter_workspace. When None one is
+    allocated for the call and its error word is not read."""
+    here = _here(stream)
+    xs = _rows(x, "x")
+    _at(x, "x", here)
+    T, d = x.shape
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError(f"a must be [E, r, d] and b [E, N, r], got {tuple(a.shape)} and {tuple(b.shape)}")
+    E, N, r = b.shape
+    _dev(a, x.dtype, "a", (E, r, d), here)
+    _dev(b, x.dtype, "b", None, here)
+    _dev(offsets, torch.int32, "offsets", (E + 1,), here)
+    if rows is not None:
+        _dev(rows, torch.int32, "rows", (T,), here)
+    if scale is not None:
+        _dev(scale, torch.float32, "scale", (E,), here)
+    like = base if base is not None else out if out is not None else x
+    if like.dtype != x.dtype and like.dtype != torch.float32:
+        raise ValueError(f"base and out must be {x.dtype} or float32, got {like.dtype}")
+    bs = 0
+    if base is not None:
+        bs = _rows(base, "base", None, (T, N))
+        _at(base, "base", here)
+    if out is not None:
+        os_ = _rows(out, "out", like.dtype, (T, N))
+        _at(out, "out", here)
+    else:
+        os_ = N
+    if ws is not None:
+        _at(ws, "ws", here)
+    cfg = (T, d, N, r, E, _DTYPES[x.dtype], _DTYPES[like.dtype])
+    with _on(stream, base, x, a, b, offsets, rows, scale, out, ws):
+        if ws is None:
+            ws = _empty(torch.uint8, _adapter_ws(*cfg))
+        if out is None:
+            out = _empty(like.dtype, T, N)
+        _check(lib().moe_adapter_add(_struct(AdapterConfig, *cfg), x.data_ptr(), xs, a.data_ptr(), b.data_ptr(),
+                                     _ptr(scale), offsets.data_ptr(), _ptr(rows), _ptr(base), bs, out.data_ptr(),
+                                     os_, ws.data_ptr(), ws.numel(), _raw_stream(stream, here)),
+               "moe_adapter_add")
     return out
 
 

@@ -562,4 +562,37 @@ cudaError_t launch_int8_vec(const Int8Args& a, cudaStream_t s);
 size_t int8_tc_workspace(int M, int K);
 cudaError_t launch_int8_tc(const Int8Args& a, bool wide, cudaStream_t s);
 
+struct BlockNormArgs {
+    int R, d, dtype, layer, post;  // layer: layer norm, else RMS; post: y is normalised
+    float alpha, eps;
+    const void *x, *y, *gate_elem;  // gate_elem: a gate per element
+    long long x_stride, y_stride, gate_stride;
+    const float *gate, *post_w, *post_b, *w, *b;  // gate: one per column
+    float* stats;         // forward: written, or NULL; backward: read
+    void *out, *n;        // forward: x', n (or NULL); backward: out is dx
+    const void *dn, *dxo; // backward, either may be NULL
+    long long dn_stride, dxo_stride;
+    void *dy, *dgate_elem;
+    float *dgate, *dpost_w, *dpost_b, *dw, *db;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s);
+// Floats of workspace that the backward's column sums go through.
+size_t block_norm_bwd_floats(int R, int d, bool layer);
+// ws: those floats, or NULL where no parameter's gradient is wanted.
+cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, float* ws, cudaStream_t s);
+
+struct AdapterArgs {
+    int T, d, N, r, E, dtype, out_dtype;
+    const void *x, *a, *b, *base;  // base: NULL for zeros
+    long long x_stride, base_stride, out_stride;
+    const float* scale;      // NULL: 1
+    const int32_t *offsets, *rows;
+    void* out;
+    int in_place;            // out is base
+    int* err;                // the workspace, its error word first
+    float* v;
+};
+size_t adapter_workspace(int T, int r);
+cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
+
 }  // namespace moe

@@ -1,6 +1,6 @@
 // C entry points of the operators around the layer (declared in
-// include/moe.h): layer norm, group-limited routing, row quantisation and the
-// 8-bit expert products. Host-side validation, then the launchers.
+// include/moe.h): layer norm, the norms on both sides of a block, group-limited
+// routing, row quantisation, the 8-bit expert products and low-rank adapters. Host-side validation, then the launchers.
 #include <math.h>
 #include <stdlib.h>
 
@@ -240,4 +240,172 @@ MOE_API moe_status moe_matmul_int8(const moe_int8_config* cfg, const int8_t* a, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const Int8Form f = int8_form(c);
     return cuda_status(f == INT8_VEC ? launch_int8_vec(g, s) : launch_int8_tc(g, f == INT8_WIDE, s));
+}
+
+namespace {
+
+moe_status check_block_norm(const moe_block_norm_config& c) {
+    const moe_status v = check_rows(c.R, c.d, c.dtype, c.d);
+    if (v != MOE_OK) return v;
+    if (c.kind != MOE_NORM_LAYER && c.kind != MOE_NORM_RMS) return MOE_ERR_INVALID_ARG;
+    if (c.post != 0 && c.post != 1) return MOE_ERR_INVALID_ARG;
+    if (c.gate < MOE_GATE_NONE || c.gate > MOE_GATE_ELEMENT) return MOE_ERR_INVALID_ARG;
+    if (!(c.eps >= 0.0f) || !(c.alpha == c.alpha)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+// A [R, d] operand of the config's type: its pitch, and its address where it is there.
+bool rows_ok(const moe_block_norm_config& c, const void* p, int64_t stride) {
+    if (p == nullptr) return true;
+    return check_rows(c.R, c.d, c.dtype, stride) == MOE_OK && aligned(p, elem_size(c.dtype));
+}
+
+// What both directions take; false where it does not fit together.
+bool block_norm_args(const moe_block_norm_config& c, const void* x, int64_t x_stride, const void* y, int64_t y_stride,
+                     const void* gate, int64_t gate_stride, const float* post_w, const float* post_b, const float* w,
+                     BlockNormArgs& a) {
+    if (!x || !rows_ok(c, x, x_stride) || !rows_ok(c, y, y_stride)) return false;
+    if (!y && (c.post || c.gate != MOE_GATE_NONE)) return false;
+    if ((gate == nullptr) != (c.gate == MOE_GATE_NONE)) return false;
+    if (c.gate == MOE_GATE_ELEMENT && !rows_ok(c, gate, gate_stride)) return false;
+    if (c.gate == MOE_GATE_CHANNEL && !aligned(gate, 4)) return false;
+    if (!c.post && (post_w || post_b)) return false;
+    if (c.kind == MOE_NORM_RMS && post_b) return false;
+    if (!aligned(post_w, 4) || !aligned(post_b, 4) || !aligned(w, 4)) return false;
+    a.R = c.R; a.d = c.d; a.dtype = c.dtype;
+    a.layer = c.kind == MOE_NORM_LAYER; a.post = c.post; a.eps = c.eps;
+    a.alpha = y != nullptr ? c.alpha : 1.0f;
+    a.x = x; a.x_stride = x_stride;
+    a.y = y; a.y_stride = y_stride;
+    if (c.gate == MOE_GATE_ELEMENT) {
+        a.gate_elem = gate;
+        a.gate_stride = gate_stride;
+    } else {
+        a.gate = static_cast<const float*>(gate);
+    }
+    a.post_w = post_w; a.post_b = post_b; a.w = w;
+    return true;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_block_norm(const moe_block_norm_config* cfg, const void* x, int64_t x_stride, const void* y,
+                                  int64_t y_stride, const void* gate, int64_t gate_stride, const float* post_w,
+                                  const float* post_b, const float* w, const float* b, void* out, void* n,
+                                  float* stats, void* stream) {
+    if (!cfg) return MOE_ERR_INVALID_ARG;
+    const moe_block_norm_config& c = *cfg;
+    const moe_status v = check_block_norm(c);
+    if (v != MOE_OK || c.R == 0) return v;
+    BlockNormArgs a{};
+    if (!block_norm_args(c, x, x_stride, y, y_stride, gate, gate_stride, post_w, post_b, w, a)) return MOE_ERR_INVALID_ARG;
+    if ((out == nullptr) != (y == nullptr) || (!out && !n)) return MOE_ERR_INVALID_ARG;
+    if (!n && (w || b)) return MOE_ERR_INVALID_ARG;
+    if (c.kind == MOE_NORM_RMS && b) return MOE_ERR_INVALID_ARG;
+    const size_t es = elem_size(c.dtype);
+    if (!aligned(out, es) || !aligned(n, es) || !aligned(b, 4) || !aligned(stats, 4)) return MOE_ERR_INVALID_ARG;
+    a.b = b; a.out = out; a.n = n; a.stats = stats;
+    return cuda_status(launch_block_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+MOE_API moe_status moe_block_norm_backward_workspace_size(const moe_block_norm_config* cfg, size_t* bytes) {
+    if (!cfg || !bytes) return MOE_ERR_INVALID_ARG;
+    const moe_status v = check_block_norm(*cfg);
+    if (v != MOE_OK) return v;
+    *bytes = cfg->R == 0 ? 0 : block_norm_bwd_floats(cfg->R, cfg->d, cfg->kind == MOE_NORM_LAYER) * 4;
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_block_norm_backward(const moe_block_norm_config* cfg, const void* x, int64_t x_stride,
+                                           const void* y, int64_t y_stride, const void* gate, int64_t gate_stride,
+                                           const float* post_w, const float* post_b, const float* w,
+                                           const float* stats, const void* dn, int64_t dn_stride, const void* dxo,
+                                           int64_t dxo_stride, void* dx, void* dy, void* dgate, float* dpost_w,
+                                           float* dpost_b, float* dw, float* db, void* ws, size_t ws_bytes,
+                                           void* stream) {
+    if (!cfg) return MOE_ERR_INVALID_ARG;
+    const moe_block_norm_config& c = *cfg;
+    const moe_status v = check_block_norm(c);
+    if (v != MOE_OK) return v;
+    const size_t es = elem_size(c.dtype);
+    const bool rms = c.kind == MOE_NORM_RMS;
+    if (!c.post && (dpost_w || dpost_b)) return MOE_ERR_INVALID_ARG;
+    if (rms && (dpost_b || db)) return MOE_ERR_INVALID_ARG;
+    if (c.gate == MOE_GATE_NONE && dgate) return MOE_ERR_INVALID_ARG;
+    float* dgate_col = c.gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
+    if (!aligned(dpost_w, 4) || !aligned(dpost_b, 4) || !aligned(dw, 4) || !aligned(db, 4) || !aligned(dgate_col, 4))
+        return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (c.R == 0) {  // sums over no rows
+        for (float* p : {dgate_col, dpost_w, dpost_b, dw, db})
+            if (p && cudaMemsetAsync(p, 0, static_cast<size_t>(c.d) * 4, s) != cudaSuccess) return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    BlockNormArgs a{};
+    if (!block_norm_args(c, x, x_stride, y, y_stride, gate, gate_stride, post_w, post_b, w, a)) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(c, dn, dn_stride) || !rows_ok(c, dxo, dxo_stride) || (!dn && !dxo)) return MOE_ERR_INVALID_ARG;
+    if (!dn && (w || dw || db)) return MOE_ERR_INVALID_ARG;
+    if (!dx || (dy == nullptr) != (y == nullptr) || !aligned(dx, es) || !aligned(dy, es)) return MOE_ERR_INVALID_ARG;
+    if (c.gate == MOE_GATE_ELEMENT && !aligned(dgate, es)) return MOE_ERR_INVALID_ARG;
+    if ((c.post || dn) && (!stats || !aligned(stats, 4))) return MOE_ERR_INVALID_ARG;
+    const bool cols = dgate_col || dpost_w || dpost_b || dw || db;
+    if (cols) {
+        if (!ws || !aligned(ws, 16)) return MOE_ERR_INVALID_ARG;
+        if (ws_bytes < block_norm_bwd_floats(c.R, c.d, !rms) * 4) return MOE_ERR_WORKSPACE;
+    }
+    a.stats = const_cast<float*>(stats);
+    a.dn = dn; a.dn_stride = dn_stride;
+    a.dxo = dxo; a.dxo_stride = dxo_stride;
+    a.out = dx; a.dy = dy;
+    if (c.gate == MOE_GATE_ELEMENT) a.dgate_elem = dgate;
+    a.dgate = dgate_col; a.dpost_w = dpost_w; a.dpost_b = dpost_b; a.dw = dw; a.db = db;
+    return cuda_status(launch_block_norm_bwd(a, cols ? static_cast<float*>(ws) : nullptr, s));
+}
+
+namespace {
+
+moe_status check_adapter(const moe_adapter_config& c) {
+    if (c.T < 0 || c.d < 1 || c.N < 1 || c.r < 1 || c.E < 1 || !known_dtype(c.dtype)) return MOE_ERR_INVALID_ARG;
+    if (c.out_dtype != c.dtype && c.out_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+    if (c.r > 256 || c.E > 1024 || c.d > (1 << 24) || c.N > (1 << 24) || c.T > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+}  // namespace
+
+MOE_API moe_status moe_adapter_add_workspace_size(const moe_adapter_config* cfg, size_t* bytes) {
+    if (!cfg || !bytes) return MOE_ERR_INVALID_ARG;
+    const moe_status v = check_adapter(*cfg);
+    if (v != MOE_OK) return v;
+    *bytes = cfg->T == 0 ? 0 : adapter_workspace(cfg->T, cfg->r);
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_adapter_add(const moe_adapter_config* cfg, const void* x, int64_t x_stride, const void* a,
+                                   const void* b, const float* scale, const int32_t* offsets, const int32_t* rows,
+                                   const void* base, int64_t base_stride, void* out, int64_t out_stride, void* ws,
+                                   size_t ws_bytes, void* stream) {
+    if (!cfg) return MOE_ERR_INVALID_ARG;
+    const moe_adapter_config& c = *cfg;
+    moe_status v = check_adapter(c);
+    if (v != MOE_OK || c.T == 0) return v;
+    const size_t es = elem_size(c.dtype), eo = elem_size(c.out_dtype);
+    if (check_rows(c.T, c.d, c.dtype, x_stride) != MOE_OK || check_rows(c.T, c.N, c.out_dtype, out_stride) != MOE_OK ||
+        (base && check_rows(c.T, c.N, c.out_dtype, base_stride) != MOE_OK))
+        return MOE_ERR_INVALID_ARG;
+    if (!x || !a || !b || !offsets || !out || !aligned(x, es) || !aligned(a, es) || !aligned(b, es) ||
+        !aligned(base, eo) || !aligned(out, eo) || !aligned(scale, 4) || !aligned(offsets, 4) || !aligned(rows, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (out == base && c.T > 1 && base_stride != out_stride) return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < adapter_workspace(c.T, c.r)) return MOE_ERR_WORKSPACE;
+    AdapterArgs g{};
+    g.T = c.T; g.d = c.d; g.N = c.N; g.r = c.r; g.E = c.E; g.dtype = c.dtype; g.out_dtype = c.out_dtype;
+    g.x = x; g.a = a; g.b = b; g.base = base;
+    g.x_stride = x_stride; g.base_stride = base_stride; g.out_stride = out_stride;
+    g.scale = scale; g.offsets = offsets; g.rows = rows;
+    g.out = out; g.in_place = out == base;
+    g.err = static_cast<int*>(ws);
+    g.v = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
+    return cuda_status(launch_adapter(g, static_cast<cudaStream_t>(stream)));
 }
