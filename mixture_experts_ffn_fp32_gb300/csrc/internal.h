@@ -580,6 +580,14 @@ cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s);
 size_t block_norm_bwd_floats(int R, int d, bool layer);
 // ws: those floats, or NULL where no parameter's gradient is wanted.
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a, float* ws, cudaStream_t s);
+// The two by type, and the parameters' gradients from n partial rows of column sums.
+cudaError_t block_norm_f32(const BlockNormArgs& a, cudaStream_t s);
+cudaError_t block_norm_bf16(const BlockNormArgs& a, cudaStream_t s);
+cudaError_t block_norm_f16(const BlockNormArgs& a, cudaStream_t s);
+cudaError_t block_norm_bwd_f32(const BlockNormArgs& a, float* ws, cudaStream_t s);
+cudaError_t block_norm_bwd_bf16(const BlockNormArgs& a, float* ws, cudaStream_t s);
+cudaError_t block_norm_bwd_f16(const BlockNormArgs& a, float* ws, cudaStream_t s);
+cudaError_t launch_block_norm_params(const BlockNormArgs& a, int n, const float* part, cudaStream_t s);
 
 struct AdapterArgs {
     int T, d, N, r, E, dtype, out_dtype;

@@ -41,66 +41,6 @@ constexpr int BWD_MAX_D = 8192;
 constexpr int FWD_DEPTH = 3;
 constexpr int BWD_DEPTH = 2;
 
-// 1 / sqrt(var + eps); a variance that rounding took below zero is zero, a NaN stays.
-MOE_DEV float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
-
-// A mean and what rounding left in it, which is no number where the mean is infinite.
-MOE_DEV float joined(float m, float rest) { return rest == rest ? m + rest : m; }
-
-// Mean and variance of a row from its threads' NV x VEC values (in pairs), left
-// as v - m, m a mean the warp took of its own. Its sums of the differences and of
-// their squares follow, and the CTA joins the warps' numbers (m, r, q of n values)
-// behind one sync:
-//   m0 = sum n m / d,  rest = sum (n (m - m0) + r) / d
-//   var = sum (q + 2 (m - m0) r + n (m - m0)^2) / d - rest^2
-// `rest` is what rounding left in m0; shift = m - (m0 + rest).
-template <int VEC, int NV, int TPR>
-MOE_DEV void row_moments(F2 (&v)[NV * VEC / 2], int d, int t, float inv_d, float4* scratch, int& turn, float& mean,
-                         float& shift, float& var) {
-    constexpr int W = TPR <= 32 ? 1 : TPR / 32, N2 = NV * VEC / 2;
-    const int w = W == 1 ? 0 : static_cast<int>(threadIdx.x >> 5);
-    constexpr int S = TPR < 32 ? TPR : 32;  // threads that sum by shuffles
-    float n = 0.0f;  // the warp's values, cut at d
-#pragma unroll
-    for (int i = 0; i < NV; ++i) n += static_cast<float>(min(max(d - (i * TPR + w * 32) * VEC, 0), S * VEC));
-    F2 s2 = v[0];
-#pragma unroll
-    for (int k = 1; k < N2; ++k) s2 = add2(s2, v[k]);
-    const float s = seg_sum<S>(both(s2));
-    const float m = W == 1 ? s * inv_d : (n > 0.0f ? s / n : 0.0f);
-    F2 r2 = f2(0.0f, 0.0f), q2 = r2;
-#pragma unroll
-    for (int k = 0; k < N2; ++k) {
-        // zeros past the end stay zeros
-        const float ma = (2 * k / VEC * TPR + t) * VEC < d ? -m : 0.0f;
-        const float mb = VEC > 1 ? ma : ((2 * k + 1) * TPR + t < d ? -m : 0.0f);
-        v[k] = add2(v[k], f2(ma, mb));
-        r2 = add2(r2, v[k]);
-        q2 = fma2(v[k], v[k], q2);
-    }
-    const float r = seg_sum<S>(both(r2)), q = seg_sum<S>(both(q2));
-    if constexpr (W == 1) {
-        const float rest = r * inv_d;
-        mean = joined(m, rest);
-        shift = -rest;
-        var = q * inv_d - rest * rest;
-    } else {
-        float4* sc = scratch + (turn & 1) * W;  // two turns: see row_sum2
-        ++turn;
-        if (lane_id() == 0) sc[w] = make_float4(m, r, q, n);
-        __syncthreads();
-        const int l = static_cast<int>(lane_id());
-        float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (l < W) e = sc[l];
-        const float m0 = group_sum<W>(e.w * e.x) * inv_d;
-        const float dm = e.x - m0;
-        const float rest = group_sum<W>(e.w * dm + e.y) * inv_d;
-        var = group_sum<W>(e.z + 2.0f * dm * e.y + e.w * dm * dm) * inv_d - rest * rest;
-        mean = joined(m0, rest);
-        shift = (m - m0) - rest;
-    }
-}
-
 template <typename T, int VEC, int NV, int TPR>
 struct Forward {
     static constexpr int THREADS = RowThreads<TPR>::THREADS;
