@@ -5,54 +5,59 @@
 namespace moe {
 namespace {
 
-// The parameters' gradients from n partial rows, each column's sums in a fixed
-// order: 32 threads take every 32nd row, then theirs are added in order.
-constexpr int COL_ROWS = 32;
+// The parameters' gradients from n partial rows, each column's sums in a fixed order:
+// a CTA takes 8 columns (a sector of a row), 32 threads of each every 32nd row, and theirs
+// are added in order.
+constexpr int COLS = 8, SLOTS = 32;
 template <int NS>
-__global__ void __launch_bounds__(32 * COL_ROWS)
+__global__ void __launch_bounds__(COLS * SLOTS)
 block_norm_params_kernel(const __grid_constant__ BlockNormArgs a, int n, const float* __restrict__ part) {
-    __shared__ float s[COL_ROWS][32];
-    const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + cx;
+    __shared__ float s[NS][SLOTS][COLS];
+    const int cx = threadIdx.x % COLS, slot = threadIdx.x / COLS;
+    const int c = blockIdx.x * COLS + cx;
     pdl_wait();
     pdl_trigger();
-    float sum[NS];
+    float v[NS] = {};
+    if (c < a.d) {
+        for (int r0 = slot; r0 < n; r0 += 4 * SLOTS) {
+            float e[4][NS];
 #pragma unroll
-    for (int q = 0; q < NS; ++q) {
-        float v = 0.0f;
-        if (c < a.d) {
-            for (int r0 = ry; r0 < n; r0 += 10 * COL_ROWS) {
-                float e[10];
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + i * SLOTS;
 #pragma unroll
-                for (int i = 0; i < 10; ++i) {
-                    const int r = r0 + i * COL_ROWS;
-                    e[i] = r < n ? part[(static_cast<long long>(r) * NS + q) * a.d + c] : 0.0f;
-                }
-                v += (((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]))) + (e[8] + e[9]);
+                for (int q = 0; q < NS; ++q) e[i][q] = r < n ? part[(static_cast<long long>(r) * NS + q) * a.d + c] : 0.0f;
             }
-        }
-        s[ry][cx] = v;
-        __syncthreads();
-        v = s[0][cx];
 #pragma unroll
-        for (int i = 1; i < COL_ROWS; ++i) v += s[i][cx];
-        sum[q] = v;
-        __syncthreads();
+            for (int q = 0; q < NS; ++q) v[q] += (e[0][q] + e[1][q]) + (e[2][q] + e[3][q]);
+        }
     }
-    if (ry != 0 || c >= a.d) return;
-    const float s1 = sum[0], s2 = NS == 4 ? sum[NS / 2 - 1] : 0.0f, s3 = sum[NS / 2], s4 = NS == 4 ? sum[NS - 1] : 0.0f;
-    const float g = weight(a.gate, c);
-    if (a.dw != nullptr) a.dw[c] = s3;
-    if (a.db != nullptr) a.db[c] = s4;
-    if (a.dpost_w != nullptr) a.dpost_w[c] = g * s1;
-    if (a.dpost_b != nullptr) a.dpost_b[c] = g * s2;
-    if (a.dgate != nullptr) a.dgate[c] = a.post ? weight(a.post_w, c) * s1 + offset(a.post_b, c) * s2 : s1;
+#pragma unroll
+    for (int q = 0; q < NS; ++q) s[q][slot][cx] = v[q];
+    __syncthreads();
+    if (slot >= NS) return;
+    float sum = s[slot][0][cx];
+#pragma unroll
+    for (int i = 1; i < SLOTS; ++i) sum += s[slot][i][cx];
+    // the first warp: slot q has the columns' S(q + 1) (RMS: S1, S3)
+    constexpr unsigned WARP = NS == 4 ? 0xffffffffu : 0xffffu;
+    const float s2 = NS == 4 ? __shfl_sync(WARP, sum, COLS + cx) : 0.0f;
+    if (c >= a.d) return;
+    if (slot == 0) {
+        const float g = weight(a.gate, c);
+        if (a.dpost_w != nullptr) a.dpost_w[c] = g * sum;
+        if (a.dpost_b != nullptr) a.dpost_b[c] = g * s2;
+        if (a.dgate != nullptr) a.dgate[c] = a.post ? weight(a.post_w, c) * sum + offset(a.post_b, c) * s2 : sum;
+    } else if (slot == NS / 2) {
+        if (a.dw != nullptr) a.dw[c] = sum;
+    } else if (slot == NS - 1) {
+        if (a.db != nullptr) a.db[c] = sum;
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm_params(const BlockNormArgs& a, int n, const float* part, cudaStream_t s) {
-    const dim3 grid((a.d + 31) / 32), block(32 * COL_ROWS);
+    const dim3 grid((a.d + COLS - 1) / COLS), block(COLS * SLOTS);
     return a.layer ? launch_pdl(block_norm_params_kernel<4>, grid, block, 0, s, a, n, part)
                    : launch_pdl(block_norm_params_kernel<2>, grid, block, 0, s, a, n, part);
 }

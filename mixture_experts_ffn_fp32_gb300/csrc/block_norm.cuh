@@ -353,8 +353,9 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
 #pragma unroll
     for (int s = 0; s < D; ++s) {
         const long long r = row + s * step;
-        fx.issue(s, r, r < a.R);
         if (block) fy.issue(s, r, r < a.R);
+        cp_async_commit();
+        fx.issue(s, r, r < a.R);
         if (elem) fg.issue(s, r, r < a.R);
         cp_async_commit();
     }
@@ -379,7 +380,8 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
     }
     int slot = 0;
     for (; L::first(row) < a.R; row += step) {
-        cp_async_wait<D - 1>();
+        // y and the rest travel in groups of their own: each has a whole row's time
+        cp_async_wait<2 * D - 1>();
         const bool there = row < a.R;
         const long long next = row + D * step;
         F2 v[N2];
@@ -388,6 +390,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
             F2 y[N2];
             fy.read(slot, row, there, y);
             fy.issue(slot, next, next < a.R);
+            cp_async_commit();
             if (post) row_stats<VEC, NV, TPR, LAYER>(y, d, t, inv_d, a.eps, scratch, turn, ym, shift, yr);
             if constexpr (!KEEP) vectors_post();
             const F2 sh2 = f2(shift, shift), r2 = f2(yr, yr), al2 = f2(a.alpha, a.alpha);
@@ -396,6 +399,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
                 if constexpr (LAYER) y[k] = fma2(mul2(add2(y[k], sh2), r2), wp[k], bp[k]);
                 else y[k] = mul2(mul2(y[k], r2), wp[k]);
             }
+            cp_async_wait<2 * D - 1>();
             if (elem) {
                 fg.read(slot, row, there, v);
                 fg.issue(slot, next, next < a.R);
@@ -407,6 +411,8 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
             for (int k = 0; k < N2; ++k) v[k] = fma2(v[k], al2, y[k]);
             if (there) put<T, VEC, NV, TPR>(p.out + row * d, d, t, v);
         } else {
+            cp_async_commit();
+            cp_async_wait<2 * D - 1>();
             fx.read(slot, row, there, v);
         }
         fx.issue(slot, next, next < a.R);
@@ -489,6 +495,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
             fx.issue(s, r, r < a.R);
             fn.issue(s, r, r < a.R);
         }
+        cp_async_commit();
         if (stream) fo.issue(s, r, r < a.R);
         if (block) fy.issue(s, r, r < a.R);
         if (elem) fg.issue(s, r, r < a.R);
@@ -509,7 +516,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         const bool there = row < a.R;
         const long long next = row + D * step;
         const bool more = next < a.R;
-        cp_async_wait<D - 1>();
+        cp_async_wait<2 * D - 1>();  // two groups a row, as in the forward
         const float ymc = ym, yrc = yr, xmc = xm, xrc = xr;
         statistics(row + step);
         F2 u[N2], v[N2];
@@ -528,6 +535,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
             fn.read(slot, row, there, v);
             gone(v);
             fn.issue(slot, next, more);
+            cp_async_commit();
             const F2 nm = f2(-xmc, -xmc), r2 = f2(xrc, xrc);
             F2 a1 = f2(0.0f, 0.0f), a2 = a1;
             F2 w[N2];
@@ -550,7 +558,10 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
             const F2 n1 = f2(s1, s1), n2 = f2(s2, s2);
 #pragma unroll
             for (int k = 0; k < N2; ++k) v[k] = mul2(fma2(u[k], n2, LAYER ? add2(v[k], n1) : v[k]), r2);
+        } else {
+            cp_async_commit();
         }
+        cp_async_wait<2 * D - 1>();
         if (stream) {
             fo.read(slot, row, there, u);
             gone(u);
