@@ -598,9 +598,11 @@ struct AdapterArgs {
     void* out;
     int in_place;            // out is base
     int* err;                // the workspace, its error word first
-    float* v;
+    float* v;                // inner values: FP32 [T, r]; 16-bit types [slices, T, rp]
+    int rp, slices;          // set by launch_adapter: r rounded up to 16, slices of d
+    int col_parts;           // ranges of columns a tile is dealt out in
 };
-size_t adapter_workspace(int T, int r);
+size_t adapter_workspace(int T, int d, int r, int E, int dtype);
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
 
 }  // namespace moe
