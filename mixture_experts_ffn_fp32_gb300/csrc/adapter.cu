@@ -6,97 +6,10 @@
 // of `rows`; positions from offsets[E] on have no adapter. Two launches: the first
 // computes v = s_e x[t] A_e^T into the workspace (by position, FP32), the second adds
 // v B_e^T to base.
-#include <algorithm>
-
-#include "elem.cuh"
-#include "internal.h"
+#include "adapter.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int MAXE = 1024;
-constexpr int THREADS = 256;
-
-// Tiles of TM positions: how many come before each group, and where a group begins.
-// Group E is what has no adapter.
-struct Groups {
-    int tp[MAXE + 2], lo[MAXE + 2];
-};
-
-// Fills the table (all threads of the CTA; ends with a sync) and returns the number of
-// tiles. Offsets are clamped to [0, T]; a group that ends before it begins is empty.
-template <int TM>
-MOE_DEV int group_table(const AdapterArgs& a, bool rest, Groups& g) {
-    __shared__ int wsum[THREADS / 32];
-    constexpr int PER = (MAXE + 1 + THREADS - 1) / THREADS;
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int G = a.E + 1, per = (G + THREADS - 1) / THREADS;
-    int lo[PER], c[PER], sum = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = t * per + i;
-        lo[i] = c[i] = 0;
-        if (i < per && e < G) {
-            lo[i] = min(max(__ldg(a.offsets + e), 0), a.T);
-            const int hi = e < a.E ? min(max(__ldg(a.offsets + e + 1), 0), a.T) : (rest ? a.T : lo[i]);
-            c[i] = hi > lo[i] ? (hi - lo[i] + TM - 1) / TM : 0;
-            g.lo[e] = lo[i];
-        }
-        sum += c[i];
-    }
-    int x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) wsum[w] = x;
-    __syncthreads();
-    int before = x - sum, total = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        before += i < w ? wsum[i] : 0;
-        total += wsum[i];
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = t * per + i;
-        if (i < per && e < G) g.tp[e] = before;
-        before += c[i];
-    }
-    if (t == 0) {
-        g.tp[G] = total;
-        g.lo[G] = a.T;
-    }
-    __syncthreads();
-    return total;
-}
-
-struct Tile {
-    int e, pos, n;  // group, first position, positions
-};
-template <int TM>
-MOE_DEV Tile tile_of(int u, const AdapterArgs& a, const Groups& g) {
-    int lo = 0, hi = a.E + 1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (g.tp[mid] <= u) lo = mid;
-        else hi = mid;
-    }
-    // a group's end is the next one's begin (offsets ascend); the last tile of one may be short
-    const int end = lo < a.E ? min(max(__ldg(a.offsets + lo + 1), 0), a.T) : a.T;
-    Tile t;
-    t.e = lo;
-    t.pos = g.lo[lo] + (u - g.tp[lo]) * TM;
-    t.n = min(TM, end - t.pos);
-    return t;
-}
-
-// The row that position i stands for, -1 where the index names none.
-MOE_DEV int row_of(const AdapterArgs& a, int i) {
-    const int r = a.rows != nullptr ? __ldg(a.rows + i) : i;
-    return r >= 0 && r < a.T ? r : -1;
-}
 
 // ---------------------------------------------------------------------------
 // any type, width, rank and alignment
@@ -252,27 +165,27 @@ MOE_DEV uint2 load4(const T* p, int n) {
     return v;
 }
 
-// v = s x A^T of 16 MT positions by 8 NT ranks and one slice of d: the CTA's warps take
-// every eighth 32 of the slice, and their sums are added in order.
+// v = s x A^T of 16 MT positions by 8 NT ranks and one slice of d, by a warp; what reads v
+// adds the slices in order.
 //   a.v [slices][T][rp], rp = r rounded up to 16 and the ranks behind r zero.
 template <int MT, int NT>
 struct Shrink {
     // chunks of 32 a warp has in flight, as registers allow
-    static constexpr int AHEAD = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 10 ? 2 : 1;
+    static constexpr int AHEAD = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 6 ? 3 : 2;
 };
 template <typename T, int MT, int NT, bool VEC>
 __global__ void __launch_bounds__(THREADS, 2) adapter_shrink_mma_kernel(const __grid_constant__ AdapterArgs a) {
     constexpr int WARPS = THREADS / 32, U = Shrink<MT, NT>::AHEAD;
     __shared__ Groups g;
-    __shared__ float red[WARPS][NT * 4][32];
     pdl_wait();
     pdl_trigger();
     const int tiles = group_table<16 * MT>(a, false, g);
-    const int lane = static_cast<int>(lane_id()), w = threadIdx.x >> 5, gi = lane >> 2, ti = lane & 3;
+    const int lane = static_cast<int>(lane_id()), gi = lane >> 2, ti = lane & 3;
     const int rb = (a.rp + 8 * NT - 1) / (8 * NT), parts = rb * a.slices;
     const int len = ((a.d + a.slices - 1) / a.slices + 31) / 32 * 32;
     const T* x = static_cast<const T*>(a.x);
-    for (long long u = blockIdx.x; u < static_cast<long long>(tiles) * parts; u += gridDim.x) {
+    const long long units = static_cast<long long>(tiles) * parts, step = static_cast<long long>(gridDim.x) * WARPS;
+    for (long long u = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); u < units; u += step) {
         const Tile t = tile_of<16 * MT>(static_cast<int>(u / parts), a, g);
         const int part = static_cast<int>(u % parts), j0 = part % rb * 8 * NT, slice = part / rb;
         const int k0 = slice * len, k1 = min(a.d, k0 + len);
@@ -289,226 +202,225 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_shrink_mma_kernel(const __
                     else if (ti == 0) atomicOr(a.err, ERRBIT_INDEX);
                 }
             }
-        const T* A = static_cast<const T*>(a.a) + static_cast<long long>(t.e) * a.r * a.d;
+        const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + j0 + gi) * a.d;
         float acc[MT][NT][4] = {};
-        for (int k = k0 + 32 * w; k < k1; k += 32 * WARPS * U) {
-            uint4 fx[U][MT][2], fa[U][NT];
-#pragma unroll
-            for (int c = 0; c < U; ++c) {
-                const int at = k + 32 * WARPS * c + 8 * ti, n = k1 - at;
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) fx[c][m][h] = load8<T, VEC>(xr[m][h] + at, xr[m][h] != nullptr ? n : 0);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int rank = j0 + 8 * j + gi;
-                    fa[c][j] = load8<T, VEC>(A + static_cast<long long>(rank) * a.d + at, rank < a.r ? n : 0);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < U; ++c)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        mma16816<T>(acc[m][j], fx[c][m][0].x, fx[c][m][1].x, fx[c][m][0].y, fx[c][m][1].y, fa[c][j].x, fa[c][j].y);
-                        mma16816<T>(acc[m][j], fx[c][m][0].z, fx[c][m][1].z, fx[c][m][0].w, fx[c][m][1].w, fa[c][j].z, fa[c][j].w);
-                    }
-        }
-        const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
-        float* out = a.v + static_cast<long long>(slice) * a.T * a.rp;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) red[w][4 * j + i][lane] = acc[m][j][i];
-            __syncthreads();
-            for (int i = threadIdx.x; i < NT * 128; i += THREADS) {
-                const int q = i >> 5, l = i & 31;
-                float v = red[0][q][l];
-#pragma unroll
-                for (int o = 1; o < WARPS; ++o) v += red[o][q][l];
-                const int p = 16 * m + 8 * (q >> 1 & 1) + (l >> 2), rank = j0 + 8 * (q >> 2) + 2 * (l & 3) + (q & 1);
-                if (p < t.n && rank < a.rp) out[static_cast<long long>(t.pos + p) * a.rp + rank] = rank < a.r ? s * v : 0.0f;
-            }
-            __syncthreads();
-        }
-    }
-}
-
-// v in pieces of T that add up to it: 2 for 16-bit outputs (bf16: 16 bits of v), 3 for FP32.
-// FP16 first takes a row to below 2^15 by a power of two.
-template <typename T>
-MOE_DEV uint32_t pack2(T x, T y) {
-    return static_cast<uint32_t>(*reinterpret_cast<unsigned short*>(&x)) |
-           static_cast<uint32_t>(*reinterpret_cast<unsigned short*>(&y)) << 16;
-}
-template <typename T, int NP>
-MOE_DEV void split(float v, T (&p)[NP]) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        p[i] = from_f32<T>(v);
-        const float f = to_f32(p[i]);
-        v = fabsf(f) <= 3.4e38f ? v - f : 0.0f;  // nothing is left of an infinity or a NaN
-    }
-}
-
-// out = base + v B^T of 16 MT positions by a range of columns. A warp takes 32 columns at a
-// time: column 2 i + c of its instruction j stands for column 8 i + 2 j + c, so that a lane
-// ends with 8 consecutive columns of its two rows.
-template <typename T, typename O, int MT, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) adapter_expand_mma_kernel(const __grid_constant__ AdapterArgs a) {
-    constexpr int WARPS = THREADS / 32, NP = sizeof(O) == 4 ? 3 : 2, ROWS = 16 * MT;
-    constexpr bool SCALED = __is_same(T, __half);
-    __shared__ Groups g;
-    __shared__ int srow[ROWS];
-    __shared__ float sscale[SCALED ? ROWS : 1];
-    extern __shared__ __align__(16) uint4 frag[];  // [rp / 16][NP][MT][32]
-    pdl_wait();
-    pdl_trigger();
-    const int tiles = group_table<ROWS>(a, !a.in_place, g);
-    const int lane = static_cast<int>(lane_id()), w = threadIdx.x >> 5, gi = lane >> 2, ti = lane & 3;
-    const int KS = a.rp / 16, nb = a.col_parts, len = ((a.N + nb - 1) / nb + 31) / 32 * 32;
-    const O* base = static_cast<const O*>(a.base);
-    O* out = static_cast<O*>(a.out);
-    const long long plane = static_cast<long long>(a.T) * a.rp;
-    auto inner = [&](int p, int k) {
-        const float* v = a.v + static_cast<long long>(p) * a.rp + k;
-        float4 s = *reinterpret_cast<const float4*>(v);
-        for (int i = 1; i < a.slices; ++i) {
-            const float4 o = *reinterpret_cast<const float4*>(v + i * plane);
-            s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
-        }
-        return s;
-    };
-    for (long long u = blockIdx.x; u < static_cast<long long>(tiles) * nb; u += gridDim.x) {
-        const Tile t = tile_of<ROWS>(static_cast<int>(u / nb), a, g);
-        const int c0 = static_cast<int>(u % nb) * len, c1 = min(a.N, c0 + len);
-        const bool adapted = t.e < a.E;
-        __syncthreads();
-        if (threadIdx.x < ROWS) srow[threadIdx.x] = threadIdx.x < t.n ? row_of(a, t.pos + threadIdx.x) : -1;
-        if (adapted) {
-            if constexpr (SCALED) {
-                constexpr int PER = THREADS / ROWS;  // threads a row, within a warp
-                const int row = threadIdx.x / PER;
-                float m = 0.0f;
-                for (int k = threadIdx.x % PER * 4; row < t.n && k < a.rp; k += PER * 4) {
-                    const float4 v = inner(t.pos + row, k);
-                    for (float f : {v.x, v.y, v.z, v.w})
-                        if (fabsf(f) <= 3.4e38f) m = fmaxf(m, fabsf(f));
-                }
-#pragma unroll
-                for (int o = PER / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                // 2^(14 - e) for a largest value of [2^e, 2^(e + 1))
-                const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
-                if (threadIdx.x % PER == 0) sscale[row] = __uint_as_float(static_cast<uint32_t>(min(max(14 - e, -126), 126) + 127) << 23);
-                __syncthreads();
-            }
-            for (int i = threadIdx.x; i < KS * MT * 32; i += THREADS) {
-                const int l = i & 31, m = i / 32 % MT, ks = i / (32 * MT), k = 16 * ks + 4 * (l & 3);
-                T q[2][4][NP];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int p = 16 * m + 8 * h + (l >> 2);
-                    float4 v = p < t.n ? inner(t.pos + p, k) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if constexpr (SCALED) {
-                        const float f = sscale[p];
-                        v.x *= f; v.y *= f; v.z *= f; v.w *= f;
-                    }
-                    split<T, NP>(v.x, q[h][0]);
-                    split<T, NP>(v.y, q[h][1]);
-                    split<T, NP>(v.z, q[h][2]);
-                    split<T, NP>(v.w, q[h][3]);
-                }
-#pragma unroll
-                for (int o = 0; o < NP; ++o)
-                    frag[((ks * NP + o) * MT + m) * 32 + l] =
-                        make_uint4(pack2(q[0][0][o], q[0][1][o]), pack2(q[1][0][o], q[1][1][o]), pack2(q[0][2][o], q[0][3][o]),
-                                   pack2(q[1][2][o], q[1][3][o]));
-            }
-        }
-        __syncthreads();
-        const T* B = static_cast<const T*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
-        for (int n0 = c0 + 32 * w; n0 < c1; n0 += 32 * WARPS) {
-            const int col = n0 + 8 * ti, cols = min(8, c1 - col);
-            float acc[MT][4][4] = {};
-            float add[MT][2][8];
+        uint4 fx[U][MT][2], fa[U][NT];
+        auto load = [&](int c, int k) {
+            const int at = k + 8 * ti, n = k1 - at;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = srow[16 * m + 8 * h + gi];
-                    const bool there = base != nullptr && row >= 0 && cols > 0;
-                    const O* p = base + row * a.base_stride + col;
-                    if constexpr (VEC) {
-                        constexpr int W = 16 / sizeof(O);
+                for (int h = 0; h < 2; ++h) fx[c][m][h] = load8<T, VEC>(xr[m][h] + at, xr[m][h] != nullptr ? n : 0);
 #pragma unroll
-                        for (int i = 0; i < 8; i += W) {
-                            Raw<O, W> v;
-                            v.clear();
-                            if (there) v.v = *reinterpret_cast<const uint4*>(p + i);
-                            float f[W];
-                            v.get(f);
+            for (int j = 0; j < NT; ++j)
+                fa[c][j] = load8<T, VEC>(A + static_cast<long long>(8 * j) * a.d + at, j0 + 8 * j + gi < a.r ? n : 0);
+        };
 #pragma unroll
-                            for (int q = 0; q < W; ++q) add[m][h][i + q] = f[q];
-                        }
-                    } else {
+        for (int c = 0; c < U; ++c) load(c, k0 + 32 * c);
+        for (int k = k0; k < k1; k += 32 * U) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) add[m][h][i] = there && i < cols ? to_f32(p[i]) : 0.0f;
+            for (int c = 0; c < U; ++c) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {  // chunks behind the slice are zeros
+                        mma16816<T>(acc[m][j], fx[c][m][0].x, fx[c][m][1].x, fx[c][m][0].y, fx[c][m][1].y, fa[c][j].x, fa[c][j].y);
+                        mma16816<T>(acc[m][j], fx[c][m][0].z, fx[c][m][1].z, fx[c][m][0].w, fx[c][m][1].w, fa[c][j].z, fa[c][j].w);
+                    }
+                load(c, k + 32 * (c + U));
+            }
+        }
+        const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
+        float* out = a.v + (static_cast<long long>(slice) * a.T + t.pos) * a.rp;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = 16 * m + 8 * h + gi;
+                if (i >= t.n) continue;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int rank = j0 + 8 * j + 2 * ti;
+                    if (rank < a.rp)
+                        *reinterpret_cast<float2*>(out + i * a.rp + rank) =
+                            make_float2(rank < a.r ? s * acc[m][j][2 * h] : 0.0f, rank + 1 < a.r ? s * acc[m][j][2 * h + 1] : 0.0f);
+                }
+            }
+    }
+}
+
+// out = base + v B^T. A warp takes 16 MT positions by a range of columns, 32 at a time and
+// the next 32 of base under way; its pieces of v stay in shared memory, each lane its own,
+// so warps wait for nobody. The warps of a CTA take neighbouring tiles and the same columns:
+// where those have one adapter, B comes from L1. Column 2 i + c of a warp's instruction j
+// stands for column 8 i + 2 j + c, so that a lane ends with 8 consecutive columns of its rows.
+//
+// KB: steps of 16 ranks whose B is loaded at once, the next ones under way. From two steps on a
+// lane's ranks are 8 consecutive ones of 32 (rp a multiple of 16 KB), else 4 of 16.
+template <typename T, typename O, int MT, int KB, bool VEC>
+__global__ void __launch_bounds__(THREADS, 2) adapter_expand_mma_kernel(const __grid_constant__ AdapterArgs a) {
+    constexpr int WARPS = THREADS / 32, NP = sizeof(O) == 4 ? 3 : 2;
+    constexpr bool SCALED = __is_same(T, __half);
+    constexpr bool AHEAD = KB == 1;  // the next columns' base too: where B takes few registers
+    __shared__ Groups g;
+    extern __shared__ __align__(16) uint4 frags[];  // [WARPS][rp / 16][NP][MT][32]
+    // what the call was given is complete before the launch before this one could begin
+    const int tiles = group_table<16 * MT>(a, !a.in_place, g);
+    const int lane = static_cast<int>(lane_id()), w = threadIdx.x >> 5, gi = lane >> 2, ti = lane & 3;
+    const int KS = a.rp / 16, nb = a.col_parts, len = ((a.N + nb - 1) / nb + 31) / 32 * 32;
+    uint4* frag = frags + w * KS * NP * MT * 32 + lane;
+    const O* base = static_cast<const O*>(a.base);
+    O* out = static_cast<O*>(a.out);
+    bool waited = false;
+    for (int u = blockIdx.x; u < (tiles + WARPS - 1) / WARPS * nb; u += gridDim.x) {
+        const int tile = u / nb * WARPS + w;
+        if (tile >= tiles) continue;
+        const Tile t = tile_of<16 * MT>(tile, a, g);
+        const int c0 = u % nb * len, c1 = min(a.N, c0 + len);
+        const bool adapted = t.e < a.E;
+        const T* B = static_cast<const T*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
+        int row[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = 16 * m + 8 * h + gi;
+                row[m][h] = i < t.n ? row_of(a, t.pos + i) : -1;
+            }
+        Cols<O, VEC> add[MT][2];
+        auto load_base = [&](int n0) {
+            const int col = n0 + 8 * ti;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    add[m][h].load(base + row[m][h] * a.base_stride + col, base != nullptr && row[m][h] >= 0 ? c1 - col : 0);
+        };
+        uint2 fb[KB][4];
+        auto rank_of = [&](int ks) { return KB == 1 ? 16 * ks + 4 * ti : 32 * (ks >> 1) + 8 * ti + 4 * (ks & 1); };
+        auto load_b = [&](int n0, int ks) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = n0 + 8 * (gi >> 1) + 2 * j + (gi & 1);
+                const T* p = B + static_cast<long long>(n) * a.r;
+                if constexpr (KB == 1) {
+                    const int k = rank_of(ks);
+                    fb[0][j] = load4<T, VEC>(p + k, adapted && n < c1 ? a.r - k : 0);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < KB; q += 2) {
+                        const int k = rank_of(ks + q);
+                        const uint4 v = load8<T, VEC>(p + k, adapted && n < c1 ? a.r - k : 0);
+                        fb[q][j] = make_uint2(v.x, v.y);
+                        fb[q + 1][j] = make_uint2(v.z, v.w);
                     }
                 }
-            if (adapted) {
-                for (int ks = 0; ks < KS; ++ks) {
-                    const int k = 16 * ks + 4 * ti;
-                    uint2 fb[4];
+            }
+        };
+        load_b(c0, 0);
+        if constexpr (AHEAD) load_base(c0);
+        if (!waited) {  // v
+            pdl_wait();
+            pdl_trigger();
+            waited = true;
+        }
+        float back[MT][2];
+        if (adapted) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int n = n0 + 8 * (gi >> 1) + 2 * j + (gi & 1);
-                        fb[j] = load4<T, VEC>(B + static_cast<long long>(n) * a.r + k, n < c1 ? a.r - k : 0);
+            for (int m = 0; m < MT; ++m) {
+                float scale[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    scale[h] = back[m][h] = 1.0f;
+                    if constexpr (SCALED) {
+                        const int i = 16 * m + 8 * h + gi;
+                        float most = 0.0f;
+                        for (int k = 4 * ti; i < t.n && k < a.rp; k += 16) most = largest_finite(inner4(a, t.pos + i, k), most);
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                        row_scale(most, scale[h], back[m][h]);
                     }
+                }
+                for (int ks = 0; ks < KS; ++ks) {
+                    T q[2][4][NP];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = 16 * m + 8 * h + gi;
+                        const float4 v = i < t.n ? inner4(a, t.pos + i, rank_of(ks)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        split<T, NP>(v.x * scale[h], q[h][0]);
+                        split<T, NP>(v.y * scale[h], q[h][1]);
+                        split<T, NP>(v.z * scale[h], q[h][2]);
+                        split<T, NP>(v.w * scale[h], q[h][3]);
+                    }
+#pragma unroll
+                    for (int o = 0; o < NP; ++o)
+                        frag[((ks * NP + o) * MT + m) * 32] =
+                            make_uint4(pack2(q[0][0][o], q[0][1][o]), pack2(q[1][0][o], q[1][1][o]), pack2(q[0][2][o], q[0][3][o]),
+                                       pack2(q[1][2][o], q[1][3][o]));
+                }
+            }
+        }
+        for (int n0 = c0; n0 < c1; n0 += 32) {
+            Cols<O, VEC> here[MT][2];
+            if constexpr (AHEAD) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) here[m][h] = add[m][h];
+                load_base(n0 + 32);
+            } else {
+                load_base(n0);
+            }
+            float acc[MT][4][4] = {};
+            for (int ks = 0; ks < KS; ks += KB) {
+                uint2 cur[KB][4];
+#pragma unroll
+                for (int q = 0; q < KB; ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cur[q][j] = fb[q][j];
+                if (ks + KB < KS) load_b(n0, ks + KB);
+                else load_b(n0 + 32, 0);
+                if (!adapted) break;
+#pragma unroll
+                for (int q = 0; q < KB; ++q)
 #pragma unroll
                     for (int o = 0; o < NP; ++o)
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            const uint4 f = frag[((ks * NP + o) * MT + m) * 32 + lane];
+                            const uint4 f = frag[(((ks + q) * NP + o) * MT + m) * 32];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) mma16816<T>(acc[m][j], f.x, f.y, f.z, f.w, fb[j].x, fb[j].y);
+                            for (int j = 0; j < 4; ++j) mma16816<T>(acc[m][j], f.x, f.y, f.z, f.w, cur[q][j].x, cur[q][j].y);
                         }
-                }
             }
+            if constexpr (!AHEAD) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) here[m][h] = add[m][h];
+            }
+            const int col = n0 + 8 * ti;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int p = 16 * m + 8 * h + gi, row = srow[p];
-                    if (row < 0 || cols <= 0) continue;
+                    if (row[m][h] < 0 || col >= c1) continue;
                     float f[8];
-                    const float back = SCALED && adapted ? 1.0f / sscale[p] : 1.0f;  // a power of two
+                    here[m][h].get(f);
+                    if (adapted) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = fmaf(acc[m][i >> 1][2 * h + (i & 1)], back, add[m][h][i]);
-                    O* o = out + row * a.out_stride + col;
-                    if constexpr (VEC) {
-                        constexpr int W = 16 / sizeof(O);
-#pragma unroll
-                        for (int i = 0; i < 8; i += W) {
-                            float e[W];
-#pragma unroll
-                            for (int q = 0; q < W; ++q) e[q] = f[i + q];
-                            Raw<O, W> v;
-                            v.set(e);
-                            v.store(o + i);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (i < cols) o[i] = from_f32<O>(f[i]);
+                        for (int i = 0; i < 8; ++i) f[i] = fmaf(acc[m][i >> 1][2 * h + (i & 1)], back[m][h], f[i]);
                     }
+                    Cols<O, VEC>::store(out + row[m][h] * a.out_stride + col, c1 - col, f);
                 }
         }
     }
+    if (!waited) {  // never done before the launch before it
+        pdl_wait();
+        pdl_trigger();
+    }
 }
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // Tiles of tm positions at most: a part full one a group, or a position each.
 long long most_tiles(const AdapterArgs& a, int tm) {
@@ -531,28 +443,38 @@ cudaError_t launch_simt(const AdapterArgs& a, cudaStream_t s) {
 
 template <typename T, int MT, bool VEC>
 cudaError_t shrink_mma(const AdapterArgs& a, cudaStream_t s) {
+    constexpr int WARPS = THREADS / 32;
     const long long tiles = most_tiles(a, 16 * MT) * a.slices;
-    if (a.rp <= 16) return launch_units(adapter_shrink_mma_kernel<T, MT, 2, VEC>, tiles, 4, 0, s, a);
-    if (a.rp <= 32) return launch_units(adapter_shrink_mma_kernel<T, MT, 4, VEC>, tiles, 4, 0, s, a);
-    return launch_units(adapter_shrink_mma_kernel<T, MT, 8, VEC>, tiles * ((a.rp + 63) / 64), 4, 0, s, a);
+    if (a.rp <= 16) return launch_units(adapter_shrink_mma_kernel<T, MT, 2, VEC>, (tiles + WARPS - 1) / WARPS, 4, 0, s, a);
+    return launch_units(adapter_shrink_mma_kernel<T, MT, 4, VEC>, (tiles * ((a.rp + 31) / 32) + WARPS - 1) / WARPS, 4, 0, s, a);
 }
 
-template <typename T, typename O, int MT, bool VEC>
-cudaError_t expand_mma(AdapterArgs a, cudaStream_t s) {
-    const long long tiles = most_tiles(a, 16 * MT);
-    // a range of columns a CTA: 256 (one turn of its warps) while the CTAs are few, else up to 1024
-    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + 255) / 256, (8LL * num_sms() + tiles - 1) / tiles)));
-    constexpr int STEP = (sizeof(O) == 4 ? 3 : 2) * MT * 512;  // of 16 ranks
+constexpr int EXPAND_SMEM = 200 << 10;  // the pieces of v of 256 ranks and one tile a warp
+
+template <typename T, typename O, int MT, int KB, bool VEC>
+cudaError_t expand_mma_k(AdapterArgs a, cudaStream_t s) {
+    constexpr int WARPS = THREADS / 32, STEP = (sizeof(O) == 4 ? 3 : 2) * MT * 512 * WARPS;  // of 16 ranks
     static bool done[64] = {};
-    if (!allow_smem(adapter_expand_mma_kernel<T, O, MT, VEC>, 16 * STEP, done)) return cudaErrorInvalidValue;
-    const size_t smem = static_cast<size_t>(a.rp / 16) * STEP;
-    return launch_units(adapter_expand_mma_kernel<T, O, MT, VEC>, tiles * a.col_parts, 4, smem, s, a);
+    if (!allow_smem(adapter_expand_mma_kernel<T, O, MT, KB, VEC>, std::min(16 * STEP, EXPAND_SMEM), done)) return cudaErrorInvalidValue;
+    const long long groups = (most_tiles(a, 16 * MT) + WARPS - 1) / WARPS;
+    // ranges of columns: as many as give every SM two CTAs twice over, 32 columns at least
+    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + 31) / 32, (4LL * num_sms() + groups - 1) / groups)));
+    return launch_units(adapter_expand_mma_kernel<T, O, MT, KB, VEC>, groups * a.col_parts, 4, static_cast<size_t>(a.rp / 16) * STEP, s, a);
 }
-
-bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+template <typename T, typename O, int MT, bool VEC>
+cudaError_t expand_mma(const AdapterArgs& a, cudaStream_t s) {
+    if constexpr (VEC && MT == 1) {
+        if (a.r % 8 == 0 && aligned_to(a.b, 16)) {
+            if (a.rp % 64 == 0) return expand_mma_k<T, O, 1, 4, true>(a, s);
+            if (a.rp % 32 == 0) return expand_mma_k<T, O, 1, 2, true>(a, s);
+        }
+    }
+    return expand_mma_k<T, O, MT, 1, VEC>(a, s);
+}
 
 template <typename T, typename O>
 cudaError_t launch_mma(const AdapterArgs& a, cudaStream_t s) {
+    if (adapter_tc_takes(a)) return launch_adapter_tc(a, s);
     const bool in = a.d % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.a, 16);
     const bool out = a.N % 8 == 0 && a.r % 4 == 0 && aligned_to(a.b, 8) && aligned_to(a.out, 16) &&
                      a.out_stride * sizeof(O) % 16 == 0 && aligned_to(a.base, 16) && a.base_stride * sizeof(O) % 16 == 0;
@@ -561,28 +483,29 @@ cudaError_t launch_mma(const AdapterArgs& a, cudaStream_t s) {
     if (many) e = in ? shrink_mma<T, 2, true>(a, s) : shrink_mma<T, 2, false>(a, s);
     else e = in ? shrink_mma<T, 1, true>(a, s) : shrink_mma<T, 1, false>(a, s);
     if (e != cudaSuccess) return e;
-    if (many) return out ? expand_mma<T, O, 2, true>(a, s) : expand_mma<T, O, 2, false>(a, s);
+    // two tiles a warp while their pieces of v leave room for two CTAs an SM
+    if (many && a.rp / 16 * (sizeof(O) == 4 ? 3 : 2) * 8192 <= 96 << 10) return out ? expand_mma<T, O, 2, true>(a, s) : expand_mma<T, O, 2, false>(a, s);
     return out ? expand_mma<T, O, 1, true>(a, s) : expand_mma<T, O, 1, false>(a, s);
 }
 
-// Slices of d: enough for two CTAs an SM, of 512 at least.
-int adapter_slices(int T, int d, int E) {
-    const long long tiles = (T + 31) / 32 + std::min<long long>(E, T);
-    return static_cast<int>(std::max<long long>(1, std::min<long long>({(2LL * num_sms() + tiles - 1) / tiles, d / 512, 8})));
+// Slices of d: warps for all SMs from the tiles there may be, 256 of d at least.
+int adapter_slices(int T, int d, int r, int E) {
+    const long long units = ((T + 31) / 32 + std::min<long long>(E, T)) * ((r + 31) / 32), warps = 16LL * num_sms();
+    return static_cast<int>(std::max<long long>(1, std::min<long long>({(warps + units - 1) / units, d / 256, 8})));
 }
 
 }  // namespace
 
 size_t adapter_workspace(int T, int d, int r, int E, int dtype) {
     if (dtype == MOE_F32) return 256 + static_cast<size_t>(T) * r * 4;
-    return 256 + static_cast<size_t>(T) * ((r + 15) / 16 * 16) * 4 * adapter_slices(T, d, E);
+    return 256 + static_cast<size_t>(T) * ((r + 15) / 16 * 16) * 4 * std::max(adapter_slices(T, d, r, E), adapter_tc_slices(T, d, E));
 }
 
 cudaError_t launch_adapter(const AdapterArgs& args, cudaStream_t s) {
     AdapterArgs a = args;
     if (a.dtype == MOE_F32) return launch_simt<float, float>(a, s);
     a.rp = (a.r + 15) / 16 * 16;
-    a.slices = adapter_slices(a.T, a.d, a.E);
+    a.slices = adapter_slices(a.T, a.d, a.r, a.E);
     const bool wide = a.out_dtype == MOE_F32;
     if (a.dtype == MOE_BF16) return wide ? launch_mma<__nv_bfloat16, float>(a, s) : launch_mma<__nv_bfloat16, __nv_bfloat16>(a, s);
     return wide ? launch_mma<__half, float>(a, s) : launch_mma<__half, __half>(a, s);

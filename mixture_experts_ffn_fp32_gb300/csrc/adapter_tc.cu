@@ -1,0 +1,435 @@
+// Low-rank adapters (adapter.cu) of many rows on the 5th-generation tensor cores, 16-bit
+// types. Tiles of 128 positions of one adapter.
+//
+// The first launch computes v = s x A^T: a stage is 64 of d, 128 rows of x (gathered) and the
+// adapter's rank rows of A, copied asynchronously into 128-byte-swizzled rows; one thread
+// issues the MMAs (128 x rp x 16), the accumulator [128, rp] stays in tensor memory. Tiles are
+// dealt out in slices of d, so that there is a CTA for every SM's two places; what reads v adds
+// the slices in order.
+//
+// The second computes out = base + v B^T in blocks of 128 columns: v in pieces of T (split) is
+// the A operand, [v_1 | v_2 | ..] against the same rows of B, so that the product keeps 16 bits
+// of v (FP32 output: 24). Two accumulators take turns: the MMAs of a block run under the
+// last one's output. B's rows stand in an order in which a lane that reads 16 x 256 bits of
+// tensor memory ends with 8 consecutive columns of its rows.
+//
+// Every wait is bounded (common.cuh); one that runs out leaves NaN in what is not stored yet.
+#include <math_constants.h>
+
+#include "adapter.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int ROWS = 128, BLOCK = 16384;  // a block: 128 rows of 64 elements of 16 bits
+constexpr int MAX_RP = 128;
+
+MOE_DEV void cp_async_16z(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// 16-byte piece c of row r of a 128-byte-swizzled tile.
+MOE_DEV uint32_t swizzled(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+MOE_DEV uint32_t elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(e));
+    return e;
+}
+
+// FP32 accumulator; A and B K-major, of T; 128 x N.
+template <typename T>
+constexpr uint32_t idesc(int N) {
+    const uint32_t type = __is_same(T, __half) ? 0u : 1u;
+    return (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(ROWS >> 4) << 24);
+}
+
+// 16 lanes x 32 columns: register 4 j + i of lane (g, t) holds column 8 j + 2 t + (i & 1) of row
+// g + 8 (i >> 1).
+MOE_DEV void tc_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+MOE_DEV uint8_t* align_1k(uint8_t* p) {
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
+}
+
+template <typename T, int STAGES>
+__global__ void __launch_bounds__(THREADS, 2)
+adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int cols, unsigned long long timeout_ns) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Groups g;
+    __shared__ __align__(8) uint64_t bars[STAGES];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    uint8_t* smem = align_1k(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int stage_bytes = BLOCK + a.rp * 128;
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](uint32_t i) { return smem_u32(&bars[i]); };
+    if (tid == 0) {
+        for (int i = 0; i < STAGES; ++i) mbar_init(bar(i), 1);
+        abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), cols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    tc_fence_before();
+    const int tiles = group_table<ROWS>(a, false, g);
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const WaitCtx wc{a.err, &abort_flag, timeout_ns};
+    const int len = ((a.d + a.slices - 1) / a.slices + 63) / 64 * 64;
+    const T* x = static_cast<const T*>(a.x);
+    const int c16 = tid & 7, r0 = tid >> 3;  // this thread's 16-byte piece, its rows r0 + 32 i
+    bool alive = true;
+    uint32_t it = 0;  // stages consumed: stage it % STAGES, its (it / STAGES)th use
+    for (int u = blockIdx.x; u < tiles * a.slices; u += gridDim.x) {
+        const Tile t = tile_of<ROWS>(u / a.slices, a, g);
+        const int slice = u % a.slices, k0 = slice * len, k1 = min(a.d, k0 + len), n = k1 > k0 ? (k1 - k0 + 63) / 64 : 0;
+        const T* xr[ROWS / 32];
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; ++i) {
+            const int p = r0 + 32 * i;
+            xr[i] = nullptr;
+            if (p < t.n) {
+                const int r = row_of(a, t.pos + p);
+                if (r >= 0) xr[i] = x + r * a.x_stride;
+                else if (c16 == 0) atomicOr(a.err, ERRBIT_INDEX);
+            }
+        }
+        const T* A = static_cast<const T*>(a.a) + static_cast<long long>(t.e) * a.r * a.d;
+        auto load = [&](int kb, uint32_t stage) {
+            const int k = k0 + 64 * kb + 8 * c16;
+            const uint32_t at = sbase + stage * stage_bytes;
+#pragma unroll
+            for (int i = 0; i < ROWS / 32; ++i) {
+                const bool there = xr[i] != nullptr && k < k1;
+                cp_async_16z(at + swizzled(r0 + 32 * i, c16), there ? xr[i] + k : x, there);
+            }
+            for (int r = r0; r < a.rp; r += 32) {
+                const bool there = r < a.r && k < k1;
+                cp_async_16z(at + BLOCK + swizzled(r, c16), there ? A + static_cast<long long>(r) * a.d + k : A, there);
+            }
+        };
+        for (int s = 0; s < STAGES - 1; ++s) {
+            if (s < n) load(s, (it + s) % STAGES);
+            cp_async_commit();
+        }
+        for (int kb = 0; kb < n; ++kb, ++it) {
+            cp_async_wait<STAGES - 2>();
+            fence_proxy_async_smem();
+            alive = __syncthreads_and(alive);
+            const uint32_t stage = it % STAGES;
+            if (warp == 0 && alive) {
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t at = sbase + stage * stage_bytes;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tc_mma_bf16(tmem, smem_desc_sw128(at + 32 * q, 16, 1024), smem_desc_sw128(at + BLOCK + 32 * q, 16, 1024),
+                                    idesc<T>(a.rp), kb > 0 || q > 0);
+                    tc_commit(bar(stage));
+                }
+                __syncwarp();
+            }
+            if (kb + STAGES - 1 < n) {
+                // the stage before this one, once its MMAs have read it
+                const uint32_t last = it + STAGES - 1;
+                if (kb > 0 && alive) alive = bounded_wait(bar(last % STAGES), (it - 1) / STAGES & 1, wc);
+                load(kb + STAGES - 1, last % STAGES);
+            }
+            cp_async_commit();
+        }
+        if (alive && n > 0) alive = bounded_wait(bar((it - 1) % STAGES), (it - 1) / STAGES & 1, wc);
+        tc_fence_after();
+        const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
+        const int row = 32 * (warp & 3) + lane;
+        float* out = a.v + (static_cast<long long>(slice) * a.T + t.pos + row) * a.rp;
+        for (int c = 16 * (warp >> 2); c < a.rp; c += 32) {
+            uint32_t v[16];
+            tc_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
+            tc_wait_ld();
+            if (row < t.n) {
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    float f[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f[i] = c + q + i >= a.r || n == 0 ? 0.0f : !alive ? CUDART_NAN_F : s * __uint_as_float(v[q + i]);
+                    *reinterpret_cast<float4*>(out + c + q) = make_float4(f[0], f[1], f[2], f[3]);
+                }
+            }
+        }
+        tc_fence_before();
+        alive = __syncthreads_and(alive);  // the accumulator is free
+        tc_fence_after();
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, cols);
+}
+
+constexpr int COLS = 128;     // columns of a block
+constexpr int B_STAGES = 3;
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(THREADS, 2)
+adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long long timeout_ns) {
+    constexpr int NP = sizeof(O) == 4 ? 3 : 2;
+    constexpr bool SCALED = __is_same(T, __half);
+    constexpr int AHEAD = sizeof(O) == 2 ? 2 : 1;  // quarters of a block whose base is under way
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Groups g;
+    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ int srow[ROWS];
+    __shared__ float sback[SCALED ? ROWS : 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    uint8_t* smem = align_1k(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gi = lane >> 2, ti = lane & 3;
+    const int a_bytes = (NP * a.rp + 63) / 64 * BLOCK, b_bytes = (a.rp + 63) / 64 * BLOCK;
+    const uint32_t sA = smem_u32(smem), sB = sA + a_bytes;
+    if (tid == 0) {
+        mbar_init(smem_u32(&bars[0]), 1);
+        mbar_init(smem_u32(&bars[1]), 1);
+        abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), 2 * COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    // what the call was given is complete before the launch before this one could begin
+    const int tiles = group_table<ROWS>(a, !a.in_place, g);
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const WaitCtx wc{a.err, &abort_flag, timeout_ns};
+    const int nb = a.col_parts, len = ((a.N + nb - 1) / nb + COLS - 1) / COLS * COLS;
+    const O* base = static_cast<const O*>(a.base);
+    O* out = static_cast<O*>(a.out);
+    const int pieces = a.rp / 8;  // of 16 bytes in a row of B
+    bool alive = true, waited = false;
+    uint32_t uses[2] = {0, 0};
+    for (int u = blockIdx.x; u < tiles * nb; u += gridDim.x) {
+        const Tile t = tile_of<ROWS>(u / nb, a, g);
+        const int c0 = u % nb * len, c1 = min(a.N, c0 + len), n = c1 > c0 ? (c1 - c0 + COLS - 1) / COLS : 0;
+        const bool adapted = t.e < a.E;
+        const T* B = static_cast<const T*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
+        auto load_b = [&](int b) {
+            const uint32_t at = sB + b % B_STAGES * b_bytes;
+            for (int i = tid; i < COLS * pieces; i += THREADS) {
+                const int col = i / pieces, c = i % pieces, m = col & 31;
+                // column 8 i + 2 j + c of 32 at row 8 j + 2 i + c
+                const int row = (col & ~31) | (m >> 1 & 3) << 3 | (m >> 3) << 1 | (m & 1);
+                const bool there = c0 + COLS * b + col < c1 && 8 * c < a.r;
+                cp_async_16z(at + (c >> 3) * BLOCK + swizzled(row, c & 7), there ? B + static_cast<long long>(c0 + COLS * b + col) * a.r + 8 * c : B, there);
+            }
+        };
+        __syncthreads();  // the last tile's rows have been read
+        if (tid < ROWS) srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+        for (int b = 0; b < 2; ++b) {
+            if (adapted && b < n) load_b(b);
+            cp_async_commit();
+        }
+        if (!waited) {  // v
+            pdl_wait();
+            pdl_trigger();
+            waited = true;
+        }
+        if (adapted) {
+            const int p = tid >> 1, half = tid & 1;  // a row's pieces by two threads
+            const int pos = t.pos + p;
+            float scale = 1.0f;
+            if constexpr (SCALED) {
+                float most = 0.0f, back;
+                for (int k = half * (a.rp / 2); p < t.n && k < (half + 1) * (a.rp / 2); k += 4) most = largest_finite(inner4(a, pos, k), most);
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                row_scale(most, scale, back);
+                if (half == 0) sback[p] = back;
+            }
+            for (int k = half * (a.rp / 2); k < (half + 1) * (a.rp / 2); k += 8) {
+                T q[8][NP];
+#pragma unroll
+                for (int h = 0; h < 8; h += 4) {
+                    const float4 v = p < t.n ? inner4(a, pos, k + h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    split<T, NP>(v.x * scale, q[h]);
+                    split<T, NP>(v.y * scale, q[h + 1]);
+                    split<T, NP>(v.z * scale, q[h + 2]);
+                    split<T, NP>(v.w * scale, q[h + 3]);
+                }
+#pragma unroll
+                for (int o = 0; o < NP; ++o) {
+                    const int at = o * a.rp + k;
+                    *reinterpret_cast<uint4*>(smem + (at >> 6) * BLOCK + swizzled(p, (at & 63) >> 3)) =
+                        make_uint4(pack2(q[0][o], q[1][o]), pack2(q[2][o], q[3][o]), pack2(q[4][o], q[5][o]), pack2(q[6][o], q[7][o]));
+                }
+            }
+            fence_proxy_async_smem();
+        }
+        __syncthreads();
+        // This warp's 32 rows (its tensor-memory lanes) and 64 of a block's columns.
+        const int r32 = 32 * (warp & 3), c64 = 64 * (warp >> 2);
+        int row[2][2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) row[m][h] = srow[r32 + 16 * m + 8 * h + gi];
+        Cols<O, true> add[AHEAD][2][2];
+        auto load_base = [&](int b, int q, int slot) {
+            const int col = c0 + COLS * b + c64 + 32 * q + 8 * ti;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    add[slot][m][h].load(base + row[m][h] * a.base_stride + col, base != nullptr && row[m][h] >= 0 ? c1 - col : 0);
+        };
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) load_base(0, q, q);
+        for (int b = 0; b <= n; ++b) {
+            if (adapted && b < n) {
+                cp_async_wait<1>();
+                fence_proxy_async_smem();
+                alive = __syncthreads_and(alive);
+                if (warp == 0 && alive) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t d = tmem + (b & 1) * COLS, sb = sB + b % B_STAGES * b_bytes;
+                        for (int o = 0; o < NP; ++o)
+                            for (int ks = 0; ks < a.rp / 16; ++ks) {
+                                const int k = o * a.rp + 16 * ks;
+                                tc_mma_bf16(d, smem_desc_sw128(sA + (k >> 6) * BLOCK + (k & 63) * 2, 16, 1024),
+                                            smem_desc_sw128(sb + (ks >> 2) * BLOCK + (ks & 3) * 32, 16, 1024), idesc<T>(COLS), o > 0 || ks > 0);
+                            }
+                        tc_commit(smem_u32(&bars[b & 1]));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (b > 0) {
+                const int at = b - 1;
+                if (adapted) {
+                    if (alive) alive = bounded_wait(smem_u32(&bars[at & 1]), uses[at & 1] & 1, wc);
+                    ++uses[at & 1];
+                    alive = __all_sync(0xffffffffu, alive);
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int col = c0 + COLS * at + c64 + 32 * q + 8 * ti;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t acc[16];
+                        if (adapted) {
+                            tc_ld_16x256b_x4(tmem + (static_cast<uint32_t>(r32 + 16 * m) << 16) + (at & 1) * COLS + c64 + 32 * q, acc);
+                            tc_wait_ld();
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float f[8];
+                            add[q % AHEAD][m][h].get(f);
+                            if (adapted) {
+                                const float back = SCALED ? sback[r32 + 16 * m + 8 * h + gi] : 1.0f;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    f[i] = alive ? fmaf(__uint_as_float(acc[4 * (i >> 1) + 2 * h + (i & 1)]), back, f[i]) : CUDART_NAN_F;
+                            }
+                            if (row[m][h] >= 0 && col < c1) Cols<O, true>::store(out + row[m][h] * a.out_stride + col, 8, f);
+                        }
+                    }
+                    if (AHEAD == 2) load_base(at + 1, q, q);
+                    else load_base(q == 0 ? at : at + 1, 1 - q, 0);
+                }
+                tc_fence_before();
+            }
+            if (adapted && b + 2 < n) load_b(b + 2);  // over the block whose MMAs were waited for
+            cp_async_commit();
+        }
+    }
+    if (!waited) {  // never done before the launch before it
+        pdl_wait();
+        pdl_trigger();
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 2 * COLS);
+}
+
+long long most_tiles(int T, int E) { return (T + ROWS - 1) / ROWS + std::min<long long>(E + 1, T); }
+
+// Parts to deal `tiles` tiles out in, at most `most`: the fewest whose last wave of two CTAs an
+// SM wastes least.
+int parts_of(long long tiles, int most) {
+    const long long places = 2LL * num_sms();
+    int best = 1;
+    double least = 1e30;
+    for (int p = 1; p <= most; ++p) {
+        const double t = static_cast<double>((tiles * p + places - 1) / places) / p;
+        if (t < 0.95 * least) {
+            least = t;
+            best = p;
+        }
+    }
+    return best;
+}
+
+template <typename T, int STAGES>
+cudaError_t shrink(const AdapterArgs& a, cudaStream_t s) {
+    static bool done[64] = {};
+    const int smem = STAGES * (BLOCK + a.rp * 128) + 1024;
+    if (!allow_smem(adapter_shrink_tc_kernel<T, STAGES>, 110 << 10, done)) return cudaErrorInvalidValue;
+    const long long units = most_tiles(a.T, a.E) * a.slices, cap = 2LL * num_sms();
+    int cols = 32;
+    while (cols < a.rp) cols *= 2;
+    return launch_pdl(adapter_shrink_tc_kernel<T, STAGES>, dim3(static_cast<unsigned>(std::min(units, cap))), dim3(THREADS), smem, s, a,
+                      cols, static_cast<unsigned long long>(wait_timeout_ns()));
+}
+
+template <typename T, typename O>
+cudaError_t launch_t(AdapterArgs a, cudaStream_t s) {
+    a.slices = adapter_tc_slices(a.T, a.d, a.E);
+    const cudaError_t e = a.rp <= 32 ? shrink<T, 5>(a, s) : a.rp <= 64 ? shrink<T, 4>(a, s) : shrink<T, 3>(a, s);
+    if (e != cudaSuccess) return e;
+    constexpr int NP = sizeof(O) == 4 ? 3 : 2;
+    const int smem = ((NP * a.rp + 63) / 64 + B_STAGES * ((a.rp + 63) / 64)) * BLOCK + 1024;
+    static bool done[64] = {};
+    if (!allow_smem(adapter_expand_tc_kernel<T, O>, ((NP * MAX_RP + 63) / 64 + B_STAGES * (MAX_RP / 64)) * BLOCK + 1024, done))
+        return cudaErrorInvalidValue;
+    const long long tiles = most_tiles(a.T, a.E), cap = 2LL * num_sms();
+    a.col_parts = parts_of(tiles, std::min(16, (a.N + COLS - 1) / COLS));
+    return launch_pdl(adapter_expand_tc_kernel<T, O>, dim3(static_cast<unsigned>(std::min(tiles * a.col_parts, cap))), dim3(THREADS),
+                      smem, s, a, static_cast<unsigned long long>(wait_timeout_ns()));
+}
+
+bool on(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace
+
+int adapter_tc_slices(int T, int d, int E) { return parts_of(most_tiles(T, E), std::max(1, std::min(8, d / 512))); }
+
+bool adapter_tc_takes(const AdapterArgs& a) {
+    const int eo = a.out_dtype == MOE_F32 ? 4 : 2;
+    return a.T >= 1024 && a.rp <= MAX_RP && a.d % 8 == 0 && a.x_stride % 8 == 0 && on(a.x, 16) && on(a.a, 16) && a.r % 8 == 0 &&
+           on(a.b, 16) && a.N % 8 == 0 && on(a.out, 16) && a.out_stride * eo % 16 == 0 && on(a.base, 16) && a.base_stride * eo % 16 == 0;
+}
+
+cudaError_t launch_adapter_tc(const AdapterArgs& a, cudaStream_t s) {
+    const bool wide = a.out_dtype == MOE_F32;
+    if (a.dtype == MOE_BF16) return wide ? launch_t<__nv_bfloat16, float>(a, s) : launch_t<__nv_bfloat16, __nv_bfloat16>(a, s);
+    return wide ? launch_t<__half, float>(a, s) : launch_t<__half, __half>(a, s);
+}
+
+}  // namespace moe

@@ -604,5 +604,10 @@ struct AdapterArgs {
 };
 size_t adapter_workspace(int T, int d, int r, int E, int dtype);
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
+// The tensor-core kernels of many rows: whether they take a call (rp set), the slices of d
+// that they deal out, and the call.
+bool adapter_tc_takes(const AdapterArgs& a);
+int adapter_tc_slices(int T, int d, int E);
+cudaError_t launch_adapter_tc(const AdapterArgs& a, cudaStream_t s);
 
 }  // namespace moe
