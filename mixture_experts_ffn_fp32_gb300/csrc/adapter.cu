@@ -12,101 +12,166 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------------------
-// any type, width, rank and alignment
+// FP32
 // ---------------------------------------------------------------------------
-constexpr int SH_ROWS = 4, SH_RANKS = 8;        // of a warp
-constexpr int SH_TILE = SH_ROWS * THREADS / 32;
+// v = s x A^T of 4 positions by 8 ranks and one slice of d, by a warp: its lanes take
+// neighbouring elements of d, and the 32 sums are scattered over the lanes as they are added.
+constexpr int F32_ROWS = 4, F32_RANKS = 8;
 
-template <typename T>
-__global__ void __launch_bounds__(THREADS) adapter_shrink_kernel(const __grid_constant__ AdapterArgs a) {
+template <bool VEC>
+__global__ void __launch_bounds__(THREADS, 3) adapter_shrink_f32_kernel(const __grid_constant__ AdapterArgs a) {
+    constexpr int W = VEC ? 4 : 1;  // elements a lane loads at once
     __shared__ Groups g;
     pdl_wait();
     pdl_trigger();
-    const int tiles = group_table<SH_TILE>(a, false, g);
-    const int lane = static_cast<int>(lane_id()), w = threadIdx.x >> 5;
-    const int rb = (a.r + SH_RANKS - 1) / SH_RANKS;
-    const T* x = static_cast<const T*>(a.x);
-    for (long long u = blockIdx.x; u < static_cast<long long>(tiles) * rb; u += gridDim.x) {
-        const Tile t = tile_of<SH_TILE>(static_cast<int>(u / rb), a, g);
-        const int j0 = static_cast<int>(u % rb) * SH_RANKS;
-        const int p0 = t.pos + w * SH_ROWS;
-        if (p0 >= t.pos + t.n) continue;
-        const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + j0) * a.d;
-        const T* xr[SH_ROWS];
+    const int tiles = group_table<F32_ROWS>(a, false, g);
+    const int lane = static_cast<int>(lane_id());
+    const int rb = (a.rp + F32_RANKS - 1) / F32_RANKS, parts = rb * a.slices;
+    const int len = ((a.d + a.slices - 1) / a.slices + 31) / 32 * 32;
+    const float* x = static_cast<const float*>(a.x);
+    const long long units = static_cast<long long>(tiles) * parts, step = static_cast<long long>(gridDim.x) * (THREADS / 32);
+    for (long long u = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < units; u += step) {
+        const Tile t = tile_of<F32_ROWS>(static_cast<int>(u / parts), a, g);
+        const int part = static_cast<int>(u % parts), j0 = part % rb * F32_RANKS, slice = part / rb;
+        const int k0 = slice * len, k1 = min(a.d, k0 + len);
+        const float* xr[F32_ROWS];
 #pragma unroll
-        for (int i = 0; i < SH_ROWS; ++i) {
-            const int r = p0 + i < t.pos + t.n ? row_of(a, p0 + i) : 0;
+        for (int i = 0; i < F32_ROWS; ++i) {
+            const int r = i < t.n ? row_of(a, t.pos + i) : 0;
             if (r < 0 && lane == 0) atomicOr(a.err, ERRBIT_INDEX);
             xr[i] = x + max(r, 0) * a.x_stride;
         }
-        float acc[SH_ROWS][SH_RANKS] = {};
-        for (int k = lane; k < a.d; k += 32) {
-            float xv[SH_ROWS];
+        const float* A = static_cast<const float*>(a.a) + (static_cast<long long>(t.e) * a.r + j0) * a.d;
+        float acc[F32_ROWS * F32_RANKS] = {};
+#pragma unroll 2
+        for (int k = k0 + lane * W; k < k1; k += 32 * W) {
+            float xv[F32_ROWS][W], av[F32_RANKS][W];
 #pragma unroll
-            for (int i = 0; i < SH_ROWS; ++i) xv[i] = to_f32(xr[i][k]);
+            for (int i = 0; i < F32_ROWS; ++i) load_f32<W>(xr[i] + k, xv[i]);
 #pragma unroll
-            for (int j = 0; j < SH_RANKS; ++j) {
-                const float av = j0 + j < a.r ? to_f32(A[static_cast<long long>(j) * a.d + k]) : 0.0f;
+            for (int j = 0; j < F32_RANKS; ++j) {
+                // ranks behind r read the last one, and are not stored
+                load_f32<W>(A + static_cast<long long>(min(j, a.r - 1 - j0)) * a.d + k, av[j]);
+            }
 #pragma unroll
-                for (int i = 0; i < SH_ROWS; ++i) acc[i][j] = fmaf(xv[i], av, acc[i][j]);
+            for (int i = 0; i < F32_ROWS; ++i)
+#pragma unroll
+                for (int j = 0; j < F32_RANKS; ++j)
+#pragma unroll
+                    for (int q = 0; q < W; ++q) acc[i * F32_RANKS + j] = fmaf(xv[i][q], av[j][q], acc[i * F32_RANKS + j]);
+        }
+        // each turn halves the sums a lane holds: lane l ends with sum l
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+                const float keep = up ? acc[i + o] : acc[i], give = up ? acc[i] : acc[i + o];
+                acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
             }
         }
+        const int p = lane / F32_RANKS, rank = j0 + lane % F32_RANKS;
         const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
-#pragma unroll
-        for (int i = 0; i < SH_ROWS; ++i)
-#pragma unroll
-            for (int j = 0; j < SH_RANKS; ++j) {
-                const float v = seg_sum<32>(acc[i][j]);
-                if (lane == 0 && p0 + i < t.pos + t.n && j0 + j < a.r)
-                    a.v[static_cast<long long>(p0 + i) * a.r + j0 + j] = s * v;
-            }
+        if (p < t.n && rank < a.rp)
+            a.v[(static_cast<long long>(slice) * a.T + t.pos + p) * a.rp + rank] = rank < a.r ? s * acc[0] : 0.0f;
     }
 }
 
-constexpr int EX_TILE = 16, EX_RANKS = 16;
+// out = base + v B^T of 64 positions by ranges of 128 columns: a warp has 8 rows, a lane 4
+// columns of each. B is turned around on its way into shared memory, 32 ranks at a time.
+constexpr int F32_TILE = 64, F32_COLS = 128, F32_STEP = 32;
 
-template <typename T, typename O>
-__global__ void __launch_bounds__(THREADS) adapter_expand_kernel(const __grid_constant__ AdapterArgs a) {
+template <bool VEC>
+__global__ void __launch_bounds__(THREADS, 2) adapter_expand_f32_kernel(const __grid_constant__ AdapterArgs a) {
+    constexpr int PER = F32_TILE / (THREADS / 32);
     __shared__ Groups g;
-    __shared__ __align__(16) float sv[EX_TILE][EX_RANKS];
-    __shared__ int srow[EX_TILE];
+    __shared__ __align__(16) float sv[F32_TILE][F32_STEP];
+    __shared__ __align__(16) float sb[F32_STEP][F32_COLS + 4];
+    __shared__ int srow[F32_TILE];
+    const int tiles = group_table<F32_TILE>(a, !a.in_place, g);
+    const int lane = static_cast<int>(lane_id()), w = threadIdx.x >> 5;
+    const int nb = a.col_parts, len = ((a.N + nb - 1) / nb + F32_COLS - 1) / F32_COLS * F32_COLS;
+    const float* base = static_cast<const float*>(a.base);
+    float* out = static_cast<float*>(a.out);
+    auto column = [&](int i) { return VEC ? 4 * lane + i : lane + 32 * i; };  // of a range, the lane's i-th
     pdl_wait();
     pdl_trigger();
-    const int tiles = group_table<EX_TILE>(a, !a.in_place, g);
-    const int nb = (a.N + THREADS - 1) / THREADS;
-    const O* base = static_cast<const O*>(a.base);
-    O* out = static_cast<O*>(a.out);
     for (long long u = blockIdx.x; u < static_cast<long long>(tiles) * nb; u += gridDim.x) {
-        const Tile t = tile_of<EX_TILE>(static_cast<int>(u / nb), a, g);
-        const int n = static_cast<int>(u % nb) * THREADS + threadIdx.x;
+        const Tile t = tile_of<F32_TILE>(static_cast<int>(u / nb), a, g);
+        const int c0 = static_cast<int>(u % nb) * len, c1 = min(a.N, c0 + len);
+        const int ranks = t.e < a.E ? a.r : 0;
+        const float* B = static_cast<const float*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
         __syncthreads();
-        if (threadIdx.x < EX_TILE) srow[threadIdx.x] = threadIdx.x < t.n ? row_of(a, t.pos + threadIdx.x) : -1;
-        float acc[EX_TILE] = {};
-        for (int j0 = 0; t.e < a.E && j0 < a.r; j0 += EX_RANKS) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < EX_TILE * EX_RANKS; i += THREADS) {
-                const int row = i / EX_RANKS, j = j0 + i % EX_RANKS;
-                sv[row][i % EX_RANKS] = row < t.n && j < a.r ? a.v[static_cast<long long>(t.pos + row) * a.r + j] : 0.0f;
+        if (threadIdx.x < F32_TILE) srow[threadIdx.x] = threadIdx.x < t.n ? row_of(a, t.pos + threadIdx.x) : -1;
+        __syncthreads();
+        int row[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) row[i] = srow[w * PER + i];
+        for (int n0 = c0; n0 < c1; n0 += F32_COLS) {
+            float add[PER][4];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const bool there = base != nullptr && row[i] >= 0;
+                const float* p = base + row[i] * a.base_stride + n0;
+                if constexpr (VEC) {  // base may be out: no read-only loads
+                    const float4 v = there && n0 + column(0) < c1 ? *reinterpret_cast<const float4*>(p + column(0)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    add[i][0] = v.x; add[i][1] = v.y; add[i][2] = v.z; add[i][3] = v.w;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) add[i][q] = there && n0 + column(q) < c1 ? p[column(q)] : 0.0f;
+                }
             }
-            float b[EX_RANKS];
-            const T* B = static_cast<const T*>(a.b) + (static_cast<long long>(t.e) * a.N + n) * a.r + j0;
+            float acc[PER][4] = {};
+            for (int j0 = 0; j0 < ranks; j0 += F32_STEP) {
+                const int steps = min(F32_STEP, (a.rp - j0 + 3) / 4 * 4);  // v is there up to rp, a multiple of 4
+                __syncthreads();
+                for (int i = threadIdx.x; i < F32_TILE * F32_STEP / 4; i += THREADS) {
+                    const int r = i / (F32_STEP / 4), j = i % (F32_STEP / 4) * 4;
+                    if (j < steps)
+                        *reinterpret_cast<float4*>(&sv[r][j]) = r < t.n ? inner4(a, t.pos + r, j0 + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                // a column's ranks by neighbouring threads: read in lines, written 4 banks apart at most
+                for (int i = threadIdx.x; i < F32_COLS * steps; i += THREADS) {
+                    const int n = i / steps, j = i % steps;
+                    sb[j][n] = n0 + n < c1 && j0 + j < a.r ? __ldg(B + static_cast<long long>(n0 + n) * a.r + j0 + j) : 0.0f;
+                }
+                __syncthreads();
+                for (int j = 0; j < steps; j += 4) {
+                    float b[4][4];
 #pragma unroll
-            for (int j = 0; j < EX_RANKS; ++j) b[j] = n < a.N && j0 + j < a.r ? to_f32(B[j]) : 0.0f;
-            __syncthreads();
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int i = 0; i < EX_TILE; ++i)
+                        for (int i = 0; i < 4; i += VEC ? 4 : 1) {
+                            if constexpr (VEC) {
+                                const float4 v = *reinterpret_cast<const float4*>(&sb[j + q][4 * lane]);
+                                b[q][0] = v.x; b[q][1] = v.y; b[q][2] = v.z; b[q][3] = v.w;
+                            } else {
+                                b[q][i] = sb[j + q][column(i)];
+                            }
+                        }
 #pragma unroll
-                for (int j = 0; j < EX_RANKS; ++j)
-                    if (j0 + j < a.r) acc[i] = fmaf(sv[i][j], b[j], acc[i]);
-        }
-        __syncthreads();
-        if (n >= a.N) continue;
-        for (int i = 0; i < t.n; ++i) {
-            const int row = srow[i];
-            if (row < 0) continue;
-            float v = base != nullptr ? to_f32(base[row * a.base_stride + n]) : 0.0f;
-            if (t.e < a.E) v += acc[i];
-            out[row * a.out_stride + n] = from_f32<O>(v);
+                    for (int i = 0; i < PER; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(&sv[w * PER + i][j]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            acc[i][q] = fmaf(v.w, b[3][q], fmaf(v.z, b[2][q], fmaf(v.y, b[1][q], fmaf(v.x, b[0][q], acc[i][q]))));
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (row[i] < 0) continue;
+                float* o = out + row[i] * a.out_stride + n0;
+                if constexpr (VEC) {
+                    if (n0 + column(0) < c1)
+                        *reinterpret_cast<float4*>(o + column(0)) =
+                            make_float4(add[i][0] + acc[i][0], add[i][1] + acc[i][1], add[i][2] + acc[i][2], add[i][3] + acc[i][3]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (n0 + column(q) < c1) o[column(q)] = add[i][q] + acc[i][q];
+                }
+            }
         }
     }
 }
@@ -185,7 +250,8 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_shrink_mma_kernel(const __
     const int len = ((a.d + a.slices - 1) / a.slices + 31) / 32 * 32;
     const T* x = static_cast<const T*>(a.x);
     const long long units = static_cast<long long>(tiles) * parts, step = static_cast<long long>(gridDim.x) * WARPS;
-    for (long long u = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); u < units; u += step) {
+    // units go to every CTA's first warp, then to the second ones: few spread over all SMs
+    for (long long u = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < units; u += step) {
         const Tile t = tile_of<16 * MT>(static_cast<int>(u / parts), a, g);
         const int part = static_cast<int>(u % parts), j0 = part % rb * 8 * NT, slice = part / rb;
         const int k0 = slice * len, k1 = min(a.d, k0 + len);
@@ -434,19 +500,22 @@ cudaError_t launch_units(K kernel, long long units, int per_sm, size_t smem, cud
     return launch_pdl(kernel, dim3(static_cast<unsigned>(units < cap ? units : cap)), dim3(THREADS), smem, s, a);
 }
 
-template <typename T, typename O>
-cudaError_t launch_simt(const AdapterArgs& a, cudaStream_t s) {
-    cudaError_t e = launch_units(adapter_shrink_kernel<T>, most_tiles(a, SH_TILE) * ((a.r + SH_RANKS - 1) / SH_RANKS), 8, 0, s, a);
+cudaError_t launch_f32(AdapterArgs a, cudaStream_t s) {
+    const bool in = a.d % 4 == 0 && a.x_stride % 4 == 0 && aligned_to(a.x, 16) && aligned_to(a.a, 16);
+    const long long units = most_tiles(a, F32_ROWS) * ((a.rp + F32_RANKS - 1) / F32_RANKS) * a.slices;
+    const cudaError_t e = launch_units(in ? adapter_shrink_f32_kernel<true> : adapter_shrink_f32_kernel<false>, units, 3, 0, s, a);
     if (e != cudaSuccess) return e;
-    return launch_units(adapter_expand_kernel<T, O>, most_tiles(a, EX_TILE) * ((a.N + THREADS - 1) / THREADS), 8, 0, s, a);
+    const bool out = a.N % 4 == 0 && aligned_to(a.out, 16) && a.out_stride % 4 == 0 && aligned_to(a.base, 16) && a.base_stride % 4 == 0;
+    const long long tiles = most_tiles(a, F32_TILE);
+    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + F32_COLS - 1) / F32_COLS, 8LL * num_sms() / tiles)));
+    return launch_units(out ? adapter_expand_f32_kernel<true> : adapter_expand_f32_kernel<false>, tiles * a.col_parts, 4, 0, s, a);
 }
 
 template <typename T, int MT, bool VEC>
 cudaError_t shrink_mma(const AdapterArgs& a, cudaStream_t s) {
-    constexpr int WARPS = THREADS / 32;
-    const long long tiles = most_tiles(a, 16 * MT) * a.slices;
-    if (a.rp <= 16) return launch_units(adapter_shrink_mma_kernel<T, MT, 2, VEC>, (tiles + WARPS - 1) / WARPS, 4, 0, s, a);
-    return launch_units(adapter_shrink_mma_kernel<T, MT, 4, VEC>, (tiles * ((a.rp + 31) / 32) + WARPS - 1) / WARPS, 4, 0, s, a);
+    const long long units = most_tiles(a, 16 * MT) * a.slices;
+    if (a.rp <= 16) return launch_units(adapter_shrink_mma_kernel<T, MT, 2, VEC>, units, 2, 0, s, a);
+    return launch_units(adapter_shrink_mma_kernel<T, MT, 4, VEC>, units * ((a.rp + 31) / 32), 2, 0, s, a);
 }
 
 constexpr int EXPAND_SMEM = 200 << 10;  // the pieces of v of 256 ranks and one tile a warp
@@ -457,9 +526,9 @@ cudaError_t expand_mma_k(AdapterArgs a, cudaStream_t s) {
     static bool done[64] = {};
     if (!allow_smem(adapter_expand_mma_kernel<T, O, MT, KB, VEC>, std::min(16 * STEP, EXPAND_SMEM), done)) return cudaErrorInvalidValue;
     const long long groups = (most_tiles(a, 16 * MT) + WARPS - 1) / WARPS;
-    // ranges of columns: as many as give every SM two CTAs twice over, 32 columns at least
-    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + 31) / 32, (4LL * num_sms() + groups - 1) / groups)));
-    return launch_units(adapter_expand_mma_kernel<T, O, MT, KB, VEC>, groups * a.col_parts, 4, static_cast<size_t>(a.rp / 16) * STEP, s, a);
+    // ranges of columns: as many as give every SM its two CTAs, 32 columns at least
+    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + 31) / 32, 2LL * num_sms() / groups)));
+    return launch_units(adapter_expand_mma_kernel<T, O, MT, KB, VEC>, groups * a.col_parts, 2, static_cast<size_t>(a.rp / 16) * STEP, s, a);
 }
 template <typename T, typename O, int MT, bool VEC>
 cudaError_t expand_mma(const AdapterArgs& a, cudaStream_t s) {
@@ -491,21 +560,20 @@ cudaError_t launch_mma(const AdapterArgs& a, cudaStream_t s) {
 // Slices of d: warps for all SMs from the tiles there may be, 256 of d at least.
 int adapter_slices(int T, int d, int r, int E) {
     const long long units = ((T + 31) / 32 + std::min<long long>(E, T)) * ((r + 31) / 32), warps = 16LL * num_sms();
-    return static_cast<int>(std::max<long long>(1, std::min<long long>({(warps + units - 1) / units, d / 256, 8})));
+    return static_cast<int>(std::max<long long>(1, std::min<long long>({(warps + units - 1) / units, d / 256, 16})));
 }
 
 }  // namespace
 
-size_t adapter_workspace(int T, int d, int r, int E, int dtype) {
-    if (dtype == MOE_F32) return 256 + static_cast<size_t>(T) * r * 4;
+size_t adapter_workspace(int T, int d, int r, int E) {
     return 256 + static_cast<size_t>(T) * ((r + 15) / 16 * 16) * 4 * std::max(adapter_slices(T, d, r, E), adapter_tc_slices(T, d, E));
 }
 
 cudaError_t launch_adapter(const AdapterArgs& args, cudaStream_t s) {
     AdapterArgs a = args;
-    if (a.dtype == MOE_F32) return launch_simt<float, float>(a, s);
     a.rp = (a.r + 15) / 16 * 16;
     a.slices = adapter_slices(a.T, a.d, a.r, a.E);
+    if (a.dtype == MOE_F32) return launch_f32(a, s);
     const bool wide = a.out_dtype == MOE_F32;
     if (a.dtype == MOE_BF16) return wide ? launch_mma<__nv_bfloat16, float>(a, s) : launch_mma<__nv_bfloat16, __nv_bfloat16>(a, s);
     return wide ? launch_mma<__half, float>(a, s) : launch_mma<__half, __half>(a, s);

@@ -213,7 +213,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
         tmem_relinquish();
     }
     tc_fence_before();
-    // what the call was given is complete before the launch before this one could begin
+    pdl_trigger();
     const int tiles = group_table<ROWS>(a, !a.in_place, g);
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
@@ -222,7 +222,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
     const O* base = static_cast<const O*>(a.base);
     O* out = static_cast<O*>(a.out);
     const int pieces = a.rp / 8;  // of 16 bytes in a row of B
-    bool alive = true, waited = false;
+    bool alive = true;
     uint32_t uses[2] = {0, 0};
     for (int u = blockIdx.x; u < tiles * nb; u += gridDim.x) {
         const Tile t = tile_of<ROWS>(u / nb, a, g);
@@ -244,11 +244,6 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
         for (int b = 0; b < 2; ++b) {
             if (adapted && b < n) load_b(b);
             cp_async_commit();
-        }
-        if (!waited) {  // v
-            pdl_wait();
-            pdl_trigger();
-            waited = true;
         }
         if (adapted) {
             const int p = tid >> 1, half = tid & 1;  // a row's pieces by two threads
@@ -359,10 +354,6 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
             cp_async_commit();
         }
     }
-    if (!waited) {  // never done before the launch before it
-        pdl_wait();
-        pdl_trigger();
-    }
     cp_async_wait<0>();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, 2 * COLS);
@@ -370,21 +361,23 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
 
 long long most_tiles(int T, int E) { return (T + ROWS - 1) / ROWS + std::min<long long>(E + 1, T); }
 
-// Parts to deal `tiles` tiles out in, at most `most`: the fewest whose last wave of two CTAs an
-// SM wastes least.
-int parts_of(long long tiles, int most) {
+// Parts to deal `tiles` tiles out in, at most `most`, with two CTAs an SM: the waves of parts,
+// each of which takes 3 us before it begins beside its share of the tile's `us`.
+int parts_of(long long tiles, int most, double us) {
     const long long places = 2LL * num_sms();
     int best = 1;
     double least = 1e30;
     for (int p = 1; p <= most; ++p) {
-        const double t = static_cast<double>((tiles * p + places - 1) / places) / p;
-        if (t < 0.95 * least) {
+        const double t = static_cast<double>((tiles * p + places - 1) / places) * (3.0 + us / p);
+        if (t < least) {
             least = t;
             best = p;
         }
     }
     return best;
 }
+// us of n bytes for one of two CTAs on each SM at the memory's rate
+double share_us(double n) { return n * 2 * num_sms() / 6.8e6; }
 
 template <typename T, int STAGES>
 cudaError_t shrink(const AdapterArgs& a, cudaStream_t s) {
@@ -409,16 +402,21 @@ cudaError_t launch_t(AdapterArgs a, cudaStream_t s) {
     if (!allow_smem(adapter_expand_tc_kernel<T, O>, ((NP * MAX_RP + 63) / 64 + B_STAGES * (MAX_RP / 64)) * BLOCK + 1024, done))
         return cudaErrorInvalidValue;
     const long long tiles = most_tiles(a.T, a.E), cap = 2LL * num_sms();
-    a.col_parts = parts_of(tiles, std::min(16, (a.N + COLS - 1) / COLS));
-    return launch_pdl(adapter_expand_tc_kernel<T, O>, dim3(static_cast<unsigned>(std::min(tiles * a.col_parts, cap))), dim3(THREADS),
-                      smem, s, a, static_cast<unsigned long long>(wait_timeout_ns()));
+    a.col_parts = parts_of(tiles, std::min(16, (a.N + COLS - 1) / COLS), share_us(2.0 * ROWS * a.N * sizeof(O)));
+    // Not begun under the first launch: beside CTAs that take all shared memory its loads in flight
+    // would have the 28 KB of L1 that those leave (16384 x 2048 x 2816, rank 16: 71 us for 62;
+    // 8192 x 4096 x 4096, rank 64: 77 for 70).
+    note_launch();
+    adapter_expand_tc_kernel<T, O><<<static_cast<unsigned>(std::min(tiles * a.col_parts, cap)), THREADS, smem, s>>>(
+        a, static_cast<unsigned long long>(wait_timeout_ns()));
+    return cudaGetLastError();
 }
 
 bool on(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 }  // namespace
 
-int adapter_tc_slices(int T, int d, int E) { return parts_of(most_tiles(T, E), std::max(1, std::min(8, d / 512))); }
+int adapter_tc_slices(int T, int d, int E) { return parts_of(most_tiles(T, E), std::max(1, std::min(8, d / 512)), share_us(2.0 * ROWS * d)); }
 
 bool adapter_tc_takes(const AdapterArgs& a) {
     const int eo = a.out_dtype == MOE_F32 ? 4 : 2;
