@@ -19,7 +19,7 @@ namespace {
 constexpr int F32_ROWS = 4, F32_RANKS = 8;
 
 template <bool VEC>
-__global__ void __launch_bounds__(THREADS, 3) adapter_shrink_f32_kernel(const __grid_constant__ AdapterArgs a) {
+__global__ void __launch_bounds__(THREADS, 2) adapter_shrink_f32_kernel(const __grid_constant__ AdapterArgs a) {
     constexpr int W = VEC ? 4 : 1;  // elements a lane loads at once
     __shared__ Groups g;
     pdl_wait();
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_expand_f32_kernel(const __
             }
             float acc[PER][4] = {};
             for (int j0 = 0; j0 < ranks; j0 += F32_STEP) {
-                const int steps = min(F32_STEP, (a.rp - j0 + 3) / 4 * 4);  // v is there up to rp, a multiple of 4
+                const int steps = min(F32_STEP, a.rp - j0);  // a multiple of 4
                 __syncthreads();
                 for (int i = threadIdx.x; i < F32_TILE * F32_STEP / 4; i += THREADS) {
                     const int r = i / (F32_STEP / 4), j = i % (F32_STEP / 4) * 4;
@@ -198,162 +198,262 @@ MOE_DEV void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// n <= 8 (4) elements from p, the rest zeros: one load where they are aligned.
+// The 16 bytes at p of a 32-byte window [lo, hi] that begins s < 16 bytes before p.
+MOE_DEV uint4 window(uint4 lo, uint4 hi, uint32_t s) {
+    uint32_t w[7] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z};
+    const uint32_t last = hi.w;
+    if (s & 8) {
+        w[0] = w[2]; w[1] = w[3]; w[2] = w[4]; w[3] = w[5]; w[4] = w[6]; w[5] = last;
+    }
+    if (s & 4) {
+        w[0] = w[1]; w[1] = w[2]; w[2] = w[3]; w[3] = w[4]; w[4] = w[5];
+    }
+    if (s & 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 elements from p, zeros from the n-th on; `before` elements of the row lie in front of p.
+// VEC: 16-byte aligned, n a multiple of 8. Else two aligned loads where both lie within the row.
 template <typename T, bool VEC>
-MOE_DEV uint4 load8(const T* p, int n) {
-    uint4 v = make_uint4(0, 0, 0, 0);
+MOE_DEV uint4 load8(const T* p, int before, int n) {
     if constexpr (VEC) {
-        if (n > 0) v = __ldg(reinterpret_cast<const uint4*>(p));
+        return n > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
     } else {
+        const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+        if (s == 0 ? n >= 8 : before >= 8 && n >= 16) {
+            const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - s);
+            const uint4 lo = __ldg(q);
+            return s == 0 ? lo : window(lo, __ldg(q + 1), s);
+        }
         uint32_t w[4] = {0, 0, 0, 0};
         const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n) w[i / 2] |= static_cast<uint32_t>(__ldg(q + i)) << (16 * (i & 1));
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return v;
 }
-template <typename T, bool VEC>
-MOE_DEV uint2 load4(const T* p, int n) {
-    uint2 v = make_uint2(0, 0);
-    if constexpr (VEC) {
-        if (n > 0) v = __ldg(reinterpret_cast<const uint2*>(p));
-    } else {
-        uint32_t w[2] = {0, 0};
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+// 4 elements from p, zeros from the n-th on; vec: 8-byte aligned, n a multiple of 4.
+template <typename T>
+MOE_DEV uint2 load4(const T* p, int n, bool vec) {
+    if (vec) return n > 0 ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+    uint32_t w[2] = {0, 0};
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) w[i / 2] |= static_cast<uint32_t>(__ldg(q + i)) << (16 * (i & 1));
-        v = make_uint2(w[0], w[1]);
-    }
+    for (int i = 0; i < 4; ++i)
+        if (i < n) w[i / 2] |= static_cast<uint32_t>(__ldg(q + i)) << (16 * (i & 1));
+    return make_uint2(w[0], w[1]);
+}
+
+MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+MOE_DEV float4 ld_shared_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 
-// v = s x A^T of 16 MT positions by 8 NT ranks and one slice of d, by a warp; what reads v
-// adds the slices in order.
-//   a.v [slices][T][rp], rp = r rounded up to 16 and the ranks behind r zero.
-template <int MT, int NT>
-struct Shrink {
-    // chunks of 32 a warp has in flight, as registers allow
-    static constexpr int AHEAD = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 6 ? 3 : 2;
+// Both products of a tile of 16 MT positions by a cluster of C CTAs, in one launch.
+//   v: CTA c takes the c-th part of d, its warps every eighth 32 of that, 8 NT ranks a pass;
+//   the warps' sums are added in order through shared memory, then the CTAs' in order through
+//   the cluster's. B and base are on their way to L2 meanwhile.
+//   out: CTA c takes the c-th part of N, a warp 32 columns at a time. Column 2 i + q of its
+//   instruction j stands for column 8 i + 2 j + q, so that a lane ends with 8 consecutive
+//   columns of its rows.
+// KB: steps of 16 ranks whose B is loaded at once, the next ones under way. From two steps on a
+// lane's ranks are 8 consecutive ones of 32 (rp a multiple of 16 KB), else 4 of 16.
+// Every CTA makes the same number of turns, whatever the offsets: cluster barriers always pair.
+template <typename T, typename O, int MT, int NT, int KB, bool VEC>
+struct Fused {
+    static constexpr int WARPS = THREADS / 32, ROWS = 16 * MT;
+    static constexpr int NP = sizeof(O) == 4 ? 3 : 2;
+    // chunks of 32 of d a warp has in flight, as registers allow
+    static constexpr int U = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 6 ? 3 : 2;
+    static constexpr int STAGE_OUT = VEC ? 0 : WARPS * 16 * 33 * 4;
+    static constexpr int RED0 = WARPS * MT * NT * 512, RED = RED0 > STAGE_OUT ? RED0 : STAGE_OUT;
+    static size_t smem(int rp) {  // [part][red, then the sums and the columns on their way out][pieces]
+        const int sums = ROWS * rp * 4;
+        return static_cast<size_t>(sums) + (RED > sums ? RED : sums) + static_cast<size_t>(rp / 16) * NP * MT * 512;
+    }
+    // two CTAs an SM below 110 KB
+    static constexpr int MOST = ROWS * 256 * 4 + (RED > ROWS * 1024 ? RED : ROWS * 1024) + 16 * NP * MT * 512;
 };
-template <typename T, int MT, int NT, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) adapter_shrink_mma_kernel(const __grid_constant__ AdapterArgs a) {
-    constexpr int WARPS = THREADS / 32, U = Shrink<MT, NT>::AHEAD;
+template <typename T, typename O, int MT, int NT, int KB, bool VEC>
+__global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_constant__ AdapterArgs a, int turns) {
+    using F = Fused<T, O, MT, NT, KB, VEC>;
+    constexpr int WARPS = F::WARPS, ROWS = F::ROWS, NP = F::NP, U = F::U;
+    constexpr bool SCALED = __is_same(T, __half);
+    constexpr bool AHEAD = VEC && KB == 1;  // the next columns' base too: where B takes few registers
     __shared__ Groups g;
+    __shared__ int srow[ROWS];
+    __shared__ float sscale[SCALED ? ROWS : 1], sback[SCALED ? ROWS : 1];
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int rp = a.rp, KS = rp / 16, C = a.cluster;
+    float* part = reinterpret_cast<float*>(smem);  // [ROWS][rp], this CTA's part of d
+    float* red = part + ROWS * rp;                 // [WARPS][MT * NT * 4][32], then [ROWS][rp]
+    uint4* frag = reinterpret_cast<uint4*>(red + (F::RED / 4 > ROWS * rp ? F::RED / 4 : ROWS * rp));  // [KS][NP][MT][32]
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gi = lane >> 2, ti = lane & 3;
+    const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int clusters = gridDim.x / C, id = blockIdx.x / C;
     pdl_wait();
     pdl_trigger();
-    const int tiles = group_table<16 * MT>(a, false, g);
-    const int lane = static_cast<int>(lane_id()), gi = lane >> 2, ti = lane & 3;
-    const int rb = (a.rp + 8 * NT - 1) / (8 * NT), parts = rb * a.slices;
-    const int len = ((a.d + a.slices - 1) / a.slices + 31) / 32 * 32;
+    const int tiles = group_table<ROWS>(a, !a.in_place, g);
+    const int klen = ((a.d + C - 1) / C + 31) / 32 * 32, nlen = ((a.N + C - 1) / C + 31) / 32 * 32;
+    const int k0 = min(a.d, rank * klen), k1 = min(a.d, k0 + klen), c0 = min(a.N, rank * nlen), c1 = min(a.N, c0 + nlen);
     const T* x = static_cast<const T*>(a.x);
-    const long long units = static_cast<long long>(tiles) * parts, step = static_cast<long long>(gridDim.x) * WARPS;
-    // units go to every CTA's first warp, then to the second ones: few spread over all SMs
-    for (long long u = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; u < units; u += step) {
-        const Tile t = tile_of<16 * MT>(static_cast<int>(u / parts), a, g);
-        const int part = static_cast<int>(u % parts), j0 = part % rb * 8 * NT, slice = part / rb;
-        const int k0 = slice * len, k1 = min(a.d, k0 + len);
-        const T* xr[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = 16 * m + 8 * h + gi;
-                xr[m][h] = nullptr;
-                if (i < t.n) {
-                    const int r = row_of(a, t.pos + i);
-                    if (r >= 0) xr[m][h] = x + r * a.x_stride;
-                    else if (ti == 0) atomicOr(a.err, ERRBIT_INDEX);
-                }
+    const O* base = static_cast<const O*>(a.base);
+    O* out = static_cast<O*>(a.out);
+    const bool bvec = a.r % 4 == 0 && reinterpret_cast<uintptr_t>(a.b) % 8 == 0;
+    for (int turn = 0; turn < turns; ++turn) {
+        const int tile = turn * clusters + id;
+        Tile t{a.E, 0, 0};
+        if (tile < tiles) t = tile_of<ROWS>(tile, a, g);
+        const bool adapted = t.e < a.E;
+        const T* B = static_cast<const T*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
+        __syncthreads();  // the last turn's rows have been read
+        if (tid < ROWS) {
+            srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+            if (tid < t.n && srow[tid] < 0 && rank == 0) atomicOr(a.err, ERRBIT_INDEX);
+        }
+        __syncthreads();
+        if (adapted) {
+            const char* b0 = reinterpret_cast<const char*>(B + static_cast<long long>(c0) * a.r);
+            const int bytes = (c1 - c0) * a.r * static_cast<int>(sizeof(T));
+            for (int i = tid * 128; i < bytes; i += THREADS * 128) prefetch_l2(b0 + i);
+        }
+        if (base != nullptr && c1 > c0) {
+            const int lines = ((c1 - c0) * static_cast<int>(sizeof(O)) + 127) / 128;
+            for (int i = tid; i < t.n * lines; i += THREADS) {
+                const int row = srow[i / lines];
+                if (row >= 0) prefetch_l2(reinterpret_cast<const char*>(base + row * a.base_stride + c0) + i % lines * 128);
             }
-        const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + j0 + gi) * a.d;
-        float acc[MT][NT][4] = {};
-        uint4 fx[U][MT][2], fa[U][NT];
-        auto load = [&](int c, int k) {
-            const int at = k + 8 * ti, n = k1 - at;
+        }
+        if (adapted) {
+            int row[MT][2];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) fx[c][m][h] = load8<T, VEC>(xr[m][h] + at, xr[m][h] != nullptr ? n : 0);
+                for (int h = 0; h < 2; ++h) row[m][h] = srow[16 * m + 8 * h + gi];
+            for (int j0 = 0; j0 < rp; j0 += 8 * NT) {
+                const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + j0 + gi) * a.d;
+                float acc[MT][NT][4] = {};
+                uint4 fx[U][MT][2], fa[U][NT];
+                auto load = [&](int c, int k) {
+                    const int at = k + 8 * ti, n = k1 - at;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                fa[c][j] = load8<T, VEC>(A + static_cast<long long>(8 * j) * a.d + at, j0 + 8 * j + gi < a.r ? n : 0);
-        };
+                    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int c = 0; c < U; ++c) load(c, k0 + 32 * c);
-        for (int k = k0; k < k1; k += 32 * U) {
+                        for (int h = 0; h < 2; ++h)
+                            fx[c][m][h] = load8<T, VEC>(x + max(row[m][h], 0) * a.x_stride + at, at, row[m][h] >= 0 ? n : 0);
 #pragma unroll
-            for (int c = 0; c < U; ++c) {
+                    for (int j = 0; j < NT; ++j)
+                        fa[c][j] = load8<T, VEC>(A + static_cast<long long>(8 * j) * a.d + at, at, j0 + 8 * j + gi < a.r ? n : 0);
+                };
+                const int first = k0 + 32 * w;
+#pragma unroll
+                for (int c = 0; c < U; ++c) load(c, first + 32 * WARPS * c);
+                for (int k = first; k < k1; k += 32 * WARPS * U) {
+#pragma unroll
+                    for (int c = 0; c < U; ++c) {
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j) {  // chunks behind the part are zeros
+                                mma16816<T>(acc[m][j], fx[c][m][0].x, fx[c][m][1].x, fx[c][m][0].y, fx[c][m][1].y, fa[c][j].x, fa[c][j].y);
+                                mma16816<T>(acc[m][j], fx[c][m][0].z, fx[c][m][1].z, fx[c][m][0].w, fx[c][m][1].w, fa[c][j].z, fa[c][j].w);
+                            }
+                        load(c, k + 32 * WARPS * (c + U));
+                    }
+                }
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {  // chunks behind the slice are zeros
-                        mma16816<T>(acc[m][j], fx[c][m][0].x, fx[c][m][1].x, fx[c][m][0].y, fx[c][m][1].y, fa[c][j].x, fa[c][j].y);
-                        mma16816<T>(acc[m][j], fx[c][m][0].z, fx[c][m][1].z, fx[c][m][0].w, fx[c][m][1].w, fa[c][j].z, fa[c][j].w);
-                    }
-                load(c, k + 32 * (c + U));
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) red[((w * MT + m) * NT + j) * 128 + 32 * i + lane] = acc[m][j][i];
+                __syncthreads();
+                for (int i = tid; i < MT * NT * 128; i += THREADS) {
+                    float v = red[i];
+#pragma unroll
+                    for (int o = 1; o < WARPS; ++o) v += red[o * MT * NT * 128 + i];
+                    const int l = i & 31, q = i >> 5 & 3, j = i / 128 % NT, m = i / (128 * NT);
+                    const int col = j0 + 8 * j + 2 * (l & 3) + (q & 1);
+                    if (col < rp) part[(16 * m + 8 * (q >> 1) + (l >> 2)) * rp + col] = v;
+                }
+                __syncthreads();
             }
         }
-        const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
-        float* out = a.v + (static_cast<long long>(slice) * a.T + t.pos) * a.rp;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int i = 16 * m + 8 * h + gi;
-                if (i >= t.n) continue;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int rank = j0 + 8 * j + 2 * ti;
-                    if (rank < a.rp)
-                        *reinterpret_cast<float2*>(out + i * a.rp + rank) =
-                            make_float2(rank < a.r ? s * acc[m][j][2 * h] : 0.0f, rank + 1 < a.r ? s * acc[m][j][2 * h + 1] : 0.0f);
+        if (C > 1) cluster_sync();  // all parts of d are there
+        if (adapted) {
+            const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
+            for (int i = tid; i < ROWS * rp / 4; i += THREADS) {
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (C > 1) {
+                    const uint32_t at = smem_u32(part + 4 * i);
+#pragma unroll 4
+                    for (int c = 0; c < C; ++c) {
+                        const float4 o = ld_shared_cluster_v4(map_shared_rank(at, c));
+                        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                    }
+                } else {
+                    v = *reinterpret_cast<const float4*>(part + 4 * i);
                 }
+                const int k = 4 * i % rp;  // ranks behind r are zeros whatever x holds
+                v.x = k < a.r ? v.x * s : 0.0f;
+                v.y = k + 1 < a.r ? v.y * s : 0.0f;
+                v.z = k + 2 < a.r ? v.z * s : 0.0f;
+                v.w = k + 3 < a.r ? v.w * s : 0.0f;
+                *reinterpret_cast<float4*>(red + 4 * i) = v;
             }
-    }
-}
-
-// out = base + v B^T. A warp takes 16 MT positions by a range of columns, 32 at a time and
-// the next 32 of base under way; its pieces of v stay in shared memory, each lane its own,
-// so warps wait for nobody. The warps of a CTA take neighbouring tiles and the same columns:
-// where those have one adapter, B comes from L1. Column 2 i + c of a warp's instruction j
-// stands for column 8 i + 2 j + c, so that a lane ends with 8 consecutive columns of its rows.
-//
-// KB: steps of 16 ranks whose B is loaded at once, the next ones under way. From two steps on a
-// lane's ranks are 8 consecutive ones of 32 (rp a multiple of 16 KB), else 4 of 16.
-template <typename T, typename O, int MT, int KB, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) adapter_expand_mma_kernel(const __grid_constant__ AdapterArgs a) {
-    constexpr int WARPS = THREADS / 32, NP = sizeof(O) == 4 ? 3 : 2;
-    constexpr bool SCALED = __is_same(T, __half);
-    constexpr bool AHEAD = KB == 1;  // the next columns' base too: where B takes few registers
-    __shared__ Groups g;
-    extern __shared__ __align__(16) uint4 frags[];  // [WARPS][rp / 16][NP][MT][32]
-    // what the call was given is complete before the launch before this one could begin
-    const int tiles = group_table<16 * MT>(a, !a.in_place, g);
-    const int lane = static_cast<int>(lane_id()), w = threadIdx.x >> 5, gi = lane >> 2, ti = lane & 3;
-    const int KS = a.rp / 16, nb = a.col_parts, len = ((a.N + nb - 1) / nb + 31) / 32 * 32;
-    uint4* frag = frags + w * KS * NP * MT * 32 + lane;
-    const O* base = static_cast<const O*>(a.base);
-    O* out = static_cast<O*>(a.out);
-    bool waited = false;
-    for (int u = blockIdx.x; u < (tiles + WARPS - 1) / WARPS * nb; u += gridDim.x) {
-        const int tile = u / nb * WARPS + w;
-        if (tile >= tiles) continue;
-        const Tile t = tile_of<16 * MT>(tile, a, g);
-        const int c0 = u % nb * len, c1 = min(a.N, c0 + len);
-        const bool adapted = t.e < a.E;
-        const T* B = static_cast<const T*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
+        }
+        if (C > 1) cluster_arrive();  // the others' parts have been read
+        __syncthreads();
+        if (adapted) {
+            if constexpr (SCALED) {
+                constexpr int PER = THREADS / ROWS;  // threads a row, within a warp
+                const int p = tid / PER;
+                float most = 0.0f;
+                for (int k = tid % PER * 4; k < rp; k += PER * 4) most = largest_finite(*reinterpret_cast<const float4*>(red + p * rp + k), most);
+#pragma unroll
+                for (int o = PER / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                if (tid % PER == 0) row_scale(most, sscale[p], sback[p]);
+                __syncthreads();
+            }
+            for (int i = tid; i < KS * MT * 32; i += THREADS) {
+                const int l = i & 31, m = i / 32 % MT, ks = i / (32 * MT);
+                const int k = KB == 1 ? 16 * ks + 4 * (l & 3) : 32 * (ks >> 1) + 8 * (l & 3) + 4 * (ks & 1);
+                T q[2][4][NP];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int p = 16 * m + 8 * h + (l >> 2);
+                    const float4 v = *reinterpret_cast<const float4*>(red + p * rp + k);
+                    const float f = SCALED ? sscale[p] : 1.0f;
+                    split<T, NP>(v.x * f, q[h][0]);
+                    split<T, NP>(v.y * f, q[h][1]);
+                    split<T, NP>(v.z * f, q[h][2]);
+                    split<T, NP>(v.w * f, q[h][3]);
+                }
+#pragma unroll
+                for (int o = 0; o < NP; ++o)
+                    frag[((ks * NP + o) * MT + m) * 32 + l] =
+                        make_uint4(pack2(q[0][0][o], q[0][1][o]), pack2(q[1][0][o], q[1][1][o]), pack2(q[0][2][o], q[0][3][o]),
+                                   pack2(q[1][2][o], q[1][3][o]));
+            }
+            __syncthreads();
+        }
         int row[MT][2];
+        float back[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int i = 16 * m + 8 * h + gi;
-                row[m][h] = i < t.n ? row_of(a, t.pos + i) : -1;
+                row[m][h] = srow[16 * m + 8 * h + gi];
+                back[m][h] = SCALED && adapted ? sback[16 * m + 8 * h + gi] : 1.0f;
             }
-        Cols<O, VEC> add[MT][2];
+        Cols<O, true> add[MT][2];
         auto load_base = [&](int n0) {
             const int col = n0 + 8 * ti;
 #pragma unroll
@@ -363,78 +463,37 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_expand_mma_kernel(const __
                     add[m][h].load(base + row[m][h] * a.base_stride + col, base != nullptr && row[m][h] >= 0 ? c1 - col : 0);
         };
         uint2 fb[KB][4];
-        auto rank_of = [&](int ks) { return KB == 1 ? 16 * ks + 4 * ti : 32 * (ks >> 1) + 8 * ti + 4 * (ks & 1); };
         auto load_b = [&](int n0, int ks) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = n0 + 8 * (gi >> 1) + 2 * j + (gi & 1);
                 const T* p = B + static_cast<long long>(n) * a.r;
                 if constexpr (KB == 1) {
-                    const int k = rank_of(ks);
-                    fb[0][j] = load4<T, VEC>(p + k, adapted && n < c1 ? a.r - k : 0);
+                    const int k = 16 * ks + 4 * ti;
+                    fb[0][j] = load4<T>(p + k, adapted && n < c1 ? a.r - k : 0, VEC || bvec);
                 } else {
 #pragma unroll
                     for (int q = 0; q < KB; q += 2) {
-                        const int k = rank_of(ks + q);
-                        const uint4 v = load8<T, VEC>(p + k, adapted && n < c1 ? a.r - k : 0);
+                        const int k = 16 * (ks + q) + 8 * ti;
+                        const uint4 v = load8<T, true>(p + k, k, adapted && n < c1 ? a.r - k : 0);
                         fb[q][j] = make_uint2(v.x, v.y);
                         fb[q + 1][j] = make_uint2(v.z, v.w);
                     }
                 }
             }
         };
-        load_b(c0, 0);
-        if constexpr (AHEAD) load_base(c0);
-        if (!waited) {  // v
-            pdl_wait();
-            pdl_trigger();
-            waited = true;
-        }
-        float back[MT][2];
-        if (adapted) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float scale[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    scale[h] = back[m][h] = 1.0f;
-                    if constexpr (SCALED) {
-                        const int i = 16 * m + 8 * h + gi;
-                        float most = 0.0f;
-                        for (int k = 4 * ti; i < t.n && k < a.rp; k += 16) most = largest_finite(inner4(a, t.pos + i, k), most);
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                        row_scale(most, scale[h], back[m][h]);
-                    }
-                }
-                for (int ks = 0; ks < KS; ++ks) {
-                    T q[2][4][NP];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int i = 16 * m + 8 * h + gi;
-                        const float4 v = i < t.n ? inner4(a, t.pos + i, rank_of(ks)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        split<T, NP>(v.x * scale[h], q[h][0]);
-                        split<T, NP>(v.y * scale[h], q[h][1]);
-                        split<T, NP>(v.z * scale[h], q[h][2]);
-                        split<T, NP>(v.w * scale[h], q[h][3]);
-                    }
-#pragma unroll
-                    for (int o = 0; o < NP; ++o)
-                        frag[((ks * NP + o) * MT + m) * 32] =
-                            make_uint4(pack2(q[0][0][o], q[0][1][o]), pack2(q[1][0][o], q[1][1][o]), pack2(q[0][2][o], q[0][3][o]),
-                                       pack2(q[1][2][o], q[1][3][o]));
-                }
-            }
-        }
-        for (int n0 = c0; n0 < c1; n0 += 32) {
-            Cols<O, VEC> here[MT][2];
+        constexpr int STEP = 32 * WARPS;
+        load_b(c0 + 32 * w, 0);
+        if constexpr (AHEAD) load_base(c0 + 32 * w);
+        for (int n0 = c0 + 32 * w; t.n > 0 && n0 < c1; n0 += STEP) {
+            Cols<O, true> here[MT][2];
             if constexpr (AHEAD) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) here[m][h] = add[m][h];
-                load_base(n0 + 32);
-            } else {
+                load_base(n0 + STEP);
+            } else if constexpr (VEC) {
                 load_base(n0);
             }
             float acc[MT][4][4] = {};
@@ -445,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_expand_mma_kernel(const __
 #pragma unroll
                     for (int j = 0; j < 4; ++j) cur[q][j] = fb[q][j];
                 if (ks + KB < KS) load_b(n0, ks + KB);
-                else load_b(n0 + 32, 0);
+                else load_b(n0 + STEP, 0);
                 if (!adapted) break;
 #pragma unroll
                 for (int q = 0; q < KB; ++q)
@@ -453,36 +512,55 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_expand_mma_kernel(const __
                     for (int o = 0; o < NP; ++o)
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
-                            const uint4 f = frag[(((ks + q) * NP + o) * MT + m) * 32];
+                            const uint4 f = frag[(((ks + q) * NP + o) * MT + m) * 32 + lane];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) mma16816<T>(acc[m][j], f.x, f.y, f.z, f.w, cur[q][j].x, cur[q][j].y);
                         }
             }
-            if constexpr (!AHEAD) {
+            if constexpr (VEC) {
+                const int col = n0 + 8 * ti;
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) here[m][h] = add[m][h];
-            }
-            const int col = n0 + 8 * ti;
+                    for (int h = 0; h < 2; ++h) {
+                        if (row[m][h] < 0 || col >= c1) continue;
+                        float f[8];
+                        if constexpr (AHEAD) here[m][h].get(f);
+                        else add[m][h].get(f);
+                        if (adapted) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (row[m][h] < 0 || col >= c1) continue;
-                    float f[8];
-                    here[m][h].get(f);
-                    if (adapted) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = fmaf(acc[m][i >> 1][2 * h + (i & 1)], back[m][h], f[i]);
+                            for (int i = 0; i < 8; ++i) f[i] = fmaf(acc[m][i >> 1][2 * h + (i & 1)], back[m][h], f[i]);
+                        }
+                        Cols<O, true>::store(out + row[m][h] * a.out_stride + col, 8, f);
                     }
-                    Cols<O, VEC>::store(out + row[m][h] * a.out_stride + col, c1 - col, f);
+            } else {
+                // rows on no 16 bytes: 16 rows of the warp's columns through shared memory, then a row's
+                // 32 columns by the 32 lanes
+                float* mine = red + w * 16 * 33;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) mine[(8 * h + gi) * 33 + 8 * ti + i] = acc[m][i >> 1][2 * h + (i & 1)] * back[m][h];
+                    __syncwarp();
+                    const int col = n0 + lane;
+                    O old[16];
+#pragma unroll
+                    for (int p = 0; p < 16; ++p) {
+                        const int r = srow[16 * m + p];
+                        old[p] = base != nullptr && r >= 0 && col < c1 ? base[r * a.base_stride + col] : from_f32<O>(0.0f);
+                    }
+#pragma unroll
+                    for (int p = 0; p < 16; ++p) {
+                        const int r = srow[16 * m + p];
+                        if (r >= 0 && col < c1) out[r * a.out_stride + col] = adapted ? from_f32<O>(to_f32(old[p]) + mine[p * 33 + lane]) : old[p];
+                    }
                 }
+            }
         }
-    }
-    if (!waited) {  // never done before the launch before it
-        pdl_wait();
-        pdl_trigger();
+        if (C > 1) cluster_wait();
     }
 }
 
@@ -490,8 +568,7 @@ bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 
 // Tiles of tm positions at most: a part full one a group, or a position each.
 long long most_tiles(const AdapterArgs& a, int tm) {
-    const long long part = a.E + 1 < a.T ? a.E + 1 : a.T;
-    return (a.T + tm - 1) / tm + part;
+    return std::min<long long>(a.T, (a.T + tm - 1) / tm + a.E + 1);
 }
 
 template <typename K>
@@ -511,70 +588,63 @@ cudaError_t launch_f32(AdapterArgs a, cudaStream_t s) {
     return launch_units(out ? adapter_expand_f32_kernel<true> : adapter_expand_f32_kernel<false>, tiles * a.col_parts, 4, 0, s, a);
 }
 
-template <typename T, int MT, bool VEC>
-cudaError_t shrink_mma(const AdapterArgs& a, cudaStream_t s) {
-    const long long units = most_tiles(a, 16 * MT) * a.slices;
-    if (a.rp <= 16) return launch_units(adapter_shrink_mma_kernel<T, MT, 2, VEC>, units, 2, 0, s, a);
-    return launch_units(adapter_shrink_mma_kernel<T, MT, 4, VEC>, units * ((a.rp + 31) / 32), 2, 0, s, a);
-}
-
-constexpr int EXPAND_SMEM = 200 << 10;  // the pieces of v of 256 ranks and one tile a warp
-
-template <typename T, typename O, int MT, int KB, bool VEC>
-cudaError_t expand_mma_k(AdapterArgs a, cudaStream_t s) {
-    constexpr int WARPS = THREADS / 32, STEP = (sizeof(O) == 4 ? 3 : 2) * MT * 512 * WARPS;  // of 16 ranks
+template <typename T, typename O, int MT, int NT, int KB, bool VEC>
+cudaError_t fused_k(AdapterArgs a, cudaStream_t s) {
+    using F = Fused<T, O, MT, NT, KB, VEC>;
     static bool done[64] = {};
-    if (!allow_smem(adapter_expand_mma_kernel<T, O, MT, KB, VEC>, std::min(16 * STEP, EXPAND_SMEM), done)) return cudaErrorInvalidValue;
-    const long long groups = (most_tiles(a, 16 * MT) + WARPS - 1) / WARPS;
-    // ranges of columns: as many as give every SM its two CTAs, 32 columns at least
-    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + 31) / 32, 2LL * num_sms() / groups)));
-    return launch_units(adapter_expand_mma_kernel<T, O, MT, KB, VEC>, groups * a.col_parts, 2, static_cast<size_t>(a.rp / 16) * STEP, s, a);
-}
-template <typename T, typename O, int MT, bool VEC>
-cudaError_t expand_mma(const AdapterArgs& a, cudaStream_t s) {
-    if constexpr (VEC && MT == 1) {
-        if (a.r % 8 == 0 && aligned_to(a.b, 16)) {
-            if (a.rp % 64 == 0) return expand_mma_k<T, O, 1, 4, true>(a, s);
-            if (a.rp % 32 == 0) return expand_mma_k<T, O, 1, 2, true>(a, s);
-        }
-    }
-    return expand_mma_k<T, O, MT, 1, VEC>(a, s);
+    if (!allow_smem(adapter_mma_kernel<T, O, MT, NT, KB, VEC>, F::MOST, done)) return cudaErrorInvalidValue;
+    const long long tiles = most_tiles(a, 16 * MT), places = 2LL * num_sms();
+    // as many CTAs a tile as there are places for, while each has 256 of d and of N
+    a.cluster = 1;
+    while (a.cluster < 8 && tiles * a.cluster * 2 <= places && std::min(a.d, a.N) >= 512 * a.cluster) a.cluster *= 2;
+    const long long clusters = std::min(tiles, places / a.cluster);
+    const int turns = static_cast<int>((tiles + clusters - 1) / clusters);
+    return launch_pdl_cluster(adapter_mma_kernel<T, O, MT, NT, KB, VEC>, dim3(static_cast<unsigned>(clusters * a.cluster)), dim3(THREADS),
+                              F::smem(a.rp), s, a.cluster, a, turns);
 }
 
 template <typename T, typename O>
 cudaError_t launch_mma(const AdapterArgs& a, cudaStream_t s) {
     if (adapter_tc_takes(a)) return launch_adapter_tc(a, s);
-    const bool in = a.d % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.a, 16);
-    const bool out = a.N % 8 == 0 && a.r % 4 == 0 && aligned_to(a.b, 8) && aligned_to(a.out, 16) &&
-                     a.out_stride * sizeof(O) % 16 == 0 && aligned_to(a.base, 16) && a.base_stride * sizeof(O) % 16 == 0;
-    const bool many = a.T >= 24LL * (a.E + 1);
-    cudaError_t e;
-    if (many) e = in ? shrink_mma<T, 2, true>(a, s) : shrink_mma<T, 2, false>(a, s);
-    else e = in ? shrink_mma<T, 1, true>(a, s) : shrink_mma<T, 1, false>(a, s);
-    if (e != cudaSuccess) return e;
-    // two tiles a warp while their pieces of v leave room for two CTAs an SM
-    if (many && a.rp / 16 * (sizeof(O) == 4 ? 3 : 2) * 8192 <= 96 << 10) return out ? expand_mma<T, O, 2, true>(a, s) : expand_mma<T, O, 2, false>(a, s);
-    return out ? expand_mma<T, O, 1, true>(a, s) : expand_mma<T, O, 1, false>(a, s);
+    const bool vec = a.d % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.a, 16) && a.N % 8 == 0 && a.r % 4 == 0 &&
+                     aligned_to(a.b, 8) && aligned_to(a.out, 16) && a.out_stride * sizeof(O) % 16 == 0 && aligned_to(a.base, 16) &&
+                     a.base_stride * sizeof(O) % 16 == 0;
+    const bool many = a.T >= 24LL * (a.E + 1);  // tiles of 32 rows are mostly full
+    if (many) {
+        if (a.rp <= 16) return vec ? fused_k<T, O, 2, 2, 1, true>(a, s) : fused_k<T, O, 2, 2, 1, false>(a, s);
+        return vec ? fused_k<T, O, 2, 4, 1, true>(a, s) : fused_k<T, O, 2, 4, 1, false>(a, s);
+    }
+    if (a.rp <= 16) return vec ? fused_k<T, O, 1, 2, 1, true>(a, s) : fused_k<T, O, 1, 2, 1, false>(a, s);
+    if (!vec) return fused_k<T, O, 1, 4, 1, false>(a, s);
+    const bool wide = a.r % 8 == 0 && aligned_to(a.b, 16);
+    if (wide && a.rp % 64 == 0) return fused_k<T, O, 1, 4, 4, true>(a, s);
+    if (wide && a.rp % 32 == 0) return fused_k<T, O, 1, 4, 2, true>(a, s);
+    return fused_k<T, O, 1, 4, 1, true>(a, s);
 }
 
-// Slices of d: warps for all SMs from the tiles there may be, 256 of d at least.
+// Slices of d of the FP32 kernels: warps for all SMs from the tiles there may be, 256 of d at least.
 int adapter_slices(int T, int d, int r, int E) {
-    const long long units = ((T + 31) / 32 + std::min<long long>(E, T)) * ((r + 31) / 32), warps = 16LL * num_sms();
-    return static_cast<int>(std::max<long long>(1, std::min<long long>({(warps + units - 1) / units, d / 256, 16})));
+    const long long units = std::min<long long>(T, (T + F32_ROWS - 1) / F32_ROWS + E + 1) * ((r + F32_RANKS - 1) / F32_RANKS);
+    return static_cast<int>(std::max<long long>(1, std::min<long long>({16LL * num_sms() / units, d / 256, 16})));
 }
 
 }  // namespace
 
-size_t adapter_workspace(int T, int d, int r, int E) {
-    return 256 + static_cast<size_t>(T) * ((r + 15) / 16 * 16) * 4 * std::max(adapter_slices(T, d, r, E), adapter_tc_slices(T, d, E));
+size_t adapter_workspace(int T, int d, int r, int E, int dtype) {
+    const int rp = dtype == MOE_F32 ? (r + 3) / 4 * 4 : (r + 15) / 16 * 16;
+    const int slices = dtype == MOE_F32 ? adapter_slices(T, d, r, E) : adapter_tc_slices(T, d, E);
+    return 256 + static_cast<size_t>(T) * rp * 4 * slices;
 }
 
 cudaError_t launch_adapter(const AdapterArgs& args, cudaStream_t s) {
     AdapterArgs a = args;
-    a.rp = (a.r + 15) / 16 * 16;
-    a.slices = adapter_slices(a.T, a.d, a.r, a.E);
-    if (a.dtype == MOE_F32) return launch_f32(a, s);
     const bool wide = a.out_dtype == MOE_F32;
+    if (a.dtype == MOE_F32) {
+        a.rp = (a.r + 3) / 4 * 4;
+        a.slices = adapter_slices(a.T, a.d, a.r, a.E);
+        return launch_f32(a, s);
+    }
+    a.rp = (a.r + 15) / 16 * 16;
     if (a.dtype == MOE_BF16) return wide ? launch_mma<__nv_bfloat16, float>(a, s) : launch_mma<__nv_bfloat16, __nv_bfloat16>(a, s);
     return wide ? launch_mma<__half, float>(a, s) : launch_mma<__half, __half>(a, s);
 }

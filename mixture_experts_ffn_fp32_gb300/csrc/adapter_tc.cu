@@ -359,7 +359,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
     if (warp == 1) tmem_dealloc(tmem, 2 * COLS);
 }
 
-long long most_tiles(int T, int E) { return (T + ROWS - 1) / ROWS + std::min<long long>(E + 1, T); }
+long long most_tiles(int T, int E) { return std::min<long long>(T, (T + ROWS - 1) / ROWS + E + 1); }
 
 // Parts to deal `tiles` tiles out in, at most `most`, with two CTAs an SM: the waves of parts,
 // each of which takes 3 us before it begins beside its share of the tile's `us`.

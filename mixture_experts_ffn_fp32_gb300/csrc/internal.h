@@ -599,10 +599,12 @@ struct AdapterArgs {
     int in_place;            // out is base
     int* err;                // the workspace, its error word first
     float* v;                // inner values, [slices, T, rp]
-    int rp, slices;          // set by launch_adapter: r rounded up to 16, slices of d
+    // set by launch_adapter and what it calls
+    int rp, slices;          // r rounded up (FP32: to 4, else 16), slices of d
     int col_parts;           // ranges of columns a tile is dealt out in
+    int cluster;             // CTAs a tile
 };
-size_t adapter_workspace(int T, int d, int r, int E);
+size_t adapter_workspace(int T, int d, int r, int E, int dtype);
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
 // The tensor-core kernels of many rows: whether they take a call (rp set), the slices of d
 // that they deal out, and the call.
