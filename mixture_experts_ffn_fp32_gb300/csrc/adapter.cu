@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_expand_f32_kernel(const __
                 for (int i = threadIdx.x; i < F32_TILE * F32_STEP / 4; i += THREADS) {
                     const int r = i / (F32_STEP / 4), j = i % (F32_STEP / 4) * 4;
                     if (j < steps)
-                        *reinterpret_cast<float4*>(&sv[r][j]) = r < t.n ? inner4(a, t.pos + r, j0 + j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        *reinterpret_cast<float4*>(&sv[r][j]) = r < t.n ? inner4(a, t.pos + r, j0 + j, a.slices) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
                 // a column's ranks by neighbouring threads: read in lines, written 4 banks apart at most
                 for (int i = threadIdx.x; i < F32_COLS * steps; i += THREADS) {
@@ -249,12 +249,6 @@ MOE_DEV uint2 load4(const T* p, int n, bool vec) {
 }
 
 MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-MOE_DEV float4 ld_shared_cluster_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
 
 // Both products of a tile of 16 MT positions by a cluster of C CTAs, in one launch.
 //   v: CTA c takes the c-th part of d, its warps every eighth 32 of that, 8 NT ranks a pass;
@@ -632,8 +626,8 @@ int adapter_slices(int T, int d, int r, int E) {
 
 size_t adapter_workspace(int T, int d, int r, int E, int dtype) {
     const int rp = dtype == MOE_F32 ? (r + 3) / 4 * 4 : (r + 15) / 16 * 16;
-    const int slices = dtype == MOE_F32 ? adapter_slices(T, d, r, E) : adapter_tc_slices(T, d, E);
-    return 256 + static_cast<size_t>(T) * rp * 4 * slices;
+    if (dtype == MOE_F32) return 256 + static_cast<size_t>(T) * rp * 4 * adapter_slices(T, d, r, E);
+    return 256 + (T >= TC_ROWS ? adapter_tc_workspace(T, rp) : 0);
 }
 
 cudaError_t launch_adapter(const AdapterArgs& args, cudaStream_t s) {

@@ -157,15 +157,15 @@ struct Cols {
 };
 
 // The sum of the slices of 4 consecutive inner values.
-MOE_DEV float4 inner4(const AdapterArgs& a, int pos, int k) {
+MOE_DEV float4 inner4(const AdapterArgs& a, int pos, int k, int slices) {
     const float* v = a.v + static_cast<long long>(pos) * a.rp + k;
     const long long plane = static_cast<long long>(a.T) * a.rp;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i = 0; i < a.slices; i += 8) {
+    for (int i = 0; i < slices; i += 8) {
         float4 o[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            o[q] = i + q < a.slices ? *reinterpret_cast<const float4*>(v + (i + q) * plane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            o[q] = i + q < slices ? *reinterpret_cast<const float4*>(v + (i + q) * plane) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             s.x += o[q].x;
@@ -186,6 +186,12 @@ MOE_DEV void row_scale(float most, float& scale, float& back) {
     const int e = min(max(14 + 127 - static_cast<int>(__float_as_uint(most) >> 23), -126), 126);
     scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
     back = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
+MOE_DEV float4 ld_shared_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 }  // namespace

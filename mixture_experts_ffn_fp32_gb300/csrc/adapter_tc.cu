@@ -1,14 +1,13 @@
 // Low-rank adapters (adapter.cu) of many rows on the 5th-generation tensor cores, 16-bit
 // types. Tiles of 128 positions of one adapter.
 //
-// The first launch computes v = s x A^T: a stage is 64 of d, 128 rows of x (gathered) and the
-// adapter's rank rows of A, copied asynchronously into 128-byte-swizzled rows; one thread
-// issues the MMAs (128 x rp x 16), the accumulator [128, rp] stays in tensor memory. Tiles are
-// dealt out in slices of d, so that there is a CTA for every SM's two places; what reads v adds
-// the slices in order.
+// The first launch computes v = s x A^T and leaves it in pieces of T: a stage is 64 of d, 128
+// rows of x (gathered) and the adapter's rank rows of A, copied asynchronously into
+// 128-byte-swizzled rows; one thread issues the MMAs (128 x rp x 16), the accumulator [128, rp]
+// stays in tensor memory.
 //
-// The second computes out = base + v B^T in blocks of 128 columns: v in pieces of T (split) is
-// the A operand, [v_1 | v_2 | ..] against the same rows of B, so that the product keeps 16 bits
+// The second computes out = base + v B^T in blocks of 128 columns: v's pieces are the A
+// operand, [v_1 | v_2 | ..] against the same rows of B, so that the product keeps 16 bits
 // of v (FP32 output: 24). Two accumulators take turns: the MMAs of a block run under the
 // last one's output. B's rows stand in an order in which a lane that reads 16 x 256 bits of
 // tensor memory ends with 8 consecutive columns of its rows.
@@ -62,9 +61,14 @@ MOE_DEV uint8_t* align_1k(uint8_t* p) {
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
 }
 
-template <typename T, int STAGES>
+// A cluster of CTAs a tile, each with a part of d. Their sums meet in distributed shared
+// memory, in order; each CTA then writes v of its share of the rows, in pieces of T:
+//   vp [T][NP][rp], and for FP16 back [T], the inverse of a row's scale.
+// Every CTA makes the same number of turns, whatever the offsets: cluster barriers always pair.
+template <typename T, int NP, int STAGES>
 __global__ void __launch_bounds__(THREADS, 2)
-adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int cols, unsigned long long timeout_ns) {
+adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int cols, unsigned long long timeout_ns) {
+    constexpr bool SCALED = __is_same(T, __half);
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups g;
     __shared__ __align__(8) uint64_t bars[STAGES];
@@ -72,9 +76,11 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int cols, unsign
     __shared__ int abort_flag;
     uint8_t* smem = align_1k(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int stage_bytes = BLOCK + a.rp * 128;
+    const int rp = a.rp, stage_bytes = BLOCK + rp * 128;
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](uint32_t i) { return smem_u32(&bars[i]); };
+    const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int clusters = gridDim.x / C, id = blockIdx.x / C;
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(bar(i), 1);
         abort_flag = 0;
@@ -91,94 +97,146 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int cols, unsign
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const WaitCtx wc{a.err, &abort_flag, timeout_ns};
-    const int len = ((a.d + a.slices - 1) / a.slices + 63) / 64 * 64;
+    const int steps = (a.d + 63) / 64, mine = (steps + C - 1) / C;
+    const int k0 = min(a.d, 64 * mine * rank), k1 = min(a.d, k0 + 64 * mine), n = (k1 - k0 + 63) / 64;
     const T* x = static_cast<const T*>(a.x);
     const int c16 = tid & 7, r0 = tid >> 3;  // this thread's 16-byte piece, its rows r0 + 32 i
+    float* part = reinterpret_cast<float*>(smem);  // [ROWS][rp], over the stages
+    const int share = ROWS / C;
+    float* sum = part + ROWS * rp;                 // [share][rp]
+    T* vp = static_cast<T*>(a.vp);
     bool alive = true;
     uint32_t it = 0;  // stages consumed: stage it % STAGES, its (it / STAGES)th use
-    for (int u = blockIdx.x; u < tiles * a.slices; u += gridDim.x) {
-        const Tile t = tile_of<ROWS>(u / a.slices, a, g);
-        const int slice = u % a.slices, k0 = slice * len, k1 = min(a.d, k0 + len), n = k1 > k0 ? (k1 - k0 + 63) / 64 : 0;
-        const T* xr[ROWS / 32];
-#pragma unroll
-        for (int i = 0; i < ROWS / 32; ++i) {
-            const int p = r0 + 32 * i;
-            xr[i] = nullptr;
-            if (p < t.n) {
-                const int r = row_of(a, t.pos + p);
-                if (r >= 0) xr[i] = x + r * a.x_stride;
-                else if (c16 == 0) atomicOr(a.err, ERRBIT_INDEX);
-            }
-        }
-        const T* A = static_cast<const T*>(a.a) + static_cast<long long>(t.e) * a.r * a.d;
-        auto load = [&](int kb, uint32_t stage) {
-            const int k = k0 + 64 * kb + 8 * c16;
-            const uint32_t at = sbase + stage * stage_bytes;
+    for (int turn = 0; turn < turns; ++turn) {
+        const int tile = turn * clusters + id;
+        const bool there_is = tile < tiles;
+        if (there_is) {
+            const Tile t = tile_of<ROWS>(tile, a, g);
+            const T* xr[ROWS / 32];
 #pragma unroll
             for (int i = 0; i < ROWS / 32; ++i) {
-                const bool there = xr[i] != nullptr && k < k1;
-                cp_async_16z(at + swizzled(r0 + 32 * i, c16), there ? xr[i] + k : x, there);
-            }
-            for (int r = r0; r < a.rp; r += 32) {
-                const bool there = r < a.r && k < k1;
-                cp_async_16z(at + BLOCK + swizzled(r, c16), there ? A + static_cast<long long>(r) * a.d + k : A, there);
-            }
-        };
-        for (int s = 0; s < STAGES - 1; ++s) {
-            if (s < n) load(s, (it + s) % STAGES);
-            cp_async_commit();
-        }
-        for (int kb = 0; kb < n; ++kb, ++it) {
-            cp_async_wait<STAGES - 2>();
-            fence_proxy_async_smem();
-            alive = __syncthreads_and(alive);
-            const uint32_t stage = it % STAGES;
-            if (warp == 0 && alive) {
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t at = sbase + stage * stage_bytes;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tc_mma_bf16(tmem, smem_desc_sw128(at + 32 * q, 16, 1024), smem_desc_sw128(at + BLOCK + 32 * q, 16, 1024),
-                                    idesc<T>(a.rp), kb > 0 || q > 0);
-                    tc_commit(bar(stage));
+                const int p = r0 + 32 * i;
+                xr[i] = nullptr;
+                if (p < t.n) {
+                    const int r = row_of(a, t.pos + p);
+                    if (r >= 0) xr[i] = x + r * a.x_stride;
+                    else if (c16 == 0 && rank == 0) atomicOr(a.err, ERRBIT_INDEX);
                 }
-                __syncwarp();
             }
-            if (kb + STAGES - 1 < n) {
-                // the stage before this one, once its MMAs have read it
-                const uint32_t last = it + STAGES - 1;
-                if (kb > 0 && alive) alive = bounded_wait(bar(last % STAGES), (it - 1) / STAGES & 1, wc);
-                load(kb + STAGES - 1, last % STAGES);
+            const T* A = static_cast<const T*>(a.a) + static_cast<long long>(t.e) * a.r * a.d;
+            auto load = [&](int kb, uint32_t stage) {
+                const int k = k0 + 64 * kb + 8 * c16;
+                const uint32_t at = sbase + stage * stage_bytes;
+#pragma unroll
+                for (int i = 0; i < ROWS / 32; ++i) {
+                    const bool there = xr[i] != nullptr && k < k1;
+                    cp_async_16z(at + swizzled(r0 + 32 * i, c16), there ? xr[i] + k : x, there);
+                }
+                for (int r = r0; r < rp; r += 32) {
+                    const bool there = r < a.r && k < k1;
+                    cp_async_16z(at + BLOCK + swizzled(r, c16), there ? A + static_cast<long long>(r) * a.d + k : A, there);
+                }
+            };
+            for (int s = 0; s < STAGES - 1; ++s) {
+                if (s < n) load(s, (it + s) % STAGES);
+                cp_async_commit();
             }
-            cp_async_commit();
-        }
-        if (alive && n > 0) alive = bounded_wait(bar((it - 1) % STAGES), (it - 1) / STAGES & 1, wc);
-        tc_fence_after();
-        const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
-        const int row = 32 * (warp & 3) + lane;
-        float* out = a.v + (static_cast<long long>(slice) * a.T + t.pos + row) * a.rp;
-        for (int c = 16 * (warp >> 2); c < a.rp; c += 32) {
-            uint32_t v[16];
-            tc_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
-            tc_wait_ld();
-            if (row < t.n) {
+            for (int kb = 0; kb < n; ++kb, ++it) {
+                cp_async_wait<STAGES - 2>();
+                fence_proxy_async_smem();
+                alive = __syncthreads_and(alive);
+                const uint32_t stage = it % STAGES;
+                if (warp == 0 && alive) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = sbase + stage * stage_bytes;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            tc_mma_bf16(tmem, smem_desc_sw128(at + 32 * q, 16, 1024), smem_desc_sw128(at + BLOCK + 32 * q, 16, 1024),
+                                        idesc<T>(rp), kb > 0 || q > 0);
+                        tc_commit(bar(stage));
+                    }
+                    __syncwarp();
+                }
+                if (kb + STAGES - 1 < n) {
+                    // the stage before this one, once its MMAs have read it
+                    const uint32_t last = it + STAGES - 1;
+                    if (kb > 0 && alive) alive = bounded_wait(bar(last % STAGES), (it - 1) / STAGES & 1, wc);
+                    load(kb + STAGES - 1, last % STAGES);
+                }
+                cp_async_commit();
+            }
+            if (alive && n > 0) alive = bounded_wait(bar((it - 1) % STAGES), (it - 1) / STAGES & 1, wc);
+            tc_fence_after();
+            cp_async_wait<0>();
+            alive = __syncthreads_and(alive);  // the stages are free
+            const int row = 32 * (warp & 3) + lane;
+            for (int c = 16 * (warp >> 2); c < rp; c += 32) {
+                uint32_t v[16];
+                tc_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
+                tc_wait_ld();
 #pragma unroll
                 for (int q = 0; q < 16; q += 4) {
                     float f[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        f[i] = c + q + i >= a.r || n == 0 ? 0.0f : !alive ? CUDART_NAN_F : s * __uint_as_float(v[q + i]);
-                    *reinterpret_cast<float4*>(out + c + q) = make_float4(f[0], f[1], f[2], f[3]);
+                    for (int i = 0; i < 4; ++i) f[i] = !alive ? CUDART_NAN_F : n == 0 ? 0.0f : __uint_as_float(v[q + i]);
+                    *reinterpret_cast<float4*>(part + row * rp + c + q) = make_float4(f[0], f[1], f[2], f[3]);
                 }
             }
+            tc_fence_before();
         }
-        tc_fence_before();
-        alive = __syncthreads_and(alive);  // the accumulator is free
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+        if (there_is) {
+            const Tile t = tile_of<ROWS>(tile, a, g);
+            const float s = a.scale != nullptr ? __ldg(a.scale + t.e) : 1.0f;
+            for (int i = tid; i < share * rp / 4; i += THREADS) {
+                const uint32_t at = smem_u32(part + rank * share * rp + 4 * i);
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (C > 1) {
+#pragma unroll 4
+                    for (int c = 0; c < C; ++c) {
+                        const float4 o = ld_shared_cluster_v4(map_shared_rank(at, c));
+                        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                    }
+                } else {
+                    v = *reinterpret_cast<const float4*>(part + 4 * i);
+                }
+                const int k = 4 * i % rp;  // ranks behind r are zeros whatever x holds
+                v.x = k < a.r ? v.x * s : 0.0f;
+                v.y = k + 1 < a.r ? v.y * s : 0.0f;
+                v.z = k + 2 < a.r ? v.z * s : 0.0f;
+                v.w = k + 3 < a.r ? v.w * s : 0.0f;
+                *reinterpret_cast<float4*>(sum + 4 * i) = v;
+            }
+        }
+        if (C > 1) cluster_arrive();  // the others' parts have been read
+        __syncthreads();
+        if (there_is) {
+            const Tile t = tile_of<ROWS>(tile, a, g);
+            for (int i = tid; i < share * rp / 8; i += THREADS) {
+                const int r = i / (rp / 8), k = i % (rp / 8) * 8, p = rank * share + r;
+                if (p >= t.n) continue;
+                float scale = 1.0f;
+                if constexpr (SCALED) {
+                    float most = 0.0f, back;
+                    for (int q = 0; q < rp; q += 4) most = largest_finite(*reinterpret_cast<const float4*>(sum + r * rp + q), most);
+                    row_scale(most, scale, back);
+                    if (k == 0) a.back[t.pos + p] = back;
+                }
+                T q[8][NP];
+#pragma unroll
+                for (int h = 0; h < 8; ++h) split<T, NP>(sum[r * rp + k + h] * scale, q[h]);
+#pragma unroll
+                for (int o = 0; o < NP; ++o)
+                    *reinterpret_cast<uint4*>(vp + (static_cast<long long>(t.pos + p) * NP + o) * rp + k) =
+                        make_uint4(pack2(q[0][o], q[1][o]), pack2(q[2][o], q[3][o]), pack2(q[4][o], q[5][o]), pack2(q[6][o], q[7][o]));
+            }
+        }
+        if (C > 1) cluster_wait();
+        alive = __syncthreads_and(alive);  // the accumulator and the stages are free
         tc_fence_after();
     }
-    cp_async_wait<0>();
-    __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, cols);
 }
 
@@ -218,15 +276,22 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const WaitCtx wc{a.err, &abort_flag, timeout_ns};
-    const int nb = a.col_parts, len = ((a.N + nb - 1) / nb + COLS - 1) / COLS * COLS;
+    // the tiles' blocks of columns in ranges of equal length over the CTAs, across the tiles' ends:
+    // every SM has the same work, whatever the number of tiles
+    const int per = (a.N + COLS - 1) / COLS;
+    const long long total = static_cast<long long>(tiles) * per;
+    const T* vp = static_cast<const T*>(a.vp);
     const O* base = static_cast<const O*>(a.base);
     O* out = static_cast<O*>(a.out);
     const int pieces = a.rp / 8;  // of 16 bytes in a row of B
     bool alive = true;
     uint32_t uses[2] = {0, 0};
-    for (int u = blockIdx.x; u < tiles * nb; u += gridDim.x) {
-        const Tile t = tile_of<ROWS>(u / nb, a, g);
-        const int c0 = u % nb * len, c1 = min(a.N, c0 + len), n = c1 > c0 ? (c1 - c0 + COLS - 1) / COLS : 0;
+    const long long end = total * (blockIdx.x + 1) / gridDim.x;
+    for (long long from = total * blockIdx.x / gridDim.x; from < end;) {
+        const int tile = static_cast<int>(from / per), c0 = static_cast<int>(from % per) * COLS;
+        const int n = static_cast<int>(min(static_cast<long long>(per - c0 / COLS), end - from)), c1 = min(a.N, c0 + COLS * n);
+        from += n;
+        const Tile t = tile_of<ROWS>(tile, a, g);
         const bool adapted = t.e < a.E;
         const T* B = static_cast<const T*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
         auto load_b = [&](int b) {
@@ -241,39 +306,17 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
         };
         __syncthreads();  // the last tile's rows have been read
         if (tid < ROWS) srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+        if (adapted) {  // the pieces of v, in the first block's group
+            const int row16 = NP * a.rp / 8;
+            for (int i = tid; i < ROWS * row16; i += THREADS) {
+                const int p = i / row16, c = i % row16;
+                cp_async_16z(sA + (c >> 3) * BLOCK + swizzled(p, c & 7), vp + (p < t.n ? (t.pos + p) * static_cast<long long>(NP * a.rp) + 8 * c : 0), p < t.n);
+            }
+            if (SCALED && tid < ROWS) sback[tid] = tid < t.n ? a.back[t.pos + tid] : 1.0f;
+        }
         for (int b = 0; b < 2; ++b) {
             if (adapted && b < n) load_b(b);
             cp_async_commit();
-        }
-        if (adapted) {
-            const int p = tid >> 1, half = tid & 1;  // a row's pieces by two threads
-            const int pos = t.pos + p;
-            float scale = 1.0f;
-            if constexpr (SCALED) {
-                float most = 0.0f, back;
-                for (int k = half * (a.rp / 2); p < t.n && k < (half + 1) * (a.rp / 2); k += 4) most = largest_finite(inner4(a, pos, k), most);
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                row_scale(most, scale, back);
-                if (half == 0) sback[p] = back;
-            }
-            for (int k = half * (a.rp / 2); k < (half + 1) * (a.rp / 2); k += 8) {
-                T q[8][NP];
-#pragma unroll
-                for (int h = 0; h < 8; h += 4) {
-                    const float4 v = p < t.n ? inner4(a, pos, k + h) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    split<T, NP>(v.x * scale, q[h]);
-                    split<T, NP>(v.y * scale, q[h + 1]);
-                    split<T, NP>(v.z * scale, q[h + 2]);
-                    split<T, NP>(v.w * scale, q[h + 3]);
-                }
-#pragma unroll
-                for (int o = 0; o < NP; ++o) {
-                    const int at = o * a.rp + k;
-                    *reinterpret_cast<uint4*>(smem + (at >> 6) * BLOCK + swizzled(p, (at & 63) >> 3)) =
-                        make_uint4(pack2(q[0][o], q[1][o]), pack2(q[2][o], q[3][o]), pack2(q[4][o], q[5][o]), pack2(q[6][o], q[7][o]));
-                }
-            }
-            fence_proxy_async_smem();
         }
         __syncthreads();
         // This warp's 32 rows (its tensor-memory lanes) and 64 of a block's columns.
@@ -361,53 +404,41 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
 
 long long most_tiles(int T, int E) { return std::min<long long>(T, (T + ROWS - 1) / ROWS + E + 1); }
 
-// Parts to deal `tiles` tiles out in, at most `most`, with two CTAs an SM: the waves of parts,
-// each of which takes 3 us before it begins beside its share of the tile's `us`.
-int parts_of(long long tiles, int most, double us) {
-    const long long places = 2LL * num_sms();
-    int best = 1;
-    double least = 1e30;
-    for (int p = 1; p <= most; ++p) {
-        const double t = static_cast<double>((tiles * p + places - 1) / places) * (3.0 + us / p);
-        if (t < least) {
-            least = t;
-            best = p;
-        }
-    }
-    return best;
-}
-// us of n bytes for one of two CTAs on each SM at the memory's rate
-double share_us(double n) { return n * 2 * num_sms() / 6.8e6; }
-
-template <typename T, int STAGES>
-cudaError_t shrink(const AdapterArgs& a, cudaStream_t s) {
+template <typename T, int NP, int STAGES>
+cudaError_t shrink(AdapterArgs a, cudaStream_t s) {
     static bool done[64] = {};
-    const int smem = STAGES * (BLOCK + a.rp * 128) + 1024;
-    if (!allow_smem(adapter_shrink_tc_kernel<T, STAGES>, 110 << 10, done)) return cudaErrorInvalidValue;
-    const long long units = most_tiles(a.T, a.E) * a.slices, cap = 2LL * num_sms();
+    // the stages, and over them the sums: [ROWS][rp] and a CTA's share
+    const int smem = std::max(STAGES * (BLOCK + a.rp * 128), 2 * ROWS * a.rp * 4) + 1024;
+    if (!allow_smem(adapter_shrink_tc_kernel<T, NP, STAGES>, 132 << 10, done)) return cudaErrorInvalidValue;
+    const long long tiles = most_tiles(a.T, a.E), places = 2LL * num_sms();
+    // as many CTAs a tile as there are places for, while each has 256 of d
+    a.cluster = 1;
+    while (a.cluster < 8 && tiles * a.cluster * 2 <= places && a.d >= 512 * a.cluster) a.cluster *= 2;
+    const long long clusters = std::min(tiles, places / a.cluster);
+    const int turns = static_cast<int>((tiles + clusters - 1) / clusters);
     int cols = 32;
     while (cols < a.rp) cols *= 2;
-    return launch_pdl(adapter_shrink_tc_kernel<T, STAGES>, dim3(static_cast<unsigned>(std::min(units, cap))), dim3(THREADS), smem, s, a,
-                      cols, static_cast<unsigned long long>(wait_timeout_ns()));
+    return launch_pdl_cluster(adapter_shrink_tc_kernel<T, NP, STAGES>, dim3(static_cast<unsigned>(clusters * a.cluster)), dim3(THREADS), smem, s,
+                              a.cluster, a, turns, cols, static_cast<unsigned long long>(wait_timeout_ns()));
 }
 
 template <typename T, typename O>
 cudaError_t launch_t(AdapterArgs a, cudaStream_t s) {
-    a.slices = adapter_tc_slices(a.T, a.d, a.E);
-    const cudaError_t e = a.rp <= 32 ? shrink<T, 5>(a, s) : a.rp <= 64 ? shrink<T, 4>(a, s) : shrink<T, 3>(a, s);
-    if (e != cudaSuccess) return e;
     constexpr int NP = sizeof(O) == 4 ? 3 : 2;
+    a.vp = a.v;
+    a.back = reinterpret_cast<float*>(static_cast<char*>(a.vp) + static_cast<size_t>(a.T) * NP * a.rp * 2);
+    const cudaError_t e = a.rp <= 32 ? shrink<T, NP, 5>(a, s) : a.rp <= 64 ? shrink<T, NP, 4>(a, s) : shrink<T, NP, 3>(a, s);
+    if (e != cudaSuccess) return e;
+    const long long tiles = most_tiles(a.T, a.E), cap = 2LL * num_sms();
     const int smem = ((NP * a.rp + 63) / 64 + B_STAGES * ((a.rp + 63) / 64)) * BLOCK + 1024;
     static bool done[64] = {};
     if (!allow_smem(adapter_expand_tc_kernel<T, O>, ((NP * MAX_RP + 63) / 64 + B_STAGES * (MAX_RP / 64)) * BLOCK + 1024, done))
         return cudaErrorInvalidValue;
-    const long long tiles = most_tiles(a.T, a.E), cap = 2LL * num_sms();
-    a.col_parts = parts_of(tiles, std::min(16, (a.N + COLS - 1) / COLS), share_us(2.0 * ROWS * a.N * sizeof(O)));
     // Not begun under the first launch: beside CTAs that take all shared memory its loads in flight
     // would have the 28 KB of L1 that those leave (16384 x 2048 x 2816, rank 16: 71 us for 62;
     // 8192 x 4096 x 4096, rank 64: 77 for 70).
     note_launch();
-    adapter_expand_tc_kernel<T, O><<<static_cast<unsigned>(std::min(tiles * a.col_parts, cap)), THREADS, smem, s>>>(
+    adapter_expand_tc_kernel<T, O><<<static_cast<unsigned>(std::min(tiles * ((a.N + COLS - 1) / COLS), cap)), THREADS, smem, s>>>(
         a, static_cast<unsigned long long>(wait_timeout_ns()));
     return cudaGetLastError();
 }
@@ -416,11 +447,11 @@ bool on(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 
 
 }  // namespace
 
-int adapter_tc_slices(int T, int d, int E) { return parts_of(most_tiles(T, E), std::max(1, std::min(8, d / 512)), share_us(2.0 * ROWS * d)); }
+size_t adapter_tc_workspace(int T, int rp) { return static_cast<size_t>(T) * (3 * rp * 2 + 4); }
 
 bool adapter_tc_takes(const AdapterArgs& a) {
     const int eo = a.out_dtype == MOE_F32 ? 4 : 2;
-    return a.T >= 1024 && a.rp <= MAX_RP && a.d % 8 == 0 && a.x_stride % 8 == 0 && on(a.x, 16) && on(a.a, 16) && a.r % 8 == 0 &&
+    return a.T >= TC_ROWS && a.rp <= MAX_RP && a.d % 8 == 0 && a.x_stride % 8 == 0 && on(a.x, 16) && on(a.a, 16) && a.r % 8 == 0 &&
            on(a.b, 16) && a.N % 8 == 0 && on(a.out, 16) && a.out_stride * eo % 16 == 0 && on(a.base, 16) && a.base_stride * eo % 16 == 0;
 }
 

@@ -598,18 +598,21 @@ struct AdapterArgs {
     void* out;
     int in_place;            // out is base
     int* err;                // the workspace, its error word first
-    float* v;                // inner values, [slices, T, rp]
+    float* v;                // FP32: inner values, [slices, T, rp]
     // set by launch_adapter and what it calls
-    int rp, slices;          // r rounded up (FP32: to 4, else 16), slices of d
-    int col_parts;           // ranges of columns a tile is dealt out in
-    int cluster;             // CTAs a tile
+    int rp, slices;          // r rounded up (FP32: to 4, else 16), FP32: slices of d
+    int col_parts;           // FP32: ranges of columns a tile is dealt out in
+    int cluster;             // 16-bit types: CTAs a tile
+    void* vp;                // many rows: inner values in pieces [T, pieces, rp], FP16: their rows'
+    float* back;             // inverse scales [T]
 };
 size_t adapter_workspace(int T, int d, int r, int E, int dtype);
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
-// The tensor-core kernels of many rows: whether they take a call (rp set), the slices of d
-// that they deal out, and the call.
+// The tensor-core kernels of many rows: whether they take a call (rp set), their workspace
+// behind the error word, and the call.
+constexpr int TC_ROWS = 1024;
 bool adapter_tc_takes(const AdapterArgs& a);
-int adapter_tc_slices(int T, int d, int E);
+size_t adapter_tc_workspace(int T, int rp);
 cudaError_t launch_adapter_tc(const AdapterArgs& a, cudaStream_t s);
 
 }  // namespace moe
