@@ -447,14 +447,14 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                 row[m][h] = srow[16 * m + 8 * h + gi];
                 back[m][h] = SCALED && adapted ? sback[16 * m + 8 * h + gi] : 1.0f;
             }
-        Cols<O, true> add[MT][2];
+        Cols<O> add[MT][2];
         auto load_base = [&](int n0) {
             const int col = n0 + 8 * ti;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    add[m][h].load(base + row[m][h] * a.base_stride + col, base != nullptr && row[m][h] >= 0 ? c1 - col : 0);
+                    add[m][h].load(base + row[m][h] * a.base_stride + col, base != nullptr && row[m][h] >= 0 && col < c1);
         };
         uint2 fb[KB][4];
         auto load_b = [&](int n0, int ks) {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
         load_b(c0 + 32 * w, 0);
         if constexpr (AHEAD) load_base(c0 + 32 * w);
         for (int n0 = c0 + 32 * w; t.n > 0 && n0 < c1; n0 += STEP) {
-            Cols<O, true> here[MT][2];
+            Cols<O> here[MT][2];
             if constexpr (AHEAD) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -518,14 +518,16 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (row[m][h] < 0 || col >= c1) continue;
-                        float f[8];
-                        if constexpr (AHEAD) here[m][h].get(f);
-                        else add[m][h].get(f);
+                        const Cols<O>& old = AHEAD ? here[m][h] : add[m][h];
+                        O* to = out + row[m][h] * a.out_stride + col;
                         if (adapted) {
+                            F2 v[4];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) f[i] = fmaf(acc[m][i >> 1][2 * h + (i & 1)], back[m][h], f[i]);
+                            for (int j = 0; j < 4; ++j) v[j] = f2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+                            old.add_to(to, v, back[m][h]);
+                        } else {
+                            old.copy_to(to);
                         }
-                        Cols<O, true>::store(out + row[m][h] * a.out_stride + col, 8, f);
                     }
             } else {
                 // rows on no 16 bytes: 16 rows of the warp's columns through shared memory, then a row's

@@ -109,50 +109,35 @@ MOE_DEV void split(float v, T (&p)[NP]) {
     }
 }
 
-// 8 consecutive elements of base as loaded.
-template <typename O, bool VEC>
+// 8 consecutive elements of base as loaded (16-byte aligned, all or none).
+template <typename O>
 struct Cols {
     static constexpr int N = 8 * sizeof(O) / 16, W = 8 / N;
     Raw<O, W> v[N];
-    MOE_DEV void load(const O* p, int n) {
+    MOE_DEV void load(const O* p, bool there) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             v[i].clear();
-            if constexpr (VEC) {  // base may be out: no read-only loads
-                if (n > 0) v[i].v = *reinterpret_cast<const uint4*>(p + i * W);
-            } else {
-                O* e = reinterpret_cast<O*>(&v[i].v);
-#pragma unroll
-                for (int q = 0; q < W; ++q)
-                    if (i * W + q < n) e[q] = p[i * W + q];
-            }
+            if (there) v[i].v = *reinterpret_cast<const uint4*>(p + i * W);  // base may be out: no read-only loads
         }
     }
-    MOE_DEV void get(float (&f)[8]) const {
+    // acc times `by`, added to these elements and stored, two at a time.
+    MOE_DEV void add_to(O* p, const F2 (&acc)[4], float by) const {
+        const F2 s = f2(by, by);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float e[W];
             v[i].get(e);
 #pragma unroll
-            for (int q = 0; q < W; ++q) f[i * W + q] = e[q];
+            for (int q = 0; q < W; q += 2) unpack(fma2(acc[(i * W + q) / 2], s, f2(e[q], e[q + 1])), e[q], e[q + 1]);
+            Raw<O, W> o;
+            o.set(e);
+            o.store(p + i * W);
         }
     }
-    MOE_DEV static void store(O* p, int n, const float (&f)[8]) {
+    MOE_DEV void copy_to(O* p) const {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float e[W];
-#pragma unroll
-            for (int q = 0; q < W; ++q) e[q] = f[i * W + q];
-            if constexpr (VEC) {
-                Raw<O, W> o;
-                o.set(e);
-                o.store(p + i * W);
-            } else {
-#pragma unroll
-                for (int q = 0; q < W; ++q)
-                    if (i * W + q < n) p[i * W + q] = from_f32<O>(e[q]);
-            }
-        }
+        for (int i = 0; i < N; ++i) v[i].store(p + i * W);
     }
 };
 

@@ -321,19 +321,26 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
         __syncthreads();
         // This warp's 32 rows (its tensor-memory lanes) and 64 of a block's columns.
         const int r32 = 32 * (warp & 3), c64 = 64 * (warp >> 2);
-        int row[2][2];
+        const O* from_row[2][2];
+        O* to_row[2][2];  // NULL: no row
+        float back[2][2];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) row[m][h] = srow[r32 + 16 * m + 8 * h + gi];
-        Cols<O, true> add[AHEAD][2][2];
+            for (int h = 0; h < 2; ++h) {
+                const int p = r32 + 16 * m + 8 * h + gi, row = srow[p];
+                from_row[m][h] = base != nullptr && row >= 0 ? base + row * a.base_stride + c0 + c64 + 8 * ti : nullptr;
+                to_row[m][h] = row >= 0 ? out + row * a.out_stride + c0 + c64 + 8 * ti : nullptr;
+                back[m][h] = SCALED && adapted ? sback[p] : 1.0f;
+            }
+        const int width = c1 - c0 - c64 - 8 * ti;  // columns from this lane's first one on
+        Cols<O> add[AHEAD][2][2];
         auto load_base = [&](int b, int q, int slot) {
-            const int col = c0 + COLS * b + c64 + 32 * q + 8 * ti;
+            const int at = COLS * b + 32 * q;
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    add[slot][m][h].load(base + row[m][h] * a.base_stride + col, base != nullptr && row[m][h] >= 0 ? c1 - col : 0);
+                for (int h = 0; h < 2; ++h) add[slot][m][h].load(from_row[m][h] + at, from_row[m][h] != nullptr && at < width);
         };
 #pragma unroll
         for (int q = 0; q < AHEAD; ++q) load_base(0, q, q);
@@ -365,27 +372,30 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
                     alive = __all_sync(0xffffffffu, alive);
                     tc_fence_after();
                 }
+                if (!alive) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) back[m][0] = back[m][1] = CUDART_NAN_F;
+                }
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int col = c0 + COLS * at + c64 + 32 * q + 8 * ti;
+                    const int off = COLS * at + 32 * q;
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        uint32_t acc[16];
                         if (adapted) {
-                            tc_ld_16x256b_x4(tmem + (static_cast<uint32_t>(r32 + 16 * m) << 16) + (at & 1) * COLS + c64 + 32 * q, acc);
+                            uint32_t r[16];
+                            tc_ld_16x256b_x4(tmem + (static_cast<uint32_t>(r32 + 16 * m) << 16) + (at & 1) * COLS + c64 + 32 * q, r);
                             tc_wait_ld();
-                        }
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float f[8];
-                            add[q % AHEAD][m][h].get(f);
-                            if (adapted) {
-                                const float back = SCALED ? sback[r32 + 16 * m + 8 * h + gi] : 1.0f;
+                            for (int h = 0; h < 2; ++h) {
+                                F2 acc[4];
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    f[i] = alive ? fmaf(__uint_as_float(acc[4 * (i >> 1) + 2 * h + (i & 1)]), back, f[i]) : CUDART_NAN_F;
+                                for (int j = 0; j < 4; ++j) acc[j] = f2(__uint_as_float(r[4 * j + 2 * h]), __uint_as_float(r[4 * j + 2 * h + 1]));
+                                if (to_row[m][h] != nullptr && off < width) add[q % AHEAD][m][h].add_to(to_row[m][h] + off, acc, back[m][h]);
                             }
-                            if (row[m][h] >= 0 && col < c1) Cols<O, true>::store(out + row[m][h] * a.out_stride + col, 8, f);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (to_row[m][h] != nullptr && off < width) add[q % AHEAD][m][h].copy_to(to_row[m][h] + off);
                         }
                     }
                     if (AHEAD == 2) load_base(at + 1, q, q);
