@@ -558,7 +558,13 @@ moe_status moe_adapter_add_workspace_size(const moe_adapter_config* cfg, size_t*
  * ws: 256-byte aligned. Offsets are clamped to [0, T]; a row index outside
  * [0, T) is skipped and sets MOE_ERR_DEVICE_INDEX in the workspace's error word,
  * which the call adds to and never clears; a row that no position names is not
- * written, and what a row named twice holds is not specified. */
+ * written, and what a row named twice holds is not specified. A bounded device
+ * wait that runs out makes the outputs that are not stored yet NaN and sets
+ * MOE_ERR_TIMEOUT.
+ *   The form is chosen from rows, ranks, adapters and alignment; the environment
+ * variable MOE_ADAPTER_FORM, read at each call, overrides it for tests and tuning
+ * ("few", "many": rows; "many" only where 16-byte rows, widths and ranks that are
+ * multiples of 8 and a rank up to 128 allow it). Forms differ in rounding only. */
 moe_status moe_adapter_add(const moe_adapter_config* cfg, const void* x, int64_t x_stride, const void* a,
                            const void* b, const float* scale, const int32_t* offsets, const int32_t* rows,
                            const void* base, int64_t base_stride, void* out, int64_t out_stride, void* ws,

@@ -6,6 +6,8 @@
 // of `rows`; positions from offsets[E] on have no adapter. Two launches: the first
 // computes v = s_e x[t] A_e^T into the workspace (by position, FP32), the second adds
 // v B_e^T to base.
+#include <stdlib.h>
+
 #include "adapter.cuh"
 
 namespace moe {
@@ -599,9 +601,25 @@ cudaError_t fused_k(AdapterArgs a, cudaStream_t s) {
                               F::smem(a.rp), s, a.cluster, a, turns);
 }
 
+// Whether a call of 16-bit types goes to the kernels of many rows, where its operands allow it:
+// from a number of inner values on, and while adapters have 16 rows of rank 64 (64 of rank 16)
+// each if all have any. (us, few rows' kernel : many rows', d and N 4096 unless given. 1024 rows
+// of 8 adapters, rank 64, 31 : 24; rank 16, 17 : 18; 512 of 4, rank 128, 2048 x 2048, 30 : 19; 4096
+// rows of 64, rank 64, 102 : 60; rank 16, 46 : 47; 4096 of 256, rank 16, 56 : 85; 8192 of 512, rank
+// 16, 94 : 158; 16384 of 4, rank 16, 108 : 85.) MOE_ADAPTER_FORM overrides the choice for tests
+// and tuning.
+bool adapter_many(const AdapterArgs& a) {
+    if (!adapter_tc_takes(a)) return false;
+    if (const char* e = getenv("MOE_ADAPTER_FORM")) {
+        if (e[0] == 'm') return true;
+        if (e[0] == 'f') return false;
+    }
+    return static_cast<long long>(a.T) * a.rp >= std::max(65536LL, 1024LL * a.E);
+}
+
 template <typename T, typename O>
 cudaError_t launch_mma(const AdapterArgs& a, cudaStream_t s) {
-    if (adapter_tc_takes(a)) return launch_adapter_tc(a, s);
+    if (adapter_many(a)) return launch_adapter_tc(a, s);
     const bool vec = a.d % 8 == 0 && a.x_stride % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.a, 16) && a.N % 8 == 0 && a.r % 4 == 0 &&
                      aligned_to(a.b, 8) && aligned_to(a.out, 16) && a.out_stride * sizeof(O) % 16 == 0 && aligned_to(a.base, 16) &&
                      a.base_stride * sizeof(O) % 16 == 0;
@@ -629,7 +647,7 @@ int adapter_slices(int T, int d, int r, int E) {
 size_t adapter_workspace(int T, int d, int r, int E, int dtype) {
     const int rp = dtype == MOE_F32 ? (r + 3) / 4 * 4 : (r + 15) / 16 * 16;
     if (dtype == MOE_F32) return 256 + static_cast<size_t>(T) * rp * 4 * adapter_slices(T, d, r, E);
-    return 256 + (T >= TC_ROWS ? adapter_tc_workspace(T, rp) : 0);
+    return 256 + adapter_tc_workspace(T, rp);  // whichever form the call takes
 }
 
 cudaError_t launch_adapter(const AdapterArgs& args, cudaStream_t s) {

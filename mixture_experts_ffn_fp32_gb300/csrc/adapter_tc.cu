@@ -21,13 +21,26 @@ namespace moe {
 namespace {
 
 constexpr int ROWS = 128, BLOCK = 16384;  // a block: 128 rows of 64 elements of 16 bits
-constexpr int MAX_RP = 128;
 
 MOE_DEV void cp_async_16z(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 // 16-byte piece c of row r of a 128-byte-swizzled tile.
 MOE_DEV uint32_t swizzled(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// The same of a tile whose rows are 32 bytes (16 elements, one MMA's reduction), 32-byte
+// swizzled: no space is lost to ranks below 64.
+constexpr int STEP_BYTES = ROWS * 32;
+MOE_DEV uint32_t swizzled32(int r, int c) { return static_cast<uint32_t>(r * 32 + ((c ^ (r >> 2 & 1)) << 4)); }
+MOE_DEV uint64_t smem_desc_sw32(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= 1ull << 16;
+    d |= static_cast<uint64_t>(256 >> 4) << 32;  // between groups of 8 rows
+    d |= 1ull << 46;
+    d |= 6ull << 61;
+    return d;
+}
 
 MOE_DEV uint32_t elect_one() {
     uint32_t e;
@@ -65,7 +78,11 @@ MOE_DEV uint8_t* align_1k(uint8_t* p) {
 // memory, in order; each CTA then writes v of its share of the rows, in pieces of T:
 //   vp [T][NP][rp], and for FP16 back [T], the inverse of a row's scale.
 // Every CTA makes the same number of turns, whatever the offsets: cluster barriers always pair.
-template <typename T, int NP, int STAGES>
+// Three stages: the second launch begins under this one, and the loads that it has in flight want
+// what shared memory leaves of L1 (five stages, 28 KB of L1: 16384 x 2048 x 2816, rank 16, 71 us for 58).
+constexpr int STAGES = 3;
+
+template <typename T, int NP>
 __global__ void __launch_bounds__(THREADS, 2)
 adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int cols, unsigned long long timeout_ns) {
     constexpr bool SCALED = __is_same(T, __half);
@@ -258,7 +275,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
     __shared__ int abort_flag;
     uint8_t* smem = align_1k(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gi = lane >> 2, ti = lane & 3;
-    const int a_bytes = (NP * a.rp + 63) / 64 * BLOCK, b_bytes = (a.rp + 63) / 64 * BLOCK;
+    const int KS = a.rp / 16, a_bytes = NP * KS * STEP_BYTES, b_bytes = KS * STEP_BYTES;
     const uint32_t sA = smem_u32(smem), sB = sA + a_bytes;
     if (tid == 0) {
         mbar_init(smem_u32(&bars[0]), 1);
@@ -271,7 +288,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
         tmem_relinquish();
     }
     tc_fence_before();
-    pdl_trigger();
+    // what the call was given is complete before the launch before this one could begin
     const int tiles = group_table<ROWS>(a, !a.in_place, g);
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
@@ -301,21 +318,24 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
                 // column 8 i + 2 j + c of 32 at row 8 j + 2 i + c
                 const int row = (col & ~31) | (m >> 1 & 3) << 3 | (m >> 3) << 1 | (m & 1);
                 const bool there = c0 + COLS * b + col < c1 && 8 * c < a.r;
-                cp_async_16z(at + (c >> 3) * BLOCK + swizzled(row, c & 7), there ? B + static_cast<long long>(c0 + COLS * b + col) * a.r + 8 * c : B, there);
+                cp_async_16z(at + (c >> 1) * STEP_BYTES + swizzled32(row, c & 1), there ? B + static_cast<long long>(c0 + COLS * b + col) * a.r + 8 * c : B, there);
             }
         };
         __syncthreads();  // the last tile's rows have been read
         if (tid < ROWS) srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
-        if (adapted) {  // the pieces of v, in the first block's group
+        if (adapted) load_b(0);
+        pdl_wait();  // v
+        pdl_trigger();
+        if (adapted) {  // its pieces, in the first block's group
             const int row16 = NP * a.rp / 8;
             for (int i = tid; i < ROWS * row16; i += THREADS) {
                 const int p = i / row16, c = i % row16;
-                cp_async_16z(sA + (c >> 3) * BLOCK + swizzled(p, c & 7), vp + (p < t.n ? (t.pos + p) * static_cast<long long>(NP * a.rp) + 8 * c : 0), p < t.n);
+                cp_async_16z(sA + (c >> 1) * STEP_BYTES + swizzled32(p, c & 1), vp + (p < t.n ? (t.pos + p) * static_cast<long long>(NP * a.rp) + 8 * c : 0), p < t.n);
             }
             if (SCALED && tid < ROWS) sback[tid] = tid < t.n ? a.back[t.pos + tid] : 1.0f;
         }
         for (int b = 0; b < 2; ++b) {
-            if (adapted && b < n) load_b(b);
+            if (adapted && b > 0 && b < n) load_b(b);
             cp_async_commit();
         }
         __syncthreads();
@@ -354,11 +374,9 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
                     if (elect_one()) {
                         const uint32_t d = tmem + (b & 1) * COLS, sb = sB + b % B_STAGES * b_bytes;
                         for (int o = 0; o < NP; ++o)
-                            for (int ks = 0; ks < a.rp / 16; ++ks) {
-                                const int k = o * a.rp + 16 * ks;
-                                tc_mma_bf16(d, smem_desc_sw128(sA + (k >> 6) * BLOCK + (k & 63) * 2, 16, 1024),
-                                            smem_desc_sw128(sb + (ks >> 2) * BLOCK + (ks & 3) * 32, 16, 1024), idesc<T>(COLS), o > 0 || ks > 0);
-                            }
+                            for (int ks = 0; ks < KS; ++ks)
+                                tc_mma_bf16(d, smem_desc_sw32(sA + (o * KS + ks) * STEP_BYTES), smem_desc_sw32(sb + ks * STEP_BYTES), idesc<T>(COLS),
+                                            o > 0 || ks > 0);
                         tc_commit(smem_u32(&bars[b & 1]));
                     }
                     __syncwarp();
@@ -407,6 +425,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
             cp_async_commit();
         }
     }
+    pdl_wait();  // never done before the launch before this one
     cp_async_wait<0>();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, 2 * COLS);
@@ -414,12 +433,12 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
 
 long long most_tiles(int T, int E) { return std::min<long long>(T, (T + ROWS - 1) / ROWS + E + 1); }
 
-template <typename T, int NP, int STAGES>
+template <typename T, int NP>
 cudaError_t shrink(AdapterArgs a, cudaStream_t s) {
     static bool done[64] = {};
     // the stages, and over them the sums: [ROWS][rp] and a CTA's share
     const int smem = std::max(STAGES * (BLOCK + a.rp * 128), 2 * ROWS * a.rp * 4) + 1024;
-    if (!allow_smem(adapter_shrink_tc_kernel<T, NP, STAGES>, 132 << 10, done)) return cudaErrorInvalidValue;
+    if (!allow_smem(adapter_shrink_tc_kernel<T, NP>, 132 << 10, done)) return cudaErrorInvalidValue;
     const long long tiles = most_tiles(a.T, a.E), places = 2LL * num_sms();
     // as many CTAs a tile as there are places for, while each has 256 of d
     a.cluster = 1;
@@ -428,7 +447,7 @@ cudaError_t shrink(AdapterArgs a, cudaStream_t s) {
     const int turns = static_cast<int>((tiles + clusters - 1) / clusters);
     int cols = 32;
     while (cols < a.rp) cols *= 2;
-    return launch_pdl_cluster(adapter_shrink_tc_kernel<T, NP, STAGES>, dim3(static_cast<unsigned>(clusters * a.cluster)), dim3(THREADS), smem, s,
+    return launch_pdl_cluster(adapter_shrink_tc_kernel<T, NP>, dim3(static_cast<unsigned>(clusters * a.cluster)), dim3(THREADS), smem, s,
                               a.cluster, a, turns, cols, static_cast<unsigned long long>(wait_timeout_ns()));
 }
 
@@ -437,20 +456,15 @@ cudaError_t launch_t(AdapterArgs a, cudaStream_t s) {
     constexpr int NP = sizeof(O) == 4 ? 3 : 2;
     a.vp = a.v;
     a.back = reinterpret_cast<float*>(static_cast<char*>(a.vp) + static_cast<size_t>(a.T) * NP * a.rp * 2);
-    const cudaError_t e = a.rp <= 32 ? shrink<T, NP, 5>(a, s) : a.rp <= 64 ? shrink<T, NP, 4>(a, s) : shrink<T, NP, 3>(a, s);
+    const cudaError_t e = shrink<T, NP>(a, s);
     if (e != cudaSuccess) return e;
     const long long tiles = most_tiles(a.T, a.E), cap = 2LL * num_sms();
-    const int smem = ((NP * a.rp + 63) / 64 + B_STAGES * ((a.rp + 63) / 64)) * BLOCK + 1024;
+    const int smem = (NP + B_STAGES) * (a.rp / 16) * STEP_BYTES + 1024;
     static bool done[64] = {};
-    if (!allow_smem(adapter_expand_tc_kernel<T, O>, ((NP * MAX_RP + 63) / 64 + B_STAGES * (MAX_RP / 64)) * BLOCK + 1024, done))
+    if (!allow_smem(adapter_expand_tc_kernel<T, O>, (NP + B_STAGES) * (TC_RANKS / 16) * STEP_BYTES + 1024, done))
         return cudaErrorInvalidValue;
-    // Not begun under the first launch: beside CTAs that take all shared memory its loads in flight
-    // would have the 28 KB of L1 that those leave (16384 x 2048 x 2816, rank 16: 71 us for 62;
-    // 8192 x 4096 x 4096, rank 64: 77 for 70).
-    note_launch();
-    adapter_expand_tc_kernel<T, O><<<static_cast<unsigned>(std::min(tiles * ((a.N + COLS - 1) / COLS), cap)), THREADS, smem, s>>>(
-        a, static_cast<unsigned long long>(wait_timeout_ns()));
-    return cudaGetLastError();
+    return launch_pdl(adapter_expand_tc_kernel<T, O>, dim3(static_cast<unsigned>(std::min(tiles * ((a.N + COLS - 1) / COLS), cap))), dim3(THREADS),
+                      smem, s, a, static_cast<unsigned long long>(wait_timeout_ns()));
 }
 
 bool on(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -461,7 +475,7 @@ size_t adapter_tc_workspace(int T, int rp) { return static_cast<size_t>(T) * (3 
 
 bool adapter_tc_takes(const AdapterArgs& a) {
     const int eo = a.out_dtype == MOE_F32 ? 4 : 2;
-    return a.T >= TC_ROWS && a.rp <= MAX_RP && a.d % 8 == 0 && a.x_stride % 8 == 0 && on(a.x, 16) && on(a.a, 16) && a.r % 8 == 0 &&
+    return a.rp <= TC_RANKS && a.d % 8 == 0 && a.x_stride % 8 == 0 && on(a.x, 16) && on(a.a, 16) && a.r % 8 == 0 &&
            on(a.b, 16) && a.N % 8 == 0 && on(a.out, 16) && a.out_stride * eo % 16 == 0 && on(a.base, 16) && a.base_stride * eo % 16 == 0;
 }
 

@@ -608,9 +608,9 @@ struct AdapterArgs {
 };
 size_t adapter_workspace(int T, int d, int r, int E, int dtype);
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
-// The tensor-core kernels of many rows: whether they take a call (rp set), their workspace
-// behind the error word, and the call.
-constexpr int TC_ROWS = 1024;
+// The tensor-core kernels of many rows: whether a call's operands suit them (rp set, up to
+// TC_RANKS), their workspace behind the error word, and the call.
+constexpr int TC_RANKS = 128;
 bool adapter_tc_takes(const AdapterArgs& a);
 size_t adapter_tc_workspace(int T, int rp);
 cudaError_t launch_adapter_tc(const AdapterArgs& a, cudaStream_t s);

@@ -17,6 +17,15 @@ def A():
     return api
 
 
+@pytest.fixture(params=["chosen", "few", "many"])
+def form(request, monkeypatch):
+    """Each form by itself, where a call's operands let it; FP32 has one."""
+    if request.param == "chosen":
+        monkeypatch.delenv("MOE_ADAPTER_FORM", raising=False)
+    else:
+        monkeypatch.setenv("MOE_ADAPTER_FORM", request.param)
+
+
 def make(T, d, N, r, E, dt=torch.bfloat16, out=None, ids=None, pad=0, seed=0, order=True):
     g = torch.Generator(device="cuda").manual_seed(seed)
 
@@ -49,14 +58,14 @@ SIZES = [(1, 64, 64, 16, 1), (1, 4096, 2048, 16, 8), (2, 128, 96, 8, 300), (17, 
 
 @pytest.mark.parametrize("dt,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
 @pytest.mark.parametrize("size", SIZES, ids=str)
-def test_sizes(A, size, dt, out):
+def test_sizes(A, form, size, dt, out):
     s = make(*size, DT[dt], DT[out])
     check(A.adapter_add(**s), s)
 
 
 @pytest.mark.parametrize("dt", list(DT))
 @pytest.mark.parametrize("pad", [1, 4, 8])
-def test_pitches(A, dt, pad):
+def test_pitches(A, form, dt, pad):
     s = make(150, 256, 192, 16, 6, DT[dt], pad=pad)
     check(A.adapter_add(**s), s)
     s = make(150, 257, 193, 16, 6, DT[dt], pad=pad)
@@ -64,7 +73,7 @@ def test_pitches(A, dt, pad):
 
 
 @pytest.mark.parametrize("per", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 64, 127, 128, 129, 255, 257])
-def test_rows_per_adapter(A, per):
+def test_rows_per_adapter(A, form, per):
     """Groups of equal length around every tile's."""
     E = 5
     ids = torch.arange(E).repeat_interleave(per)
@@ -76,14 +85,14 @@ def test_rows_per_adapter(A, per):
 
 
 @pytest.mark.parametrize("T,r", [(1, 16), (64, 16), (900, 64)])
-def test_nobody_has_one(A, T, r):
+def test_nobody_has_one(A, form, T, r):
     s = make(T, 128, 256, r, 4, ids=torch.full((T,), 4))
     assert torch.equal(A.adapter_add(**s), s["base"])
 
 
 @pytest.mark.parametrize("T", [3, 300, 3000])
 @pytest.mark.parametrize("base", [True, False])
-def test_unscaled_and_without_base(A, T, base):
+def test_unscaled_and_without_base(A, form, T, base):
     s = make(T, 192, 136, 16, 5)
     s["scale"] = None
     if not base:
@@ -98,7 +107,7 @@ def test_unscaled_and_without_base(A, T, base):
 
 @pytest.mark.parametrize("T,r", [(6, 16), (250, 16), (4000, 64)])
 @pytest.mark.parametrize("dt", list(DT))
-def test_in_place(A, T, r, dt):
+def test_in_place(A, form, T, r, dt):
     s = make(T, 256, 384, r, 3, DT[dt], pad=8)
     want = A.adapter_add(**s)
     got = A.adapter_add(**s, out=s["base"])
@@ -106,7 +115,7 @@ def test_in_place(A, T, r, dt):
 
 
 @pytest.mark.parametrize("T", [40, 2000])
-def test_rows_not_named_stay(A, T):
+def test_rows_not_named_stay(A, form, T):
     """Bad indices are skipped and flagged; the rows that no position names are not written."""
     s = make(T, 128, 128, 16, 3, ids=torch.arange(T) % 3)
     ws = A.alloc_adapter_workspace(T, 128, 128, 16, 3)
@@ -123,7 +132,7 @@ def test_rows_not_named_stay(A, T):
 
 
 @pytest.mark.parametrize("T", [30, 3000])
-def test_offsets_out_of_range(A, T):
+def test_offsets_out_of_range(A, form, T):
     """Clamped: nothing is read or written outside."""
     s = make(T, 128, 128, 16, 4, ids=torch.arange(T) % 4)
     s["offsets"] = torch.tensor([0, T // 2, T // 2, T + 1000, T + 2000], dtype=torch.int32, device="cuda")
@@ -132,7 +141,7 @@ def test_offsets_out_of_range(A, T):
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("T", [50, 3000])
-def test_infinite_rows_stay_alone(A, T, dt):
+def test_infinite_rows_stay_alone(A, form, T, dt):
     """A row's infinity or NaN reaches that row alone, and an infinity with weights of one sign stays one."""
     s = make(T, 256, 128, 12, 3, DT[dt], ids=torch.arange(T) % 3)
     want = A.adapter_add(**s)
@@ -149,7 +158,7 @@ def test_infinite_rows_stay_alone(A, T, dt):
 
 
 @pytest.mark.parametrize("T", [20, 2000])
-def test_large_inner_values(A, T):
+def test_large_inner_values(A, form, T):
     """FP16 adapters whose inner values leave FP16's range, and some far below their row's largest."""
     s = make(T, 512, 136, 16, 2, torch.float16, torch.float32, ids=torch.arange(T) % 2)
     s["x"] *= 64
@@ -170,7 +179,7 @@ def test_dispatch_gives_the_groups(A):
     check(got, s)
 
 
-def test_streams_and_graphs(A):
+def test_streams_and_graphs(A, form):
     for T in (60, 3000):
         s = make(T, 256, 512, 16, 9)
         eager = A.adapter_add(**s)
