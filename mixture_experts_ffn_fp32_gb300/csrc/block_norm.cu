@@ -1,5 +1,7 @@
 // The norms on both sides of a block (block_norm.cuh): what their types share. The
 // kernels of a type are compiled by a unit of its own.
+#include <algorithm>
+
 #include "block_norm.cuh"
 
 namespace moe {
@@ -63,7 +65,8 @@ cudaError_t launch_block_norm_params(const BlockNormArgs& a, int n, const float*
 }
 
 size_t block_norm_bwd_floats(int R, int d, bool layer) {
-    return static_cast<size_t>(bwd_parts(R, d)) * (layer ? 4 : 2) * d + (d > BWD_MAX_D ? 2 * static_cast<size_t>(R) : 0);
+    // whichever the operands' alignment lets it take
+    return static_cast<size_t>(std::max(bwd_parts(R, d, true), bwd_parts(R, d, false))) * (layer ? 4 : 2) * d + (d > BWD_MAX_D ? 2 * static_cast<size_t>(R) : 0);
 }
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {

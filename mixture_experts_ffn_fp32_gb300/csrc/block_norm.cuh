@@ -285,35 +285,21 @@ MOE_DEV void row_stats(F2 (&v)[NV * VEC / 2], int d, int t, float inv_d, float e
 }
 
 // A thread's columns of the rows of one operand, D rows ahead in shared memory (RowFetch);
-// elements that cp.async cannot move are read when they are wanted.
+// elements that cp.async cannot move wait in registers, one row ahead.
 template <typename T, int VEC, int NV, int TPR, int D>
 struct Rows {
     using F = RowFetch<T, VEC, NV, TPR, RowThreads<TPR>::THREADS, D>;
     static constexpr int SMEM = F::SMEM;
     F f;
     MOE_DEV void init(void* smem, const T* base, long long pitch, int d, int t) { f.init(smem, base, pitch, d, t); }
-    MOE_DEV void issue(int s, long long row, bool there) {
-        if constexpr (F::ASYNC) f.issue(s, row, there);
-    }
-    // Row `row` (in slot s) as pairs, zeros past its end and where it is not there.
-    MOE_DEV void read(int s, long long row, bool there, F2 (&p)[NV * VEC / 2]) const {
-        if constexpr (F::ASYNC) {
-            f.pairs(s, p);
-        } else {
-            float v[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = i * TPR + f.t;
-                v[i] = there && c < f.d ? to_f32(f.base[row * f.pitch + c]) : 0.0f;
-            }
-#pragma unroll
-            for (int k = 0; k < NV / 2; ++k) p[k] = f2(v[2 * k], v[2 * k + 1]);
-        }
-    }
+    MOE_DEV void issue(int s, long long row, bool there) { f.issue(s, row, there); }
+    // The row in slot s as pairs, zeros past its end.
+    MOE_DEV void read(int s, F2 (&p)[NV * VEC / 2]) const { f.pairs(s, p); }
 };
 // Rows ahead: what fills `bytes` a CTA and operand, at most `most`.
 template <typename T, int NV, int VEC, int TPR>
 constexpr int depth(int bytes, int most) {
+    if (VEC * sizeof(T) < 4) return 1;
     const int row = NV * VEC * static_cast<int>(sizeof(T)) * RowThreads<TPR>::THREADS;
     return bytes / row < 1 ? 1 : bytes / row < most ? bytes / row : most;
 }
@@ -322,9 +308,9 @@ template <typename T, int VEC, int NV, int TPR, bool LAYER>
 struct Forward {
     static constexpr int THREADS = RowThreads<TPR>::THREADS;
     static constexpr int COLS = NV * VEC;
-    static constexpr int PER_SM = (TPR == 1024 ? 1024 : COLS <= 8 ? 1024 : VEC == 1 || TPR == 512 || COLS > 16 || LAYER ? 512 : 768) / THREADS;
+    static constexpr int PER_SM = (TPR == 1024 ? 1024 : VEC == 1 ? 512 : COLS <= 8 ? 1024 : TPR == 512 || LAYER ? 512 : 768) / THREADS;
     // the vectors of an RMS norm stay in registers where a thread has few columns
-    static constexpr bool KEEP = !LAYER && VEC > 1 && COLS <= 16 && TPR < 1024;
+    static constexpr bool KEEP = COLS <= 16 && TPR < 1024;
     static constexpr int D = depth<T, NV, VEC, TPR>(16384, 3);
     using Fetch = Rows<T, VEC, NV, TPR, D>;
 };
@@ -360,7 +346,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
         cp_async_commit();
     }
     // z = yh wp + bp; a gate per channel is taken into both
-    F2 wp[N2], bp[LAYER ? N2 : 1], w[N2];
+    F2 wp[N2], bp[LAYER ? N2 : 1], w[N2], b[LAYER ? N2 : 1];
     auto vectors_post = [&] {
         if (!block) return;
         columns<VEC, NV, TPR>(a.post_w, 1.0f, d, t, wp);
@@ -377,6 +363,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
     if constexpr (KEEP) {
         vectors_post();
         columns<VEC, NV, TPR>(a.w, 1.0f, d, t, w);
+        if constexpr (LAYER) columns<VEC, NV, TPR>(a.b, 0.0f, d, t, b);
     }
     int slot = 0;
     for (; L::first(row) < a.R; row += step) {
@@ -388,7 +375,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
         float ym = 0.0f, yr = 1.0f, xm = 0.0f, xr = 1.0f, shift = 0.0f;
         if (block) {
             F2 y[N2];
-            fy.read(slot, row, there, y);
+            fy.read(slot, y);
             fy.issue(slot, next, next < a.R);
             cp_async_commit();
             if (post) row_stats<VEC, NV, TPR, LAYER>(y, d, t, inv_d, a.eps, scratch, turn, ym, shift, yr);
@@ -401,19 +388,19 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
             }
             cp_async_wait<2 * D - 1>();
             if (elem) {
-                fg.read(slot, row, there, v);
+                fg.read(slot, v);
                 fg.issue(slot, next, next < a.R);
 #pragma unroll
                 for (int k = 0; k < N2; ++k) y[k] = mul2(y[k], v[k]);
             }
-            fx.read(slot, row, there, v);
+            fx.read(slot, v);
 #pragma unroll
             for (int k = 0; k < N2; ++k) v[k] = fma2(v[k], al2, y[k]);
             if (there) put<T, VEC, NV, TPR>(p.out + row * d, d, t, v);
         } else {
             cp_async_commit();
             cp_async_wait<2 * D - 1>();
-            fx.read(slot, row, there, v);
+            fx.read(slot, v);
         }
         fx.issue(slot, next, next < a.R);
         cp_async_commit();
@@ -423,8 +410,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
             if constexpr (!KEEP) columns<VEC, NV, TPR>(a.w, 1.0f, d, t, w);
             const F2 sh2 = f2(shift, shift), r2 = f2(xr, xr);
             if constexpr (LAYER) {
-                F2 b[N2];
-                columns<VEC, NV, TPR>(a.b, 0.0f, d, t, b);
+                if constexpr (!KEEP) columns<VEC, NV, TPR>(a.b, 0.0f, d, t, b);
 #pragma unroll
                 for (int k = 0; k < N2; ++k) v[k] = fma2(mul2(add2(v[k], sh2), r2), w[k], b[k]);
             } else {
@@ -445,10 +431,12 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
 }
 
 // Threads per row of the backward at width d, and CTAs of them on an SM.
-constexpr int bwd_threads(int d) {
+// (Single elements: 8 columns a thread.)
+constexpr int bwd_threads(int d, bool vec) {
+    if (!vec) return d <= 8 * 8 ? 8 : d <= 32 * 8 ? 32 : d <= 64 * 8 ? 64 : d <= 128 * 8 ? 128 : d <= 192 * 8 ? 192 : d <= 256 * 8 ? 256 : d <= 512 * 8 ? 512 : 1024;
     return d <= 8 * 8 ? 8 : d <= 16 * 8 ? 16 : d <= 32 * 16 ? 32 : d <= 96 * 8 ? 96 : d <= 128 * 16 ? 128 : d <= 256 * 16 ? 256 : d <= 384 * 16 ? 384 : 512;
 }
-constexpr int bwd_per_sm(int tpr) { return 512 / (tpr <= 32 ? 128 : tpr); }
+constexpr int bwd_per_sm(int tpr) { return tpr > 512 ? 1 : 512 / (tpr <= 32 ? 128 : tpr); }
 
 template <typename T, int VEC, int NV, int TPR>
 struct Backward {
@@ -529,10 +517,10 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         };
         // u: xh, v: h, then t
         if (norm) {
-            fx.read(slot, row, there, u);
+            fx.read(slot, u);
             gone(u);
             fx.issue(slot, next, more);
-            fn.read(slot, row, there, v);
+            fn.read(slot, v);
             gone(v);
             fn.issue(slot, next, more);
             cp_async_commit();
@@ -563,7 +551,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         }
         cp_async_wait<2 * D - 1>();
         if (stream) {
-            fo.read(slot, row, there, u);
+            fo.read(slot, u);
             gone(u);
             fo.issue(slot, next, more);
 #pragma unroll
@@ -577,7 +565,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         }
         if (block) {
             // u: yh, v: t, t g, k, dy
-            fy.read(slot, row, there, u);
+            fy.read(slot, u);
             gone(u);
             fy.issue(slot, next, more);
             if (post) {
@@ -598,7 +586,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
                     }
                     if (there) put<T, VEC, NV, TPR>(p.dgate + row * d, d, t, z);
                 }
-                fg.read(slot, row, there, z);
+                fg.read(slot, z);
                 fg.issue(slot, next, more);
 #pragma unroll
                 for (int k = 0; k < N2; ++k) v[k] = mul2(v[k], z[k]);
@@ -707,12 +695,21 @@ cudaError_t fwd_v(const BlockNormArgs& a, cudaStream_t s) {
     const int d = a.d;
     if (d <= 8 * 8) return fwd_k<T, VEC, 8 / VEC, 8, LAYER>(a, s);
     if (d <= 32 * 8) return fwd_k<T, VEC, 8 / VEC, 32, LAYER>(a, s);
-    if (d <= 32 * 16) return fwd_k<T, VEC, 16 / VEC, 32, LAYER>(a, s);
-    if (d <= 128 * 8) return fwd_k<T, VEC, 8 / VEC, 128, LAYER>(a, s);
-    if (d <= 128 * 16) return fwd_k<T, VEC, 16 / VEC, 128, LAYER>(a, s);
-    if (d <= 256 * 16) return fwd_k<T, VEC, 16 / VEC, 256, LAYER>(a, s);
-    if (d <= 384 * 16) return fwd_k<T, VEC, 16 / VEC, 384, LAYER>(a, s);
-    if (d <= 512 * 16) return fwd_k<T, VEC, 16 / VEC, 512, LAYER>(a, s);
+    if constexpr (VEC == 1) {  // 8 columns a thread: what a row needs, its vectors too, stays in registers
+        if (d <= 64 * 8) return fwd_k<T, 1, 8, 64, LAYER>(a, s);
+        if (d <= 128 * 8) return fwd_k<T, 1, 8, 128, LAYER>(a, s);
+        if (d <= 192 * 8) return fwd_k<T, 1, 8, 192, LAYER>(a, s);
+        if (d <= 256 * 8) return fwd_k<T, 1, 8, 256, LAYER>(a, s);
+        if (d <= 512 * 8) return fwd_k<T, 1, 8, 512, LAYER>(a, s);
+        if (d <= 1024 * 8) return fwd_k<T, 1, 8, 1024, LAYER>(a, s);
+    } else {
+        if (d <= 32 * 16) return fwd_k<T, VEC, 16 / VEC, 32, LAYER>(a, s);
+        if (d <= 128 * 8) return fwd_k<T, VEC, 8 / VEC, 128, LAYER>(a, s);
+        if (d <= 128 * 16) return fwd_k<T, VEC, 16 / VEC, 128, LAYER>(a, s);
+        if (d <= 256 * 16) return fwd_k<T, VEC, 16 / VEC, 256, LAYER>(a, s);
+        if (d <= 384 * 16) return fwd_k<T, VEC, 16 / VEC, 384, LAYER>(a, s);
+        if (d <= 512 * 16) return fwd_k<T, VEC, 16 / VEC, 512, LAYER>(a, s);
+    }
     return fwd_k<T, VEC, 16 / VEC, 1024, LAYER>(a, s);
 }
 
@@ -725,9 +722,9 @@ cudaError_t fwd_t(const BlockNormArgs& a, cudaStream_t s) {
     return a.layer ? fwd_v<T, 1, true>(a, s) : fwd_v<T, 1, false>(a, s);
 }
 
-int bwd_parts(int R, int d) {
+int bwd_parts(int R, int d, bool vec) {
     if (d > BWD_MAX_D) return R < LONG_PARTS ? R : LONG_PARTS;
-    const int t = bwd_threads(d);
+    const int t = bwd_threads(d, vec);
     return grid_rows(R, t <= 32 ? 128 / t : 1, bwd_per_sm(t));
 }
 
@@ -742,26 +739,40 @@ cudaError_t bwd_k(const BlockNormArgs& a, int grid, float* part, cudaStream_t s)
 
 template <typename T, int VEC, bool LAYER>
 cudaError_t bwd_v(const BlockNormArgs& a, int n, float* part, cudaStream_t s) {
-    switch (bwd_threads(a.d)) {
-        case 8: return bwd_k<T, VEC, 8 / VEC, 8, LAYER>(a, n, part, s);
-        case 16: return bwd_k<T, VEC, 8 / VEC, 16, LAYER>(a, n, part, s);
-        case 32:
-            if (a.d <= 32 * 8) return bwd_k<T, VEC, 8 / VEC, 32, LAYER>(a, n, part, s);
-            return bwd_k<T, VEC, 16 / VEC, 32, LAYER>(a, n, part, s);
-        case 96: return bwd_k<T, VEC, 8 / VEC, 96, LAYER>(a, n, part, s);
-        case 128:
-            if (a.d <= 128 * 8) return bwd_k<T, VEC, 8 / VEC, 128, LAYER>(a, n, part, s);
-            return bwd_k<T, VEC, 16 / VEC, 128, LAYER>(a, n, part, s);
-        case 256: return bwd_k<T, VEC, 16 / VEC, 256, LAYER>(a, n, part, s);
-        case 384: return bwd_k<T, VEC, 16 / VEC, 384, LAYER>(a, n, part, s);
-        default: return bwd_k<T, VEC, 16 / VEC, 512, LAYER>(a, n, part, s);
+    if constexpr (VEC == 1) {
+        switch (bwd_threads(a.d, false)) {
+            case 8: return bwd_k<T, 1, 8, 8, LAYER>(a, n, part, s);
+            case 32: return bwd_k<T, 1, 8, 32, LAYER>(a, n, part, s);
+            case 64: return bwd_k<T, 1, 8, 64, LAYER>(a, n, part, s);
+            case 128: return bwd_k<T, 1, 8, 128, LAYER>(a, n, part, s);
+            case 192: return bwd_k<T, 1, 8, 192, LAYER>(a, n, part, s);
+            case 256: return bwd_k<T, 1, 8, 256, LAYER>(a, n, part, s);
+            case 512: return bwd_k<T, 1, 8, 512, LAYER>(a, n, part, s);
+            default: return bwd_k<T, 1, 8, 1024, LAYER>(a, n, part, s);
+        }
+    } else {
+        switch (bwd_threads(a.d, true)) {
+            case 8: return bwd_k<T, VEC, 8 / VEC, 8, LAYER>(a, n, part, s);
+            case 16: return bwd_k<T, VEC, 8 / VEC, 16, LAYER>(a, n, part, s);
+            case 32:
+                if (a.d <= 32 * 8) return bwd_k<T, VEC, 8 / VEC, 32, LAYER>(a, n, part, s);
+                return bwd_k<T, VEC, 16 / VEC, 32, LAYER>(a, n, part, s);
+            case 96: return bwd_k<T, VEC, 8 / VEC, 96, LAYER>(a, n, part, s);
+            case 128:
+                if (a.d <= 128 * 8) return bwd_k<T, VEC, 8 / VEC, 128, LAYER>(a, n, part, s);
+                return bwd_k<T, VEC, 16 / VEC, 128, LAYER>(a, n, part, s);
+            case 256: return bwd_k<T, VEC, 16 / VEC, 256, LAYER>(a, n, part, s);
+            case 384: return bwd_k<T, VEC, 16 / VEC, 384, LAYER>(a, n, part, s);
+            default: return bwd_k<T, VEC, 16 / VEC, 512, LAYER>(a, n, part, s);
+        }
     }
 }
 
 template <typename T>
 cudaError_t bwd_t(const BlockNormArgs& a, float* ws, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
-    const int n = bwd_parts(a.R, a.d);
+    const bool vec = all_vec(a, sizeof(T));
+    const int n = bwd_parts(a.R, a.d, vec);
     cudaError_t e;
     if (a.d > BWD_MAX_D) {
         float* m12 = ws == nullptr ? nullptr : ws + static_cast<long long>(n) * (a.layer ? 4 : 2) * a.d;
@@ -769,7 +780,7 @@ cudaError_t bwd_t(const BlockNormArgs& a, float* ws, cudaStream_t s) {
         if (e == cudaSuccess && ws != nullptr)
             e = launch_pdl(block_norm_bwd_cols_kernel<T>, dim3((a.d + 255) / 256, n), dim3(256), 0, s, a, io_of<T>(a),
                            static_cast<const float*>(m12), ws);
-    } else if (all_vec(a, sizeof(T))) {
+    } else if (vec) {
         e = a.layer ? bwd_v<T, V, true>(a, n, ws, s) : bwd_v<T, V, false>(a, n, ws, s);
     } else {
         e = a.layer ? bwd_v<T, 1, true>(a, n, ws, s) : bwd_v<T, 1, false>(a, n, ws, s);
