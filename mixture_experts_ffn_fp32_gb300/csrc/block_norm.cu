@@ -66,7 +66,7 @@ cudaError_t launch_block_norm_params(const BlockNormArgs& a, int n, const float*
 
 size_t block_norm_bwd_floats(int R, int d, bool layer) {
     // whichever the operands' alignment lets it take
-    return static_cast<size_t>(std::max(bwd_parts(R, d, true), bwd_parts(R, d, false))) * (layer ? 4 : 2) * d + (d > BWD_MAX_D ? 2 * static_cast<size_t>(R) : 0);
+    return static_cast<size_t>(std::max({bwd_parts(R, d, BWD_SINGLE), bwd_parts(R, d, BWD_8), bwd_parts(R, d, BWD_16)})) * (layer ? 4 : 2) * d + (d > BWD_MAX_D ? 2 * static_cast<size_t>(R) : 0);
 }
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {

@@ -284,25 +284,12 @@ MOE_DEV void row_stats(F2 (&v)[NV * VEC / 2], int d, int t, float inv_d, float e
     }
 }
 
-// A thread's columns of the rows of one operand, D rows ahead in shared memory (RowFetch);
-// elements that cp.async cannot move wait in registers, one row ahead.
-template <typename T, int VEC, int NV, int TPR, int D>
-struct Rows {
-    using F = RowFetch<T, VEC, NV, TPR, RowThreads<TPR>::THREADS, D>;
-    static constexpr int SMEM = F::SMEM;
-    F f;
-    MOE_DEV void init(void* smem, const T* base, long long pitch, int d, int t) { f.init(smem, base, pitch, d, t); }
-    MOE_DEV void issue(int s, long long row, bool there) { f.issue(s, row, there); }
-    // The row in slot s as pairs, zeros past its end.
-    MOE_DEV void read(int s, F2 (&p)[NV * VEC / 2]) const { f.pairs(s, p); }
-};
-// Rows ahead: what fills `bytes` a CTA and operand, at most `most`.
-template <typename T, int NV, int VEC, int TPR>
-constexpr int depth(int bytes, int most) {
-    if (VEC * sizeof(T) < 4) return 1;
-    const int row = NV * VEC * static_cast<int>(sizeof(T)) * RowThreads<TPR>::THREADS;
-    return bytes / row < 1 ? 1 : bytes / row < most ? bytes / row : most;
-}
+// A thread's columns of one operand's next row, under way while it works on this one: in
+// shared memory (RowFetch), or in registers where elements are too short for cp.async. One row
+// ahead is enough, and what more shared memory would take from L1 is missed there by the
+// vectors (backward of 16384 x 2048 BF16: 86 us one row ahead, 146 two; forward 43, 49).
+template <typename T, int VEC, int NV, int TPR>
+using Ahead = RowFetch<T, VEC, NV, TPR, RowThreads<TPR>::THREADS, 1>;
 
 template <typename T, int VEC, int NV, int TPR, bool LAYER>
 struct Forward {
@@ -311,8 +298,7 @@ struct Forward {
     static constexpr int PER_SM = (TPR == 1024 ? 1024 : VEC == 1 ? 512 : COLS <= 8 ? 1024 : TPR == 512 || LAYER ? 512 : 768) / THREADS;
     // the vectors of an RMS norm stay in registers where a thread has few columns
     static constexpr bool KEEP = COLS <= 16 && TPR < 1024;
-    static constexpr int D = depth<T, NV, VEC, TPR>(16384, 3);
-    using Fetch = Rows<T, VEC, NV, TPR, D>;
+    using Fetch = Ahead<T, VEC, NV, TPR>;
 };
 
 template <typename T, int VEC, int NV, int TPR, bool LAYER>
@@ -320,7 +306,7 @@ __global__ void __launch_bounds__(Forward<T, VEC, NV, TPR, LAYER>::THREADS, Forw
 block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant__ Io<T> p) {
     using F = typename Forward<T, VEC, NV, TPR, LAYER>::Fetch;
     using L = RowThreads<TPR>;
-    constexpr int D = Forward<T, VEC, NV, TPR, LAYER>::D, N2 = NV * VEC / 2;
+    constexpr int N2 = NV * VEC / 2;
     constexpr bool KEEP = Forward<T, VEC, NV, TPR, LAYER>::KEEP;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float4 scratch[TPR > 32 ? 2 * (TPR / 32) : 1];
@@ -336,15 +322,11 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
     fx.init(smem, p.x, a.x_stride, d, t);
     fy.init(smem + F::SMEM, p.y, a.y_stride, d, t);
     fg.init(smem + 2 * F::SMEM, p.g, a.gate_stride, d, t);
-#pragma unroll
-    for (int s = 0; s < D; ++s) {
-        const long long r = row + s * step;
-        if (block) fy.issue(s, r, r < a.R);
-        cp_async_commit();
-        fx.issue(s, r, r < a.R);
-        if (elem) fg.issue(s, r, r < a.R);
-        cp_async_commit();
-    }
+    if (block) fy.issue(0, row, row < a.R);
+    cp_async_commit();
+    fx.issue(0, row, row < a.R);
+    if (elem) fg.issue(0, row, row < a.R);
+    cp_async_commit();
     // z = yh wp + bp; a gate per channel is taken into both
     F2 wp[N2], bp[LAYER ? N2 : 1], w[N2], b[LAYER ? N2 : 1];
     auto vectors_post = [&] {
@@ -365,18 +347,17 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
         columns<VEC, NV, TPR>(a.w, 1.0f, d, t, w);
         if constexpr (LAYER) columns<VEC, NV, TPR>(a.b, 0.0f, d, t, b);
     }
-    int slot = 0;
     for (; L::first(row) < a.R; row += step) {
         // y and the rest travel in groups of their own: each has a whole row's time
-        cp_async_wait<2 * D - 1>();
+        cp_async_wait<1>();
         const bool there = row < a.R;
-        const long long next = row + D * step;
+        const long long next = row + step;
         F2 v[N2];
         float ym = 0.0f, yr = 1.0f, xm = 0.0f, xr = 1.0f, shift = 0.0f;
         if (block) {
             F2 y[N2];
-            fy.read(slot, y);
-            fy.issue(slot, next, next < a.R);
+            fy.pairs(0, y);
+            fy.issue(0, next, next < a.R);
             cp_async_commit();
             if (post) row_stats<VEC, NV, TPR, LAYER>(y, d, t, inv_d, a.eps, scratch, turn, ym, shift, yr);
             if constexpr (!KEEP) vectors_post();
@@ -386,25 +367,24 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
                 if constexpr (LAYER) y[k] = fma2(mul2(add2(y[k], sh2), r2), wp[k], bp[k]);
                 else y[k] = mul2(mul2(y[k], r2), wp[k]);
             }
-            cp_async_wait<2 * D - 1>();
+            cp_async_wait<1>();
             if (elem) {
-                fg.read(slot, v);
-                fg.issue(slot, next, next < a.R);
+                fg.pairs(0, v);
+                fg.issue(0, next, next < a.R);
 #pragma unroll
                 for (int k = 0; k < N2; ++k) y[k] = mul2(y[k], v[k]);
             }
-            fx.read(slot, v);
+            fx.pairs(0, v);
 #pragma unroll
             for (int k = 0; k < N2; ++k) v[k] = fma2(v[k], al2, y[k]);
             if (there) put<T, VEC, NV, TPR>(p.out + row * d, d, t, v);
         } else {
             cp_async_commit();
-            cp_async_wait<2 * D - 1>();
-            fx.read(slot, v);
+            cp_async_wait<1>();
+            fx.pairs(0, v);
         }
-        fx.issue(slot, next, next < a.R);
+        fx.issue(0, next, next < a.R);
         cp_async_commit();
-        if (++slot == D) slot = 0;
         if (norm) {
             row_stats<VEC, NV, TPR, LAYER>(v, d, t, inv_d, a.eps, scratch, turn, xm, shift, xr);
             if constexpr (!KEEP) columns<VEC, NV, TPR>(a.w, 1.0f, d, t, w);
@@ -431,9 +411,14 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant
 }
 
 // Threads per row of the backward at width d, and CTAs of them on an SM.
-// (Single elements: 8 columns a thread.)
-constexpr int bwd_threads(int d, bool vec) {
-    if (!vec) return d <= 8 * 8 ? 8 : d <= 32 * 8 ? 32 : d <= 64 * 8 ? 64 : d <= 128 * 8 ? 128 : d <= 192 * 8 ? 192 : d <= 256 * 8 ? 256 : d <= 512 * 8 ? 512 : 1024;
+// 16 columns a thread where the sums and what a row needs fit the registers: RMS of 16-bit types
+// in vectors; else 8 (us, 16 : 8 columns, 100 to 200 MB: RMS, BF16, 8192 x 4096, 86 : 98, 65536 x 512,
+// 69 : 89; layer, BF16, 8192 x 4096, 127 : 117, 65536 x 512, 109 : 102; layer, FP32, 8192 x 2048, 102 :
+// 77). Single elements past 4096 columns: 1024 threads, else 16 columns.
+enum BwdShape { BWD_SINGLE, BWD_8, BWD_16 };
+constexpr int bwd_threads(int d, BwdShape shape) {
+    if (shape != BWD_16)
+        return d <= 8 * 8 ? 8 : d <= 32 * 8 ? 32 : d <= 64 * 8 ? 64 : d <= 96 * 8 ? 96 : d <= 128 * 8 ? 128 : d <= 192 * 8 ? 192 : d <= 256 * 8 ? 256 : d <= 512 * 8 || shape == BWD_8 ? 512 : 1024;
     return d <= 8 * 8 ? 8 : d <= 16 * 8 ? 16 : d <= 32 * 16 ? 32 : d <= 96 * 8 ? 96 : d <= 128 * 16 ? 128 : d <= 256 * 16 ? 256 : d <= 384 * 16 ? 384 : 512;
 }
 constexpr int bwd_per_sm(int tpr) { return tpr > 512 ? 1 : 512 / (tpr <= 32 ? 128 : tpr); }
@@ -441,8 +426,7 @@ constexpr int bwd_per_sm(int tpr) { return tpr > 512 ? 1 : 512 / (tpr <= 32 ? 12
 template <typename T, int VEC, int NV, int TPR>
 struct Backward {
     static constexpr int THREADS = RowThreads<TPR>::THREADS;
-    static constexpr int D = depth<T, NV, VEC, TPR>(8192, 4);
-    using Fetch = Rows<T, VEC, NV, TPR, D>;
+    using Fetch = Ahead<T, VEC, NV, TPR>;
 };
 
 // A CTA walks rows and keeps its threads' columns of the sums in registers;
@@ -452,7 +436,7 @@ __global__ void __launch_bounds__(Backward<T, VEC, NV, TPR>::THREADS, bwd_per_sm
 block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_constant__ Io<T> p, float* __restrict__ part) {
     using F = typename Backward<T, VEC, NV, TPR>::Fetch;
     using L = RowThreads<TPR>;
-    constexpr int D = Backward<T, VEC, NV, TPR>::D, N2 = NV * VEC / 2, NS = LAYER ? 4 : 2;
+    constexpr int N2 = NV * VEC / 2, NS = LAYER ? 4 : 2;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float scratch[TPR > 32 ? 4 * (TPR / 32) : 1];
     __shared__ float gather[TPR <= 32 ? NV * VEC * TPR : 1];
@@ -476,19 +460,15 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
     fo.init(smem + 2 * F::SMEM, p.dxo, a.dxo_stride, d, t);
     fy.init(smem + 3 * F::SMEM, p.y, a.y_stride, d, t);
     fg.init(smem + 4 * F::SMEM, p.g, a.gate_stride, d, t);
-#pragma unroll
-    for (int s = 0; s < D; ++s) {
-        const long long r = row + s * step;
-        if (norm) {
-            fx.issue(s, r, r < a.R);
-            fn.issue(s, r, r < a.R);
-        }
-        cp_async_commit();
-        if (stream) fo.issue(s, r, r < a.R);
-        if (block) fy.issue(s, r, r < a.R);
-        if (elem) fg.issue(s, r, r < a.R);
-        cp_async_commit();
+    if (norm) {
+        fx.issue(0, row, row < a.R);
+        fn.issue(0, row, row < a.R);
     }
+    cp_async_commit();
+    if (stream) fo.issue(0, row, row < a.R);
+    if (block) fy.issue(0, row, row < a.R);
+    if (elem) fg.issue(0, row, row < a.R);
+    cp_async_commit();
     float ym = 0.0f, yr = 1.0f, xm = 0.0f, xr = 1.0f;  // of the next row
     auto statistics = [&](long long r) {
         if (r >= a.R) return;
@@ -499,12 +479,11 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         if (norm) xr = __ldg(stat(a, 3, i));
     };
     statistics(row);
-    int slot = 0;
     for (; L::first(row) < a.R; row += step) {
         const bool there = row < a.R;
-        const long long next = row + D * step;
+        const long long next = row + step;
         const bool more = next < a.R;
-        cp_async_wait<2 * D - 1>();  // two groups a row, as in the forward
+        cp_async_wait<1>();  // two groups a row, as in the forward
         const float ymc = ym, yrc = yr, xmc = xm, xrc = xr;
         statistics(row + step);
         F2 u[N2], v[N2];
@@ -517,12 +496,12 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         };
         // u: xh, v: h, then t
         if (norm) {
-            fx.read(slot, u);
+            fx.pairs(0, u);
             gone(u);
-            fx.issue(slot, next, more);
-            fn.read(slot, v);
+            fx.issue(0, next, more);
+            fn.pairs(0, v);
             gone(v);
-            fn.issue(slot, next, more);
+            fn.issue(0, next, more);
             cp_async_commit();
             const F2 nm = f2(-xmc, -xmc), r2 = f2(xrc, xrc);
             F2 a1 = f2(0.0f, 0.0f), a2 = a1;
@@ -549,11 +528,11 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         } else {
             cp_async_commit();
         }
-        cp_async_wait<2 * D - 1>();
+        cp_async_wait<1>();
         if (stream) {
-            fo.read(slot, u);
+            fo.pairs(0, u);
             gone(u);
-            fo.issue(slot, next, more);
+            fo.issue(0, next, more);
 #pragma unroll
             for (int k = 0; k < N2; ++k) v[k] = norm ? add2(v[k], u[k]) : u[k];
         }
@@ -565,9 +544,9 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         }
         if (block) {
             // u: yh, v: t, t g, k, dy
-            fy.read(slot, u);
+            fy.pairs(0, u);
             gone(u);
-            fy.issue(slot, next, more);
+            fy.issue(0, next, more);
             if (post) {
                 const F2 nm = f2(-ymc, -ymc), r2 = f2(yrc, yrc);
 #pragma unroll
@@ -586,8 +565,8 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
                     }
                     if (there) put<T, VEC, NV, TPR>(p.dgate + row * d, d, t, z);
                 }
-                fg.read(slot, z);
-                fg.issue(slot, next, more);
+                fg.pairs(0, z);
+                fg.issue(0, next, more);
 #pragma unroll
                 for (int k = 0; k < N2; ++k) v[k] = mul2(v[k], z[k]);
             }
@@ -623,7 +602,6 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
             if (there) put<T, VEC, NV, TPR>(p.dy + row * d, d, t, v);
         }
         cp_async_commit();
-        if (++slot == D) slot = 0;
     }
     if (part == nullptr) return;
     float* out = part + static_cast<long long>(blockIdx.x) * NS * d;
@@ -722,9 +700,9 @@ cudaError_t fwd_t(const BlockNormArgs& a, cudaStream_t s) {
     return a.layer ? fwd_v<T, 1, true>(a, s) : fwd_v<T, 1, false>(a, s);
 }
 
-int bwd_parts(int R, int d, bool vec) {
+int bwd_parts(int R, int d, BwdShape shape) {
     if (d > BWD_MAX_D) return R < LONG_PARTS ? R : LONG_PARTS;
-    const int t = bwd_threads(d, vec);
+    const int t = bwd_threads(d, shape);
     return grid_rows(R, t <= 32 ? 128 / t : 1, bwd_per_sm(t));
 }
 
@@ -737,21 +715,11 @@ cudaError_t bwd_k(const BlockNormArgs& a, int grid, float* part, cudaStream_t s)
     return launch_pdl(block_norm_bwd_kernel<T, VEC, NV, TPR, LAYER>, dim3(grid), dim3(C::THREADS), smem, s, a, io_of<T>(a), part);
 }
 
-template <typename T, int VEC, bool LAYER>
-cudaError_t bwd_v(const BlockNormArgs& a, int n, float* part, cudaStream_t s) {
-    if constexpr (VEC == 1) {
-        switch (bwd_threads(a.d, false)) {
-            case 8: return bwd_k<T, 1, 8, 8, LAYER>(a, n, part, s);
-            case 32: return bwd_k<T, 1, 8, 32, LAYER>(a, n, part, s);
-            case 64: return bwd_k<T, 1, 8, 64, LAYER>(a, n, part, s);
-            case 128: return bwd_k<T, 1, 8, 128, LAYER>(a, n, part, s);
-            case 192: return bwd_k<T, 1, 8, 192, LAYER>(a, n, part, s);
-            case 256: return bwd_k<T, 1, 8, 256, LAYER>(a, n, part, s);
-            case 512: return bwd_k<T, 1, 8, 512, LAYER>(a, n, part, s);
-            default: return bwd_k<T, 1, 8, 1024, LAYER>(a, n, part, s);
-        }
-    } else {
-        switch (bwd_threads(a.d, true)) {
+template <typename T, int VEC, bool LAYER, BwdShape SHAPE>
+cudaError_t bwd_v(const BlockNormArgs& a, float* part, cudaStream_t s) {
+    const int n = bwd_parts(a.R, a.d, SHAPE);
+    if constexpr (SHAPE == BWD_16) {
+        switch (bwd_threads(a.d, SHAPE)) {
             case 8: return bwd_k<T, VEC, 8 / VEC, 8, LAYER>(a, n, part, s);
             case 16: return bwd_k<T, VEC, 8 / VEC, 16, LAYER>(a, n, part, s);
             case 32:
@@ -765,14 +733,32 @@ cudaError_t bwd_v(const BlockNormArgs& a, int n, float* part, cudaStream_t s) {
             case 384: return bwd_k<T, VEC, 16 / VEC, 384, LAYER>(a, n, part, s);
             default: return bwd_k<T, VEC, 16 / VEC, 512, LAYER>(a, n, part, s);
         }
+    } else {
+        switch (bwd_threads(a.d, SHAPE)) {
+            case 8: return bwd_k<T, VEC, 8 / VEC, 8, LAYER>(a, n, part, s);
+            case 32: return bwd_k<T, VEC, 8 / VEC, 32, LAYER>(a, n, part, s);
+            case 64: return bwd_k<T, VEC, 8 / VEC, 64, LAYER>(a, n, part, s);
+            case 96: return bwd_k<T, VEC, 8 / VEC, 96, LAYER>(a, n, part, s);
+            case 128: return bwd_k<T, VEC, 8 / VEC, 128, LAYER>(a, n, part, s);
+            case 192: return bwd_k<T, VEC, 8 / VEC, 192, LAYER>(a, n, part, s);
+            case 256: return bwd_k<T, VEC, 8 / VEC, 256, LAYER>(a, n, part, s);
+            case 512:
+                if constexpr (SHAPE == BWD_8)
+                    if (a.d > 512 * 8) return bwd_k<T, VEC, 16 / VEC, 512, LAYER>(a, n, part, s);
+                return bwd_k<T, VEC, 8 / VEC, 512, LAYER>(a, n, part, s);
+            default:
+                if constexpr (SHAPE == BWD_SINGLE) return bwd_k<T, VEC, 8 / VEC, 1024, LAYER>(a, n, part, s);
+                return cudaErrorInvalidValue;  // no such number of threads
+        }
     }
 }
 
 template <typename T>
 cudaError_t bwd_t(const BlockNormArgs& a, float* ws, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
+    constexpr BwdShape RMS = sizeof(T) == 2 ? BWD_16 : BWD_8;
     const bool vec = all_vec(a, sizeof(T));
-    const int n = bwd_parts(a.R, a.d, vec);
+    const int n = bwd_parts(a.R, a.d, !vec ? BWD_SINGLE : a.layer ? BWD_8 : RMS);
     cudaError_t e;
     if (a.d > BWD_MAX_D) {
         float* m12 = ws == nullptr ? nullptr : ws + static_cast<long long>(n) * (a.layer ? 4 : 2) * a.d;
@@ -781,9 +767,9 @@ cudaError_t bwd_t(const BlockNormArgs& a, float* ws, cudaStream_t s) {
             e = launch_pdl(block_norm_bwd_cols_kernel<T>, dim3((a.d + 255) / 256, n), dim3(256), 0, s, a, io_of<T>(a),
                            static_cast<const float*>(m12), ws);
     } else if (vec) {
-        e = a.layer ? bwd_v<T, V, true>(a, n, ws, s) : bwd_v<T, V, false>(a, n, ws, s);
+        e = a.layer ? bwd_v<T, V, true, BWD_8>(a, ws, s) : bwd_v<T, V, false, RMS>(a, ws, s);
     } else {
-        e = a.layer ? bwd_v<T, 1, true>(a, n, ws, s) : bwd_v<T, 1, false>(a, n, ws, s);
+        e = a.layer ? bwd_v<T, 1, true, BWD_SINGLE>(a, ws, s) : bwd_v<T, 1, false, BWD_SINGLE>(a, ws, s);
     }
     if (e != cudaSuccess || ws == nullptr) return e;
     return launch_block_norm_params(a, n, ws, s);
