@@ -84,7 +84,7 @@ constexpr int STAGES = 3;
 
 template <typename T, int NP>
 __global__ void __launch_bounds__(THREADS, 2)
-adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int cols, unsigned long long timeout_ns) {
+adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int cols, int sums, unsigned long long timeout_ns) {
     constexpr bool SCALED = __is_same(T, __half);
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups g;
@@ -104,7 +104,7 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
         fence_mbarrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&tmem_slot), cols);
+        tmem_alloc(smem_u32(&tmem_slot), cols * sums);
         tmem_relinquish();
     }
     pdl_wait();
@@ -169,8 +169,8 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
                         const uint32_t at = sbase + stage * stage_bytes;
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            tc_mma_bf16(tmem, smem_desc_sw128(at + 32 * q, 16, 1024), smem_desc_sw128(at + BLOCK + 32 * q, 16, 1024),
-                                        idesc<T>(rp), kb > 0 || q > 0);
+                            tc_mma_bf16(tmem + kb % sums * cols, smem_desc_sw128(at + 32 * q, 16, 1024),
+                                        smem_desc_sw128(at + BLOCK + 32 * q, 16, 1024), idesc<T>(rp), kb >= sums || q > 0);
                         tc_commit(bar(stage));
                     }
                     __syncwarp();
@@ -189,16 +189,18 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
             alive = __syncthreads_and(alive);  // the stages are free
             const int row = 32 * (warp & 3) + lane;
             for (int c = 16 * (warp >> 2); c < rp; c += 32) {
-                uint32_t v[16];
-                tc_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
-                tc_wait_ld();
+                float f[16];
 #pragma unroll
-                for (int q = 0; q < 16; q += 4) {
-                    float f[4];
+                for (int i = 0; i < 16; ++i) f[i] = alive ? 0.0f : CUDART_NAN_F;
+                for (int o = 0; o < min(sums, n); ++o) {
+                    uint32_t v[16];
+                    tc_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + o * cols + c, v);
+                    tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = !alive ? CUDART_NAN_F : n == 0 ? 0.0f : __uint_as_float(v[q + i]);
-                    *reinterpret_cast<float4*>(part + row * rp + c + q) = make_float4(f[0], f[1], f[2], f[3]);
+                    for (int i = 0; i < 16; ++i) f[i] += __uint_as_float(v[i]);
                 }
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(part + row * rp + c + q) = make_float4(f[q], f[q + 1], f[q + 2], f[q + 3]);
             }
             tc_fence_before();
         }
@@ -254,7 +256,7 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
         alive = __syncthreads_and(alive);  // the accumulator and the stages are free
         tc_fence_after();
     }
-    if (warp == 1) tmem_dealloc(tmem, cols);
+    if (warp == 1) tmem_dealloc(tmem, cols * sums);
 }
 
 constexpr int COLS = 128;     // columns of a block
@@ -373,10 +375,10 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t d = tmem + (b & 1) * COLS, sb = sB + b % B_STAGES * b_bytes;
-                        for (int o = 0; o < NP; ++o)
+                        for (int o = NP - 1; o >= 0; --o)  // the small pieces first: what an addition drops grows with the sum
                             for (int ks = 0; ks < KS; ++ks)
                                 tc_mma_bf16(d, smem_desc_sw32(sA + (o * KS + ks) * STEP_BYTES), smem_desc_sw32(sb + ks * STEP_BYTES), idesc<T>(COLS),
-                                            o > 0 || ks > 0);
+                                            o < NP - 1 || ks > 0);
                         tc_commit(smem_u32(&bars[b & 1]));
                     }
                     __syncwarp();
@@ -447,8 +449,9 @@ cudaError_t shrink(AdapterArgs a, cudaStream_t s) {
     const int turns = static_cast<int>((tiles + clusters - 1) / clusters);
     int cols = 32;
     while (cols < a.rp) cols *= 2;
+    const int sums = std::min(4, 256 / cols);  // two CTAs share the 512 columns
     return launch_pdl_cluster(adapter_shrink_tc_kernel<T, NP>, dim3(static_cast<unsigned>(clusters * a.cluster)), dim3(THREADS), smem, s,
-                              a.cluster, a, turns, cols, static_cast<unsigned long long>(wait_timeout_ns()));
+                              a.cluster, a, turns, cols, sums, static_cast<unsigned long long>(wait_timeout_ns()));
 }
 
 template <typename T, typename O>
