@@ -641,11 +641,15 @@ int adapter_slices(int T, int d, int r, int E) {
     return static_cast<int>(std::max<long long>(1, std::min<long long>({16LL * num_sms() / units, d / 256, 16})));
 }
 
+// Rows of v in all slices, at most: no more for fewer rows, so that a workspace serves them too.
+// (A unit takes 4 rows or less, so T slices <= 64 SMs where there is more than one slice.)
+long long f32_rows(int T) { return std::max<long long>(T, std::min<long long>(16LL * T, 64LL * num_sms())); }
+
 }  // namespace
 
-size_t adapter_workspace(int T, int d, int r, int E, int dtype) {
+size_t adapter_workspace(int T, int r, int dtype) {
     const int rp = dtype == MOE_F32 ? (r + 3) / 4 * 4 : (r + 15) / 16 * 16;
-    if (dtype == MOE_F32) return 256 + static_cast<size_t>(T) * rp * 4 * adapter_slices(T, d, r, E);
+    if (dtype == MOE_F32) return 256 + static_cast<size_t>(f32_rows(T)) * rp * 4;
     return 256 + adapter_tc_workspace(T, rp);  // whichever form the call takes
 }
 

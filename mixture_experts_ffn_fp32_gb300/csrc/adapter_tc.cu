@@ -103,15 +103,17 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
         abort_flag = 0;
         fence_mbarrier_init();
     }
-    if (warp == 1) {
+    pdl_wait();
+    if (warp == 1) {  // held by no CTA that waits for another launch
         tmem_alloc(smem_u32(&tmem_slot), cols * sums);
         tmem_relinquish();
     }
-    pdl_wait();
-    pdl_trigger();
     tc_fence_before();
     const int tiles = group_table<ROWS>(a, false, g);
     tc_fence_after();
+    // Not before every CTA has its columns: those of the second launch allocate theirs before they
+    // wait for this one.
+    pdl_trigger();
     const uint32_t tmem = tmem_slot;
     const WaitCtx wc{a.err, &abort_flag, timeout_ns};
     const int steps = (a.d + 63) / 64, mine = (steps + C - 1) / C;

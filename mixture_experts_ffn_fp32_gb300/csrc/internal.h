@@ -606,7 +606,7 @@ struct AdapterArgs {
     void* vp;                // many rows: inner values in pieces [T, pieces, rp], FP16: their rows'
     float* back;             // inverse scales [T]
 };
-size_t adapter_workspace(int T, int d, int r, int E, int dtype);
+size_t adapter_workspace(int T, int r, int dtype);
 cudaError_t launch_adapter(const AdapterArgs& a, cudaStream_t s);
 // The tensor-core kernels of many rows: whether a call's operands suit them (rp set, up to
 // TC_RANKS), their workspace behind the error word, and the call.

@@ -377,7 +377,7 @@ MOE_API moe_status moe_adapter_add_workspace_size(const moe_adapter_config* cfg,
     if (!cfg || !bytes) return MOE_ERR_INVALID_ARG;
     const moe_status v = check_adapter(*cfg);
     if (v != MOE_OK) return v;
-    *bytes = cfg->T == 0 ? 0 : adapter_workspace(cfg->T, cfg->d, cfg->r, cfg->E, cfg->dtype);
+    *bytes = cfg->T == 0 ? 0 : adapter_workspace(cfg->T, cfg->r, cfg->dtype);
     return MOE_OK;
 }
 
@@ -398,7 +398,7 @@ MOE_API moe_status moe_adapter_add(const moe_adapter_config* cfg, const void* x,
         return MOE_ERR_INVALID_ARG;
     if (out == base && c.T > 1 && base_stride != out_stride) return MOE_ERR_INVALID_ARG;
     if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
-    if (ws_bytes < adapter_workspace(c.T, c.d, c.r, c.E, c.dtype)) return MOE_ERR_WORKSPACE;
+    if (ws_bytes < adapter_workspace(c.T, c.r, c.dtype)) return MOE_ERR_WORKSPACE;
     AdapterArgs g{};
     g.T = c.T; g.d = c.d; g.N = c.N; g.r = c.r; g.E = c.E; g.dtype = c.dtype; g.out_dtype = c.out_dtype;
     g.x = x; g.a = a; g.b = b; g.base = base;

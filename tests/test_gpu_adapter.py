@@ -199,3 +199,53 @@ def test_streams_and_graphs(A, form):
         torch.cuda.synchronize()
         assert torch.equal(out, A.adapter_add(**s))
         check(out, s)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_no_rows(A, dt):
+    s = make(0, 64, 96, 16, 3, DT[dt])
+    assert A.adapter_add(**s).shape == (0, 96)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_a_workspace_serves_fewer_rows(A, form, dt):
+    """One workspace, made for the largest call, for all smaller ones."""
+    ws = A.alloc_adapter_workspace(3000, 2048, 96, 16, 4, DT[dt])
+    for T in (3000, 1500, 700, 300, 90, 33, 7, 1):
+        s = make(T, 2048, 96, 16, 4, DT[dt])
+        check(A.adapter_add(**s, ws=ws), s)
+    assert A.workspace_status(ws) == A.MOE_OK
+
+
+def test_large_pitches(A, form):
+    """Offsets of rows past 32 bits."""
+    T, d, N = 70, 64, 64
+    pitch = (1 << 31) // 64
+    for T in (70, 1100):
+        s = make(T, d, N, 16, 3)
+        x = torch.empty(1, dtype=torch.bfloat16, device="cuda").new_empty(pitch * 70 + 64)
+        step = pitch * 70 // T // 8 * 8
+        s["x"] = torch.as_strided(x, (T, d), (step, 1)).copy_(s["x"])
+        check(A.adapter_add(**s), s)
+        y = x.new_empty(pitch * 70 + 64)
+        s["base"] = torch.as_strided(y, (T, N), (step, 1)).copy_(s["base"])
+        want = A.adapter_add(**s)
+        assert torch.equal(A.adapter_add(**s, out=s["base"]), want)
+        del x, y
+
+
+def test_two_calls_at_once(A, form):
+    """Calls on two streams, each with its own workspace."""
+    for T in (100, 2500):
+        cases = [make(T, 512, 640, 64, 5, seed=i) for i in range(2)]
+        want = [A.adapter_add(**s) for s in cases]
+        streams = [torch.cuda.Stream() for _ in cases]
+        for st in streams:
+            st.wait_stream(torch.cuda.current_stream())
+        got = [[], []]
+        for _ in range(10):
+            for i, (s, st) in enumerate(zip(cases, streams)):
+                got[i].append(A.adapter_add(**s, stream=st))
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(g, want[i]) for g in got[i])
