@@ -828,39 +828,60 @@ NORMS = {"layer": 0, "rms": 1}
 _GATE_NONE, _GATE_CHANNEL, _GATE_ELEMENT = range(3)
 
 
+def _vector(t, name, shape, here):
+    """_dev of an FP32 parameter, in one expression where it fits (a call has up to five)."""
+    if not (t.get_device() == here and t.dtype is torch.float32 and t.shape == shape and t.is_contiguous()):
+        _dev(t, torch.float32, name, shape, here)
+    return t.data_ptr()
+
+
+def _like(t, name, dtype, shape, here):
+    """_rows and _at of a tensor of x's type and shape; returns its address and pitch."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == here:
+        pitch, inner = t.stride()
+        if inner == 1 and pitch >= shape[1]:
+            return t.data_ptr(), pitch
+    pitch = _rows(t, name, dtype, shape)
+    _at(t, name, here)
+    return t.data_ptr(), pitch
+
+
 def _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here):
-    """The checks that both directions share: pitches of x, y and gate, the gate's shape and whether y is normalised."""
+    """What both directions check alike. Returns the number of post (0 or 1), the gate's
+    shape, and the addresses and pitches of x, y, gate, post_weight and post_bias."""
     if kind not in NORMS:
         raise ValueError(f"kind must be one of {sorted(NORMS)}, got {kind!r}")
     xs = _rows(x, "x")
     _at(x, "x", here)
-    d = x.size(1)
+    shape, dtype = x.shape, x.dtype
+    col = (shape[1],)
+    yp = gp = pw = pb = None
     ys = gs = 0
-    shape = _GATE_NONE
+    form = _GATE_NONE
     if y is None:
         if gate is not None:
             raise ValueError("a gate needs y")
         post = False
     else:
-        ys = _rows(y, "y", x.dtype, x.shape)
-        _at(y, "y", here)
+        yp, ys = _like(y, "y", dtype, shape, here)
         if gate is not None:
             if gate.dim() == 1:
-                shape = _GATE_CHANNEL
-                _dev(gate, torch.float32, "gate", (d,), here)
+                form = _GATE_CHANNEL
+                gp = _vector(gate, "gate", col, here)
             else:
-                shape = _GATE_ELEMENT
-                gs = _rows(gate, "gate", x.dtype, x.shape)
-                _at(gate, "gate", here)
-    if not post and (post_weight is not None or post_bias is not None):
-        raise ValueError("post_weight and post_bias need a norm of y")
+                form = _GATE_ELEMENT
+                gp, gs = _like(gate, "gate", dtype, shape, here)
     if post_weight is not None:
-        _dev(post_weight, torch.float32, "post_weight", (d,), here)
+        if not post:
+            raise ValueError("post_weight and post_bias need a norm of y")
+        pw = _vector(post_weight, "post_weight", col, here)
     if post_bias is not None:
+        if not post:
+            raise ValueError("post_weight and post_bias need a norm of y")
         if kind == "rms":
             raise ValueError("an RMS norm has no bias")
-        _dev(post_bias, torch.float32, "post_bias", (d,), here)
-    return xs, ys, gs, shape, 1 if post else 0
+        pb = _vector(post_bias, "post_bias", col, here)
+    return 1 if post else 0, form, (x.data_ptr(), xs, yp, ys, gp, gs, pw, pb)
 
 
 def block_norm(x: torch.Tensor, y=None, weight=None, bias=None, post_weight=None, post_bias=None, gate=None,
@@ -878,31 +899,35 @@ def block_norm(x: torch.Tensor, y=None, weight=None, bias=None, post_weight=None
     FP32 statistics that the backward takes. y None: n = Norm(x) alone, no x.
     norm=False: no norm follows, no n."""
     here = _here(stream)
-    xs, ys, gs, shape, post = _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here)
+    post, form, args = _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here)
     R, d = x.shape
-    if y is None and not norm:
-        raise ValueError("norm=False needs y")
-    if not norm and (weight is not None or bias is not None):
-        raise ValueError("weight and bias need a norm")
+    dtype = x.dtype
+    wp = bp = None
+    if not norm:
+        if y is None:
+            raise ValueError("norm=False needs y")
+        if weight is not None or bias is not None:
+            raise ValueError("weight and bias need a norm")
     if weight is not None:
-        _dev(weight, torch.float32, "weight", (d,), here)
+        wp = _vector(weight, "weight", (d,), here)
     if bias is not None:
         if kind == "rms":
             raise ValueError("an RMS norm has no bias")
-        _dev(bias, torch.float32, "bias", (d,), here)
-    cfg = _struct(BlockNormConfig, R, d, _DTYPES[x.dtype], NORMS[kind], post, shape, float(alpha), float(eps))
+        bp = _vector(bias, "bias", (d,), here)
+    cfg = _struct(BlockNormConfig, R, d, _DTYPES[dtype], NORMS[kind], post, form, float(alpha), float(eps))
     out = {}
+    xo = no = so = None
     with _on(stream, x, y, weight, bias, post_weight, post_bias, gate):
         if y is not None:
-            out["x"] = _empty(x.dtype, R, d)
+            out["x"] = t = _empty(dtype, R, d)
+            xo = t.data_ptr()
         if norm:
-            out["n"] = _empty(x.dtype, R, d)
+            out["n"] = t = _empty(dtype, R, d)
+            no = t.data_ptr()
         if stats:
-            out["stats"] = _empty(torch.float32, 2 if kind == "rms" else 4, R)
-        _check(lib().moe_block_norm(cfg, x.data_ptr(), xs, _ptr(y), ys, _ptr(gate), gs, _ptr(post_weight),
-                                    _ptr(post_bias), _ptr(weight), _ptr(bias), _ptr(out.get("x")),
-                                    _ptr(out.get("n")), _ptr(out.get("stats")), _raw_stream(stream, here)),
-               "moe_block_norm")
+            out["stats"] = t = _empty(torch.float32, 2 if kind == "rms" else 4, R)
+            so = t.data_ptr()
+        _check(lib().moe_block_norm(cfg, *args, wp, bp, xo, no, so, _raw_stream(stream, here)), "moe_block_norm")
     return out
 
 
@@ -927,47 +952,51 @@ def block_norm_backward(x: torch.Tensor, stats: torch.Tensor, y=None, dn=None, d
     and for layer norms dpost_bias and dbias. ws: uint8 of
     block_norm_backward_workspace_size(R, d, kind) bytes (allocated when None)."""
     here = _here(stream)
-    xs, ys, gs, shape, post = _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here)
-    R, d = x.shape
+    post, form, args = _block_norm_args(x, y, gate, post_weight, post_bias, kind, post, here)
+    shape, dtype = x.shape, x.dtype
+    R, d = shape
     layer = kind == "layer"
     if dn is None and dx is None:
         raise ValueError("dn or dx is required")
+    dnp = dxp = wp = None
     dns = dxs = 0
     if dn is not None:
-        dns = _rows(dn, "dn", x.dtype, x.shape)
-        _at(dn, "dn", here)
+        dnp, dns = _like(dn, "dn", dtype, shape, here)
     elif weight is not None:
         raise ValueError("weight needs dn")
     if dx is not None:
-        dxs = _rows(dx, "dx", x.dtype, x.shape)
-        _at(dx, "dx", here)
-    _dev(stats, torch.float32, "stats", (4 if layer else 2, R), here)
+        dxp, dxs = _like(dx, "dx", dtype, shape, here)
+    if stats is None:
+        raise ValueError("stats is required")
+    sp = _vector(stats, "stats", (4 if layer else 2, R), here)
     if weight is not None:
-        _dev(weight, torch.float32, "weight", (d,), here)
+        wp = _vector(weight, "weight", (d,), here)
     if ws is not None:
         _at(ws, "ws", here)
-    cfg = _struct(BlockNormConfig, R, d, _DTYPES[x.dtype], NORMS[kind], post, shape, float(alpha), 0.0)
-    out = {}
+    cfg = _struct(BlockNormConfig, R, d, _DTYPES[dtype], NORMS[kind], post, form, float(alpha), 0.0)
+    yo = go = None
+    vectors = [None] * 5  # addresses of dgate, dpost_weight, dpost_bias, dweight, dbias
     with _on(stream, x, stats, y, dn, dx, weight, post_weight, post_bias, gate, ws):
-        out["dx"] = _empty(x.dtype, R, d)
+        t = _empty(dtype, R, d)
+        out, xo = {"dx": t}, t.data_ptr()
         if y is not None:
-            out["dy"] = _empty(x.dtype, R, d)
-        if shape == _GATE_ELEMENT:
-            out["dgate"] = _empty(x.dtype, R, d)
+            out["dy"] = t = _empty(dtype, R, d)
+            yo = t.data_ptr()
+        if form == _GATE_ELEMENT:
+            out["dgate"] = t = _empty(dtype, R, d)
+            go = t.data_ptr()
         if weight_grads:
-            names = (["dgate"] if shape == _GATE_CHANNEL else []) + (["dpost_weight"] if post else []) + \
-                (["dpost_bias"] if post and layer else []) + (["dweight"] if dn is not None else []) + \
-                (["dbias"] if dn is not None and layer else [])
-            for name in names:
-                out[name] = _empty(torch.float32, d)
-            if names and ws is None:
+            for i, (there, name) in enumerate(((form == _GATE_CHANNEL, "dgate"), (post, "dpost_weight"),
+                                               (post and layer, "dpost_bias"), (dn is not None, "dweight"),
+                                               (dn is not None and layer, "dbias"))):
+                if there:
+                    out[name] = t = _empty_strided((d,), (1,), torch.float32)
+                    vectors[i] = t.data_ptr()
+            if ws is None and any(vectors):
                 ws = _empty(torch.uint8, block_norm_backward_workspace_size(R, d, kind))
         _check(lib().moe_block_norm_backward(
-            cfg, x.data_ptr(), xs, _ptr(y), ys, _ptr(gate), gs, _ptr(post_weight), _ptr(post_bias), _ptr(weight),
-            stats.data_ptr(), _ptr(dn), dns, _ptr(dx), dxs, out["dx"].data_ptr(), _ptr(out.get("dy")),
-            _ptr(out.get("dgate")), _ptr(out.get("dpost_weight")), _ptr(out.get("dpost_bias")),
-            _ptr(out.get("dweight")), _ptr(out.get("dbias")), _ptr(ws), 0 if ws is None else ws.numel(),
-            _raw_stream(stream, here)), "moe_block_norm_backward")
+            cfg, *args, wp, sp, dnp, dns, dxp, dxs, xo, yo, go if go is not None else vectors[0], *vectors[1:],
+            _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(stream, here)), "moe_block_norm_backward")
     return out
 
 
@@ -1009,40 +1038,38 @@ def adapter_add(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets
     xs = _rows(x, "x")
     _at(x, "x", here)
     T, d = x.shape
+    dtype = x.dtype
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError(f"a must be [E, r, d] and b [E, N, r], got {tuple(a.shape)} and {tuple(b.shape)}")
     E, N, r = b.shape
-    _dev(a, x.dtype, "a", (E, r, d), here)
-    _dev(b, x.dtype, "b", None, here)
+    _dev(a, dtype, "a", (E, r, d), here)
+    _dev(b, dtype, "b", None, here)
     _dev(offsets, torch.int32, "offsets", (E + 1,), here)
     if rows is not None:
         _dev(rows, torch.int32, "rows", (T,), here)
+    sp = bp = None
     if scale is not None:
-        _dev(scale, torch.float32, "scale", (E,), here)
+        sp = _vector(scale, "scale", (E,), here)
     like = base if base is not None else out if out is not None else x
-    if like.dtype != x.dtype and like.dtype != torch.float32:
-        raise ValueError(f"base and out must be {x.dtype} or float32, got {like.dtype}")
-    bs = 0
+    otype = like.dtype
+    if otype is not dtype and otype is not torch.float32:
+        raise ValueError(f"base and out must be {dtype} or float32, got {otype}")
+    bs, os_ = 0, N
     if base is not None:
-        bs = _rows(base, "base", None, (T, N))
-        _at(base, "base", here)
+        bp, bs = _like(base, "base", otype, (T, N), here)
     if out is not None:
-        os_ = _rows(out, "out", like.dtype, (T, N))
-        _at(out, "out", here)
-    else:
-        os_ = N
+        _, os_ = _like(out, "out", otype, (T, N), here)
     if ws is not None:
         _at(ws, "ws", here)
-    cfg = (T, d, N, r, E, _DTYPES[x.dtype], _DTYPES[like.dtype])
+    cfg = (T, d, N, r, E, _DTYPES[dtype], _DTYPES[otype])
     with _on(stream, base, x, a, b, offsets, rows, scale, out, ws):
         if ws is None:
             ws = _empty(torch.uint8, _adapter_ws(*cfg))
         if out is None:
-            out = _empty(like.dtype, T, N)
-        _check(lib().moe_adapter_add(_struct(AdapterConfig, *cfg), x.data_ptr(), xs, a.data_ptr(), b.data_ptr(),
-                                     _ptr(scale), offsets.data_ptr(), _ptr(rows), _ptr(base), bs, out.data_ptr(),
-                                     os_, ws.data_ptr(), ws.numel(), _raw_stream(stream, here)),
-               "moe_adapter_add")
+            out = _empty(otype, T, N)
+        _check(lib().moe_adapter_add(_struct(AdapterConfig, *cfg), x.data_ptr(), xs, a.data_ptr(), b.data_ptr(), sp,
+                                     offsets.data_ptr(), _ptr(rows), bp, bs, out.data_ptr(), os_, ws.data_ptr(),
+                                     ws.numel(), _raw_stream(stream, here)), "moe_adapter_add")
     return out
 
 
