@@ -217,26 +217,22 @@ MOE_DEV uint4 window(uint4 lo, uint4 hi, uint32_t s) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 8 elements from p, zeros from the n-th on; `before` elements of the row lie in front of p.
-// VEC: 16-byte aligned, n a multiple of 8. Else two aligned loads where both lie within the row.
-template <typename T, bool VEC>
+// 8 elements from p, zeros from the n-th on; `before` elements of the row lie in front of p. Two
+// aligned loads where both lie within the row.
+template <typename T>
 MOE_DEV uint4 load8(const T* p, int before, int n) {
-    if constexpr (VEC) {
-        return n > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-    } else {
-        const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
-        if (s == 0 ? n >= 8 : before >= 8 && n >= 16) {
-            const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - s);
-            const uint4 lo = __ldg(q);
-            return s == 0 ? lo : window(lo, __ldg(q + 1), s);
-        }
-        uint32_t w[4] = {0, 0, 0, 0};
-        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) w[i / 2] |= static_cast<uint32_t>(__ldg(q + i)) << (16 * (i & 1));
-        return make_uint4(w[0], w[1], w[2], w[3]);
+    const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+    if (s == 0 ? n >= 8 : before >= 8 && n >= 16) {
+        const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - s);
+        const uint4 lo = __ldg(q);
+        return s == 0 ? lo : window(lo, __ldg(q + 1), s);
     }
+    uint32_t w[4] = {0, 0, 0, 0};
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) w[i / 2] |= static_cast<uint32_t>(__ldg(q + i)) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // 4 elements from p, zeros from the n-th on; vec: 8-byte aligned, n a multiple of 4.
 template <typename T>
@@ -260,29 +256,35 @@ MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];
 //   out: CTA c takes the c-th part of N, a warp 32 columns at a time. Column 2 i + q of its
 //   instruction j stands for column 8 i + 2 j + q, so that a lane ends with 8 consecutive
 //   columns of its rows.
-// KB: steps of 16 ranks whose B is loaded at once, the next ones under way. From two steps on a
+// KB: steps of 16 ranks whose B is taken at once, the next ones under way. From two steps on a
 // lane's ranks are 8 consecutive ones of 32 (rp a multiple of 16 KB), else 4 of 16.
 // Every CTA makes the same number of turns, whatever the offsets: cluster barriers always pair.
 template <typename T, typename O, int MT, int NT, int KB, bool VEC>
 struct Fused {
     static constexpr int WARPS = THREADS / 32, ROWS = 16 * MT;
     static constexpr int NP = sizeof(O) == 4 ? 3 : 2;
-    // chunks of 32 of d a warp has in flight, as registers allow
-    static constexpr int U = 2 * MT + NT <= 4 ? 4 : 2 * MT + NT <= 6 ? 3 : 2;
+    // Chunks of 32 of d a warp has in flight: on their way to shared memory, each lane's fragments to
+    // its own 16-byte slots (two CTAs an SM leave 72 KB each), or, where rows are on no 16 bytes, to
+    // registers.
+    static constexpr int FRAGS = 2 * MT + NT, U = FRAGS <= 4 ? 4 : FRAGS <= 6 ? 3 : 2;
+    static constexpr int RING = VEC ? WARPS * U * FRAGS * 512 : 0;
+    // The same slots then take B: steps under way, of 16-byte slots each.
+    static constexpr int B_SLOTS = KB == 1 ? 2 : 2 * KB, B_STEPS = U * FRAGS / B_SLOTS < 8 ? U * FRAGS / B_SLOTS : 8;
     static constexpr int STAGE_OUT = VEC ? 0 : WARPS * 16 * 33 * 4;
-    static constexpr int RED0 = WARPS * MT * NT * 512, RED = RED0 > STAGE_OUT ? RED0 : STAGE_OUT;
-    static size_t smem(int rp) {  // [part][red, then the sums and the columns on their way out][pieces]
+    static constexpr int RED0 = WARPS * NT * 512, RED = RED0 > STAGE_OUT ? RED0 : STAGE_OUT;
+    static size_t smem(int rp) {  // [part][red, then the sums and the columns on their way out][pieces][slots]
         const int sums = ROWS * rp * 4;
-        return static_cast<size_t>(sums) + (RED > sums ? RED : sums) + static_cast<size_t>(rp / 16) * NP * MT * 512;
+        return static_cast<size_t>(sums) + (RED > sums ? RED : sums) + static_cast<size_t>(rp / 16) * NP * MT * 512 + RING;
     }
-    // two CTAs an SM below 110 KB
-    static constexpr int MOST = ROWS * 256 * 4 + (RED > ROWS * 1024 ? RED : ROWS * 1024) + 16 * NP * MT * 512;
+    static constexpr int MOST = ROWS * 256 * 4 + (RED > ROWS * 1024 ? RED : ROWS * 1024) + 16 * NP * MT * 512 + RING;
+    static_assert(MOST <= 220 << 10, "shared memory");
 };
 template <typename T, typename O, int MT, int NT, int KB, bool VEC>
 __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_constant__ AdapterArgs a, int turns) {
     using F = Fused<T, O, MT, NT, KB, VEC>;
     constexpr int WARPS = F::WARPS, ROWS = F::ROWS, NP = F::NP, U = F::U;
     constexpr bool SCALED = __is_same(T, __half);
+    constexpr int STEP = 32 * WARPS;
     constexpr bool AHEAD = VEC && KB == 1;  // the next columns' base too: where B takes few registers
     __shared__ Groups g;
     __shared__ int srow[ROWS];
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
     float* part = reinterpret_cast<float*>(smem);  // [ROWS][rp], this CTA's part of d
     float* red = part + ROWS * rp;                 // [WARPS][MT * NT * 4][32], then [ROWS][rp]
     uint4* frag = reinterpret_cast<uint4*>(red + (F::RED / 4 > ROWS * rp ? F::RED / 4 : ROWS * rp));  // [KS][NP][MT][32]
+    uint4* slots = frag + KS * NP * MT * 32 + (threadIdx.x >> 5) * (F::RING / WARPS / 16) + (threadIdx.x & 31);  // this lane's, 32 apart
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gi = lane >> 2, ti = lane & 3;
     const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int clusters = gridDim.x / C, id = blockIdx.x / C;
@@ -329,54 +332,142 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) row[m][h] = srow[16 * m + 8 * h + gi];
-            for (int j0 = 0; j0 < rp; j0 += 8 * NT) {
-                const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + j0 + gi) * a.d;
-                float acc[MT][NT][4] = {};
-                uint4 fx[U][MT][2], fa[U][NT];
-                auto load = [&](int c, int k) {
-                    const int at = k + 8 * ti, n = k1 - at;
+            const int first = k0 + 32 * w, chunks = first < k1 ? (k1 - first + 32 * WARPS - 1) / (32 * WARPS) : 0;
+            const int passes = (rp + 8 * NT - 1) / (8 * NT);
+            // VEC: chunk after chunk, pass after pass, on their way to the slots
+            int ip = 0, iq = 0, is = 0;
+            auto issue = [&] {
+                if (ip < passes && iq < chunks) {
+                    const int at = first + 32 * WARPS * iq + 8 * ti;
+                    uint4* slot = slots + is * F::FRAGS * 32;
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            fx[c][m][h] = load8<T, VEC>(x + max(row[m][h], 0) * a.x_stride + at, at, row[m][h] >= 0 ? n : 0);
+                            cp_async_16z(smem_u32(slot + (2 * m + h) * 32), x + max(row[m][h], 0) * a.x_stride + at, row[m][h] >= 0 && at < k1);
+                    const int rank0 = 8 * NT * ip + gi;
+                    const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + rank0) * a.d + at;
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
-                        fa[c][j] = load8<T, VEC>(A + static_cast<long long>(8 * j) * a.d + at, at, j0 + 8 * j + gi < a.r ? n : 0);
+                        cp_async_16z(smem_u32(slot + (2 * MT + j) * 32), rank0 + 8 * j < a.r ? A + static_cast<long long>(8 * j) * a.d : x,
+                                     rank0 + 8 * j < a.r && at < k1);
+                    if (++iq == chunks) {
+                        iq = 0;
+                        ++ip;
+                    }
+                }
+                if (++is == U) is = 0;
+                cp_async_commit();
+            };
+            int slot_at = 0;
+            if constexpr (VEC) {
+#pragma unroll
+                for (int c = 0; c < U; ++c) issue();
+            }
+            for (int j0 = 0; j0 < rp; j0 += 8 * NT) {
+                float acc[MT][NT][4] = {};
+                auto multiply = [&](const uint4 (&fx)[MT][2], const uint4 (&fa)[NT]) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            mma16816<T>(acc[m][j], fx[m][0].x, fx[m][1].x, fx[m][0].y, fx[m][1].y, fa[j].x, fa[j].y);
+                            mma16816<T>(acc[m][j], fx[m][0].z, fx[m][1].z, fx[m][0].w, fx[m][1].w, fa[j].z, fa[j].w);
+                        }
                 };
-                const int first = k0 + 32 * w;
+                if constexpr (VEC) {
+                    for (int q = 0; q < chunks; ++q) {
+                        cp_async_wait<U - 1>();
+                        uint4 fx[MT][2], fa[NT];
+                        const uint4* slot = slots + slot_at * F::FRAGS * 32;
 #pragma unroll
-                for (int c = 0; c < U; ++c) load(c, first + 32 * WARPS * c);
-                for (int k = first; k < k1; k += 32 * WARPS * U) {
+                        for (int i = 0; i < 2 * MT; ++i) fx[i / 2][i & 1] = slot[i * 32];
 #pragma unroll
-                    for (int c = 0; c < U; ++c) {
+                        for (int j = 0; j < NT; ++j) fa[j] = slot[(2 * MT + j) * 32];
+                        if (++slot_at == U) slot_at = 0;
+                        issue();  // into the slots just read, which are this lane's alone
+                        multiply(fx, fa);
+                    }
+                } else {
+                    const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + j0 + gi) * a.d;
+                    uint4 fx[U][MT][2], fa[U][NT];
+                    auto load = [&](int c, int k) {
+                        const int at = k + 8 * ti, n = k1 - at;
 #pragma unroll
                         for (int m = 0; m < MT; ++m)
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {  // chunks behind the part are zeros
-                                mma16816<T>(acc[m][j], fx[c][m][0].x, fx[c][m][1].x, fx[c][m][0].y, fx[c][m][1].y, fa[c][j].x, fa[c][j].y);
-                                mma16816<T>(acc[m][j], fx[c][m][0].z, fx[c][m][1].z, fx[c][m][0].w, fx[c][m][1].w, fa[c][j].z, fa[c][j].w);
-                            }
-                        load(c, k + 32 * WARPS * (c + U));
+                            for (int h = 0; h < 2; ++h)
+                                fx[c][m][h] = load8<T>(x + max(row[m][h], 0) * a.x_stride + at, at, row[m][h] >= 0 ? n : 0);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            fa[c][j] = load8<T>(A + static_cast<long long>(8 * j) * a.d + at, at, j0 + 8 * j + gi < a.r ? n : 0);
+                    };
+#pragma unroll
+                    for (int c = 0; c < U; ++c) load(c, first + 32 * WARPS * c);
+                    for (int k = first; k < k1; k += 32 * WARPS * U) {
+#pragma unroll
+                        for (int c = 0; c < U; ++c) {
+                            multiply(fx[c], fa[c]);  // chunks behind the part are zeros
+                            load(c, k + 32 * WARPS * (c + U));
+                        }
                     }
                 }
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) red[((w * MT + m) * NT + j) * 128 + 32 * i + lane] = acc[m][j][i];
-                __syncthreads();
-                for (int i = tid; i < MT * NT * 128; i += THREADS) {
-                    float v = red[i];
+                        for (int i = 0; i < 4; ++i) red[(w * NT + j) * 128 + 32 * i + lane] = acc[m][j][i];
+                    __syncthreads();
+                    for (int i = tid; i < NT * 128; i += THREADS) {
+                        float v = red[i];
 #pragma unroll
-                    for (int o = 1; o < WARPS; ++o) v += red[o * MT * NT * 128 + i];
-                    const int l = i & 31, q = i >> 5 & 3, j = i / 128 % NT, m = i / (128 * NT);
-                    const int col = j0 + 8 * j + 2 * (l & 3) + (q & 1);
-                    if (col < rp) part[(16 * m + 8 * (q >> 1) + (l >> 2)) * rp + col] = v;
+                        for (int o = 1; o < WARPS; ++o) v += red[o * NT * 128 + i];
+                        const int l = i & 31, q = i >> 5 & 3, j = i / 128;
+                        const int col = j0 + 8 * j + 2 * (l & 3) + (q & 1);
+                        if (col < rp) part[(16 * m + 8 * (q >> 1) + (l >> 2)) * rp + col] = v;
+                    }
+                    __syncthreads();
                 }
-                __syncthreads();
             }
+        }
+        // B of a step (32 columns, 16 KB ranks) by this lane, and for VEC the first ones under way
+        // while the parts meet.
+        const int nsteps = (KS + KB - 1) / KB;
+        const int blocks = adapted && c0 + 32 * w < c1 ? (c1 - c0 - 32 * w + STEP - 1) / STEP : 0;
+        int bn = 0, bk = 0, bs = 0;
+        auto issue_b = [&] {
+            if (bn < blocks) {
+                const int n0 = c0 + 32 * w + STEP * bn;
+                uint4* slot = slots + bs * F::B_SLOTS * 32;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = n0 + 8 * (gi >> 1) + 2 * j + (gi & 1);
+                    const T* p = B + static_cast<long long>(n) * a.r;
+                    if constexpr (KB == 1) {
+                        const int k = 16 * bk + 4 * ti;
+                        const bool there = n < c1 && k < a.r;
+                        cp_async_8z(smem_u32(slot + j / 2 * 32) + 8 * (j & 1), there ? p + k : B, there);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < KB; q += 2) {
+                            const int k = 16 * (KB * bk + q) + 8 * ti;
+                            const bool there = n < c1 && k < a.r;
+                            cp_async_16z(smem_u32(slot + (j * KB / 2 + q / 2) * 32), there ? p + k : B, there);
+                        }
+                    }
+                }
+                if (++bk == nsteps) {
+                    bk = 0;
+                    ++bn;
+                }
+            }
+            if (++bs == F::B_STEPS) bs = 0;
+            cp_async_commit();
+        };
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < F::B_STEPS; ++i) issue_b();
         }
         if (C > 1) cluster_sync();  // all parts of d are there
         if (adapted) {
@@ -454,28 +545,17 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                 for (int h = 0; h < 2; ++h)
                     add[m][h].load(base + row[m][h] * a.base_stride + col, base != nullptr && row[m][h] >= 0 && col < c1);
         };
-        uint2 fb[KB][4];
+        uint2 fb[4];  // !VEC: the next step's
         auto load_b = [&](int n0, int ks) {
+            const int k = 16 * ks + 4 * ti;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = n0 + 8 * (gi >> 1) + 2 * j + (gi & 1);
-                const T* p = B + static_cast<long long>(n) * a.r;
-                if constexpr (KB == 1) {
-                    const int k = 16 * ks + 4 * ti;
-                    fb[0][j] = load4<T>(p + k, adapted && n < c1 ? a.r - k : 0, VEC || bvec);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < KB; q += 2) {
-                        const int k = 16 * (ks + q) + 8 * ti;
-                        const uint4 v = load8<T, true>(p + k, k, adapted && n < c1 ? a.r - k : 0);
-                        fb[q][j] = make_uint2(v.x, v.y);
-                        fb[q + 1][j] = make_uint2(v.z, v.w);
-                    }
-                }
+                fb[j] = load4<T>(B + static_cast<long long>(n) * a.r + k, adapted && n < c1 ? a.r - k : 0, bvec);
             }
         };
-        constexpr int STEP = 32 * WARPS;
-        load_b(c0 + 32 * w, 0);
+        int b_at = 0;
+        if constexpr (!VEC) load_b(c0 + 32 * w, 0);
         if constexpr (AHEAD) load_base(c0 + 32 * w);
         for (int n0 = c0 + 32 * w; t.n > 0 && n0 < c1; n0 += STEP) {
             Cols<O> here[MT][2];
@@ -489,15 +569,32 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                 load_base(n0);
             }
             float acc[MT][4][4] = {};
-            for (int ks = 0; ks < KS; ks += KB) {
+            for (int ks = 0; adapted && ks < KS; ks += KB) {
                 uint2 cur[KB][4];
+                if constexpr (VEC) {
+                    cp_async_wait<F::B_STEPS - 1>();
+                    const uint4* slot = slots + b_at * F::B_SLOTS * 32;
 #pragma unroll
-                for (int q = 0; q < KB; ++q)
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (KB == 1) {
+                            cur[0][j] = reinterpret_cast<const uint2*>(slot + j / 2 * 32)[j & 1];
+                        } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) cur[q][j] = fb[q][j];
-                if (ks + KB < KS) load_b(n0, ks + KB);
-                else load_b(n0 + STEP, 0);
-                if (!adapted) break;
+                            for (int q = 0; q < KB; q += 2) {
+                                const uint4 v = slot[(j * KB / 2 + q / 2) * 32];
+                                cur[q][j] = make_uint2(v.x, v.y);
+                                cur[q + 1][j] = make_uint2(v.z, v.w);
+                            }
+                        }
+                    }
+                    if (++b_at == F::B_STEPS) b_at = 0;
+                    issue_b();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cur[0][j] = fb[j];
+                    if (ks + KB < KS) load_b(n0, ks + KB);
+                    else load_b(n0 + STEP, 0);
+                }
 #pragma unroll
                 for (int q = 0; q < KB; ++q)
 #pragma unroll

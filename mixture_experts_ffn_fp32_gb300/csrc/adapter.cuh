@@ -141,6 +141,14 @@ struct Cols {
     }
 };
 
+// Asynchronous copies of 16 or 8 bytes, zeros where there is nothing to copy.
+MOE_DEV void cp_async_16z(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+MOE_DEV void cp_async_8z(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+
 // The sum of the slices of 4 consecutive inner values.
 MOE_DEV float4 inner4(const AdapterArgs& a, int pos, int k, int slices) {
     const float* v = a.v + static_cast<long long>(pos) * a.rp + k;

@@ -22,9 +22,6 @@ namespace {
 
 constexpr int ROWS = 128, BLOCK = 16384;  // a block: 128 rows of 64 elements of 16 bits
 
-MOE_DEV void cp_async_16z(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
 // 16-byte piece c of row r of a 128-byte-swizzled tile.
 MOE_DEV uint32_t swizzled(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
