@@ -79,37 +79,112 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_shrink_f32_kernel(const __
     }
 }
 
-// out = base + v B^T of 64 positions by ranges of 128 columns: a warp has 8 rows, a lane 4
-// columns of each. B is turned around on its way into shared memory, 32 ranks at a time.
+// out = base + v B^T of 64 positions by ranges of 128 columns, 32 ranks at a time through shared
+// memory (the next ones in registers meanwhile): a warp has 8 rows, a lane 4 columns of each. B is
+// turned around on its way in; element (j, n) lies at n ^ 4 (j / 4), so that neither the
+// writes nor the 16-byte reads meet in a bank.
 constexpr int F32_TILE = 64, F32_COLS = 128, F32_STEP = 32;
 
 template <bool VEC>
 __global__ void __launch_bounds__(THREADS, 2) adapter_expand_f32_kernel(const __grid_constant__ AdapterArgs a) {
-    constexpr int PER = F32_TILE / (THREADS / 32);
+    constexpr int PER = F32_TILE / (THREADS / 32), BN = F32_COLS * F32_STEP / 4 / THREADS, VN = F32_TILE * F32_STEP / 4 / THREADS;
     __shared__ Groups g;
-    __shared__ __align__(16) float sv[F32_TILE][F32_STEP];
-    __shared__ __align__(16) float sb[F32_STEP][F32_COLS + 4];
+    __shared__ __align__(16) float sv[F32_TILE][F32_STEP], sb[F32_STEP][F32_COLS];
     __shared__ int srow[F32_TILE];
-    const int tiles = group_table<F32_TILE>(a, !a.in_place, g);
-    const int lane = static_cast<int>(lane_id()), w = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int nb = a.col_parts, len = ((a.N + nb - 1) / nb + F32_COLS - 1) / F32_COLS * F32_COLS;
     const float* base = static_cast<const float*>(a.base);
     float* out = static_cast<float*>(a.out);
-    auto column = [&](int i) { return VEC ? 4 * lane + i : lane + 32 * i; };  // of a range, the lane's i-th
+    const bool bvec = a.r % 4 == 0 && reinterpret_cast<uintptr_t>(a.b) % 16 == 0;
+    // ranks of a step in fours, rounded up to a power of two
+    const int quads = a.rp > 16 ? 8 : a.rp > 8 ? 4 : a.rp > 4 ? 2 : 1, ql = a.rp > 16 ? 3 : a.rp > 8 ? 2 : a.rp > 4 ? 1 : 0;
     pdl_wait();
     pdl_trigger();
+    const int tiles = group_table<F32_TILE>(a, !a.in_place, g);
     for (long long u = blockIdx.x; u < static_cast<long long>(tiles) * nb; u += gridDim.x) {
         const Tile t = tile_of<F32_TILE>(static_cast<int>(u / nb), a, g);
         const int c0 = static_cast<int>(u % nb) * len, c1 = min(a.N, c0 + len);
-        const int ranks = t.e < a.E ? a.r : 0;
+        const int ranks = t.e < a.E ? a.rp : 0;
         const float* B = static_cast<const float*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
         __syncthreads();
-        if (threadIdx.x < F32_TILE) srow[threadIdx.x] = threadIdx.x < t.n ? row_of(a, t.pos + threadIdx.x) : -1;
+        if (tid < F32_TILE) srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+        // four ranks of a column (of a row of v) by neighbouring threads
+        float4 bv[BN], vv[VN];
+        auto fetch = [&](int n0, int j0) {
+#pragma unroll
+            for (int i = 0; i < BN; ++i) {
+                const int at = tid + THREADS * i, n = n0 + (at >> ql), j = j0 + (at & (quads - 1)) * 4;
+                bv[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (at >= F32_COLS * quads || n >= c1 || j >= a.r) continue;
+                const float* p = B + static_cast<long long>(n) * a.r + j;
+                if (bvec) {
+                    bv[i] = __ldg(reinterpret_cast<const float4*>(p));
+                } else {
+                    bv[i].x = __ldg(p);
+                    if (j + 1 < a.r) bv[i].y = __ldg(p + 1);
+                    if (j + 2 < a.r) bv[i].z = __ldg(p + 2);
+                    if (j + 3 < a.r) bv[i].w = __ldg(p + 3);
+                }
+            }
+            if (n0 != c0 && ranks <= F32_STEP) return;  // v is there
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+                const int at = tid + THREADS * i, r = (at >> ql), j = j0 + (at & (quads - 1)) * 4;
+                vv[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (at < F32_TILE * quads && r < t.n && j < a.rp) vv[i] = inner4(a, t.pos + r, j, a.slices);
+            }
+        };
+        if (ranks > 0) fetch(c0, 0);
         __syncthreads();
         int row[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) row[i] = srow[w * PER + i];
+        auto column = [&](int i) { return VEC ? 4 * lane + i : lane + 32 * i; };  // of a range, the lane's i-th
         for (int n0 = c0; n0 < c1; n0 += F32_COLS) {
+            float acc[PER][4] = {};
+            for (int j0 = 0; j0 < ranks; j0 += F32_STEP) {
+                __syncthreads();  // the last step has been read
+#pragma unroll
+                for (int i = 0; i < BN; ++i) {
+                    const int at = tid + THREADS * i, n = (at >> ql), j = (at & (quads - 1)) * 4, to = n ^ j;
+                    if (at >= F32_COLS * quads) continue;
+                    sb[j][to] = bv[i].x;
+                    sb[j + 1][to] = bv[i].y;
+                    sb[j + 2][to] = bv[i].z;
+                    sb[j + 3][to] = bv[i].w;
+                }
+                if (n0 == c0 || ranks > F32_STEP) {
+#pragma unroll
+                    for (int i = 0; i < VN; ++i) {
+                        const int at = tid + THREADS * i;
+                        if (at < F32_TILE * quads) *reinterpret_cast<float4*>(&sv[(at >> ql)][(at & (quads - 1)) * 4]) = vv[i];
+                    }
+                }
+                __syncthreads();
+                if (j0 + F32_STEP < ranks) fetch(n0, j0 + F32_STEP);
+                else if (n0 + F32_COLS < c1) fetch(n0 + F32_COLS, 0);
+                const int steps = min(F32_STEP, ranks - j0);
+                for (int j = 0; j < steps; j += 4) {
+                    float b[4][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (VEC) {
+                            const float4 v = *reinterpret_cast<const float4*>(&sb[j + q][(4 * lane) ^ j]);
+                            b[q][0] = v.x; b[q][1] = v.y; b[q][2] = v.z; b[q][3] = v.w;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) b[q][i] = sb[j + q][column(i) ^ j];
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(&sv[w * PER + i][j]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            acc[i][q] = fmaf(v.w, b[3][q], fmaf(v.z, b[2][q], fmaf(v.y, b[1][q], fmaf(v.x, b[0][q], acc[i][q]))));
+                    }
+                }
+            }
             float add[PER][4];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -121,43 +196,6 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_expand_f32_kernel(const __
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) add[i][q] = there && n0 + column(q) < c1 ? p[column(q)] : 0.0f;
-                }
-            }
-            float acc[PER][4] = {};
-            for (int j0 = 0; j0 < ranks; j0 += F32_STEP) {
-                const int steps = min(F32_STEP, a.rp - j0);  // a multiple of 4
-                __syncthreads();
-                for (int i = threadIdx.x; i < F32_TILE * F32_STEP / 4; i += THREADS) {
-                    const int r = i / (F32_STEP / 4), j = i % (F32_STEP / 4) * 4;
-                    if (j < steps)
-                        *reinterpret_cast<float4*>(&sv[r][j]) = r < t.n ? inner4(a, t.pos + r, j0 + j, a.slices) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                }
-                // a column's ranks by neighbouring threads: read in lines, written 4 banks apart at most
-                for (int i = threadIdx.x; i < F32_COLS * steps; i += THREADS) {
-                    const int n = i / steps, j = i % steps;
-                    sb[j][n] = n0 + n < c1 && j0 + j < a.r ? __ldg(B + static_cast<long long>(n0 + n) * a.r + j0 + j) : 0.0f;
-                }
-                __syncthreads();
-                for (int j = 0; j < steps; j += 4) {
-                    float b[4][4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 4; i += VEC ? 4 : 1) {
-                            if constexpr (VEC) {
-                                const float4 v = *reinterpret_cast<const float4*>(&sb[j + q][4 * lane]);
-                                b[q][0] = v.x; b[q][1] = v.y; b[q][2] = v.z; b[q][3] = v.w;
-                            } else {
-                                b[q][i] = sb[j + q][column(i)];
-                            }
-                        }
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const float4 v = *reinterpret_cast<const float4*>(&sv[w * PER + i][j]);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            acc[i][q] = fmaf(v.w, b[3][q], fmaf(v.z, b[2][q], fmaf(v.y, b[1][q], fmaf(v.x, b[0][q], acc[i][q]))));
-                    }
                 }
             }
 #pragma unroll
@@ -675,8 +713,8 @@ cudaError_t launch_f32(AdapterArgs a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const bool out = a.N % 4 == 0 && aligned_to(a.out, 16) && a.out_stride % 4 == 0 && aligned_to(a.base, 16) && a.base_stride % 4 == 0;
     const long long tiles = most_tiles(a, F32_TILE);
-    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + F32_COLS - 1) / F32_COLS, 8LL * num_sms() / tiles)));
-    return launch_units(out ? adapter_expand_f32_kernel<true> : adapter_expand_f32_kernel<false>, tiles * a.col_parts, 4, 0, s, a);
+    a.col_parts = static_cast<int>(std::max<long long>(1, std::min<long long>((a.N + F32_COLS - 1) / F32_COLS, (4LL * num_sms() + tiles - 1) / tiles)));
+    return launch_units(out ? adapter_expand_f32_kernel<true> : adapter_expand_f32_kernel<false>, tiles * a.col_parts, 2, 0, s, a);
 }
 
 template <typename T, typename O, int MT, int NT, int KB, bool VEC>

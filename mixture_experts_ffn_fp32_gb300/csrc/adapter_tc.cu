@@ -12,6 +12,12 @@
 // last one's output. B's rows stand in an order in which a lane that reads 16 x 256 bits of
 // tensor memory ends with 8 consecutive columns of its rows.
 //
+// Measured (one GB300, calls among others): 16384 rows of 16 adapters (a tenth of them without),
+// 2048 x 2816, rank 16, 58 us: 20 for v (x at 3 TB/s: a wave of 16 steps a CTA, 4 us before the
+// first and 4 for the cluster behind the last) and 39 for the second product, which a plain copy of
+// base to out takes 36 for. 8192 rows of 4, 4096 x 4096, rank 64, 59 us (25 + 36). What its loads
+// in flight find of L1 counts: see STAGES.
+//
 // Every wait is bounded (common.cuh); one that runs out leaves NaN in what is not stored yet.
 #include <math_constants.h>
 
