@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
     extern __shared__ __align__(16) uint8_t smem[];
     const int rp = a.rp, KS = rp / 16, C = a.cluster;
     float* part = reinterpret_cast<float*>(smem);  // [ROWS][rp], this CTA's part of d
-    float* red = part + ROWS * rp;                 // [WARPS][MT * NT * 4][32], then [ROWS][rp]
+    float* red = part + ROWS * rp;                 // [WARPS][NT * 4][32], then [ROWS][rp]
     uint4* frag = reinterpret_cast<uint4*>(red + (F::RED / 4 > ROWS * rp ? F::RED / 4 : ROWS * rp));  // [KS][NP][MT][32]
     uint4* slots = frag + KS * NP * MT * 32 + (threadIdx.x >> 5) * (F::RING / WARPS / 16) + (threadIdx.x & 31);  // this lane's, 32 apart
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, gi = lane >> 2, ti = lane & 3;
@@ -382,7 +382,9 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            cp_async_16z(smem_u32(slot + (2 * m + h) * 32), x + max(row[m][h], 0) * a.x_stride + at, row[m][h] >= 0 && at < k1);
+                            if (16 * m + 8 * h < t.n)  // else what is there goes into rows that nobody reads
+                                cp_async_16z(smem_u32(slot + (2 * m + h) * 32), x + max(row[m][h], 0) * a.x_stride + at,
+                                             row[m][h] >= 0 && at < k1);
                     const int rank0 = 8 * NT * ip + gi;
                     const T* A = static_cast<const T*>(a.a) + (static_cast<long long>(t.e) * a.r + rank0) * a.d + at;
 #pragma unroll

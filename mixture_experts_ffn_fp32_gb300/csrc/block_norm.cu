@@ -21,16 +21,17 @@ block_norm_params_kernel(const __grid_constant__ BlockNormArgs a, int n, const f
     pdl_trigger();
     float v[NS] = {};
     if (c < a.d) {
-        for (int r0 = slot; r0 < n; r0 += 4 * SLOTS) {
-            float e[4][NS];
+        for (int r0 = slot; r0 < n; r0 += 8 * SLOTS) {
+            float e[8][NS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const int r = r0 + i * SLOTS;
 #pragma unroll
                 for (int q = 0; q < NS; ++q) e[i][q] = r < n ? part[(static_cast<long long>(r) * NS + q) * a.d + c] : 0.0f;
             }
 #pragma unroll
-            for (int q = 0; q < NS; ++q) v[q] += (e[0][q] + e[1][q]) + (e[2][q] + e[3][q]);
+            for (int q = 0; q < NS; ++q)
+                v[q] += ((e[0][q] + e[1][q]) + (e[2][q] + e[3][q])) + ((e[4][q] + e[5][q]) + (e[6][q] + e[7][q]));
         }
     }
 #pragma unroll
