@@ -336,11 +336,14 @@ moe_status moe_backward(const moe_config* cfg, const void* x, const moe_weights*
                         void* bws, size_t bws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Operators around the layer: the norm in front of it, group-limited routing,
- * and 8-bit expert products for serving. Together they make a block
+ * Operators around the layer: the norms around it, group-limited routing, 8-bit
+ * expert products and low-rank adapters for serving. Together they make a block
  *   x -> moe_layer_norm -> router logits -> moe_group_route -> moe_dispatch
  *     -> moe_quantize_rows -> moe_matmul_int8 (gate/up, SwiGLU)
  *     -> moe_quantize_rows -> moe_matmul_int8 (down) -> weighted sum per token.
+ * Between blocks moe_block_norm joins the residual stream, a block's output and
+ * the next block's norm; moe_adapter_add adds the low-rank adapters of many
+ * requests to a projection's result.
  * The row operators take rows whose elements are contiguous and whose pitch
  * (`*_stride`, in elements, >= the row's length) is the caller's; zero rows
  * are allowed and launch nothing. Outputs must not overlap inputs. Pointers
