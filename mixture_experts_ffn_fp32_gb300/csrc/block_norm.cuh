@@ -582,7 +582,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
         const float ymc = ym, yrc = yr, xmc = xm, xrc = xr;
         statistics(row + step);
         F2 u[N2], v[N2];
-        // of a warp whose other rows are there: what shared memory holds is an older row
+        // of a warp whose other rows are there: shared memory holds an older row, or what was left there
         auto gone = [&](F2 (&q)[N2]) {
             if (TPR < 32 && !there) {
 #pragma unroll
@@ -661,6 +661,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
                     if (there) put<T, VEC, NV, TPR>(p.dgate + row * d, d, t, z);
                 }
                 fg.pairs(0, z);
+                gone(z);
                 fg.issue(0, next, more);
 #pragma unroll
                 for (int k = 0; k < N2; ++k) v[k] = mul2(v[k], z[k]);

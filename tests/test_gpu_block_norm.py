@@ -50,7 +50,7 @@ def inputs(n, d, dt, pad=0, kind="rms", gate="channel", post=True, norm=True, bl
 def close(got, want, what):
     val, tol = want
     assert got.shape == val.shape, what
-    bad = (got.double() - val).abs() > tol * 1.001 + 1e-30
+    bad = ~((got.double() - val).abs() <= tol * 1.001 + 1e-30)  # a NaN is bad
     assert not bad.any(), (what, int(bad.sum()), float(((got.double() - val).abs() - tol)[bad].max()))
 
 
@@ -226,3 +226,21 @@ def test_bits_repeat(A):
                                   post_bias=s["post_bias"], gate=s["gate"], **opt) for _ in range(2)]
     for k in runs[0]:
         assert torch.equal(runs[0][k], runs[1][k])
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("kind,gate,post", [("rms", "element", True), ("layer", "element", True), ("layer", "channel", False),
+                                            ("rms", "element", False)])
+def test_part_empty_warps_after_nans(A, kind, gate, post, dt):
+    """Rows that a warp's part has no row for add nothing, whatever an earlier kernel left in shared memory."""
+    nan = float("nan")
+    for n, d in ((1, 16), (5, 16), (66, 16), (850, 16), (3, 33), (66, 32), (13, 64), (47, 6), (2, 100), (9, 128), (335, 128)):
+        s, opt, grads = inputs(n, d, DT[dt], kind=kind, gate=gate, post=post)
+        f = A.block_norm(s["x"], s["y"], s["weight"], s["bias"], s["post_weight"], s["post_bias"], s["gate"], **opt)
+        left, _, lgrads = inputs(16384, d, DT[dt], kind=kind, gate="element", post=post, vectors=False)
+        left = {k: None if v is None else torch.full_like(v, nan) for k, v in {**left, **lgrads}.items()}
+        stats = torch.full((4 if kind == "layer" else 2, 16384), nan, device="cuda")
+        # without the vectors' gradients the last kernel is the one that keeps rows in shared memory
+        A.block_norm_backward(left["x"], stats, left["y"], left["dn"], left["dx"], gate=left["gate"], weight_grads=False, **opt)
+        torch.cuda.synchronize()
+        check_backward(A, s, opt, grads, f["stats"], f["x"])
