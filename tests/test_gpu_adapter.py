@@ -249,3 +249,33 @@ def test_two_calls_at_once(A, form):
         torch.cuda.synchronize()
         for i in range(2):
             assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_what_earlier_calls_left(A, form, size, dt):
+    """NaNs in shared and tensor memory, in the workspace, between a row's end and its pitch, and in
+    rows and adapters that no position joins reach no result."""
+    T, d, N, r, E = size
+    dtype, nan = DT[dt], float("nan")
+    s = make(T, d, N, r, E, dtype, pad=8)
+    whole = {k: torch.full((T, n + 8), nan, device="cuda", dtype=dtype) for k, n in (("x", d), ("base", N))}
+    for k, n in (("x", d), ("base", N)):
+        whole[k][:, :n] = s[k]
+        s[k] = whole[k][:, :n]
+    dirty = make(2000, 512, 512, min(256, -(-r // 16) * 16), 3, dtype, ids=torch.arange(2000) % 3)
+    for k in ("x", "a", "b"):
+        dirty[k].fill_(nan)
+    ws = A.alloc_adapter_workspace(T, d, N, r, E, dtype)
+    ws[256:] = 255
+    want = {k: v.clone() if v is not None else None for k, v in s.items()}
+    s["x"][s["rows"][int(s["offsets"][E]):].long()] = nan
+    empty = (s["offsets"][1:] == s["offsets"][:-1])
+    s["a"][empty] = nan
+    s["b"][empty] = nan
+    s["scale"][empty] = nan
+    torch.cuda.synchronize()
+    A.adapter_add(**dirty)
+    got = A.adapter_add(**s, ws=ws)
+    assert A.workspace_status(ws) == A.MOE_OK
+    check(got, want)

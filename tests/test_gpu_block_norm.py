@@ -244,3 +244,19 @@ def test_part_empty_warps_after_nans(A, kind, gate, post, dt):
         A.block_norm_backward(left["x"], stats, left["y"], left["dn"], left["dx"], gate=left["gate"], weight_grads=False, **opt)
         torch.cuda.synchronize()
         check_backward(A, s, opt, grads, f["stats"], f["x"])
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("n,d,pad", [(3, 6, 2), (33, 100, 4), (40, 96, 8), (9, 1003, 5), (70, 2040, 8), (3, 8190, 2), (2, 16392, 8)])
+def test_nans_between_rows(A, n, d, pad, kind, dt):
+    """What lies between a row's end and its pitch reaches no result."""
+    s, opt, grads = inputs(n, d, DT[dt], kind=kind, gate="element")
+    for group in (s, grads):
+        for k, v in group.items():
+            if v is not None and v.dim() == 2:
+                whole = torch.full((n, d + pad), float("nan"), device="cuda", dtype=v.dtype)
+                whole[:, :d] = v
+                group[k] = whole[:, :d]
+    f = check_forward(A, s, opt)
+    check_backward(A, s, opt, grads, f["stats"], f["x"])
