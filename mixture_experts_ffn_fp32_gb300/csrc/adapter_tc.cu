@@ -18,7 +18,11 @@
 // base to out takes 36 for. 8192 rows of 4, 4096 x 4096, rank 64, 59 us (25 + 36). What its loads
 // in flight find of L1 counts: see STAGES.
 //
-// Every wait is bounded (common.cuh); one that runs out leaves NaN in what is not stored yet.
+// Waits for MMAs are bounded (common.cuh). One that runs out ends the CTA's copies into the stages and
+// its MMAs, leaves NaN in what is not stored yet, and the MMAs already issued are waited for once more
+// (drain) before shared or tensor memory has another use. The other waits always end: cluster
+// barriers because every CTA makes the same number of turns, whatever the offsets and whatever
+// ran out; allocations of tensor memory because who holds some waits for no other CTA's.
 #include <math_constants.h>
 
 #include "adapter.cuh"
@@ -73,6 +77,20 @@ MOE_DEV void tc_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr));
 }
 
+// Waits for the MMAs that the elected lane of the first warp has issued (every commit of theirs has then
+// arrived too). By the whole CTA, behind a sync, once.
+MOE_DEV void drain(uint32_t bar, const WaitCtx& wc) {
+    if (threadIdx.x < 32) {
+        if (elect_one()) {  // the same lane at every call
+            tc_commit(bar);
+            bounded_drain(bar, 0, wc.timeout_ns, wc.err);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    tc_fence_after();
+}
+
 MOE_DEV uint8_t* align_1k(uint8_t* p) {
     return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
 }
@@ -91,7 +109,7 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
     constexpr bool SCALED = __is_same(T, __half);
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups g;
-    __shared__ __align__(8) uint64_t bars[STAGES];
+    __shared__ __align__(8) uint64_t bars[STAGES + 1];  // the stages', drain's
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     uint8_t* smem = align_1k(smem_raw);
@@ -102,7 +120,7 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
     const int C = a.cluster, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int clusters = gridDim.x / C, id = blockIdx.x / C;
     if (tid == 0) {
-        for (int i = 0; i < STAGES; ++i) mbar_init(bar(i), 1);
+        for (int i = 0; i <= STAGES; ++i) mbar_init(bar(i), 1);
         abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -159,16 +177,18 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
                     cp_async_16z(at + BLOCK + swizzled(r, c16), there ? A + static_cast<long long>(r) * a.d + k : A, there);
                 }
             };
+            const bool begun = alive;  // the CTA's
             for (int s = 0; s < STAGES - 1; ++s) {
-                if (s < n) load(s, (it + s) % STAGES);
+                if (s < n && alive) load(s, (it + s) % STAGES);
                 cp_async_commit();
             }
             for (int kb = 0; kb < n; ++kb, ++it) {
                 cp_async_wait<STAGES - 2>();
                 fence_proxy_async_smem();
                 alive = __syncthreads_and(alive);
+                if (!alive) break;
                 const uint32_t stage = it % STAGES;
-                if (warp == 0 && alive) {
+                if (warp == 0) {
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t at = sbase + stage * stage_bytes;
@@ -183,15 +203,17 @@ adapter_shrink_tc_kernel(const __grid_constant__ AdapterArgs a, int turns, int c
                 if (kb + STAGES - 1 < n) {
                     // the stage before this one, once its MMAs have read it
                     const uint32_t last = it + STAGES - 1;
-                    if (kb > 0 && alive) alive = bounded_wait(bar(last % STAGES), (it - 1) / STAGES & 1, wc);
-                    load(kb + STAGES - 1, last % STAGES);
+                    if (kb > 0) alive = bounded_wait(bar(last % STAGES), (it - 1) / STAGES & 1, wc);
+                    if (alive) load(kb + STAGES - 1, last % STAGES);
                 }
                 cp_async_commit();
             }
             if (alive && n > 0) alive = bounded_wait(bar((it - 1) % STAGES), (it - 1) / STAGES & 1, wc);
             tc_fence_after();
             cp_async_wait<0>();
-            alive = __syncthreads_and(alive);  // the stages are free
+            alive = __syncthreads_and(alive);
+            if (begun && !alive) drain(bar(STAGES), wc);
+            // the stages are free
             const int row = 32 * (warp & 3) + lane;
             for (int c = 16 * (warp >> 2); c < rp; c += 32) {
                 float f[16];
@@ -275,7 +297,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
     constexpr int AHEAD = sizeof(O) == 2 ? 2 : 1;  // quarters of a block whose base is under way
     extern __shared__ uint8_t smem_raw[];
     __shared__ Groups g;
-    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ __align__(8) uint64_t bars[3];  // the accumulators', drain's
     __shared__ int srow[ROWS];
     __shared__ float sback[SCALED ? ROWS : 1];
     __shared__ uint32_t tmem_slot;
@@ -285,8 +307,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
     const int KS = a.rp / 16, a_bytes = NP * KS * STEP_BYTES, b_bytes = KS * STEP_BYTES;
     const uint32_t sA = smem_u32(smem), sB = sA + a_bytes;
     if (tid == 0) {
-        mbar_init(smem_u32(&bars[0]), 1);
-        mbar_init(smem_u32(&bars[1]), 1);
+        for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&bars[i]), 1);
         abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -330,10 +351,11 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
         };
         __syncthreads();  // the last tile's rows have been read
         if (tid < ROWS) srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
-        if (adapted) load_b(0);
+        // what a thread that has waited for all MMAs so far copies, none of them reads
+        if (adapted && alive) load_b(0);
         pdl_wait();  // v
         pdl_trigger();
-        if (adapted) {  // its pieces, in the first block's group
+        if (adapted && alive) {  // its pieces, in the first block's group
             const int row16 = NP * a.rp / 8;
             for (int i = tid; i < ROWS * row16; i += THREADS) {
                 const int p = i / row16, c = i % row16;
@@ -342,7 +364,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
             if (SCALED && tid < ROWS) sback[tid] = tid < t.n ? a.back[t.pos + tid] : 1.0f;
         }
         for (int b = 0; b < 2; ++b) {
-            if (adapted && b > 0 && b < n) load_b(b);
+            if (adapted && alive && b > 0 && b < n) load_b(b);
             cp_async_commit();
         }
         __syncthreads();
@@ -428,13 +450,13 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
                 }
                 tc_fence_before();
             }
-            if (adapted && b + 2 < n) load_b(b + 2);  // over the block whose MMAs were waited for
+            if (adapted && alive && b + 2 < n) load_b(b + 2);  // over the block whose MMAs were waited for
             cp_async_commit();
         }
     }
     pdl_wait();  // never done before the launch before this one
     cp_async_wait<0>();
-    __syncthreads();
+    if (!__syncthreads_and(alive)) drain(smem_u32(&bars[2]), wc);
     if (warp == 1) tmem_dealloc(tmem, 2 * COLS);
 }
 
