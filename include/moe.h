@@ -560,7 +560,8 @@ moe_status moe_adapter_add_workspace_size(const moe_adapter_config* cfg, size_t*
  *   experts, the last for rows without an adapter, gives offsets and rows.
  * ws: 256-byte aligned. Offsets are clamped to [0, T]; a row index outside
  * [0, T) is skipped and sets MOE_ERR_DEVICE_INDEX in the workspace's error word,
- * which the call adds to and never clears; a row that no position names is not
+ * which the call adds to and never clears (where out is base, positions from
+ * offsets[E] on are not looked at); a row that no position names is not
  * written, and what a row named twice holds is not specified. A bounded device
  * wait that runs out makes the outputs that are not stored yet NaN and sets
  * MOE_ERR_TIMEOUT.

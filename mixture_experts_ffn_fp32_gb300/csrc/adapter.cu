@@ -107,7 +107,10 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_expand_f32_kernel(const __
         const int ranks = t.e < a.E ? a.rp : 0;
         const float* B = static_cast<const float*>(a.b) + static_cast<long long>(t.e) * a.N * a.r;
         __syncthreads();
-        if (tid < F32_TILE) srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+        if (tid < F32_TILE) {
+            srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+            if (ranks == 0 && c0 == 0 && tid < t.n && srow[tid] < 0) atomicOr(a.err, ERRBIT_INDEX);  // the others': the first launch
+        }
         // four ranks of a column (of a row of v) by neighbouring threads
         float4 bv[BN], vv[VN];
         auto fetch = [&](int n0, int j0) {

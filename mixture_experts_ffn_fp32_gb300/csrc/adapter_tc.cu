@@ -350,7 +350,10 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
             }
         };
         __syncthreads();  // the last tile's rows have been read
-        if (tid < ROWS) srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+        if (tid < ROWS) {
+            srow[tid] = tid < t.n ? row_of(a, t.pos + tid) : -1;
+            if (!adapted && c0 == 0 && tid < t.n && srow[tid] < 0) atomicOr(a.err, ERRBIT_INDEX);  // the others': the first launch
+        }
         // what a thread that has waited for all MMAs so far copies, none of them reads
         if (adapted && alive) load_b(0);
         pdl_wait();  // v
