@@ -597,6 +597,15 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                 fb[j] = load4<T>(B + static_cast<long long>(n) * a.r + k, adapted && n < c1 ? a.r - k : 0, bvec);
             }
         };
+        // rank k of row p from its pieces (FP16: times the row's scale)
+        auto whole = [&](int p, int k) {
+            const int ks = KB == 1 ? k / 16 : 2 * (k / 32) + (k >> 2 & 1), l = 4 * (p & 7) + (KB == 1 ? k >> 2 & 3 : k >> 3 & 3);
+            float v = 0.0f;
+#pragma unroll
+            for (int o = 0; o < NP; ++o)
+                v += to_f32(reinterpret_cast<const T*>(frag + ((ks * NP + o) * MT + (p >> 4)) * 32 + l)[(k >> 1 & 1) * 4 + (p >> 3 & 1) * 2 + (k & 1)]);
+            return v;
+        };
         int b_at = 0;
         if constexpr (!VEC) load_b(c0 + 32 * w, 0);
         if constexpr (AHEAD) load_base(c0 + 32 * w);
@@ -651,6 +660,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
             }
             if constexpr (VEC) {
                 const int col = n0 + 8 * ti;
+                uint32_t again = 0;
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -662,11 +672,22 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                             F2 v[4];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) v[j] = f2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-                            old.add_to(to, v, back[m][h]);
+                            const bool nan = any_nan(v);
+                            if (nan) again |= 1u << (2 * m + h);
+                            else old.add_to(to, v, back[m][h]);
                         } else {
                             old.copy_to(to);
                         }
                     }
+                if (again != 0) {
+#pragma unroll 1
+                    for (int i = 0; i < 2 * MT; ++i) {
+                        if ((again >> i & 1) == 0) continue;
+                        const int p = 8 * i + gi, at = srow[p];
+                        store_again(out + at * a.out_stride + col, base != nullptr ? base + at * a.base_stride + col : nullptr,
+                                    [&](int k) { return whole(p, k); }, B + static_cast<long long>(col) * a.r, a.r, SCALED ? sback[p] : 1.0f);
+                    }
+                }
             } else {
                 // rows on no 16 bytes: 16 rows of the warp's columns through shared memory, then a row's
                 // 32 columns by the 32 lanes
@@ -678,6 +699,26 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) mine[(8 * h + gi) * 33 + 8 * ti + i] = acc[m][i >> 1][2 * h + (i & 1)] * back[m][h];
+                    uint32_t again = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        F2 v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = f2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+                        if (any_nan(v) && row[m][h] >= 0) again |= 1u << h;
+                    }
+                    if (adapted && again != 0) {
+                        const int at = n0 + 8 * ti;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            if ((again >> h & 1) == 0) continue;
+                            const int p = 16 * m + 8 * h + gi;
+                            float s[8];
+                            sums_again(s, [&](int k) { return whole(p, k); }, B + static_cast<long long>(at) * a.r, a.r, c1 - at);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) mine[(8 * h + gi) * 33 + 8 * ti + i] = s[i] * (SCALED ? sback[p] : 1.0f);
+                        }
+                    }
                     __syncwarp();
                     const int col = n0 + lane;
                     O old[16];

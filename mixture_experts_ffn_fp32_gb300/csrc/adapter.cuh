@@ -109,6 +109,36 @@ MOE_DEV void split(float v, T (&p)[NP]) {
     }
 }
 
+// Pieces of v against an infinite element of B: their products have different signs, or one is 0 inf,
+// and the sum is NaN where v B^T is an infinity. So 8 consecutive columns of a row whose sums hold a NaN
+// are not stored but taken again, from v whole: v(k) of the row, rows of B r apart. A NaN in v stays
+// what it is (the first one ends the loop). Behind all stores of a block, so that these wait for no
+// branch (at each store: 16384 x 2048 x 2816, rank 16, 82 us for 58).
+MOE_DEV bool any_nan(const F2 (&acc)[4]) {
+    const float s = both(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+    return s != s;
+}
+template <typename T, typename V>
+MOE_DEV void sums_again(float (&s)[8], V v, const T* b, int r, int columns) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < r; ++k) {
+        const float x = v(k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < columns) s[j] = fmaf(x, to_f32(b[static_cast<long long>(j) * r + k]), s[j]);
+        if (x != x) return;
+    }
+}
+template <typename T, typename O, typename V>
+MOE_DEV void store_again(O* to, const O* base, V v, const T* b, int r, float back) {
+    float s[8];
+    sums_again(s, v, b, r, 8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) to[j] = from_f32<O>(fmaf(s[j], back, base != nullptr ? to_f32(base[j]) : 0.0f));
+}
+
 // 8 consecutive elements of base as loaded (16-byte aligned, all or none).
 template <typename O>
 struct Cols {

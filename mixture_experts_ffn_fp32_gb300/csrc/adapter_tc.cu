@@ -426,6 +426,7 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
 #pragma unroll
                     for (int m = 0; m < 2; ++m) back[m][0] = back[m][1] = CUDART_NAN_F;
                 }
+                uint32_t again = 0;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int off = COLS * at + 32 * q;
@@ -440,7 +441,9 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
                                 F2 acc[4];
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) acc[j] = f2(__uint_as_float(r[4 * j + 2 * h]), __uint_as_float(r[4 * j + 2 * h + 1]));
-                                if (to_row[m][h] != nullptr && off < width) add[q % AHEAD][m][h].add_to(to_row[m][h] + off, acc, back[m][h]);
+                                const bool there = to_row[m][h] != nullptr && off < width, nan = any_nan(acc);
+                                if (there && !nan) add[q % AHEAD][m][h].add_to(to_row[m][h] + off, acc, back[m][h]);
+                                if (there && nan) again |= 1u << (4 * q + 2 * m + h);
                             }
                         } else {
 #pragma unroll
@@ -450,6 +453,22 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
                     }
                     if (AHEAD == 2) load_base(at + 1, q, q);
                     else load_base(q == 0 ? at : at + 1, 1 - q, 0);
+                }
+                if (again != 0) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        if ((again >> i & 1) == 0) continue;
+                        const int p = r32 + 8 * (i & 3) + gi, row = srow[p], col = c0 + COLS * at + c64 + 32 * (i >> 2) + 8 * ti;
+                        const T* v = vp + (t.pos + p) * static_cast<long long>(NP * a.rp);
+                        auto whole = [&](int k) {
+                            float s = 0.0f;
+#pragma unroll
+                            for (int o = 0; o < NP; ++o) s += to_f32(v[o * a.rp + k]);
+                            return s;
+                        };
+                        store_again(out + row * a.out_stride + col, base != nullptr ? base + row * a.base_stride + col : nullptr, whole,
+                                    B + static_cast<long long>(col) * a.r, a.r, !alive ? CUDART_NAN_F : SCALED ? sback[p] : 1.0f);
+                    }
                 }
                 tc_fence_before();
             }
