@@ -326,7 +326,12 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
     constexpr int WARPS = F::WARPS, ROWS = F::ROWS, NP = F::NP, U = F::U;
     constexpr bool SCALED = __is_same(T, __half);
     constexpr int STEP = 32 * WARPS;
-    constexpr bool AHEAD = VEC && KB == 1;  // the next columns' base too: where B takes few registers
+    // FP32 outputs of more than 16 ranks: the small pieces of v are summed apart, since what an addition
+    // drops grows with the sum (in one accumulator, 256 rows of 128, rank 64: 2.7e-7 off for 1.3e-7)
+    constexpr bool APART = sizeof(O) == 4 && NT > 2;
+    // the next columns' base too: where B and the sums take few registers (32 rows and two accumulators: 2000 rows
+    // of 8, 1024 x 4096, rank 28, 37 us with it, 29 without)
+    constexpr bool AHEAD = VEC && KB == 1 && !(APART && MT == 2);
     __shared__ Groups g;
     __shared__ int srow[ROWS];
     __shared__ float sscale[SCALED ? ROWS : 1], sback[SCALED ? ROWS : 1];
@@ -620,7 +625,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
             } else if constexpr (VEC) {
                 load_base(n0);
             }
-            float acc[MT][4][4] = {};
+            float acc[MT][4][4] = {}, less[APART ? MT : 1][4][4] = {};
             for (int ks = 0; adapted && ks < KS; ks += KB) {
                 uint2 cur[KB][4];
                 if constexpr (VEC) {
@@ -655,8 +660,17 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
                         for (int m = 0; m < MT; ++m) {
                             const uint4 f = frag[(((ks + q) * NP + o) * MT + m) * 32 + lane];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) mma16816<T>(acc[m][j], f.x, f.y, f.z, f.w, cur[q][j].x, cur[q][j].y);
+                            for (int j = 0; j < 4; ++j)
+                                mma16816<T>(APART && o > 0 ? less[APART ? m : 0][j] : acc[m][j], f.x, f.y, f.z, f.w, cur[q][j].x, cur[q][j].y);
                         }
+            }
+            if constexpr (APART) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[m][j][i] += less[m][j][i];
             }
             if constexpr (VEC) {
                 const int col = n0 + 8 * ti;
