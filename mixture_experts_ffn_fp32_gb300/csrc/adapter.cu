@@ -782,13 +782,17 @@ cudaError_t fused_k(AdapterArgs a, cudaStream_t s) {
     using F = Fused<T, O, MT, NT, KB, VEC>;
     static bool done[64] = {};
     if (!allow_smem(adapter_mma_kernel<T, O, MT, NT, KB, VEC>, F::MOST, done)) return cudaErrorInvalidValue;
-    const long long tiles = most_tiles(a, 16 * MT), places = 2LL * num_sms();
+    const long long tiles = most_tiles(a, 16 * MT), per_sm = ctas_an_sm(F::smem(a.rp)), places = per_sm * num_sms();
     // As many CTAs a tile as there are places for, while each has 256 of d and of N; a tenth more
     // may wait, as tiles are counted for adapters that all have rows (256 rows of 64, 2048 x 8192,
     // rank 32: 4 CTAs 16 us, 2 CTAs 25; but twice the places, 256 of 128, 4096 x 4096, rank 64: 47 for 39).
-    const long long most = places * 11 / 10;
+    // Where an SM holds one (large ranks, 4096 x 4096) a third more, but no more than the places for clusters of
+    // 8, which the SMs' groups have less room for (256 rows of 32, rank 128, FP32 output, 49 tiles counted and 32
+    // there: 4 CTAs 25 us, 2 CTAs 39; 64 of 16: 8 CTAs 31 us, 4 CTAs 22; 256 of 16, rank 256: 8 CTAs 55, 4 CTAs 41).
+    const long long most = per_sm == 2 ? places * 11 / 10 : places * 4 / 3;
     a.cluster = 1;
-    while (a.cluster < 8 && tiles * a.cluster * 2 <= most && std::min(a.d, a.N) >= 512 * a.cluster) a.cluster *= 2;
+    while (a.cluster < 8 && tiles * a.cluster * 2 <= (per_sm == 1 && a.cluster == 4 ? places : most) && std::min(a.d, a.N) >= 512 * a.cluster)
+        a.cluster *= 2;
     const long long clusters = tiles * a.cluster <= most ? tiles : places / a.cluster;
     const int turns = static_cast<int>((tiles + clusters - 1) / clusters);
     return launch_pdl_cluster(adapter_mma_kernel<T, O, MT, NT, KB, VEC>, dim3(static_cast<unsigned>(clusters * a.cluster)), dim3(THREADS),

@@ -68,6 +68,10 @@ MOE_DEV int group_table(const AdapterArgs& a, bool rest, Groups& g) {
     return total;
 }
 
+// CTAs with so many bytes of dynamic shared memory that an SM holds (the registers leave two): of its 228 KB
+// each takes 1 KB more, and the table above with less than 512 bytes of other variables.
+constexpr int ctas_an_sm(size_t smem) { return smem + sizeof(Groups) + 512 + 1024 <= (228 << 10) / 2 ? 2 : 1; }
+
 struct Tile {
     int e, pos, n;  // group, first position, positions
 };

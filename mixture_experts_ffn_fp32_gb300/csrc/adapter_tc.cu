@@ -484,16 +484,23 @@ adapter_expand_tc_kernel(const __grid_constant__ AdapterArgs a, unsigned long lo
 
 long long most_tiles(int T, int E) { return std::min<long long>(T, (T + ROWS - 1) / ROWS + E + 1); }
 
+// Shared memory of the first launch: the stages, and over them the sums [ROWS][rp] and a CTA's share of them.
+// A tile of one CTA past rank 96 would keep an SM to itself; halves of it do not.
+constexpr int shrink_smem(int rp, int cluster) {
+    return std::max(STAGES * (BLOCK + rp * 128), (ROWS + ROWS / cluster) * rp * 4) + 1024;
+}
+static_assert(ctas_an_sm(shrink_smem(96, 1)) == 2 && ctas_an_sm(shrink_smem(TC_RANKS, 2)) == 2, "two CTAs an SM");
+
 template <typename T, int NP>
 cudaError_t shrink(AdapterArgs a, cudaStream_t s) {
     static bool done[64] = {};
-    // the stages, and over them the sums: [ROWS][rp] and a CTA's share
-    const int smem = std::max(STAGES * (BLOCK + a.rp * 128), 2 * ROWS * a.rp * 4) + 1024;
-    if (!allow_smem(adapter_shrink_tc_kernel<T, NP>, 132 << 10, done)) return cudaErrorInvalidValue;
+    if (!allow_smem(adapter_shrink_tc_kernel<T, NP>, shrink_smem(TC_RANKS, 2), done)) return cudaErrorInvalidValue;
     const long long tiles = most_tiles(a.T, a.E), places = 2LL * num_sms();
     // as many CTAs a tile as there are places for, while each has 256 of d
     a.cluster = 1;
     while (a.cluster < 8 && tiles * a.cluster * 2 <= places && a.d >= 512 * a.cluster) a.cluster *= 2;
+    if (a.rp > 96 && a.cluster == 1) a.cluster = 2;
+    const int smem = shrink_smem(a.rp, a.cluster);
     const long long clusters = std::min(tiles, places / a.cluster);
     const int turns = static_cast<int>((tiles + clusters - 1) / clusters);
     int cols = 32;
