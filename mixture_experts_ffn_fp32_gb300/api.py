@@ -545,6 +545,13 @@ def _at(t, name, here):
         raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{here}")
 
 
+def _scratch(ws, here):
+    """A caller's workspace: its elements are its memory, so that their number bounds it."""
+    _at(ws, "ws", here)
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+
+
 def _rows(t, name, dtype=None, shape=None):
     """A [rows, n] CUDA tensor with contiguous rows at any pitch; returns its pitch."""
     if t is None:
@@ -567,7 +574,6 @@ def _rows(t, name, dtype=None, shape=None):
     if pitch < n:
         raise ValueError(f"{name}'s rows must not overlap")
     return pitch
-
 
 
 def _empty(dtype, n, m=None):
@@ -662,7 +668,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     if weight is not None:
         _dev(weight, torch.float32, "weight", (d,), here)
     if ws is not None:
-        _at(ws, "ws", here)
+        _scratch(ws, here)
     with _on(stream, dy, x, mean, rstd, weight, ws):
         out = {"dx": _empty(x.dtype, R, d)}
         if weight_grads:
@@ -812,7 +818,7 @@ def matmul_int8(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale
         M = rows.size(0)
     cfg = _int8_config(M, Ma, K, N, E, swiglu, out_dtype)
     if ws is not None:
-        _at(ws, "ws", here)
+        _scratch(ws, here)
     with _on(stream, a, a_scale, b, b_scale, offsets, rows, ws):
         if ws is None:
             ws = _empty(torch.uint8, _int8_ws(*cfg))
@@ -972,7 +978,7 @@ def block_norm_backward(x: torch.Tensor, stats: torch.Tensor, y=None, dn=None, d
     if weight is not None:
         wp = _vector(weight, "weight", (d,), here)
     if ws is not None:
-        _at(ws, "ws", here)
+        _scratch(ws, here)
     cfg = _struct(BlockNormConfig, R, d, _DTYPES[dtype], NORMS[kind], post, form, float(alpha), 0.0)
     yo = go = None
     vectors = [None] * 5  # addresses of dgate, dpost_weight, dpost_bias, dweight, dbias
@@ -1060,7 +1066,7 @@ def adapter_add(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets
     if out is not None:
         _, os_ = _like(out, "out", otype, (T, N), here)
     if ws is not None:
-        _at(ws, "ws", here)
+        _scratch(ws, here)
     cfg = (T, d, N, r, E, _DTYPES[dtype], _DTYPES[otype])
     with _on(stream, base, x, a, b, offsets, rows, scale, out, ws):
         if ws is None:
