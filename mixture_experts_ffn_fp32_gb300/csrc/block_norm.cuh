@@ -77,7 +77,7 @@ MOE_DEV void long_stats(V value, int d, bool layer, float eps, float* scratch, i
     row_sum2<LONG_THREADS>(r1, r2, scratch, turn);
     const float rest = layer ? r1 / static_cast<float>(d) : 0.0f;  // what rounding left in m0
     rstd = rstd_of(r2 / static_cast<float>(d) - rest * rest, eps);
-    mean = m0 + rest;
+    mean = joined(m0, rest);
 }
 
 template <typename T>
