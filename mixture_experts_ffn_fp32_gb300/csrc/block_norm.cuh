@@ -598,14 +598,14 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
             gone(v);
             fn.issue(0, next, more);
             cp_async_commit();
-            const F2 nm = f2(-xmc, -xmc), r2 = f2(xrc, xrc);
+            const F2 r2 = f2(xrc, xrc);
             F2 a1 = f2(0.0f, 0.0f), a2 = a1;
             F2 w[N2];
             kept<N2, THREADS>(sw, w);
 #pragma unroll
             for (int k = 0; k < N2; ++k) {
                 // past the row's end dn is zero, and with it every term
-                u[k] = LAYER ? mul2(add2(u[k], nm), r2) : mul2(u[k], r2);
+                u[k] = mul2(LAYER ? less<VEC, TPR>(u[k], xmc, k, d, t) : u[k], r2);
                 sum[S3][k] = fma2(v[k], u[k], sum[S3][k]);
                 if constexpr (LAYER) sum[S4][k] = add2(sum[S4][k], v[k]);
                 v[k] = mul2(v[k], w[k]);
@@ -643,9 +643,9 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, const __grid_cons
             gone(u);
             fy.issue(0, next, more);
             if (post) {
-                const F2 nm = f2(-ymc, -ymc), r2 = f2(yrc, yrc);
+                const F2 r2 = f2(yrc, yrc);
 #pragma unroll
-                for (int k = 0; k < N2; ++k) u[k] = LAYER ? mul2(add2(u[k], nm), r2) : mul2(u[k], r2);
+                for (int k = 0; k < N2; ++k) u[k] = mul2(LAYER ? less<VEC, TPR>(u[k], ymc, k, d, t) : u[k], r2);
             }
             if (elem) {
                 F2 z[N2];

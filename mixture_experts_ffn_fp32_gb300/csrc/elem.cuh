@@ -234,6 +234,14 @@ MOE_DEV void row_moments(F2 (&v)[NV * VEC / 2], int d, int t, float inv_d, float
     }
 }
 
+// The k-th pair of a thread's columns less m, zeros (as loaded) past the row's end. Of a row of large values
+// without any variance (v - m) r would pass FP32's range there, and take the row's sums with it.
+template <int VEC, int TPR>
+MOE_DEV F2 less(F2 v, float m, int k, int d, int t) {
+    const float a = (2 * k / VEC * TPR + t) * VEC < d ? -m : 0.0f;
+    return add2(v, f2(a, VEC > 1 ? a : ((2 * k + 1) * TPR + t < d ? -m : 0.0f)));
+}
+
 // VEC consecutive floats (16-byte aligned where VEC >= 4).
 template <int VEC>
 MOE_DEV void load_f32(const float* p, float (&f)[VEC]) {

@@ -264,12 +264,12 @@ layer_norm_bwd_kernel(int R, int d, const T* __restrict__ dy, long long dys, con
         issue(slot, row + D * step);
         if (++slot == D) slot = 0;
         if constexpr (!KEEP) columns();
-        const F2 nm = f2(-mc, -mc), rc2 = f2(rc, rc);
+        const F2 rc2 = f2(rc, rc);
         F2 a1 = f2(0.0f, 0.0f), a2 = a1;
 #pragma unroll
         for (int k = 0; k < N2; ++k) {
             // past the row's end dy is zero, and with it every term
-            xh[k] = mul2(add2(xh[k], nm), rc2);
+            xh[k] = mul2(less<VEC, TPR>(xh[k], mc, k, d, t), rc2);
             dg2[k] = fma2(g[k], xh[k], dg2[k]);
             db2[k] = add2(db2[k], g[k]);
             g[k] = mul2(g[k], ga[k]);
