@@ -488,7 +488,9 @@ typedef struct moe_block_norm_config {
     float eps;      /* >= 0 */
 } moe_block_norm_config;
 
-/* The norms on both sides of a block, fused with its gate and the residual:
+/* The norms on both sides of a block, fused with its gate and the residual (a layer
+ * norm by itself is moe_layer_norm, which is made for it; an RMS norm by itself is
+ * this call without y):
  *     z  = post ? Norm(y; post_w, post_b) : y       y: the block's output
  *     x' = alpha x + gate z                         the new residual stream
  *     n  = Norm(x'; w, b)                           the next block's input
@@ -549,9 +551,13 @@ moe_status moe_adapter_add_workspace_size(const moe_adapter_config* cfg, size_t*
 /* Low-rank adapters of many requests beside a shared projection, whose result
  * is base:
  *     out[t] = base[t] + scale[e] (x[t] a[e]^T) b[e]^T,   e the adapter of row t
- * FP32 sums, both products; out rounded once. Rows are grouped by adapter:
- * those of adapter e are rows[offsets[e]] .. rows[offsets[e + 1] - 1], and rows
- * from position offsets[E] on have none: out[t] = base[t].
+ * FP32 sums, both products; out rounded once. With an FP32 output the second
+ * product takes the inner values scale x a^T whole; with a 16-bit one it takes 16
+ * of their 24 bits (BF16; at most 2^-16 of each is left out, where rounding out
+ * takes 2^-8) or 22 (FP16; what lies 2^-39 below the row's largest is zero).
+ * Infinities and NaN go as in the formula. Rows are grouped by adapter: those of
+ * adapter e are rows[offsets[e]] .. rows[offsets[e + 1] - 1], and rows from
+ * position offsets[E] on have none: out[t] = base[t].
  *   x [T, d], a [E, r, d], b [E, N, r] (contiguous); scale [E] FP32 or NULL (1);
  *   offsets [E + 1] int32, ascending from 0, at most T; rows [T] int32, each row
  *   once, or NULL (row i at position i); base, out [T, N] at any pitch, base NULL:
@@ -565,6 +571,9 @@ moe_status moe_adapter_add_workspace_size(const moe_adapter_config* cfg, size_t*
  * written, and what a row named twice holds is not specified. A bounded device
  * wait that runs out makes the outputs that are not stored yet NaN and sets
  * MOE_ERR_TIMEOUT.
+ *   Rows on 16 bytes and widths and ranks that are multiples of 8 serve best: others
+ * never reach the tensor-core form of many rows. a and b whose rank is padded with
+ * zeros to a multiple of 8 give the same result of rows without infinities.
  *   The form is chosen from rows, ranks, adapters and alignment; the environment
  * variable MOE_ADAPTER_FORM, read at each call, overrides it for tests and tuning
  * ("few", "many": rows; "many" only where 16-byte rows, widths and ranks that are

@@ -1037,7 +1037,8 @@ def adapter_add(base, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, offsets
     adapter e at positions offsets[e] to offsets[e + 1] (int32 [E + 1]); rows from
     offsets[E] on have no adapter. ``dispatch`` of the rows' adapter ids with K = 1 and
     E + 1 experts, the last for rows without one, gives both (its offsets without the
-    last entry, its sorted_token). out: [T, N] to write, or base itself for an update in
+    last entry, its sorted_token). Rows on 16 bytes, widths and ranks that are multiples
+    of 8 serve best (see the header). out: [T, N] to write, or base itself for an update in
     place (allocated when None). ws: see alloc_adapter_workspace. When None one is
     allocated for the call and its error word is not read."""
     here = _here(stream)

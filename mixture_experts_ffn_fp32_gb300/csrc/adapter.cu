@@ -3,9 +3,12 @@
 //   out[t] = base[t] + s_e (x[t] A_e^T) B_e^T,   e the adapter of row t
 //
 // Rows come grouped by adapter: group e is the positions offsets[e] to offsets[e + 1]
-// of `rows`; positions from offsets[E] on have no adapter. Two launches: the first
-// computes v = s_e x[t] A_e^T into the workspace (by position, FP32), the second adds
-// v B_e^T to base.
+// of `rows`; positions from offsets[E] on have no adapter. Three forms:
+//   FP32: two launches, the first leaves the inner values v = s_e x[t] A_e^T in the workspace
+//     (FP32, by position), the second adds v B_e^T to base.
+//   16-bit types, few rows: one launch; v stays in shared memory.
+//   16-bit types, many rows (adapter_tc.cu): two launches, v in pieces of the operands' type
+//     in the workspace.
 #include <stdlib.h>
 
 #include "adapter.cuh"
@@ -305,7 +308,8 @@ struct Fused {
     static constexpr int WARPS = THREADS / 32, ROWS = 16 * MT;
     static constexpr int NP = sizeof(O) == 4 ? 3 : 2;
     // Chunks of 32 of d a warp has in flight: on their way to shared memory, each lane's fragments to
-    // its own 16-byte slots (two CTAs an SM leave 72 KB each), or, where rows are on no 16 bytes, to
+    // its own 16-byte slots (two CTAs an SM leave 72 KB each, which
+    // they are up to rank 64; larger ranks take more for v and its pieces, see ctas_an_sm), or, where rows are on no 16 bytes, to
     // registers.
     static constexpr int FRAGS = 2 * MT + NT, U = FRAGS <= 4 ? 4 : FRAGS <= 6 ? 3 : 2;
     static constexpr int RING = VEC ? WARPS * U * FRAGS * 512 : 0;
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 2) adapter_mma_kernel(const __grid_co
     constexpr bool SCALED = __is_same(T, __half);
     constexpr int STEP = 32 * WARPS;
     // FP32 outputs of more than 16 ranks: the small pieces of v are summed apart, since what an addition
-    // drops grows with the sum (in one accumulator, 256 rows of 128, rank 64: 2.7e-7 off for 1.3e-7)
+    // drops grows with the sum (in one accumulator, 256 rows of 128, rank 64: 2.7e-7 off for 1.9e-7)
     constexpr bool APART = sizeof(O) == 4 && NT > 2;
     // the next columns' base too: where B and the sums take few registers (32 rows and two accumulators: 2000 rows
     // of 8, 1024 x 4096, rank 28, 37 us with it, 29 without)

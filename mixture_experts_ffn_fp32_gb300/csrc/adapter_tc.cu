@@ -13,16 +13,19 @@
 // tensor memory ends with 8 consecutive columns of its rows.
 //
 // Measured (one GB300, calls among others): 16384 rows of 16 adapters (a tenth of them without),
-// 2048 x 2816, rank 16, 58 us: 20 for v (x at 3 TB/s: a wave of 16 steps a CTA, 4 us before the
+// 2048 x 2816, rank 16, 60 us: 20 for v (x at 3 TB/s: a wave of 16 steps a CTA, 4 us before the
 // first and 4 for the cluster behind the last) and 39 for the second product, which a plain copy of
-// base to out takes 36 for. 8192 rows of 4, 4096 x 4096, rank 64, 59 us (25 + 36). What its loads
-// in flight find of L1 counts: see STAGES.
+// base to out takes 36 for. 8192 rows of 4, 4096 x 4096, rank 64, 61 us (24 + 37). What its loads
+// in flight find of L1 counts: see STAGES. Ranks that are no multiple of 8 do not come here: rank 12 68 us, rank 4
+// 66, and 60 each when the caller pads them.
 //
 // Waits for MMAs are bounded (common.cuh). One that runs out ends the CTA's copies into the stages and
 // its MMAs, leaves NaN in what is not stored yet, and the MMAs already issued are waited for once more
 // (drain) before shared or tensor memory has another use. The other waits always end: cluster
 // barriers because every CTA makes the same number of turns, whatever the offsets and whatever
-// ran out; allocations of tensor memory because who holds some waits for no other CTA's.
+// ran out; allocations of tensor memory because the CTAs of these kernels that an SM has room for
+// take its 512 columns at most together, and the kernels here that take more than 256 leave no shared
+// memory beside them.
 #include <math_constants.h>
 
 #include "adapter.cuh"
