@@ -308,9 +308,8 @@ struct Fused {
     static constexpr int WARPS = THREADS / 32, ROWS = 16 * MT;
     static constexpr int NP = sizeof(O) == 4 ? 3 : 2;
     // Chunks of 32 of d a warp has in flight: on their way to shared memory, each lane's fragments to
-    // its own 16-byte slots (two CTAs an SM leave 72 KB each, which
-    // they are up to rank 64; larger ranks take more for v and its pieces, see ctas_an_sm), or, where rows are on no 16 bytes, to
-    // registers.
+    // its own 16-byte slots (two CTAs an SM leave 72 KB each; ranks past 64 take more for v and its
+    // pieces, see ctas_an_sm), or, where rows are on no 16 bytes, to registers.
     static constexpr int FRAGS = 2 * MT + NT, U = FRAGS <= 4 ? 4 : FRAGS <= 6 ? 3 : 2;
     static constexpr int RING = VEC ? WARPS * U * FRAGS * 512 : 0;
     // The same slots then take B: steps under way, of 16-byte slots each.
